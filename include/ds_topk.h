@@ -258,6 +258,146 @@ ds_status ds_topk_noalloc(const void* x, int32_t dtype, int64_t rows, int64_t N,
 /* Size of the fixed scratch array ds_topk_noalloc uses, in bytes. */
 size_t ds_noalloc_scratch_bytes(void);
 
+/* ======================================================================================
+ * Operators around the top-k in a decoding step: the experts' gate, the verification of
+ * drafted tokens, and a key/value cache in 4 bits with the attention that reads it.
+ *
+ * As above: calls are asynchronous on `stream`, errors found on the host are returned before
+ * anything is launched, inputs and outputs are caller-owned device memory, and a call may be
+ * captured in a graph (ds_cache_attention once it has run on that stream with arguments that
+ * need as much workspace, see there).  Launches are programmatic dependent ones: a kernel
+ * touches memory only once the kernel before it on the stream has completed.
+ * Pointers are aligned to their element unless a call says otherwise (DS_ERR_ALIGNMENT).
+ * Logits, keys, values and queries are expected finite, -inf in logits excepted; other values
+ * give undefined numbers in their own rows, never a fault.
+ * ==================================================================================== */
+
+typedef enum { DS_SOFTMAX = 0, DS_SIGMOID = 1 } ds_scoring;
+typedef enum { DS_GROUP_MAX = 0, DS_GROUP_TOP2 = 1 } ds_group_score;
+
+/*
+ * ds_route -- the gate of a mixture of experts: each row's k best experts and their weights.
+ * Scores of a row x of E logits: s = softmax(x) (DS_SOFTMAX) or 1 / (1 + exp(-x)) (DS_SIGMOID).
+ * Choice values: s + bias, or x itself without a bias (s rises with x).  groups > 1: experts
+ * lie in `groups` runs of E / groups; a run's score is its largest choice value (DS_GROUP_MAX)
+ * or the sum of its two largest (DS_GROUP_TOP2; without a bias of its two largest s), and only
+ * experts of the topk_groups best runs are eligible.  The k eligible experts of the largest
+ * choice values are returned in descending order; every tie, of experts or groups, goes to the
+ * lower index, and -0 equals +0.  weight_j = scale * s_j / (renormalise ? sum of the k s : 1);
+ * a sum of 0 gives weights of 0.  The bias moves the choice only.
+ *   logits, dtype   row r starts at element r * row_stride (any stride >= E)
+ *   rows            >= 0
+ *   E, k            1 <= k <= min(E / groups * topk_groups, 32); E <= 512, groups <= 32
+ *   bias            E floats, or NULL
+ *   out_weights     rows * k floats;  out_experts  rows * k int32
+ *   counts          E int32 or NULL: the number of rows that chose each expert is ADDED to it
+ */
+ds_status ds_route(const void* logits, int32_t dtype, int64_t rows, int32_t E, int64_t row_stride, int32_t k,
+                   int32_t scoring, const float* bias, int32_t groups, int32_t topk_groups, int32_t group_score,
+                   int32_t renormalise, float scale, float* out_weights, int32_t* out_experts, int32_t* counts,
+                   cudaStream_t stream);
+
+/*
+ * ds_route_backward -- gradient of ds_route's weights with respect to its logits, given the
+ * experts it chose (the choice is held constant, so the bias has no gradient).
+ *   grad_weights    rows * k floats
+ *   experts         rows * k int32, distinct within a row; an index outside [0, E) has no part
+ *   grad_logits     rows of E elements of dtype, row r at element r * grad_stride (>= E);
+ *                   every element is written; must not overlap logits
+ */
+ds_status ds_route_backward(const float* grad_weights, const void* logits, int32_t dtype, int64_t rows, int32_t E,
+                            int64_t row_stride, int32_t k, const int32_t* experts, int32_t scoring,
+                            int32_t renormalise, float scale, void* grad_logits, int64_t grad_stride,
+                            cudaStream_t stream);
+
+/*
+ * ds_verify_drafts -- speculative sampling's verification, per sequence b.
+ * Place i = 0 .. S has target logits x_i (the row after i accepted drafts), p_i =
+ * softmax(x_i / temperature), one-hot at the first maximum where the temperature is <= 0.
+ * Draft i (token t_i, drawn from q_i) is accepted iff drafts 0 .. i-1 were and
+ * uniforms[b, i] * q_i(t_i) < p_i(t_i).  At the first draft that is not accepted, or after the
+ * sequence's last draft, one more token is emitted: argmax_v r_v / noise[b, v], with
+ * r = max(p_i - q_i, 0) at a refused draft (p_i if that is 0 everywhere) and r = p_i after the
+ * last; ties to the lowest v.  With exponential noise the tokens are distributed as samples
+ * of the target.
+ *   logits, dtype    place i of sequence b starts at element b * seq_stride + i * row_stride;
+ *                    -inf excludes a token.  A row of -inf alone: refused, token -1, probability 0
+ *   sequences        >= 0; drafts_per_sequence S >= 0 (<= 1024); 1 <= V <= 2^30
+ *   drafts           [sequences, S] int32; a token outside [0, V) is refused
+ *   draft_lens       [sequences] int32 drafts of each sequence (clamped to 0 .. S), or NULL: S
+ *   draft_probs      q, floats, draft i of sequence b at b * probs_seq_stride + i *
+ *                    probs_row_stride; NULL: q_i is one-hot at t_i (a looked-up draft)
+ *   uniforms         [sequences, S] floats in [0, 1)
+ *   noise            [sequences, V] positive floats, sequence b at b * noise_stride: independent
+ *                    draws of the exponential distribution
+ *   temperatures     [sequences] floats, or NULL: `temperature` (>= 0, finite) for all
+ *   out_tokens       [sequences, S + 1] int32: the accepted drafts, the emitted token, then -1
+ *   out_accepted     [sequences] int32: the number of accepted drafts
+ *   out_probs        [sequences, S + 1] floats or NULL: p_i of each token, 0 after the last
+ */
+ds_status ds_verify_drafts(const void* logits, int32_t dtype, int64_t sequences, int32_t drafts_per_sequence,
+                           int64_t V, int64_t seq_stride, int64_t row_stride, const int32_t* drafts,
+                           const int32_t* draft_lens, const float* draft_probs, int64_t probs_seq_stride,
+                           int64_t probs_row_stride, const float* uniforms, const float* noise, int64_t noise_stride,
+                           const float* temperatures, float temperature, int32_t* out_tokens, int32_t* out_accepted,
+                           float* out_probs, cudaStream_t stream);
+
+/*
+ * The 4-bit cache.  A key or value row of D numbers x is held as D codes c in 0 .. 15 and a
+ * pair (s, m) of bf16, standing for s * c + m:  m = bf16(min x), s = bf16((max x - m) / 15),
+ * c = clamp(rint((x - m) / s), 0, 15) (0 where s < 2^-126), the quotients as fp32 products with
+ * 1/15 and 1/s.  Layout, caller-owned:
+ *   cache   [pages][heads][page][2][D / 2] bytes, 16-byte aligned: key, then value; number 2 j
+ *           in the low half of byte j, 2 j + 1 in the high half
+ *   scales  [pages][heads][page][4] bf16, 8-byte aligned: key s, key m, value s, value m
+ * page is a power of two, D 64 or 128 (DS_ERR_UNSUPPORTED).  Token slot t is place t % page of
+ * page t / page.
+ *
+ * ds_cache_store writes `tokens` tokens' keys and values (token i, head h at element
+ * i * token_stride + h * head_stride; base and strides multiples of 16 bytes) to slots[i]; a
+ * slot outside [0, pages * page) is skipped (a padded token).  Slots of one call are distinct.
+ * ds_cache_load reads slots back as dtype, [tokens, heads, D] each, 16-byte aligned; a slot
+ * outside gives zeros.
+ */
+ds_status ds_cache_store(const void* k, const void* v, int32_t dtype, int64_t tokens, int32_t heads, int32_t D,
+                         int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         void* cache, void* scales, int64_t pages, int32_t page, const int32_t* slots,
+                         cudaStream_t stream);
+ds_status ds_cache_load(const void* cache, const void* scales, int64_t pages, int32_t page, const int32_t* slots,
+                        int64_t tokens, int32_t heads, int32_t D, int32_t dtype, void* out_k, void* out_v,
+                        cudaStream_t stream);
+
+/*
+ * ds_cache_attention -- attention of each sequence's newest tokens over the 4-bit cache.
+ * Token i of the `tokens` of sequence b sees the positions below lens[b] - (tokens - 1 - i)
+ * (its own key and value are stored already), or those of them that its `indices` list:
+ *   out = sum_j P_j v_j,  P = softmax_j(scale * q . k_j),  lse = log sum_j exp(scale * q . k_j).
+ * Query head h reads key head h / (q_heads / heads).  A token that sees nothing has out 0 and
+ * lse -inf.
+ *   q, dtype     token i, head h of sequence b at element b * q_seq_stride + i * q_token_stride
+ *                + h * q_head_stride, D numbers
+ *   table        [sequences, table_width] int32 (row stride table_stride): position j of sequence
+ *                b lies in page table[b, j / page]; a position whose page is outside [0, pages)
+ *                is not seen
+ *   lens         [sequences] int32, clamped to 0 .. table_width * page
+ *   indices      [sequences, tokens, K] int32 positions (as ds_topk returns them), or NULL; one
+ *                outside the visible positions (-1 as padding) is not seen, one listed twice
+ *                counts twice
+ *   scale        finite;  out  [sequences, tokens, q_heads, D] dtype;  out_lse  [sequences,
+ *                tokens, q_heads] floats or NULL
+ * Products are exact in the codes; q enters in its own precision, weights in at least 16 bits,
+ * all sums in fp32.  Positions are split over CTAs whose partial results lie in a library-owned
+ * workspace of (device, stream), grown with cudaMalloc as ds_topk's is: a call under stream
+ * capture that would have to grow it returns DS_ERR_WORKSPACE.  pages * page * heads < 2^32 - 1,
+ * table_width * page <= 2^30.
+ */
+ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads,
+                             int32_t D, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+                             const void* cache, const void* scales, int64_t pages, int32_t heads, int32_t page,
+                             const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lens,
+                             const int32_t* indices, int32_t K, float scale, void* out, float* out_lse,
+                             cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

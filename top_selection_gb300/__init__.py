@@ -20,11 +20,18 @@ __all__ = [
     "ds_workspace_bytes", "ds_get_device_status", "ds_status_string", "ds_version",
     "ds_block_order", "ds_wait_probe", "ds_topk_noalloc", "ds_noalloc_scratch_bytes", "topk",
     "library_path", "load",
+    "DS_SOFTMAX", "DS_SIGMOID", "DS_GROUP_MAX", "DS_GROUP_TOP2", "ds_topk_sample", "topk_sample",
+    "ds_route", "ds_route_backward", "ds_verify_drafts", "ds_cache_store", "ds_cache_load", "ds_cache_attention",
+    "route", "route_backward", "verify_drafts", "cache_store", "cache_load", "cache_attention",
 ]
 
 DS_BF16 = 0
 DS_FP32 = 1
 DS_NSTAT = 8
+DS_SOFTMAX = 0
+DS_SIGMOID = 1
+DS_GROUP_MAX = 0
+DS_GROUP_TOP2 = 1
 
 STATUS_NAMES = {
     0: "DS_OK", 1: "DS_ERR_INVALID_ARG", 2: "DS_ERR_ALIGNMENT", 3: "DS_ERR_UNSUPPORTED",
@@ -106,6 +113,21 @@ def load():
         lib.ds_topk_sample.restype = ctypes.c_int
         lib.ds_noalloc_scratch_bytes.argtypes = []
         lib.ds_noalloc_scratch_bytes.restype = ctypes.c_size_t
+        f32 = ctypes.c_float
+        lib.ds_route.argtypes = [vp, i32, i64, i32, i64, i32, i32, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp]
+        lib.ds_route.restype = ctypes.c_int
+        lib.ds_route_backward.argtypes = [vp, vp, i32, i64, i32, i64, i32, vp, i32, i32, f32, vp, i64, vp]
+        lib.ds_route_backward.restype = ctypes.c_int
+        lib.ds_verify_drafts.argtypes = [vp, i32, i64, i32, i64, i64, i64, vp, vp, vp, i64, i64, vp, vp, i64, vp, f32,
+                                         vp, vp, vp, vp]
+        lib.ds_verify_drafts.restype = ctypes.c_int
+        lib.ds_cache_store.argtypes = [vp, vp, i32, i64, i32, i32, i64, i64, i64, i64, vp, vp, i64, i32, vp, vp]
+        lib.ds_cache_store.restype = ctypes.c_int
+        lib.ds_cache_load.argtypes = [vp, vp, i64, i32, vp, i64, i32, i32, i32, vp, vp, vp]
+        lib.ds_cache_load.restype = ctypes.c_int
+        lib.ds_cache_attention.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, i64, vp, vp, i64, i32, i32, vp, i64,
+                                           i64, vp, vp, i32, f32, vp, vp, vp]
+        lib.ds_cache_attention.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -273,3 +295,267 @@ def topk_sample(x, k: int, temperature: float, uniforms, B: int = 0, B2: int = 0
     if st != 0:
         raise DSError(st, "ds_topk_sample")
     return token, prob, vals, idx
+
+
+# --------------------------------------------- operators around the top-k ----------
+
+def ds_route(logits, dtype, rows, E, row_stride, k, scoring, bias, groups, topk_groups, group_score, renormalise,
+             scale, out_weights, out_experts, counts=0, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_route(int(logits) or None, dtype, rows, E, row_stride, k, scoring, int(bias) or None, groups,
+                           topk_groups, group_score, int(bool(renormalise)), float(scale), int(out_weights) or None,
+                           int(out_experts) or None, int(counts) or None, int(stream) or None)
+
+
+def ds_route_backward(grad_weights, logits, dtype, rows, E, row_stride, k, experts, scoring, renormalise, scale,
+                      grad_logits, grad_stride, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_route_backward(int(grad_weights) or None, int(logits) or None, dtype, rows, E, row_stride, k,
+                                    int(experts) or None, scoring, int(bool(renormalise)), float(scale),
+                                    int(grad_logits) or None, grad_stride, int(stream) or None)
+
+
+def ds_verify_drafts(logits, dtype, sequences, drafts_per_sequence, V, seq_stride, row_stride, drafts, draft_lens,
+                     draft_probs, probs_seq_stride, probs_row_stride, uniforms, noise, noise_stride, temperatures,
+                     temperature, out_tokens, out_accepted, out_probs=0, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_verify_drafts(int(logits) or None, dtype, sequences, drafts_per_sequence, V, seq_stride,
+                                   row_stride, int(drafts) or None, int(draft_lens) or None, int(draft_probs) or None,
+                                   probs_seq_stride, probs_row_stride, int(uniforms) or None, int(noise) or None,
+                                   noise_stride, int(temperatures) or None, float(temperature),
+                                   int(out_tokens) or None, int(out_accepted) or None, int(out_probs) or None,
+                                   int(stream) or None)
+
+
+def ds_cache_store(k, v, dtype, tokens, heads, D, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+                   cache, scales, pages, page, slots, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_cache_store(int(k) or None, int(v) or None, dtype, tokens, heads, D, k_token_stride,
+                                 k_head_stride, v_token_stride, v_head_stride, int(cache) or None,
+                                 int(scales) or None, pages, page, int(slots) or None, int(stream) or None)
+
+
+def ds_cache_load(cache, scales, pages, page, slots, tokens, heads, D, dtype, out_k, out_v, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_cache_load(int(cache) or None, int(scales) or None, pages, page, int(slots) or None, tokens,
+                                heads, D, dtype, int(out_k) or None, int(out_v) or None, int(stream) or None)
+
+
+def ds_cache_attention(q, dtype, sequences, tokens, q_heads, D, q_seq_stride, q_token_stride, q_head_stride, cache,
+                       scales, pages, heads, page, table, table_width, table_stride, lens, indices, K, scale, out,
+                       out_lse=0, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_cache_attention(int(q) or None, dtype, sequences, tokens, q_heads, D, q_seq_stride,
+                                     q_token_stride, q_head_stride, int(cache) or None, int(scales) or None, pages,
+                                     heads, page, int(table) or None, table_width, table_stride, int(lens) or None,
+                                     int(indices) or None, K, float(scale), int(out) or None, int(out_lse) or None,
+                                     int(stream) or None)
+
+
+_SCORING = {"softmax": DS_SOFTMAX, "sigmoid": DS_SIGMOID}
+_GROUP_SCORE = {"max": DS_GROUP_MAX, "top2": DS_GROUP_TOP2}
+
+
+def _float_code(t, what):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DS_BF16
+    if t.dtype == torch.float32:
+        return DS_FP32
+    raise TypeError(f"{what}: unsupported dtype {t.dtype}: bfloat16 and float32 only")
+
+
+def _want(t, what, shape, dtype, like, strided=False):
+    """Checks an argument tensor: dtype, shape, the device of `like`, and contiguity (or,
+    with `strided`, a unit last stride only).  None stays None."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must have dtype {dtype}, not {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{what} must be on {like.device} (there is no CPU path)")
+    if t.numel() and not (t.stride(-1) == 1 or t.shape[-1] == 1 if strided else t.is_contiguous()):
+        raise ValueError(f"{what} must {'have unit stride in its last dimension' if strided else 'be contiguous'}")
+
+
+def _cuda(t, what, dims):
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor (there is no CPU path)")
+    if t.dim() != dims:
+        raise ValueError(f"{what} must have {dims} dimensions, not {t.dim()}")
+    if t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{what} must have unit stride in its last dimension")
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _stream_of(t, stream):
+    import torch
+    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
+
+
+def _check(status, what):
+    if status != 0:
+        raise DSError(status, what)
+
+
+def route(logits, k: int, scoring: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+          group_score: str = "max", renormalise: bool = True, scale: float = 1.0, counts=None, stream=None):
+    """The experts' gate: each row's k best experts of ``logits`` (rows, E) and their weights.
+
+    Scores are a softmax or a logistic function of the logits; ``bias`` (E,) is added for the
+    choice only; with ``groups`` > 1 only experts of the ``topk_groups`` best groups are
+    eligible (a group's score: "max", or "top2", the sum of its two largest).  Weights are
+    ``scale`` times the scores, divided by their sum over the chosen with ``renormalise``.
+    ``counts`` (E,) int32, if given, is added the number of rows that chose each expert.
+    Returns (weights (rows, k) float32, experts (rows, k) int32), best first, ties to the lower
+    index."""
+    import torch
+    _cuda(logits, "logits", 2)
+    code = _float_code(logits, "logits")
+    rows, E = logits.shape
+    if scoring not in _SCORING or group_score not in _GROUP_SCORE:
+        raise ValueError('scoring is "softmax" or "sigmoid", group_score "max" or "top2"')
+    _want(bias, "bias", (E,), torch.float32, logits)
+    _want(counts, "counts", (E,), torch.int32, logits)
+    weights = torch.empty((rows, max(k, 0)), dtype=torch.float32, device=logits.device)
+    experts = torch.empty((rows, max(k, 0)), dtype=torch.int32, device=logits.device)
+    _check(ds_route(_ptr(logits), code, rows, E, logits.stride(0) if rows > 1 else E, k, _SCORING[scoring],
+                    _ptr(bias), groups, topk_groups, _GROUP_SCORE[group_score], renormalise, scale, _ptr(weights),
+                    _ptr(experts), _ptr(counts), _stream_of(logits, stream)), "ds_route")
+    return weights, experts
+
+
+def route_backward(grad_weights, logits, experts, scoring: str = "softmax", renormalise: bool = True,
+                   scale: float = 1.0, stream=None):
+    """The gradient of ``route``'s weights with respect to its ``logits`` (rows, E), for the
+    ``experts`` it chose: (rows, E) in the logits' dtype.  Other arguments as in ``route``."""
+    import torch
+    _cuda(logits, "logits", 2)
+    code = _float_code(logits, "logits")
+    if scoring not in _SCORING:
+        raise ValueError('scoring is "softmax" or "sigmoid"')
+    rows, E = logits.shape
+    k = experts.shape[-1]
+    _want(experts, "experts", (rows, k), torch.int32, logits)
+    _want(grad_weights, "grad_weights", (rows, k), torch.float32, logits)
+    grad = torch.empty((rows, E), dtype=logits.dtype, device=logits.device)
+    _check(ds_route_backward(_ptr(grad_weights), _ptr(logits), code, rows, E, logits.stride(0) if rows > 1 else E, k,
+                             _ptr(experts), _SCORING[scoring], renormalise, scale, _ptr(grad), E,
+                             _stream_of(logits, stream)), "ds_route_backward")
+    return grad
+
+
+def verify_drafts(logits, drafts, uniforms, noise, draft_probs=None, draft_lens=None, temperature=1.0, stream=None):
+    """Verifies each sequence's drafted tokens against the target's ``logits`` (B, S + 1, V) and
+    emits one more token: speculative sampling with the caller's random numbers.
+
+    ``drafts`` (B, S) int32, drawn from ``draft_probs`` (B, S, V) float32 (None: looked-up
+    drafts, one-hot); ``draft_lens`` (B,) int32 drafts of each sequence (None: S);
+    ``uniforms`` (B, S) in [0, 1); ``noise`` (B, V) exponential draws; ``temperature`` a number or
+    a (B,) float32 tensor, 0 for the likeliest token.  Returns (tokens (B, S + 1) int32 -- the
+    accepted drafts, the emitted token, then -1 -- accepted (B,) int32, and the target's
+    probability of each token (B, S + 1) float32)."""
+    import torch
+    _cuda(logits, "logits", 3)
+    code = _float_code(logits, "logits")
+    B, rows, V = logits.shape
+    S = rows - 1
+    if S < 0:
+        raise ValueError("logits must have at least one row per sequence")
+    _want(drafts, "drafts", (B, S), torch.int32, logits)
+    _want(uniforms, "uniforms", (B, S), torch.float32, logits)
+    _want(noise, "noise", (B, V), torch.float32, logits, strided=True)
+    _want(draft_probs, "draft_probs", (B, S, V), torch.float32, logits, strided=True)
+    _want(draft_lens, "draft_lens", (B,), torch.int32, logits)
+    temps = temperature if isinstance(temperature, torch.Tensor) else None
+    _want(temps, "temperature", (B,), torch.float32, logits)
+    tokens = torch.empty((B, S + 1), dtype=torch.int32, device=logits.device)
+    accepted = torch.empty(B, dtype=torch.int32, device=logits.device)
+    probs = torch.empty((B, S + 1), dtype=torch.float32, device=logits.device)
+    q_seq, q_row = (0, V) if draft_probs is None else (draft_probs.stride(0), draft_probs.stride(1) if S > 1 else V)
+    _check(ds_verify_drafts(_ptr(logits), code, B, S, V, logits.stride(0), logits.stride(1) if rows > 1 else V,
+                            _ptr(drafts), _ptr(draft_lens), _ptr(draft_probs), q_seq, q_row, _ptr(uniforms),
+                            _ptr(noise), noise.stride(0) if B > 1 else V, _ptr(temps),
+                            0.0 if temps is not None else temperature, _ptr(tokens), _ptr(accepted), _ptr(probs),
+                            _stream_of(logits, stream)), "ds_verify_drafts")
+    return tokens, accepted, probs
+
+
+def _cache_shape(cache, scales):
+    """(pages, heads, page, D) of a 4-bit cache: ``cache`` (pages, heads, page, 2, D / 2) uint8
+    and ``scales`` (pages, heads, page, 4) bfloat16, both contiguous."""
+    import torch
+    _cuda(cache, "cache", 5)
+    pages, heads, page, two, half = cache.shape
+    _want(cache, "cache", (pages, heads, page, 2, half), torch.uint8, cache)
+    _want(scales, "scales", (pages, heads, page, 4), torch.bfloat16, cache)
+    return pages, heads, page, 2 * half
+
+
+def cache_store(k, v, cache, scales, slots, stream=None) -> None:
+    """Writes keys and values ``k``, ``v`` (tokens, heads, D) to the ``slots`` (tokens,) int32 of a
+    4-bit cache: ``cache`` (pages, heads, page, 2, D / 2) uint8 and ``scales`` (pages, heads, page,
+    4) bfloat16.  Slot t is place t % page of page t / page; a negative slot is skipped."""
+    import torch
+    pages, heads, page, D = _cache_shape(cache, scales)
+    _cuda(k, "k", 3)
+    code = _float_code(k, "k")
+    T = k.shape[0]
+    _want(k, "k", (T, heads, D), k.dtype, cache, strided=True)
+    _want(v, "v", (T, heads, D), k.dtype, cache, strided=True)
+    _want(slots, "slots", (T,), torch.int32, cache)
+    strides = [s if n > 1 else D * heads for t in (k, v) for s, n in zip(t.stride()[:2], t.shape[:2])]
+    _check(ds_cache_store(_ptr(k), _ptr(v), code, T, heads, D, *strides, _ptr(cache), _ptr(scales), pages, page,
+                          _ptr(slots), _stream_of(cache, stream)), "ds_cache_store")
+
+
+def cache_load(cache, scales, slots, dtype=None, stream=None):
+    """Reads the ``slots`` (tokens,) int32 of a 4-bit cache back: keys and values (tokens, heads,
+    D) in ``dtype`` (bfloat16, the default, or float32); zeros for a slot outside the cache."""
+    import torch
+    pages, heads, page, D = _cache_shape(cache, scales)
+    T = slots.shape[0]
+    _want(slots, "slots", (T,), torch.int32, cache)
+    k = torch.empty((T, heads, D), dtype=dtype or torch.bfloat16, device=cache.device)
+    v = torch.empty_like(k)
+    _check(ds_cache_load(_ptr(cache), _ptr(scales), pages, page, _ptr(slots), T, heads, D, _float_code(k, "dtype"),
+                         _ptr(k), _ptr(v), _stream_of(cache, stream)), "ds_cache_load")
+    return k, v
+
+
+def cache_attention(q, cache, scales, table, lens, indices=None, scale=None, stream=None):
+    """Attention of each sequence's newest tokens ``q`` (B, Q, query heads, D) over a 4-bit cache.
+
+    ``table`` (B, width) int32 holds the page of each run of ``page`` positions, ``lens`` (B,) int32
+    the positions stored, the Q new ones among them: token i sees those below lens - (Q - 1 - i),
+    or those of them that ``indices`` (B, Q, K) int32 lists (``topk``'s columns; -1 pads).  ``scale``
+    is 1 / sqrt(D) by default.  Returns (out (B, Q, query heads, D) in q's dtype, lse (B, Q, query
+    heads) float32); a token that sees nothing gives 0 and -inf."""
+    import torch
+    pages, heads, page, D = _cache_shape(cache, scales)
+    _cuda(q, "q", 4)
+    code = _float_code(q, "q")
+    B, Q, hq, _ = q.shape
+    _want(q, "q", (B, Q, hq, D), q.dtype, cache, strided=True)
+    if table.dim() != 2:
+        raise ValueError("table must have 2 dimensions")
+    width = table.shape[1]
+    _want(table, "table", (B, width), torch.int32, cache, strided=True)
+    _want(lens, "lens", (B,), torch.int32, cache)
+    K = 0 if indices is None else indices.shape[-1]
+    _want(indices, "indices", (B, Q, K), torch.int32, cache)
+    if indices is not None and K == 0:  # a list of nothing: one entry that is not seen
+        indices, K = torch.full((B, Q, 1), -1, dtype=torch.int32, device=q.device), 1
+    out = torch.empty((B, Q, hq, D), dtype=q.dtype, device=q.device)
+    lse = torch.empty((B, Q, hq), dtype=torch.float32, device=q.device)
+    _check(ds_cache_attention(_ptr(q), code, B, Q, hq, D, q.stride(0), q.stride(1), q.stride(2), _ptr(cache),
+                              _ptr(scales), pages, heads, page, _ptr(table), width,
+                              table.stride(0) if B > 1 else width, _ptr(lens), _ptr(indices), K,
+                              1.0 / D ** 0.5 if scale is None else scale, _ptr(out), _ptr(lse),
+                              _stream_of(q, stream)), "ds_cache_attention")
+    return out, lse

@@ -4,13 +4,15 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libds_topk.so")
-SOURCES = [os.path.join(CSRC, "ds_topk.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("ds_topk.cu", "ds_route.cu", "ds_verify.cu", "ds_cache.cu",
+                                           "ds_attend.cu")]
 
 
 def deps() -> list:
@@ -43,10 +45,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS, "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+    # one nvcc per source, all at once, then a link
+    compile_flags = [f for f in NVCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory(prefix="ds_build_") as work:
+        objects = [os.path.join(work, os.path.basename(s) + ".o") for s in SOURCES]
+        cmds = [[_nvcc(), *compile_flags, "-c", "-o", o, s] for s, o in zip(SOURCES, objects)]
+        if verbose:
+            for cmd in cmds:
+                print(" ".join(cmd), file=sys.stderr)
+        running = [subprocess.Popen(cmd) for cmd in cmds]
+        codes = [p.wait() for p in running]
+        for cmd, rc in zip(cmds, codes):
+            if rc != 0:
+                raise subprocess.CalledProcessError(rc, cmd)
+        subprocess.run([_nvcc(), *NVCC_FLAGS, "-o", tmp, *objects], check=True)
     os.replace(tmp, LIB)
     return LIB
 

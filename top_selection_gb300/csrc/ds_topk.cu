@@ -37,6 +37,7 @@
 #include <vector>
 
 #include "ds_common.cuh"
+#include "ds_host.cuh"
 #include "ds_select.cuh"
 #include "ds_topk.h"
 
@@ -895,13 +896,6 @@ static ds_status launch_row_kernel(Kern kern, int64_t rows, size_t smem, cudaStr
 
 // ================================================================ host ============
 
-struct DevInfo {
-    int sms = 0;
-    int smem_optin = 0;
-    int smem_per_sm = 0;
-    bool ok = false;
-};
-
 static std::mutex g_mu;
 static DevInfo g_dev[64];
 static std::atomic<uint32_t> g_epoch{0};
@@ -919,14 +913,17 @@ struct Workspace {
 };
 struct WsKey {
     int dev;
+    int kind;  // what the workspace is for (WsKind): the top-k's keeps its threshold words
     cudaStream_t stream;
     std::thread::id thread;
-    bool operator==(const WsKey& o) const { return dev == o.dev && stream == o.stream && thread == o.thread; }
+    bool operator==(const WsKey& o) const {
+        return dev == o.dev && kind == o.kind && stream == o.stream && thread == o.thread;
+    }
 };
 struct WsKeyHash {
     size_t operator()(const WsKey& k) const {
         return std::hash<const void*>()(k.stream) ^ (std::hash<std::thread::id>()(k.thread) << 1) ^
-               static_cast<size_t>(k.dev) * 0x9E3779B97F4A7C15ull;
+               static_cast<size_t>(k.dev * 8 + k.kind) * 0x9E3779B97F4A7C15ull;
     }
 };
 static std::unordered_map<WsKey, Workspace, WsKeyHash> g_ws;
@@ -938,7 +935,7 @@ constexpr size_t kStaticWorkspaceBytes = size_t(4) << 20;
 static __device__ __align__(256) unsigned char g_static_ws[kStaticWorkspaceBytes];
 static void* g_static_ws_addr[64];  // device address of g_static_ws, per device
 
-static bool dev_info(int dev, DevInfo& out) {
+bool dev_info(int dev, DevInfo& out) {
     if (dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lk(g_mu);
     DevInfo& d = g_dev[dev];
@@ -1342,9 +1339,9 @@ static ds_status launch(const Plan& P, const void* x, int64_t rows, int64_t N, i
     return DS_OK;
 }
 
-static ds_status library_workspace(int dev, size_t bytes, cudaStream_t stream, void** out) {
+ds_status library_workspace(int dev, WsKind kind, size_t bytes, cudaStream_t stream, void** out) {
     const bool per_thread = stream == cudaStreamPerThread;
-    const WsKey key{dev, stream, per_thread ? std::this_thread::get_id() : std::thread::id()};
+    const WsKey key{dev, kind, stream, per_thread ? std::this_thread::get_id() : std::thread::id()};
     std::lock_guard<std::mutex> lk(g_mu);
     Workspace& w = g_ws[key];
     if (w.bytes >= bytes) {
@@ -1448,7 +1445,7 @@ ds_status ds_topk_ex(const void* x, int32_t dtype, int64_t rows, int64_t N, int6
             ws = static_cast<char*>(options->workspace);
         } else {
             void* p = nullptr;
-            st = library_workspace(dev, P.ws_bytes, stream, &p);
+            st = library_workspace(dev, kWsTopk, P.ws_bytes, stream, &p);
             if (st != DS_OK) return st;
             ws = static_cast<char*>(p);
         }
