@@ -383,7 +383,7 @@ ds_status ds_cache_load(const void* cache, const void* scales, int64_t pages, in
  *   indices      [sequences, tokens, K] int32 positions (as ds_topk returns them), or NULL; one
  *                outside the visible positions (-1 as padding) is not seen, one listed twice
  *                counts twice
- *   scale        finite;  out  [sequences, tokens, q_heads, D] dtype;  out_lse  [sequences,
+ *   scale        finite;  out  [sequences, tokens, q_heads, D] dtype, 16-byte aligned;  out_lse  [sequences,
  *                tokens, q_heads] floats or NULL
  * Products are exact in the codes; q enters in its own precision, weights in at least 16 bits,
  * all sums in fp32.  Positions are split over CTAs whose partial results lie in a library-owned
