@@ -21,9 +21,9 @@ bool dev_info(int dev, DevInfo& out);
 
 // The library-owned workspace of (device, stream, kind), zeroed when allocated and grown to
 // at least `bytes` (defined in ds_topk.cu).  Calls on one stream are ordered and share it.
-// Kinds are kept apart because the top-k's threshold words are told from stale ones by a
-// call number, which another operator's data could imitate.
-enum WsKind : int { kWsTopk = 0, kWsAttend = 1, kWsVerify = 2 };
+// Kinds are kept apart because the top-k's threshold words are told from stale ones by a call
+// number, which another operator's data could imitate.
+enum WsKind : int { kWsTopk = 0, kWsAttend = 1 };
 ds_status library_workspace(int dev, WsKind kind, size_t bytes, cudaStream_t stream, void** out);
 
 // Launches `kern` so that it may begin while the stream's previous kernel ends

@@ -26,7 +26,8 @@
 
 namespace dsk {
 
-constexpr int kRouteWarps = 8;     // rows per CTA
+constexpr int kRouteWarps = 8;     // rows at a time per CTA
+constexpr int kCountWarps = 16;    // the same where choices are counted
 constexpr int kRouteMaxE = 512;
 constexpr int kRouteMaxK = 32;     // one lane per choice
 constexpr uint32_t kFull = 0xFFFFFFFFu;
@@ -59,6 +60,13 @@ __device__ __forceinline__ float logistic(float x) { return 1.0f / (1.0f + expf(
 // and the sum of its exponentials as 1.
 __device__ __forceinline__ float row_max(float m) { return m == -INFINITY ? 0.f : m; }
 __device__ __forceinline__ float row_sum(float s) { return s == 0.f ? 1.f : s; }
+
+// exp(x) for sums of many terms, off by 2^-22 of each; a chosen expert's own term goes by expf.
+__device__ __forceinline__ float exp_term(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+    return r;
+}
 
 struct RouteParams {
     const void* logits;
@@ -95,12 +103,7 @@ __device__ __forceinline__ void load_run(const T* src, int count, float fill, fl
 }
 
 template <typename T, int EPL, bool VEC>
-__global__ void __launch_bounds__(kRouteWarps * 32) ds_route_kernel(const RouteParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
-    pdl_launch_dependents();
-    pdl_wait();
-    if (row >= p.rows) return;
+__device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int lane, int* count_in) {
     const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
     const int lanes = 1 << p.llog;
     const int grp = lane >> p.llog, pos = lane & (lanes - 1);
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) ds_route_kernel(const RouteP
         mx = row_max(warp_max_f32(m));
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s += i < count ? expf(v[i] - mx) : 0.f;
+        for (int i = 0; i < EPL; ++i) s += i < count ? exp_term(v[i] - mx) : 0.f;
         total = row_sum(warp_sum_f32(s));
     }
     // choice values; places past the run get key 0, below every value's key
@@ -208,7 +211,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32) ds_route_kernel(const RouteP
     if (lane < p.k) {
         p.weights[row * p.k + lane] = w;
         p.experts[row * p.k + lane] = mine;
-        if (p.counts) atomicAdd(p.counts + mine, 1);
+        if (count_in) atomicAdd(count_in + mine, 1);
+    }
+}
+
+// Choices are counted in shared memory and added to the caller's counts once per CTA (rows going
+// straight to the counts meet in a few lines of L2: 131072 choices of 256 experts took 8 us).
+template <typename T, int EPL, bool VEC, bool COUNT>
+__global__ void __launch_bounds__((COUNT ? kCountWarps : kRouteWarps) * 32) ds_route_kernel(const RouteParams p) {
+    constexpr int WARPS = COUNT ? kCountWarps : kRouteWarps;
+    __shared__ int sh_count[COUNT ? kRouteMaxE : 1];
+    const int lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    if (COUNT) {
+        for (int e = threadIdx.x; e < p.E; e += WARPS * 32) sh_count[e] = 0;
+        __syncthreads();
+    }
+    pdl_wait();
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5); row < p.rows;
+         row += static_cast<int64_t>(gridDim.x) * WARPS)
+        route_row<T, EPL, VEC>(p, row, lane, COUNT ? sh_count : nullptr);
+    if (COUNT) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < p.E; e += WARPS * 32)
+            if (sh_count[e]) atomicAdd(p.counts + e, sh_count[e]);
     }
 }
 
@@ -220,9 +246,10 @@ __global__ void __launch_bounds__(kRouteWarps * 32) ds_route_kernel(const RouteP
 //                  zero and D cancels: dx_j = scale * w^_j (g_j - sum_i g_i w^_i), where w^ is
 //                  the softmax of the chosen logits alone.
 // The choice itself has no gradient, so neither has the bias.
-// One warp per row: lane j < k holds choice j.  Every row of the output is written whole
-// (zeros, or -s_e sum ds s for the softmax that is not renormalised), then, after a warp
-// barrier, the chosen columns over it; both writes meet in L2.
+// LPR lanes per row (8 where k <= 8, so that a warp takes four rows): lane j < k holds choice j.
+// Every row of the output is written whole, first zeros, or for the softmax that is not
+// renormalised -s_e sum ds s, then, after a warp barrier, the chosen columns over them; both writes
+// meet in L2.
 struct RouteBackParams {
     const float* grad;
     const void* logits;
@@ -233,73 +260,129 @@ struct RouteBackParams {
     float scale;
 };
 
-template <typename T, bool VEC>
+template <int LPR>
+__device__ __forceinline__ float part_sum(float v) {
+#pragma unroll
+    for (int d = LPR / 2; d >= 1; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    return v;
+}
+template <int LPR>
+__device__ __forceinline__ float part_max(float v) {
+#pragma unroll
+    for (int d = LPR / 2; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+    return v;
+}
+
+// WHOLE: every column has a gradient (softmax, not renormalised); a lane holds up to NPL of them.
+// VEC: otherwise, the zeros may be written 16 bytes at a time.
+template <typename T, int LPR, int NPL, bool WHOLE, bool VEC>
 __global__ void __launch_bounds__(kRouteWarps * 32) ds_route_backward_kernel(const RouteBackParams p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRouteWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * (kRouteWarps * 32 / LPR) + threadIdx.x / LPR;
     pdl_launch_dependents();
     pdl_wait();
-    if (row >= p.rows) return;
+    const bool live = at < p.rows;  // the warp stays whole for its shuffles
+    const int64_t row = live ? at : p.rows - 1;
     const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
     T* out = static_cast<T*>(p.out) + row * p.out_stride;
     int e = -1;
     float g = 0.f;
-    if (lane < p.k) {
-        e = p.experts[row * p.k + lane];
+    if (sub < p.k) {
+        e = p.experts[row * p.k + sub];
         if (e < 0 || e >= p.E) e = -1;  // not a column: it has no part
-        g = p.grad[row * p.k + lane];
+        g = p.grad[row * p.k + sub];
+    }
+    float v[NPL];
+    float mx = 0.f, total = 1.f;
+    if (WHOLE) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int c = sub + i * LPR;
+            v[i] = c < p.E ? to_f32(x[c]) : -INFINITY;
+            m = fmaxf(m, v[i]);
+        }
+        mx = row_max(part_max<LPR>(m));
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            v[i] = exp_term(v[i] - mx);
+            s += v[i];
+        }
+        total = row_sum(part_sum<LPR>(s));
     }
     const bool on = e >= 0;
     if (!on) g = 0.f;
     const float t = on ? to_f32(x[e]) : -INFINITY;
-    const bool whole = !p.sigmoid && !p.renormalise;  // every column has a gradient
-    float mx = 0.f, total = 1.f;
-    if (whole) {
-        float m = -INFINITY;
-        for (int c = lane; c < p.E; c += 32) m = fmaxf(m, to_f32(x[c]));
-        mx = row_max(warp_max_f32(m));
-        float s = 0.f;
-        for (int c = lane; c < p.E; c += 32) s += expf(to_f32(x[c]) - mx);
-        total = row_sum(warp_sum_f32(s));
-    } else if (!p.sigmoid) {
-        mx = row_max(warp_max_f32(t));
-    }
+    if (!WHOLE && !p.sigmoid) mx = row_max(part_max<LPR>(t));
     const float s = !on ? 0.f : p.sigmoid ? logistic(t) : expf(t - mx) / total;
     float d = p.scale * g, back = 0.f;
     if (p.renormalise) {
-        const float sum = warp_sum_f32(s);
+        const float sum = part_sum<LPR>(s);
         const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-        const float mean = warp_sum_f32(g * s * inv);
+        const float mean = part_sum<LPR>(g * s * inv);
         d = on ? p.scale * (g - mean) * inv : 0.f;
     }
-    if (whole) back = warp_sum_f32(d * s);
+    if (WHOLE) back = part_sum<LPR>(d * s);
     const float dx = p.sigmoid ? d * s * (1.0f - s) : s * (d - back);
-
-    if (whole) {
-        for (int c = lane; c < p.E; c += 32)
-            out[c] = from_f32<T>(-back * (expf(to_f32(x[c]) - mx) / total));
-    } else if (VEC) {
-        constexpr int PER = 16 / sizeof(T);
-        for (int c = lane; c < p.E / PER; c += 32) reinterpret_cast<uint4*>(out)[c] = make_uint4(0u, 0u, 0u, 0u);
-    } else {
-        for (int c = lane; c < p.E; c += 32) out[c] = from_f32<T>(0.f);
+    if (live) {
+        if (WHOLE) {
+            const float f = -back / total;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if (sub + i * LPR < p.E) out[sub + i * LPR] = from_f32<T>(f * v[i]);
+        } else if (VEC) {
+            constexpr int PER = 16 / sizeof(T);
+            for (int c = sub; c < p.E / PER; c += LPR) reinterpret_cast<uint4*>(out)[c] = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            for (int c = sub; c < p.E; c += LPR) out[c] = from_f32<T>(0.f);
+        }
     }
     __syncwarp();
-    if (on) out[e] = from_f32<T>(dx);
+    if (live && on) out[e] = from_f32<T>(dx);
 }
 
 // ---------------------------------------------------------------- host --------------
-template <typename T, bool VEC>
-static ds_status launch_route(const RouteParams& p, int epl, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>((p.rows + kRouteWarps - 1) / kRouteWarps));
-    switch (epl) {
-        case 1: return launch_pdl(ds_route_kernel<T, 1, VEC>, grid, kRouteWarps * 32, 0, 1, stream, p);
-        case 2: return launch_pdl(ds_route_kernel<T, 2, VEC>, grid, kRouteWarps * 32, 0, 1, stream, p);
-        case 4: return launch_pdl(ds_route_kernel<T, 4, VEC>, grid, kRouteWarps * 32, 0, 1, stream, p);
-        case 8: return launch_pdl(ds_route_kernel<T, 8, VEC>, grid, kRouteWarps * 32, 0, 1, stream, p);
-        case 16: return launch_pdl(ds_route_kernel<T, 16, VEC>, grid, kRouteWarps * 32, 0, 1, stream, p);
-        default: return launch_pdl(ds_route_kernel<T, 32, VEC>, grid, kRouteWarps * 32, 0, 1, stream, p);
+template <typename T, int EPL, bool VEC>
+static ds_status launch_route_as(const RouteParams& p, int sms, cudaStream_t stream) {
+    if (!p.counts) {
+        const int64_t ctas = (p.rows + kRouteWarps - 1) / kRouteWarps;
+        return launch_pdl(ds_route_kernel<T, EPL, VEC, false>, dim3(static_cast<unsigned>(ctas)), kRouteWarps * 32, 0, 1,
+                          stream, p);
     }
+    // as many CTAs as fit at once, each for many rows: the counts are added once per CTA
+    int64_t ctas = (p.rows + kCountWarps - 1) / kCountWarps;
+    const int64_t most = static_cast<int64_t>(sms) * (EPL <= 16 ? 2 : 1);
+    if (ctas > most) ctas = most;
+    return launch_pdl(ds_route_kernel<T, EPL, VEC, true>, dim3(static_cast<unsigned>(ctas)), kCountWarps * 32, 0, 1, stream, p);
+}
+
+// 16-byte loads exist where a lane's run holds 16 bytes
+template <typename T>
+static ds_status launch_route(const RouteParams& p, int epl, bool vec, int sms, cudaStream_t stream) {
+    constexpr bool WIDE = sizeof(T) == 4;
+    switch (epl) {
+        case 1: return launch_route_as<T, 1, false>(p, sms, stream);
+        case 2: return launch_route_as<T, 2, false>(p, sms, stream);
+        case 4: return vec && WIDE ? launch_route_as<T, 4, WIDE>(p, sms, stream) : launch_route_as<T, 4, false>(p, sms, stream);
+        case 8: return vec ? launch_route_as<T, 8, true>(p, sms, stream) : launch_route_as<T, 8, false>(p, sms, stream);
+        case 16: return vec ? launch_route_as<T, 16, true>(p, sms, stream) : launch_route_as<T, 16, false>(p, sms, stream);
+        default: return vec ? launch_route_as<T, 32, true>(p, sms, stream) : launch_route_as<T, 32, false>(p, sms, stream);
+    }
+}
+
+template <typename T>
+static ds_status launch_route_backward(const RouteBackParams& p, bool vec, cudaStream_t stream) {
+    const bool whole = !p.sigmoid && !p.renormalise, narrow = p.k <= 8 && (!whole || p.E <= 64);
+    const int rows = kRouteWarps * 32 / (narrow ? 8 : 32);
+    const dim3 grid(static_cast<unsigned>((p.rows + rows - 1) / rows));
+    const auto go = [&](auto kern) { return launch_pdl(kern, grid, kRouteWarps * 32, 0, 1, stream, p); };
+    if (whole) {
+        if (narrow) return go(ds_route_backward_kernel<T, 8, 8, true, false>);
+        return p.E <= 256 ? go(ds_route_backward_kernel<T, 32, 8, true, false>) : go(ds_route_backward_kernel<T, 32, 16, true, false>);
+    }
+    if (narrow) return vec ? go(ds_route_backward_kernel<T, 8, 1, false, true>) : go(ds_route_backward_kernel<T, 8, 1, false, false>);
+    return vec ? go(ds_route_backward_kernel<T, 32, 1, false, true>) : go(ds_route_backward_kernel<T, 32, 1, false, false>);
 }
 
 }  // namespace dsk
@@ -350,9 +433,11 @@ ds_status ds_route(const void* logits, int32_t dtype, int64_t rows, int32_t E, i
     // 16-byte loads when every lane's run starts on 16 bytes; else element by element
     const bool vec = bits % 16 == 0 && row_stride * es % 16 == 0 && static_cast<int64_t>(p.n) * es % 16 == 0 &&
                      static_cast<int64_t>(p.size) * es % 16 == 0;
-    if (dtype == DS_BF16)
-        return vec ? launch_route<__nv_bfloat16, true>(p, epl, stream) : launch_route<__nv_bfloat16, false>(p, epl, stream);
-    return vec ? launch_route<float, true>(p, epl, stream) : launch_route<float, false>(p, epl, stream);
+    int dev = 0;
+    DevInfo info;
+    if (cudaGetDevice(&dev) != cudaSuccess || !dev_info(dev, info)) return DS_ERR_CUDA;
+    return dtype == DS_BF16 ? launch_route<__nv_bfloat16>(p, epl, vec, info.sms, stream)
+                            : launch_route<float>(p, epl, vec, info.sms, stream);
 }
 
 ds_status ds_route_backward(const float* grad_weights, const void* logits, int32_t dtype, int64_t rows, int32_t E,
@@ -374,13 +459,7 @@ ds_status ds_route_backward(const float* grad_weights, const void* logits, int32
     const RouteBackParams p = {grad_weights, logits, experts, grad_logits, rows, row_stride, grad_stride,
                                E, k, scoring == DS_SIGMOID, renormalise != 0, scale};
     const bool vec = gb % 16 == 0 && grad_stride * es % 16 == 0 && static_cast<int64_t>(E) * es % 16 == 0;
-    const dim3 grid(static_cast<unsigned>((rows + kRouteWarps - 1) / kRouteWarps));
-    const int threads = kRouteWarps * 32;
-    if (dtype == DS_BF16)
-        return vec ? launch_pdl(ds_route_backward_kernel<__nv_bfloat16, true>, grid, threads, 0, 1, stream, p)
-                   : launch_pdl(ds_route_backward_kernel<__nv_bfloat16, false>, grid, threads, 0, 1, stream, p);
-    return vec ? launch_pdl(ds_route_backward_kernel<float, true>, grid, threads, 0, 1, stream, p)
-               : launch_pdl(ds_route_backward_kernel<float, false>, grid, threads, 0, 1, stream, p);
+    return dtype == DS_BF16 ? launch_route_backward<__nv_bfloat16>(p, vec, stream) : launch_route_backward<float>(p, vec, stream);
 }
 
 }  // extern "C"

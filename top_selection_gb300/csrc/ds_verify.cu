@@ -11,12 +11,19 @@
 // wins with probability r_v / sum r, and no running sum over the vocabulary is needed.  The
 // emitted tokens are then distributed as the target's own samples.
 //
-// One CTA per sequence takes the rows in order and stops at the refused one: a pass for the
-// row's maximum and sum of exponentials, then one pass over the stop row, q_n and e.
+// A cluster of C CTAs takes a sequence, each CTA a slice of the vocabulary.  Rows go in rounds of
+// R: each CTA finds its slice's maximum and sum of exponentials of the round's rows in one pass
+// (online: a thread rescales its sum when its maximum rises), the cluster exchanges these over
+// distributed shared memory, and every CTA decides by itself where the sequence stops, by the same
+// arithmetic in the same order.  Rows behind the stop's round, which the answer does not need, are
+// not read.  The stop row is read a second time for the race, from L2.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "ds_common.cuh"
 #include "ds_host.cuh"
@@ -24,7 +31,11 @@
 
 namespace dsk {
 
-constexpr int kVerThreads = 1024;
+constexpr int kVerThreads = 512;
+constexpr int kVerWarps = kVerThreads / 32;
+constexpr int kVerRound = 8;                  // most rows of a round
+constexpr int kVerCluster = 16;               // most CTAs of a sequence
+constexpr uint32_t kWarp = 0xFFFFFFFFu;
 
 struct VerifyParams {
     const void* logits;
@@ -39,6 +50,8 @@ struct VerifyParams {
     const float* temps;
     float temperature;
     int32_t S, V;
+    int32_t C, R;                    // CTAs of a sequence, rows of a round
+    int32_t race_vec;                // the race's three rows may be read four numbers at a time
     int32_t* tokens;
     int32_t* accepted;
     float* probs;
@@ -55,113 +68,385 @@ __device__ __forceinline__ void best_of(float& v, int& i, float v2, int i2) {
     }
 }
 
-// exp((x - max) / temperature), 0 for -inf and for a row of -inf alone
-__device__ __forceinline__ float weight(float x, float mx, float inv_t) {
-    return x == -INFINITY ? 0.f : expf((x - mx) * inv_t);
+__device__ __forceinline__ float ver_exp2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// (x + add) * by and a + b, two numbers to an instruction
+__device__ __forceinline__ float2 scaled2(float x, float y, float add, float by) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, a, b;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 a, {%4, %4};\n\tmov.b64 b, {%5, %5};\n\t"
+        "add.rn.f32x2 x, x, a;\n\tmul.rn.f32x2 x, x, b;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x), "f"(y), "f"(add), "f"(by));
+    return r;
+}
+__device__ __forceinline__ float2 sum2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float ver_max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// A row's (or a slice's) largest logit, its first place (temperature 0 only), and the sum of
+// exp((x - m) / temperature); m = -inf and s = 0 where every logit is -inf.
+struct RowStat {
+    float m, s;
+    int at;
+};
+
+// The statistics of two disjoint slices as one; c = log2(e) / temperature.
+__device__ __forceinline__ RowStat both_stats(RowStat a, RowStat b, float c) {
+    RowStat r;
+    r.m = fmaxf(a.m, b.m);
+    r.at = a.m > b.m ? a.at : b.m > a.m ? b.at : min(a.at, b.at);
+    r.s = (a.m > -INFINITY ? a.s * ver_exp2((a.m - r.m) * c) : 0.f) +
+          (b.m > -INFINITY ? b.s * ver_exp2((b.m - r.m) * c) : 0.f);
+    return r;
+}
+// The lanes' statistics as one, in every lane.  The maximum goes by its order-preserving key.
+__device__ __forceinline__ RowStat warp_stats(RowStat a, float c, bool greedy) {
+    const float m = __uint_as_float(unkey_f32(__reduce_max_sync(kWarp, key_f32(__float_as_uint(a.m)))));
+    if (greedy) return {m, 0.f, static_cast<int>(__reduce_min_sync(kWarp, a.m == m ? static_cast<uint32_t>(a.at) : 0x7FFFFFFFu))};
+    float s = a.m > -INFINITY ? a.s * ver_exp2((a.m - m) * c) : 0.f;
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) s += __shfl_xor_sync(kWarp, s, d);
+    return {m, s, 0x7FFFFFFF};
+}
+
+// The numbers of a 16-byte word as fp32.
+template <typename T>
+struct Vec {
+    static constexpr int N = 16 / sizeof(T);
+    static __device__ __forceinline__ void unpack(uint4 w, float* x) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __uint_as_float(u[i]);
+            } else {
+                x[2 * i] = __uint_as_float(u[i] << 16);
+                x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+            }
+        }
+    }
+};
+
+// Adds M words of N numbers to a thread's statistics; word k's first place is first + k * step.
+template <int M, int N, bool GREEDY>
+__device__ __forceinline__ void add_numbers(RowStat& a, const float (&x)[M][N], int first, int step, float c) {
+    float top = x[0][0];
+#pragma unroll
+    for (int k = 0; k < M; ++k)
+#pragma unroll
+        for (int i = k == 0; i < N; i += 2) top = i + 1 < N ? ver_max3(top, x[k][i], x[k][i + 1]) : fmaxf(top, x[k][i]);
+    if (GREEDY) {
+        if (top > a.m) {  // a thread's places ascend: a later equal number is not the first
+            a.m = top;
+#pragma unroll
+            for (int k = M - 1; k >= 0; --k)
+#pragma unroll
+                for (int i = N - 1; i >= 0; --i)
+                    if (x[k][i] == top) a.at = first + k * step + i;
+        }
+        return;
+    }
+    if (top > a.m) {
+        a.s *= ver_exp2((a.m - top) * c);
+        a.m = top;
+    }
+    if (a.m > -INFINITY) {
+        if constexpr (N == 1) {
+            a.s += ver_exp2((x[0][0] - a.m) * c);
+        } else {
+            float2 sum = make_float2(a.s, 0.f);
+#pragma unroll
+            for (int k = 0; k < M; ++k)
+#pragma unroll
+                for (int i = 0; i < N; i += 2) {
+                    const float2 y = scaled2(x[k][i], x[k][i + 1], -a.m, c);
+                    sum = sum2(sum, make_float2(ver_exp2(y.x), ver_exp2(y.y)));
+                }
+            a.s = sum.x + sum.y;
+        }
+    }
+}
+
+// A thread's statistics of CTA `part`'s slice of a row of V numbers: 16-byte words from the first
+// aligned place on, the numbers before and behind them one each by the first CTA's threads.
+template <typename T, bool GREEDY>
+__device__ __forceinline__ RowStat slice_stats(const T* x, int V, int part, int parts, float c) {
+    constexpr int N = Vec<T>::N, U = 4;
+    RowStat a = {-INFINITY, 0.f, 0x7FFFFFFF};
+    const int tid = threadIdx.x;
+    const int head = min(V, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / static_cast<int>(sizeof(T)));
+    const int words = (V - head) / N;
+    const int from = static_cast<int>(static_cast<int64_t>(words) * part / parts);
+    const int to = static_cast<int>(static_cast<int64_t>(words) * (part + 1) / parts);
+    const uint4* w = reinterpret_cast<const uint4*>(x + head);
+    if (part == 0) {
+        const int tail = head + words * N;  // up to 2 (N - 1) numbers outside the words
+        const int place = tid < head ? tid : tail + tid - head;
+        if (place < V) {
+            const float one[1][1] = {{ver_f32(x[place])}};
+            add_numbers<1, 1, GREEDY>(a, one, place, 0, c);
+        }
+    }
+    RowStat b = {-INFINITY, 0.f, 0x7FFFFFFF};
+    int i = from + tid;
+    for (; i + (U - 1) * kVerThreads < to; i += U * kVerThreads) {
+        uint4 q[U];
+        float y[U][N];
+#pragma unroll
+        for (int u = 0; u < U; ++u) q[u] = w[i + u * kVerThreads];
+#pragma unroll
+        for (int u = 0; u < U; ++u) Vec<T>::unpack(q[u], y[u]);
+        add_numbers<U, N, GREEDY>(b, y, head + i * N, kVerThreads * N, c);
+    }
+    for (; i < to; i += kVerThreads) {
+        float y[1][N];
+        Vec<T>::unpack(w[i], y[0]);
+        add_numbers<1, N, GREEDY>(b, y, head + i * N, 0, c);
+    }
+    return both_stats(a, b, c);
+}
+
+struct Race {
+    float v;
+    int i;
+};
+__device__ __forceinline__ Race warp_best(Race a) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1)
+        best_of(a.v, a.i, __shfl_xor_sync(kWarp, a.v, d), __shfl_xor_sync(kWarp, a.i, d));
+    return a;
+}
+
+// A thread's best of r / e over CTA `part`'s slice; q null: the draft is one-hot at t (t < 0: r = p).
+template <typename T, int N>
+__device__ __forceinline__ Race slice_race(const T* x, const float* q, int t, const float* e, int V, int part, int parts,
+                                           float m, float c, float inv_s) {
+    float br = 0.f, be = 1.f;  // the best so far
+    int bi = 0x7FFFFFFF;
+    const int groups = V / N;
+    const int from = static_cast<int>(static_cast<int64_t>(groups) * part / parts);
+    const int to = static_cast<int>(static_cast<int64_t>(groups) * (part + 1) / parts);
+    // r / e against br / be by cross products: no quotient, no branch (a thread's bests change
+    // often while it has seen few places, and some lane's always does)
+    const auto one = [&](int v, float xv, float qv, float ev) {
+        const float r = fmaf(ver_exp2((xv - m) * c), inv_s, -qv);
+        const bool wins = r * be > br * ev;
+        br = wins ? r : br;
+        be = wins ? ev : be;
+        bi = wins ? v : bi;
+    };
+    constexpr int U = N == 4 ? 2 : 8;
+    int g = from + static_cast<int>(threadIdx.x);
+    const auto groups_at = [&](int g, auto count) {
+        constexpr int M = decltype(count)::value;
+        float xv[M][N], qv[M][N], ev[M][N];
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+            const int at = g + k * kVerThreads;
+            if constexpr (N == 4) {
+                if constexpr (sizeof(T) == 4) {
+                    const float4 w = reinterpret_cast<const float4*>(x)[at];
+                    xv[k][0] = w.x, xv[k][1] = w.y, xv[k][2] = w.z, xv[k][3] = w.w;
+                } else {
+                    const uint2 w = reinterpret_cast<const uint2*>(x)[at];
+                    xv[k][0] = __uint_as_float(w.x << 16), xv[k][1] = __uint_as_float(w.x & 0xFFFF0000u);
+                    xv[k][2] = __uint_as_float(w.y << 16), xv[k][3] = __uint_as_float(w.y & 0xFFFF0000u);
+                }
+                const float4 we = reinterpret_cast<const float4*>(e)[at];
+                ev[k][0] = we.x, ev[k][1] = we.y, ev[k][2] = we.z, ev[k][3] = we.w;
+                if (q) {
+                    const float4 wq = reinterpret_cast<const float4*>(q)[at];
+                    qv[k][0] = wq.x, qv[k][1] = wq.y, qv[k][2] = wq.z, qv[k][3] = wq.w;
+                }
+            } else {
+                xv[k][0] = ver_f32(x[at]);
+                ev[k][0] = e[at];
+                if (q) qv[k][0] = q[at];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < M; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int v = (g + k * kVerThreads) * N + i;
+                one(v, xv[k][i], q ? qv[k][i] : v == t ? 1.f : 0.f, ev[k][i]);
+            }
+    };
+    for (; g + (U - 1) * kVerThreads < to; g += U * kVerThreads) groups_at(g, std::integral_constant<int, U>{});
+    for (; g < to; g += kVerThreads) groups_at(g, std::integral_constant<int, 1>{});
+    Race a = {br / be, bi};
+    const int v = groups * N + static_cast<int>(threadIdx.x);
+    if (part == 0 && v < V) {  // a thread's places no longer ascend here
+        br = 0.f, be = 1.f, bi = 0x7FFFFFFF;
+        one(v, ver_f32(x[v]), q ? q[v] : v == t ? 1.f : 0.f, e[v]);
+        best_of(a.v, a.i, br / be, bi);
+    }
+    return a;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kVerThreads) ds_verify_kernel(const VerifyParams p) {
-    __shared__ float sh_a[32], sh_b[32];
-    __shared__ int sh_i[32], sh_j[32];
+__global__ void __launch_bounds__(kVerThreads, 2) ds_verify_kernel(const VerifyParams p) {
+    __shared__ RowStat sh_warp[kVerRound][kVerWarps];  // each warp's statistics of the round's rows
+    __shared__ RowStat sh_cta[2][kVerRound];           // the CTA's, for the cluster; by the round's parity
+    __shared__ RowStat sh_stop;                        // the stop row's
+    __shared__ Race sh_race[kVerWarps];
+    __shared__ Race sh_best[2];                        // the CTA's, for the cluster; by the attempt
+    __shared__ int sh_n;                               // accepted rows of the round
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t b = blockIdx.x;
+    const int64_t b = blockIdx.x / static_cast<uint32_t>(p.C);
+    const int part = static_cast<int>(blockIdx.x - b * p.C);
+    const auto sync_all = [&]() {
+        if (p.C > 1) cluster_sync_all();
+        else __syncthreads();
+    };
     pdl_launch_dependents();
     pdl_wait();
     const float temp = p.temps ? p.temps[b] : p.temperature;
     const bool greedy = !(temp > 0.f);
-    const float inv_t = greedy ? 1.f : 1.f / temp;
+    // a temperature too small for its inverse separates any two logits all the same
+    const float inv_t = greedy ? 1.f : fminf(1.f / temp, 1e30f);
+    const float c = inv_t * 1.4426950408889634f;
     const int len = p.lens ? min(max(p.lens[b], 0), p.S) : p.S;
+    const T* seq = static_cast<const T*>(p.logits) + b * p.seq_stride;
     int32_t* tokens = p.tokens + b * (p.S + 1);
     float* probs = p.probs ? p.probs + b * (p.S + 1) : nullptr;
+
     int n = 0;
-    for (;; ++n) {
-        const T* x = static_cast<const T*>(p.logits) + b * p.seq_stride + n * p.row_stride;
-        // the row's first maximum, and the sum of exponentials
-        float mx = -INFINITY;
-        int at = 0x7FFFFFFF;
-        for (int v = tid; v < p.V; v += kVerThreads) best_of(mx, at, ver_f32(x[v]), v);
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-            best_of(mx, at, __shfl_xor_sync(0xFFFFFFFFu, mx, d), __shfl_xor_sync(0xFFFFFFFFu, at, d));
-        if (lane == 0) sh_a[warp] = mx, sh_i[warp] = at;
-        __syncthreads();
-        mx = sh_a[lane], at = sh_i[lane];
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1)
-            best_of(mx, at, __shfl_xor_sync(0xFFFFFFFFu, mx, d), __shfl_xor_sync(0xFFFFFFFFu, at, d));
-        float sum = 0.f;
-        if (!greedy) {
-            for (int v = tid; v < p.V; v += kVerThreads) sum += weight(ver_f32(x[v]), mx, inv_t);
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-            if (lane == 0) sh_b[warp] = sum;
-            __syncthreads();
-            sum = sh_b[lane];
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        }
-        const auto prob = [&](int v, float xv) {
-            if (mx == -INFINITY) return 0.f;
-            return greedy ? (v == at ? 1.f : 0.f) : weight(xv, mx, inv_t) / sum;
-        };
-        const bool drafted = n < len;
+    for (int round = 0;; ++round) {
+        const int rows = min(p.R, len + 1 - n);
+        // warp 0, lane i: the round's i-th draft, fetched while the rows are read
         int t = -1;
-        float qt = 1.f;
-        const float* q = nullptr;
-        if (drafted) {
-            t = p.drafts[b * p.S + n];
+        float u = 0.f, qt = 1.f, xt = -INFINITY;
+        if (warp == 0 && lane < rows && n + lane < len) {
+            t = p.drafts[b * p.S + n + lane];
+            u = p.uniforms[b * p.S + n + lane];
             if (t < 0 || t >= p.V) t = -1;  // no column: refused
-            if (p.q) {
-                q = p.q + b * p.q_seq + n * p.q_row;
-                if (t >= 0) qt = q[t];
-            }
-            const float pt = t >= 0 ? prob(t, ver_f32(x[t])) : 0.f;
-            if (p.uniforms[b * p.S + n] * qt < pt) {
-                if (tid == 0) {
-                    tokens[n] = t;
-                    if (probs) probs[n] = pt;
-                }
-                __syncthreads();
-                continue;
+            if (t >= 0) {
+                xt = ver_f32(seq[(n + lane) * p.row_stride + t]);
+                if (p.q) qt = p.q[b * p.q_seq + (n + lane) * p.q_row + t];
             }
         }
-        // the stop row: the best of r / e, and of p / e should r be zero everywhere
-        const float* noise = p.noise + b * p.noise_stride;
-        float r1 = 0.f, r2 = 0.f;
-        int i1 = 0x7FFFFFFF, i2 = 0x7FFFFFFF;
-        for (int v = tid; v < p.V; v += kVerThreads) {
-            const float pv = prob(v, ver_f32(x[v])), e = noise[v];
-            const float qv = !drafted ? 0.f : q ? q[v] : v == t ? 1.f : 0.f;
-            const float r = fmaxf(pv - qv, 0.f);
-            if (r > 0.f) best_of(r1, i1, r / e, v);
-            if (pv > 0.f) best_of(r2, i2, pv / e, v);
-        }
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) {
-            best_of(r1, i1, __shfl_xor_sync(0xFFFFFFFFu, r1, d), __shfl_xor_sync(0xFFFFFFFFu, i1, d));
-            best_of(r2, i2, __shfl_xor_sync(0xFFFFFFFFu, r2, d), __shfl_xor_sync(0xFFFFFFFFu, i2, d));
+        for (int i = 0; i < rows; ++i) {
+            const T* x = seq + (n + i) * p.row_stride;
+            RowStat a = greedy ? slice_stats<T, true>(x, p.V, part, p.C, c) : slice_stats<T, false>(x, p.V, part, p.C, c);
+            a = warp_stats(a, c, greedy);
+            if (lane == 0) sh_warp[i][warp] = a;
         }
         __syncthreads();
-        if (lane == 0) sh_a[warp] = r1, sh_i[warp] = i1, sh_b[warp] = r2, sh_j[warp] = i2;
-        __syncthreads();
+        RowStat* mine = sh_cta[round & 1];
+        if (warp < rows) {
+            RowStat a = {-INFINITY, 0.f, 0x7FFFFFFF};
+            if (lane < kVerWarps) a = sh_warp[warp][lane];
+            a = warp_stats(a, c, greedy);
+            if (lane == 0) mine[warp] = a;
+        }
+        sync_all();
         if (warp == 0) {
-            r1 = sh_a[lane], i1 = sh_i[lane], r2 = sh_b[lane], i2 = sh_j[lane];
-#pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) {
-                best_of(r1, i1, __shfl_xor_sync(0xFFFFFFFFu, r1, d), __shfl_xor_sync(0xFFFFFFFFu, i1, d));
-                best_of(r2, i2, __shfl_xor_sync(0xFFFFFFFFu, r2, d), __shfl_xor_sync(0xFFFFFFFFu, i2, d));
+            RowStat a = {-INFINITY, 0.f, 0x7FFFFFFF};
+            if (lane < rows) {
+                a = mine[lane];
+                if (p.C > 1) {
+                    a = {-INFINITY, 0.f, 0x7FFFFFFF};
+                    for (int k = 0; k < p.C; ++k) {  // in one order in every CTA: the same decision
+                        const uint32_t at = map_rank(&mine[lane], k);
+                        a = both_stats(a, {__uint_as_float(ld_cluster_u32(at)), __uint_as_float(ld_cluster_u32(at + 4)),
+                                           static_cast<int>(ld_cluster_u32(at + 8))}, c);
+                    }
+                }
             }
-            const int last = i1 < p.V ? i1 : i2 < p.V ? i2 : -1;  // -1: the row has no distribution
-            const float pl = last >= 0 ? prob(last, ver_f32(x[last])) : 0.f;
-            for (int i = n + lane; i <= p.S; i += 32) {
-                tokens[i] = i == n ? last : -1;
-                if (probs) probs[i] = i == n ? pl : 0.f;
+            float pt = 0.f;
+            if (t >= 0 && a.m > -INFINITY) pt = greedy ? (t == a.at ? 1.f : 0.f) : expf((xt - a.m) * inv_t) / a.s;
+            const bool ok = lane < rows && n + lane < len && u * qt < pt;
+            const int run = __ffs(~__ballot_sync(kWarp, ok)) - 1;  // accepted rows in front (at most 8)
+            if (part == 0 && lane < run) {
+                tokens[n + lane] = t;
+                if (probs) probs[n + lane] = pt;
             }
-            if (lane == 0) p.accepted[b] = n;
+            if (lane == min(run, rows - 1)) sh_stop = a;
+            if (lane == 0) sh_n = run;
         }
-        return;
+        __syncthreads();
+        const int run = sh_n;
+        n += run;
+        if (run < rows) break;
     }
+
+    // the stop row
+    const RowStat stop = sh_stop;
+    const T* x = seq + n * p.row_stride;
+    int last = -1;
+    if (greedy) {
+        last = stop.m > -INFINITY ? stop.at : -1;
+    } else if (stop.m > -INFINITY) {
+        const bool refused = n < len;
+        const float* e = p.noise + b * p.noise_stride;
+        const float* q = refused && p.q ? p.q + b * p.q_seq + n * p.q_row : nullptr;
+        int t = refused && !p.q ? p.drafts[b * p.S + n] : -1;
+        const float inv_s = 1.f / stop.s;
+        for (int attempt = 0; attempt < 2; ++attempt) {  // the second: r was 0 everywhere, so p itself
+            Race a = p.race_vec ? slice_race<T, 4>(x, q, t, e, p.V, part, p.C, stop.m, c, inv_s)
+                                : slice_race<T, 1>(x, q, t, e, p.V, part, p.C, stop.m, c, inv_s);
+            a = warp_best(a);
+            if (lane == 0) sh_race[warp] = a;
+            __syncthreads();
+            if (warp == 0) {
+                a = {0.f, 0x7FFFFFFF};
+                if (lane < kVerWarps) a = sh_race[lane];
+                a = warp_best(a);
+                if (lane == 0) sh_best[attempt] = a;
+            }
+            sync_all();
+            a = sh_best[attempt];
+            for (int k = 0; k < p.C && p.C > 1; ++k) {
+                const uint32_t at = map_rank(&sh_best[attempt], k);
+                best_of(a.v, a.i, __uint_as_float(ld_cluster_u32(at)), static_cast<int>(ld_cluster_u32(at + 4)));
+            }
+            if (a.i < p.V) {
+                last = a.i;
+                break;
+            }
+            q = nullptr;
+            t = -1;
+        }
+    }
+    if (part == 0 && warp == 0) {
+        float pl = 0.f;
+        if (last >= 0) pl = greedy ? 1.f : expf((ver_f32(x[last]) - stop.m) * inv_t) / stop.s;
+        for (int i = n + lane; i <= p.S; i += 32) {
+            tokens[i] = i == n ? last : -1;
+            if (probs) probs[i] = i == n ? pl : 0.f;
+        }
+        if (lane == 0) p.accepted[b] = n;
+    }
+    if (p.C > 1) cluster_sync_all();  // no CTA leaves while another may read its shared memory
+}
+
+template <typename T>
+static ds_status launch_verify(const VerifyParams& p, int dev, int64_t sequences, cudaStream_t stream) {
+    // clusters above 8 are a kernel's opt-in on a device: set once
+    static std::atomic<bool> opted[64];
+    if (p.C > 8 && !opted[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(ds_verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return DS_ERR_CUDA;
+        opted[dev].store(true, std::memory_order_release);
+    }
+    return launch_pdl(ds_verify_kernel<T>, dim3(static_cast<unsigned>(sequences * p.C)), kVerThreads, 0, p.C, stream, p);
 }
 
 }  // namespace dsk
@@ -190,12 +475,43 @@ ds_status ds_verify_drafts(const void* logits, int32_t dtype, int64_t sequences,
     for (const void* w : words)
         if (reinterpret_cast<uintptr_t>(w) % 4) return DS_ERR_ALIGNMENT;
     if (reinterpret_cast<uintptr_t>(logits) % es) return DS_ERR_ALIGNMENT;
-    const VerifyParams p = {logits, seq_stride, row_stride, draft_probs, probs_seq_stride, probs_row_stride, drafts,
-                            draft_lens, uniforms, noise, noise_stride, temperatures, temperature, S,
-                            static_cast<int32_t>(V), out_tokens, out_accepted, out_probs};
-    const dim3 grid(static_cast<unsigned>(sequences));
-    return dtype == DS_BF16 ? launch_pdl(ds_verify_kernel<__nv_bfloat16>, grid, kVerThreads, 0, 1, stream, p)
-                            : launch_pdl(ds_verify_kernel<float>, grid, kVerThreads, 0, 1, stream, p);
+    int dev = 0;
+    DevInfo info;
+    if (cudaGetDevice(&dev) != cudaSuccess || !dev_info(dev, info)) return DS_ERR_CUDA;
+    VerifyParams p = {};
+    p.logits = logits;
+    p.seq_stride = seq_stride;
+    p.row_stride = row_stride;
+    p.q = draft_probs;
+    p.q_seq = probs_seq_stride;
+    p.q_row = probs_row_stride;
+    p.drafts = drafts;
+    p.lens = draft_lens;
+    p.uniforms = uniforms;
+    p.noise = noise;
+    p.noise_stride = noise_stride;
+    p.temps = temperatures;
+    p.temperature = temperature;
+    p.S = S;
+    p.V = static_cast<int32_t>(V);
+    p.tokens = out_tokens;
+    p.accepted = out_accepted;
+    p.probs = out_probs;
+    // CTAs of a sequence: as many as fit the GPU at once (two to an SM) with slices of at least 2048
+    // numbers.  64 sequences of 129280 logits: 1 CTA each 81 us, 2 54, 4 42, 8 (two waves) 61.
+    p.C = 1;
+    while (p.C < kVerCluster && sequences * p.C * 2 <= 2 * info.sms && V / (p.C * 2) >= 2048) p.C *= 2;
+    // rows of a round: all where CTAs are few and latency counts (one sequence of 4 drafts, 8 CTAs:
+    // 16.2 us, with one row to a round 21.5); else two, one of which may be read in vain, for one
+    // exchange less (64 sequences: 40.9 us, one 42.0, all 41.8; 200 of 5 short drafts 27.7, 27.8, 34.4)
+    p.R = sequences * p.C <= info.sms ? kVerRound : 2;
+    const uintptr_t mask = 4 * es - 1;
+    p.race_vec = (reinterpret_cast<uintptr_t>(logits) & mask) == 0 && (row_stride % 4 == 0 || S == 0) &&
+                 (seq_stride % 4 == 0 || sequences == 1) && aligned16(noise) && (noise_stride % 4 == 0 || sequences == 1) &&
+                 aligned16(draft_probs) && (!draft_probs || (probs_row_stride % 4 == 0 && probs_seq_stride % 4 == 0));
+    if (sequences * p.C > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
+    return dtype == DS_BF16 ? launch_verify<__nv_bfloat16>(p, dev, sequences, stream)
+                            : launch_verify<float>(p, dev, sequences, stream);
 }
 
 }  // extern "C"
