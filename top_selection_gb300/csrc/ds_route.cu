@@ -11,10 +11,12 @@
 //
 // One warp per row, the row in registers: lane l holds n consecutive experts of one group
 // (each group has a power-of-two number of lanes), so lanes ascend with the experts and the
-// lowest lane holding a maximum holds the lowest expert.  Selection is k rounds of: largest
-// key of the lane, largest of the warp (redux.sync on the order-preserving integer key),
-// lowest lane that has it (ballot), and that lane drops its first copy.  Lane j < k keeps
-// the j-th choice, reads its logit again (the row is in L1) and computes its weight.
+// lowest lane holding a maximum holds the lowest expert.  Each lane sorts its experts (in lists of
+// up to 8, by a network on the order-preserving integer key, equal keys by index); selection is
+// then k rounds of: largest head of the warp (redux.sync), lowest lane that has it (ballot), and
+// that lane moves its list up.  (Searching unsorted lanes in every round took 1172 instructions a
+// row of 256 experts, @@ this way.)  Lane j < k keeps the j-th choice, reads its logit again (the
+// row is in L1) and computes its weight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -83,6 +85,28 @@ struct RouteParams {
     float scale;
 };
 
+// Sorts L numbers, the largest first (odd-even merge networks).
+__device__ __forceinline__ void order(unsigned long long& a, unsigned long long& b) {
+    const unsigned long long hi = a > b ? a : b, lo = a > b ? b : a;
+    a = hi;
+    b = lo;
+}
+template <int L>
+__device__ __forceinline__ void sort_down(unsigned long long (&x)[L]) {
+    if constexpr (L == 2) {
+        order(x[0], x[1]);
+    } else if constexpr (L == 4) {
+        order(x[0], x[1]), order(x[2], x[3]), order(x[0], x[2]), order(x[1], x[3]), order(x[1], x[2]);
+    } else if constexpr (L == 8) {
+        order(x[0], x[1]), order(x[2], x[3]), order(x[4], x[5]), order(x[6], x[7]);
+        order(x[0], x[2]), order(x[1], x[3]), order(x[4], x[6]), order(x[5], x[7]);
+        order(x[1], x[2]), order(x[5], x[6]);
+        order(x[0], x[4]), order(x[1], x[5]), order(x[2], x[6]), order(x[3], x[7]);
+        order(x[2], x[4]), order(x[3], x[5]);
+        order(x[1], x[2]), order(x[3], x[4]), order(x[5], x[6]);
+    }
+}
+
 // Loads the lane's n experts (a run of the row) as fp32; places past the run keep `fill`.
 // VEC: rows and runs start on 16 bytes and n fills whole 16-byte words.
 template <typename T, int EPL, bool VEC>
@@ -128,13 +152,10 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
     // choice values; places past the run get key 0, below every value's key
     uint32_t key[EPL];
     if (p.bias) {
+        float b[EPL];
+        load_run<float, EPL, VEC>(p.bias + (count > 0 ? first : 0), count, 0.f, b);
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            if (i < count) {
-                const float s = p.sigmoid ? logistic(v[i]) : expf(v[i] - mx) / total;
-                v[i] = s + p.bias[first + i];
-            }
-        }
+        for (int i = 0; i < EPL; ++i) v[i] = (p.sigmoid ? logistic(v[i]) : expf(v[i] - mx) / total) + b[i];
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i)  // + 0.f: -0 and +0 are equal
@@ -167,31 +188,56 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
             }
             score = key_f32(__float_as_uint((p.size > 1 ? a + b : a) + 0.f));
         }
-        int rank = 0;
-        for (int j = 0; j < p.groups; ++j) {
-            const uint32_t o = __shfl_sync(kFull, score, j << p.llog);
-            rank += (o > score || (o == score && j < grp)) ? 1 : 0;
+        score = grp < p.groups ? max(score, 1u) : 0u;  // lanes behind the last group have none
+        bool keep = false;
+        for (int j = 0; j < p.topk_groups; ++j) {  // the best group, the lowest of equal ones, in turn
+            const uint32_t top = __reduce_max_sync(kFull, score);
+            const int from = __ffs(__ballot_sync(kFull, score == top)) - 1;
+            if (grp == from >> p.llog) {
+                keep = true;
+                score = 0u;
+            }
         }
-        if (rank >= p.topk_groups) {
+        if (!keep) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) key[i] = 0u;
         }
     }
 
+    // sorted lists: keys, and the place of each in 4 bits, the head's lowest
+    constexpr int L = EPL < 8 ? EPL : 8, NL = EPL / L;
+    uint32_t place[NL];
+#pragma unroll
+    for (int n = 0; n < NL; ++n) {
+        unsigned long long item[L];
+#pragma unroll
+        for (int i = 0; i < L; ++i) item[i] = static_cast<unsigned long long>(key[n * L + i]) << 32 | (15 - i);
+        sort_down<L>(item);
+        place[n] = 0u;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            key[n * L + i] = static_cast<uint32_t>(item[i] >> 32);
+            place[n] |= (15u - static_cast<uint32_t>(item[i])) << (4 * i);
+        }
+    }
     int mine = 0;  // lane j: the j-th choice
     for (int j = 0; j < p.k; ++j) {
-        uint32_t m = key[0];
+        uint32_t head = key[0];
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) m = max(m, key[i]);
-        const uint32_t top = __reduce_max_sync(kFull, m);
-        const int from = __ffs(__ballot_sync(kFull, m == top)) - 1;
+        for (int n = 1; n < NL; ++n) head = max(head, key[n * L]);
+        const uint32_t top = __reduce_max_sync(kFull, head);
+        const int from = __ffs(__ballot_sync(kFull, head == top)) - 1;
         int at = 0;
         bool open = lane == from;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            if (open && key[i] == top) {
-                key[i] = 0u;
-                at = i;
+        for (int n = 0; n < NL; ++n) {
+            const bool here = open && (n == NL - 1 || key[n * L] == top);
+            if (here) {
+                at = n * L + static_cast<int>(place[n] & 15u);
+                place[n] >>= 4;
+#pragma unroll
+                for (int i = 0; i + 1 < L; ++i) key[n * L + i] = key[n * L + i + 1];
+                key[n * L + L - 1] = 0u;
                 open = false;
             }
         }
