@@ -12,6 +12,7 @@ returns torch tensors (PyTorch supplies device memory and streams only).
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 
@@ -354,63 +355,33 @@ def ds_cache_attention(q, dtype, sequences, tokens, q_heads, D, q_seq_stride, q_
                                      int(stream) or None)
 
 
-_SCORING = {"softmax": DS_SOFTMAX, "sigmoid": DS_SIGMOID}
-_GROUP_SCORE = {"max": DS_GROUP_MAX, "top2": DS_GROUP_TOP2}
+class _Names(dict):
+    """Values by name; a name that is none of them is refused."""
+
+    def __missing__(self, name):
+        raise ValueError(f"{name!r} is none of {sorted(map(str, self))}")
 
 
-_torch = None        # the torch module and its stream query, looked up on first use
-_raw_stream = None
+_SCORING = _Names(softmax=DS_SOFTMAX, sigmoid=DS_SIGMOID)
+_GROUP_SCORE = _Names(max=DS_GROUP_MAX, top2=DS_GROUP_TOP2)
+_binding = None         # the compiled tensor binding (csrc/ds_torch.cpp), loaded on first use
 
 
-def _load_torch():
-    global _torch, _raw_stream
-    import torch
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _torch = torch
-    return torch
-
-
-def _float_code(t, what):
-    dtype = t.dtype
-    if dtype is _torch.bfloat16:
-        return DS_BF16
-    if dtype is _torch.float32:
-        return DS_FP32
-    raise TypeError(f"{what}: unsupported dtype {dtype}: bfloat16 and float32 only")
-
-
-def _want(t, what, shape, dtype, index, strided=False):
-    """Checks an argument tensor: dtype, shape, device index, and contiguity (or, with `strided`,
-    a unit last stride only)."""
-    if (t.dtype is dtype and t.shape == shape and t.get_device() == index
-            and (t.is_contiguous() or strided and t.stride(-1) == 1)):
-        return
-    if t.dtype is not dtype:
-        raise TypeError(f"{what} must have dtype {dtype}, not {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{what} must be on cuda:{index} (there is no CPU path), not on {t.device}")
-    raise ValueError(f"{what} must {'have unit stride in its last dimension' if strided else 'be contiguous'}")
-
-
-def _cuda(t, what, dims):
-    """Checks the argument that the others follow: a CUDA tensor of `dims` dimensions with a unit
-    last stride.  Returns its device index."""
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{what} must be a CUDA tensor (there is no CPU path)")
-    if t.dim() != dims:
-        raise ValueError(f"{what} must have {dims} dimensions, not {t.dim()}")
-    if not t.is_contiguous() and t.stride(-1) != 1:
-        raise ValueError(f"{what} must have unit stride in its last dimension")
-    return index
-
-
-def _check(status, what):
-    if status != 0:
-        raise DSError(status, what)
+def _load_binding():
+    """Loads the tensor binding: it checks tensors, allocates outputs and calls the C ABI."""
+    global _binding
+    load()
+    with _lock:
+        if _binding is None:
+            import torch  # noqa: F401  (the binding's own libraries)
+            try:
+                ops = importlib.import_module("._ops", __name__)
+            except ImportError as e:
+                raise RuntimeError("the tensor binding is missing or was built for another torch: build it with "
+                                   "`python -m top_selection_gb300.build`") from e
+            ops.set_error(DSError)
+            _binding = ops
+    return _binding
 
 
 def route(logits, k: int, scoring: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
@@ -424,45 +395,16 @@ def route(logits, k: int, scoring: str = "softmax", bias=None, groups: int = 1, 
     ``counts`` (E,) int32, if given, is added the number of rows that chose each expert.
     Returns (weights (rows, k) float32, experts (rows, k) int32), best first, ties to the lower
     index."""
-    torch = _torch or _load_torch()
-    index = _cuda(logits, "logits", 2)
-    code = _float_code(logits, "logits")
-    rows, E = logits.shape
-    if scoring not in _SCORING or group_score not in _GROUP_SCORE:
-        raise ValueError('scoring is "softmax" or "sigmoid", group_score "max" or "top2"')
-    if bias is not None:
-        _want(bias, "bias", (E,), torch.float32, index)
-    if counts is not None:
-        _want(counts, "counts", (E,), torch.int32, index)
-    shape, device = (rows, max(k, 0)), logits.device
-    weights = torch.empty(shape, dtype=torch.float32, device=device)
-    experts = torch.empty(shape, dtype=torch.int32, device=device)
-    _check(load().ds_route(logits.data_ptr(), code, rows, E, logits.stride(0) if rows > 1 else E, k, _SCORING[scoring],
-                           None if bias is None else bias.data_ptr(), groups, topk_groups, _GROUP_SCORE[group_score],
-                           bool(renormalise), scale, weights.data_ptr(), experts.data_ptr(),
-                           None if counts is None else counts.data_ptr(), _raw_stream(index) if stream is None else int(stream)), "ds_route")
-    return weights, experts
+    return (_binding or _load_binding()).route(logits, k, _SCORING[scoring], bias, groups, topk_groups,
+                                                 _GROUP_SCORE[group_score], renormalise, scale, counts, stream)
 
 
 def route_backward(grad_weights, logits, experts, scoring: str = "softmax", renormalise: bool = True,
                    scale: float = 1.0, stream=None):
     """The gradient of ``route``'s weights with respect to its ``logits`` (rows, E), for the
     ``experts`` it chose: (rows, E) in the logits' dtype.  Other arguments as in ``route``."""
-    torch = _torch or _load_torch()
-    index = _cuda(logits, "logits", 2)
-    code = _float_code(logits, "logits")
-    if scoring not in _SCORING:
-        raise ValueError('scoring is "softmax" or "sigmoid"')
-    rows, E = logits.shape
-    k = experts.shape[-1]
-    _want(experts, "experts", (rows, k), torch.int32, index)
-    _want(grad_weights, "grad_weights", (rows, k), torch.float32, index)
-    grad = torch.empty((rows, E), dtype=logits.dtype, device=logits.device)
-    _check(load().ds_route_backward(grad_weights.data_ptr(), logits.data_ptr(), code, rows, E,
-                                    logits.stride(0) if rows > 1 else E, k, experts.data_ptr(), _SCORING[scoring],
-                                    bool(renormalise), scale, grad.data_ptr(), E, _raw_stream(index) if stream is None else int(stream)),
-           "ds_route_backward")
-    return grad
+    return (_binding or _load_binding()).route_backward(grad_weights, logits, experts, _SCORING[scoring], renormalise, scale,
+                                                          stream)
 
 
 def verify_drafts(logits, drafts, uniforms, noise, draft_probs=None, draft_lens=None, temperature=1.0, stream=None):
@@ -475,91 +417,24 @@ def verify_drafts(logits, drafts, uniforms, noise, draft_probs=None, draft_lens=
     a (B,) float32 tensor, 0 for the likeliest token.  Returns (tokens (B, S + 1) int32 -- the
     accepted drafts, the emitted token, then -1 -- accepted (B,) int32, and the target's
     probability of each token (B, S + 1) float32)."""
-    torch = _torch or _load_torch()
-    index = _cuda(logits, "logits", 3)
-    code = _float_code(logits, "logits")
-    B, rows, V = logits.shape
-    S = rows - 1
-    if S < 0:
-        raise ValueError("logits must have at least one row per sequence")
-    _want(drafts, "drafts", (B, S), torch.int32, index)
-    _want(uniforms, "uniforms", (B, S), torch.float32, index)
-    _want(noise, "noise", (B, V), torch.float32, index, strided=True)
-    q, q_seq, q_row = None, 0, V
-    if draft_probs is not None:
-        _want(draft_probs, "draft_probs", (B, S, V), torch.float32, index, strided=True)
-        q, q_seq = draft_probs.data_ptr(), draft_probs.stride(0)
-        q_row = draft_probs.stride(1) if S > 1 else V
-    if draft_lens is not None:
-        _want(draft_lens, "draft_lens", (B,), torch.int32, index)
-    temps = None
-    if isinstance(temperature, torch.Tensor):
-        _want(temperature, "temperature", (B,), torch.float32, index)
-        temps, temperature = temperature.data_ptr(), 0.0
-    device = logits.device
-    tokens = torch.empty((B, rows), dtype=torch.int32, device=device)
-    accepted = torch.empty((B,), dtype=torch.int32, device=device)
-    probs = torch.empty((B, rows), dtype=torch.float32, device=device)
-    seq_stride, row_stride, _ = logits.stride()
-    _check(load().ds_verify_drafts(logits.data_ptr(), code, B, S, V, seq_stride, row_stride if rows > 1 else V,
-                                   drafts.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(), q, q_seq,
-                                   q_row, uniforms.data_ptr(), noise.data_ptr(), noise.stride(0) if B > 1 else V, temps,
-                                   temperature, tokens.data_ptr(), accepted.data_ptr(), probs.data_ptr(),
-                                   _raw_stream(index) if stream is None else int(stream)), "ds_verify_drafts")
-    return tokens, accepted, probs
-
-
-def _cache_shape(cache, scales):
-    """(pages, heads, page, D, device index) of a 4-bit cache: ``cache`` (pages, heads, page, 2, D / 2) uint8
-    and ``scales`` (pages, heads, page, 4) bfloat16, both contiguous."""
-    torch = _torch or _load_torch()
-    index = _cuda(cache, "cache", 5)
-    pages, heads, page, two, half = cache.shape
-    if two != 2:
-        raise ValueError("cache must have shape (pages, heads, page, 2, D / 2)")
-    _want(cache, "cache", cache.shape, torch.uint8, index)
-    _want(scales, "scales", (pages, heads, page, 4), torch.bfloat16, index)
-    return pages, heads, page, 2 * half, index
+    return (_binding or _load_binding()).verify_drafts(logits, drafts, uniforms, noise, draft_probs, draft_lens,
+                                                         temperature, stream)
 
 
 def cache_store(k, v, cache, scales, slots, stream=None) -> None:
     """Writes keys and values ``k``, ``v`` (tokens, heads, D) to the ``slots`` (tokens,) int32 of a
     4-bit cache: ``cache`` (pages, heads, page, 2, D / 2) uint8 and ``scales`` (pages, heads, page,
     4) bfloat16.  Slot t is place t % page of page t / page; a negative slot is skipped."""
-    torch = _torch or _load_torch()
-    pages, heads, page, D, index = _cache_shape(cache, scales)
-    _cuda(k, "k", 3)
-    code = _float_code(k, "k")
-    T = k.shape[0]
-    shape = (T, heads, D)
-    _want(k, "k", shape, k.dtype, index, strided=True)
-    _want(v, "v", shape, k.dtype, index, strided=True)
-    _want(slots, "slots", (T,), torch.int32, index)
-    k_token, k_head, _ = k.stride()
-    v_token, v_head, _ = v.stride()
-    if T == 1:  # strides of an extent of 1 are never used
-        k_token = v_token = 0
-    if heads == 1:
-        k_head = v_head = 0
-    _check(load().ds_cache_store(k.data_ptr(), v.data_ptr(), code, T, heads, D, k_token, k_head, v_token, v_head,
-                                 cache.data_ptr(), scales.data_ptr(), pages, page, slots.data_ptr(),
-                                 _raw_stream(index) if stream is None else int(stream)), "ds_cache_store")
+    (_binding or _load_binding()).cache_store(k, v, cache, scales, slots, stream)
 
 
 def cache_load(cache, scales, slots, dtype=None, stream=None):
     """Reads the ``slots`` (tokens,) int32 of a 4-bit cache back: keys and values (tokens, heads,
     D) in ``dtype`` (bfloat16, the default, or float32); zeros for a slot outside the cache."""
-    torch = _torch or _load_torch()
-    pages, heads, page, D, index = _cache_shape(cache, scales)
-    T = slots.shape[0]
-    _want(slots, "slots", (T,), torch.int32, index)
-    shape, dtype = (T, heads, D), dtype or torch.bfloat16
-    device = cache.device
-    k, v = torch.empty(shape, dtype=dtype, device=device), torch.empty(shape, dtype=dtype, device=device)
-    _check(load().ds_cache_load(cache.data_ptr(), scales.data_ptr(), pages, page, slots.data_ptr(), T, heads, D,
-                                _float_code(k, "dtype"), k.data_ptr(), v.data_ptr(), _raw_stream(index) if stream is None else int(stream)),
-           "ds_cache_load")
-    return k, v
+    ops = _binding or _load_binding()
+    if dtype is not None and str(dtype) not in ("torch.bfloat16", "torch.float32"):
+        raise TypeError(f"dtype: unsupported dtype {dtype}: bfloat16 and float32 only")
+    return ops.cache_load(cache, scales, slots, str(dtype) == "torch.float32", stream)
 
 
 def cache_attention(q, cache, scales, table, lens, indices=None, scale=None, stream=None):
@@ -570,31 +445,4 @@ def cache_attention(q, cache, scales, table, lens, indices=None, scale=None, str
     or those of them that ``indices`` (B, Q, K) int32 lists (``topk``'s columns; -1 pads).  ``scale``
     is 1 / sqrt(D) by default.  Returns (out (B, Q, query heads, D) in q's dtype, lse (B, Q, query
     heads) float32); a token that sees nothing gives 0 and -inf."""
-    torch = _torch or _load_torch()
-    pages, heads, page, D, index = _cache_shape(cache, scales)
-    _cuda(q, "q", 4)
-    code = _float_code(q, "q")
-    B, Q, hq, _ = q.shape
-    _want(q, "q", (B, Q, hq, D), q.dtype, index, strided=True)
-    if table.dim() != 2:
-        raise ValueError("table must have 2 dimensions")
-    width = table.shape[1]
-    _want(table, "table", (B, width), torch.int32, index, strided=True)
-    _want(lens, "lens", (B,), torch.int32, index)
-    K, listed = 0, None
-    if indices is not None:
-        K = indices.shape[-1]
-        _want(indices, "indices", (B, Q, K), torch.int32, index)
-        if K == 0:  # a list of nothing: one entry that is not seen
-            indices, K = indices.new_full((B, Q, 1), -1), 1
-        listed = indices.data_ptr()
-    device = q.device
-    out = torch.empty((B, Q, hq, D), dtype=q.dtype, device=device)
-    lse = torch.empty((B, Q, hq), dtype=torch.float32, device=device)
-    q_seq, q_token, q_head, _ = q.stride()
-    _check(load().ds_cache_attention(q.data_ptr(), code, B, Q, hq, D, q_seq, q_token, q_head, cache.data_ptr(),
-                                     scales.data_ptr(), pages, heads, page, table.data_ptr(), width,
-                                     table.stride(0) if B > 1 else width, lens.data_ptr(), listed, K,
-                                     D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
-                                     _raw_stream(index) if stream is None else int(stream)), "ds_cache_attention")
-    return out, lse
+    return (_binding or _load_binding()).cache_attention(q, cache, scales, table, lens, indices, scale, stream)
