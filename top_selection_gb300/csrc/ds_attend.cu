@@ -69,9 +69,9 @@ struct AttendParams {
     const int32_t* indices;        // [B, Q, K] or null
     void* out;
     float* lse;
-    float* ws_o;                   // split partials: [unit][split][rows][D]
-    float* ws_ml;                  //                 [unit][split][rows][2]
-    int64_t max_pos;               // table width * page
+    float4* ws_o;                  // split partials: [unit][split][fragment][lane]
+    float2* ws_ml;                 //                 [unit][split][rows]: maximum, sum of weights
+    int32_t max_pos, span;         // table width * page; max_pos or K
     int32_t Q, K, heads, group, page_log, pages;
     int32_t rows;                  // query rows per unit before tiling
     int32_t row_groups, splits, chunk;
@@ -169,6 +169,11 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v, float f) {
     const __nv_bfloat162 a = __floats2bfloat162_rn(v.x * f, v.y * f), b = __floats2bfloat162_rn(v.z * f, v.w * f);
     *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
+template <typename T>
+__device__ __forceinline__ T to_type(float v) {
+    if constexpr (sizeof(T) == 2) return __float2bfloat16_rn(v);
+    else return v;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -210,10 +215,57 @@ struct TileAt {
     }
 };
 
+// Writes joined output fragments of a unit, divided by the sums of the weights, and lse.
+template <typename T, int D>
+struct Emit {
+    const AttendParams& p;
+    int b, h, q0;
+    bool picked;
+    int first, rows, g, t;  // the row group's first row and its rows; the lane's place
+    __device__ __forceinline__ int64_t row_of(int r) const {  // row r of the group in the output
+        const int ur = first + r;
+        const int qi = picked ? q0 : ur / p.group;
+        const int hd = h * p.group + (picked ? ur : ur - qi * p.group);
+        return (static_cast<int64_t>(b) * p.Q + qi) * (static_cast<int64_t>(p.heads) * p.group) + hd;
+    }
+    __device__ __forceinline__ void lse(int64_t e, float top, float sum) const {
+        if (p.lse) p.lse[e] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    }
+    // the four fragments of row tile and code word `item`: numbers 8 w .. 8 w + 7 of the lane's eighth
+    __device__ __forceinline__ void four(int item, const float4 (&a)[4], float top0, float sum0, float top1,
+                                         float sum1) const {
+        const int j = item / (D / 64), w = item % (D / 64), r = 8 * j + 2 * t;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (r + c >= rows) continue;
+            const int64_t e = row_of(r + c);
+            const float sum = c ? sum1 : sum0, f = sum > 0.f ? 1.f / sum : 0.f;
+            T* dst = static_cast<T*>(p.out) + e * D + g * (D / 8) + 8 * w;
+            store4(dst, c ? make_float4(a[0].y, a[1].y, a[2].y, a[3].y) : make_float4(a[0].x, a[1].x, a[2].x, a[3].x), f);
+            store4(dst + 4, c ? make_float4(a[0].w, a[1].w, a[2].w, a[3].w) : make_float4(a[0].z, a[1].z, a[2].z, a[3].z), f);
+            if (g == 0 && w == 0) lse(e, c ? top1 : top0, sum);
+        }
+    }
+    // one fragment: numbers k and k + 4 of a word
+    __device__ __forceinline__ void one(int frag, float4 a, float top0, float sum0, float top1, float sum1) const {
+        const int j = frag / (D / 16), mt = frag % (D / 16), r = 8 * j + 2 * t;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (r + c >= rows) continue;
+            const int64_t e = row_of(r + c);
+            const float sum = c ? sum1 : sum0, f = sum > 0.f ? 1.f / sum : 0.f;
+            T* dst = static_cast<T*>(p.out) + e * D + g * (D / 8) + 8 * (mt / 4) + mt % 4;
+            dst[0] = to_type<T>((c ? a.y : a.x) * f);
+            dst[4] = to_type<T>((c ? a.w : a.z) * f);
+            if (g == 0 && mt == 0) lse(e, c ? top1 : top0, sum);
+        }
+    }
+};
+
 // CTAs per SM that the registers are cut for
 template <typename T>
 constexpr int att_resident(int D, int NT) {
-    return sizeof(T) == 4 ? (NT == 1 ? 3 : 2) : NT == 1 ? 4 : 2;
+    return sizeof(T) == 4 ? (NT == 1 ? 3 : 2) : NT == 1 ? 3 : 2;
 }
 
 // T: type of q and out.  NQ / NP: f16 parts of q and of the weights.  bf16: one part each (q is
@@ -242,7 +294,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     const bool picked = p.indices != nullptr;
     const int b = picked ? bq / p.Q : bq;
     const int q0 = picked ? bq % p.Q : 0;
-    const int len = static_cast<int>(min(static_cast<int64_t>(p.lens[b]), p.max_pos));
+    const int len = min(p.lens[b], p.max_pos);
     // query token i sees positions below len - (Q - 1 - i)
     const int end_all = max(picked ? len - (p.Q - 1 - q0) : len, 0);
     const int count = picked ? p.K : end_all;       // positions (or list entries) of this unit
@@ -254,15 +306,18 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     const int32_t* list = picked ? p.indices + static_cast<int64_t>(bq) * p.K : nullptr;
     const int page_mask = (1 << p.page_log) - 1;
 
-    const auto entry_of = [&](int j, int& pos) -> uint32_t {  // list entry or position j
-        pos = 0x7FFFFFFF;
-        if (j >= to) return kNoEntry;
-        const int at = picked ? list[j] : j;
-        if (at < 0 || at >= end_all) return kNoEntry;
-        const int page = table[at >> p.page_log];
-        if (page < 0 || page >= p.pages) return kNoEntry;
-        pos = at;
-        return ((static_cast<uint32_t>(page) * p.heads + h) << p.page_log) + (at & page_mask);
+    // Entries come in three steps, so that no load waits for another: the position at place j (a
+    // list's value), its page, and the entry, each a tile ahead of the next.  Loads are made in
+    // range whatever the values are (a list's and a table's are the caller's); the entry decides.
+    const int last = min(from + p.chunk, p.span);
+    const auto position_at = [&](int j) -> int { return j >= last ? -1 : picked ? list[j] : j; };
+    const auto page_of = [&](int at) -> int {
+        return table[(static_cast<uint32_t>(at) < static_cast<uint32_t>(p.max_pos) ? at : 0) >> p.page_log];
+    };
+    const auto entry_of = [&](int at, int page, int& pos) -> uint32_t {
+        const bool seen = at >= 0 && at < end_all && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
+        pos = seen ? at : 0x7FFFFFFF;
+        return seen ? ((static_cast<uint32_t>(page) * p.heads + h) << p.page_log) + (at & page_mask) : kNoEntry;
     };
     unsigned char* ring = smem + warp * (kAttStages * At::kBytes);
     const uint32_t ring_at = smem_u32(ring);
@@ -301,15 +356,25 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     const bool runs = !picked && p.page_log >= 5;
     const auto is_run = [&](uint32_t entry) { return runs && __all_sync(kAll, entry != kNoEntry); };
 
-    // tiles of this warp: two in flight while one is computed, and the entries of the next
+    // tiles of this warp: two in flight while one is computed
     constexpr int STRIDE = kAttWarps * kAttTile;
     int j0 = from + warp * kAttTile;
     int pos[kAttStages];  // the lane's position in each tile: current, in flight, next
-    uint32_t entry;
+    int at_ahead, page_ahead, at_far;
+    {
+        int at[kAttStages], page[kAttStages];
 #pragma unroll
-    for (int s = 0; s < kAttStages; ++s) {
-        entry = entry_of(j0 + s * STRIDE + lane, pos[s]);
-        if (s + 1 < kAttStages) issue(s, entry, is_run(entry));
+        for (int s = 0; s < kAttStages; ++s) at[s] = position_at(j0 + s * STRIDE + lane);
+        at_far = position_at(j0 + kAttStages * STRIDE + lane);
+#pragma unroll
+        for (int s = 0; s < kAttStages; ++s) page[s] = page_of(at[s]);
+#pragma unroll
+        for (int s = 0; s + 1 < kAttStages; ++s) {
+            const uint32_t entry = entry_of(at[s], page[s], pos[s]);
+            issue(s, entry, is_run(entry));
+        }
+        at_ahead = at[kAttStages - 1];
+        page_ahead = page[kAttStages - 1];
     }
 
     // q as the second operand: row g of each tile, the lane's quarter of the numbers in the
@@ -438,12 +503,15 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
         {
             int next = slot + kAttStages - 1;
             if (next >= kAttStages) next -= kAttStages;
+            const uint32_t entry = entry_of(at_ahead, page_ahead, pos[kAttStages - 1]);
             issue(next, entry, is_run(entry));
         }
         const int here = pos[0];
 #pragma unroll
         for (int i = 0; i + 1 < kAttStages; ++i) pos[i] = pos[i + 1];
-        entry = entry_of(j0 + kAttStages * STRIDE + lane, pos[kAttStages - 1]);
+        at_ahead = at_far;
+        page_ahead = page_of(at_ahead);
+        at_far = position_at(j0 + (kAttStages + 1) * STRIDE + lane);
         const unsigned char* tile = ring + slot * At::kBytes;
         if (++slot == kAttStages) slot = 0;
 
@@ -652,9 +720,12 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     copies_wait<0>();
     __syncthreads();  // every warp is done with its ring
 
-    // join the warps: sums over the lanes of a row, then shared memory
-    float* sm_o = reinterpret_cast<float*>(smem);        // [warps][ROWS][D]
-    float* sm_r = sm_o + kAttWarps * ROWS * D;           // [warps][ROWS][4]
+    // Join the warps: sums over the lanes of a row, then shared memory.  Output fragments stay as the
+    // matrix unit leaves them, one float4 a lane, in shared memory and in the workspace: every access
+    // is a run of 512 bytes.
+    constexpr int NF = NT * KS;                          // fragments of a warp
+    float4* sm_o = reinterpret_cast<float4*>(smem);      // [warps][NF][32]
+    float4* sm_r = sm_o + kAttWarps * NF * 32;           // [warps][ROWS]: maximum, sum of p, of p (m + MID s)
     const float back = 1.f / wmul;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -668,146 +739,174 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
                 zs[c] += __shfl_xor_sync(kAll, zs[c], d);
             }
             if (!CENTRE) zs[c] -= 7.5f * ones[j][c] * back;
-            const int r = 8 * j + 2 * t + c;
-            if (g == 0) {
-                float* q = sm_r + (warp * ROWS + r) * 4;
-                q[0] = ms[c], q[1] = ls[c], q[2] = zs[c];
-            }
-            // numbers of the lane: its eighth, word w, code nib (+ 4 in the fragment's second half)
-            float* dst = sm_o + (warp * ROWS + r) * D + g * (D / 8);
+            if (g == 0) sm_r[warp * ROWS + 8 * j + 2 * t + c] = make_float4(ms[c], ls[c], zs[c], 0.f);
+        }
 #pragma unroll
-            for (int mt = 0; mt < KS; ++mt) {
-                const float f = mt & 1 ? 1048576.f : 16777216.f;
-                dst[8 * (mt / 4) + mt % 4] = o[j][mt][c] * f * back;
-                dst[8 * (mt / 4) + mt % 4 + 4] = o[j][mt][c + 2] * f * back;
-            }
+        for (int mt = 0; mt < KS; ++mt) {
+            const float f = mt & 1 ? 1048576.f : 16777216.f;
+            sm_o[(warp * NF + j * KS + mt) * 32 + lane] = make_float4(o[j][mt][0] * f * back, o[j][mt][1] * f * back,
+                                                                      o[j][mt][2] * f * back, o[j][mt][3] * f * back);
         }
     }
     __syncthreads();
-    const int rows = min(ROWS, p.rows - rg * ROWS);
-    const auto result = [&](int r, int d, float4 acc, float top, float sum) {
-        const int ur = rg * ROWS + r;
-        const int qi = picked ? q0 : ur / p.group;
-        const int hd = h * p.group + (picked ? ur : ur - qi * p.group);
-        const int64_t e = (static_cast<int64_t>(b) * p.Q + qi) * (static_cast<int64_t>(p.heads) * p.group) + hd;
-        store4(static_cast<T*>(p.out) + e * D + d, acc, sum > 0.f ? 1.f / sum : 0.f);
-        if (d == 0 && p.lse) p.lse[e] = sum > 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
-    };
-    float* sm_j = sm_r + kAttWarps * ROWS * 4;           // the CTA's join, for its cluster: [ROWS][D]
-    float* sm_ml = sm_j + ROWS * D;                      // [ROWS][2]
-    for (int i = tid; i < rows * (D / 4); i += kAttWarps * 32) {
-        const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float top = kNone;
-#pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) top = fmaxf(top, sm_r[(w * ROWS + r) * 4]);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
+    // one warp joins the four fragments of a row tile j and code word w: they hold eight numbers in
+    // a row of rows 2t and 2t + 1
+    float4* sm_j = sm_r + kAttWarps * ROWS;              // the CTA's join, for its cluster: [NF][32]
+    float2* sm_ml = reinterpret_cast<float2*>(sm_j + NF * 32);  // [ROWS]
+    constexpr int ITEMS = NF / 4;
+    const Emit<T, D> emit = {p, b, h, q0, picked, rg * ROWS, min(ROWS, p.rows - rg * ROWS), g, t};
+    for (int item = warp; item < ITEMS; item += kAttWarps) {
+        const int r = 8 * (item / (D / 64)) + 2 * t;
+        float4 a0[kAttWarps], a1[kAttWarps];
+        float top0 = kNone, top1 = kNone, sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
         for (int w = 0; w < kAttWarps; ++w) {
-            const float* q = sm_r + (w * ROWS + r) * 4;
-            const float4 x = *reinterpret_cast<const float4*>(sm_o + (w * ROWS + r) * D + d);
-            const float f = exp2_fast(q[0] - top);
-            acc.x += f * (x.x + q[2]), acc.y += f * (x.y + q[2]);
-            acc.z += f * (x.z + q[2]), acc.w += f * (x.w + q[2]);
-            sum += f * q[1];
+            a0[w] = sm_r[w * ROWS + r];
+            a1[w] = sm_r[w * ROWS + r + 1];
+            top0 = fmaxf(top0, a0[w].x);
+            top1 = fmaxf(top1, a1[w].x);
+        }
+        float4 acc[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kAttWarps; ++w) {
+            const float f0 = exp2_fast(a0[w].x - top0), f1 = exp2_fast(a1[w].x - top1);
+            sum0 += f0 * a0[w].y;
+            sum1 += f1 * a1[w].y;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const float4 x = sm_o[(w * NF + item * 4 + f) * 32 + lane];
+                acc[f].x += f0 * (x.x + a0[w].z), acc[f].y += f1 * (x.y + a1[w].z);
+                acc[f].z += f0 * (x.z + a0[w].z), acc[f].w += f1 * (x.w + a1[w].z);
+            }
         }
         if (p.splits == 1) {
-            result(r, d, acc, top, sum);
-        } else if (p.cluster) {
-            *reinterpret_cast<float4*>(sm_j + r * D + d) = acc;
-            if (d == 0) *reinterpret_cast<float2*>(sm_ml + r * 2) = make_float2(top, sum);
-        } else {
-            const int64_t e = (static_cast<int64_t>(unit) * p.splits + split) * ROWS + r;
-            *reinterpret_cast<float4*>(p.ws_o + e * D + d) = acc;
-            if (d == 0) *reinterpret_cast<float2*>(p.ws_ml + e * 2) = make_float2(top, sum);
+            emit.four(item, acc, top0, sum0, top1, sum1);
+            continue;
+        }
+        float4* to = p.cluster ? sm_j : p.ws_o + (static_cast<int64_t>(unit) * p.splits + split) * (NF * 32);
+        float2* ml = p.cluster ? sm_ml : p.ws_ml + (static_cast<int64_t>(unit) * p.splits + split) * ROWS;
+#pragma unroll
+        for (int f = 0; f < 4; ++f) to[(item * 4 + f) * 32 + lane] = acc[f];
+        if (g == 0 && item % (D / 64) == 0) {
+            ml[r] = make_float2(top0, sum0);
+            ml[r + 1] = make_float2(top1, sum1);
         }
     }
     if (!p.cluster) return;
-    // every CTA of the cluster joins its share of the rows from all of them
+    // every CTA of the cluster joins its share of the items from all of them
     cluster_sync_all();
-    for (int i = split * (kAttWarps * 32) + tid; i < rows * (D / 4); i += p.splits * (kAttWarps * 32)) {
-        const int r = i / (D / 4), d = i % (D / 4) * 4;
-        float top = kNone;
-        for (int c = 0; c < p.splits; ++c)
-            top = fmaxf(top, __uint_as_float(ld_cluster_u32(map_rank(sm_ml + r * 2, c))));
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll 4
+    for (int item = warp * p.splits + split; item < ITEMS; item += kAttWarps * p.splits) {
+        const int r = 8 * (item / (D / 64)) + 2 * t;
+        float top0 = kNone, top1 = kNone, sum0 = 0.f, sum1 = 0.f;
         for (int c = 0; c < p.splits; ++c) {
-            const uint32_t ml = map_rank(sm_ml + r * 2, c);
-            const uint4 x = ld_cluster_v4(map_rank(sm_j + r * D + d, c));
-            const float f = exp2_fast(__uint_as_float(ld_cluster_u32(ml)) - top);
-            acc.x += f * __uint_as_float(x.x), acc.y += f * __uint_as_float(x.y);
-            acc.z += f * __uint_as_float(x.z), acc.w += f * __uint_as_float(x.w);
-            sum += f * __uint_as_float(ld_cluster_u32(ml + 4));
+            const uint4 ml = ld_cluster_v4(map_rank(sm_ml + r, c));  // rows r and r + 1
+            top0 = fmaxf(top0, __uint_as_float(ml.x));
+            top1 = fmaxf(top1, __uint_as_float(ml.z));
         }
-        result(r, d, acc, top, sum);
+        float4 acc[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < p.splits; ++c) {
+            const uint4 ml = ld_cluster_v4(map_rank(sm_ml + r, c));
+            const float f0 = exp2_fast(__uint_as_float(ml.x) - top0), f1 = exp2_fast(__uint_as_float(ml.z) - top1);
+            sum0 += f0 * __uint_as_float(ml.y);
+            sum1 += f1 * __uint_as_float(ml.w);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const uint4 x = ld_cluster_v4(map_rank(sm_j + (item * 4 + f) * 32 + lane, c));
+                acc[f].x += f0 * __uint_as_float(x.x), acc[f].y += f1 * __uint_as_float(x.y);
+                acc[f].z += f0 * __uint_as_float(x.z), acc[f].w += f1 * __uint_as_float(x.w);
+            }
+        }
+        emit.four(item, acc, top0, sum0, top1, sum1);
     }
     cluster_sync_all();  // the others have read this CTA's share
 }
 
-// Joins the splits of one query row: one CTA per row, its warps take the splits in turn.
-// Only the splits that hold positions are read (the others wrote nothing); their order is
-// fixed, so a call's result does not depend on timing.
-template <typename T, int D>
-__global__ void __launch_bounds__(1024) ds_attend_join_kernel(const AttendParams p, int ROWS) {
-    __shared__ __align__(16) float sh_o[32][D];
-    __shared__ float sh_l[32];
+// Joins the splits of a unit: a CTA takes FR fragments (four that belong together, or with few
+// units one, so that more CTAs read), its warps take the splits in turn.  Only the splits that
+// hold positions are read (the others wrote nothing); their order is fixed, so a call's result does
+// not depend on timing.
+template <typename T, int D, int NT, int FR>
+__global__ void __launch_bounds__(1024) ds_attend_join_kernel(const AttendParams p) {
+    constexpr int KS = D / 16, NF = NT * KS, ROWS = 8 * NT, PARTS = NF / FR;
+    extern __shared__ __align__(128) unsigned char smem[];  // [warps][FR][32] float4, [warps][8] float
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    constexpr int PER = D / 32;
+    const int g = lane >> 2, t = lane & 3;
+    float4* sh_o = reinterpret_cast<float4*>(smem);
+    float2* sh_l = reinterpret_cast<float2*>(sh_o + warps * FR * 32);
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t at = blockIdx.x;  // (sequence * Q + token) * query heads + head
-    const int hq = p.heads * p.group;
-    const int bq = static_cast<int>(blockIdx.x / static_cast<uint32_t>(hq));
-    const int hd = static_cast<int>(blockIdx.x - bq * hq);
-    const int b = bq / p.Q, qi = bq - b * p.Q;
+    const uint32_t unit = blockIdx.x / PARTS;
+    const int first = static_cast<int>(blockIdx.x % PARTS) * FR;  // the CTA's first fragment
+    const uint32_t uh = unit / static_cast<uint32_t>(p.row_groups);
+    const int rg = static_cast<int>(unit - uh * p.row_groups);
+    const int bq = static_cast<int>(uh / static_cast<uint32_t>(p.heads));
+    const int h = static_cast<int>(uh - bq * p.heads);
     const bool picked = p.indices != nullptr;
-    const int ur = picked ? hd % p.group : qi * p.group + hd % p.group;
-    const int64_t unit = (static_cast<int64_t>(picked ? bq : b) * p.heads + hd / p.group) * p.row_groups + ur / ROWS;
-    const int64_t len = min(static_cast<int64_t>(p.lens[b]), p.max_pos);
-    const int64_t count = picked ? p.K : max(len, int64_t(0));
-    const int splits = max(1, min(p.splits, static_cast<int>((count + p.chunk - 1) / p.chunk)));
-    const int64_t base = unit * p.splits * ROWS + ur % ROWS;
-    float top = kNone;
-    for (int s = lane; s < splits; s += 32) top = fmaxf(top, p.ws_ml[(base + static_cast<int64_t>(s) * ROWS) * 2]);
+    const int b = picked ? bq / p.Q : bq, q0 = picked ? bq % p.Q : 0;
+    const int count = picked ? p.K : max(min(p.lens[b], p.max_pos), 0);
+    const int splits = max(1, min(p.splits, (count + p.chunk - 1) / p.chunk));
+    const int r = 8 * (first / KS) + 2 * t;
+    const float4* ml = reinterpret_cast<const float4*>(p.ws_ml + static_cast<int64_t>(unit) * p.splits * ROWS + r);
+    const float4* part = p.ws_o + (static_cast<int64_t>(unit) * p.splits * NF + first) * 32 + lane;
+    float top0 = kNone, top1 = kNone, sum0 = 0.f, sum1 = 0.f;
+#pragma unroll 4
+    for (int s = g; s < splits; s += 8) {
+        const float4 x = ml[s * (ROWS / 2)];  // maximum and sum of rows r and r + 1
+        top0 = fmaxf(top0, x.x);
+        top1 = fmaxf(top1, x.z);
+    }
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
-    float acc[PER], sum = 0.f;
+    for (int d = 4; d <= 16; d <<= 1) {
+        top0 = fmaxf(top0, __shfl_xor_sync(kAll, top0, d));
+        top1 = fmaxf(top1, __shfl_xor_sync(kAll, top1, d));
+    }
+    float4 acc[FR];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    for (int f = 0; f < FR; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = warp; s < splits; s += warps) {
-        const int64_t e = base + static_cast<int64_t>(s) * ROWS;
-        const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + e * 2);
-        const float f = exp2_fast(ml.x - top);
-        sum += f * ml.y;
+        const float4 x = ml[s * (ROWS / 2)];
+        const float f0 = exp2_fast(x.x - top0), f1 = exp2_fast(x.z - top1);
+        sum0 += f0 * x.y;
+        sum1 += f1 * x.w;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] += f * p.ws_o[e * D + lane * PER + i];
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) sh_o[warp][lane * PER + i] = acc[i];
-    if (lane == 0) sh_l[warp] = sum;
-    __syncthreads();
-    for (int d = threadIdx.x * 4; d < D; d += blockDim.x * 4) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        float total = 0.f;
-        for (int w = 0; w < warps; ++w) {
-            const float4 x = *reinterpret_cast<const float4*>(&sh_o[w][d]);
-            y.x += x.x, y.y += x.y, y.z += x.z, y.w += x.w;
-            total += sh_l[w];
+        for (int f = 0; f < FR; ++f) {
+            const float4 y = part[(static_cast<int64_t>(s) * NF + f) * 32];
+            acc[f].x += f0 * y.x, acc[f].y += f1 * y.y, acc[f].z += f0 * y.z, acc[f].w += f1 * y.w;
         }
-        store4(static_cast<T*>(p.out) + at * D + d, y, total > 0.f ? 1.f / total : 0.f);
-        if (d == 0 && p.lse) p.lse[at] = total > 0.f ? (top + log2f(total)) * kLn2 : -INFINITY;
     }
+    if (warps > 1) {
+#pragma unroll
+        for (int f = 0; f < FR; ++f) sh_o[(warp * FR + f) * 32 + lane] = acc[f];
+        if (g == 0) sh_l[warp * 4 + t] = make_float2(sum0, sum1);
+        __syncthreads();
+        if (warp != 0) return;
+        for (int w = 1; w < warps; ++w) {
+            const float2 x = sh_l[w * 4 + t];
+            sum0 += x.x;
+            sum1 += x.y;
+#pragma unroll
+            for (int f = 0; f < FR; ++f) {
+                const float4 y = sh_o[(w * FR + f) * 32 + lane];
+                acc[f].x += y.x, acc[f].y += y.y, acc[f].z += y.z, acc[f].w += y.w;
+            }
+        }
+    }
+    const Emit<T, D> emit = {p, b, h, q0, picked, rg * ROWS, min(ROWS, p.rows - rg * ROWS), g, t};
+    if constexpr (FR == 4) emit.four(first / 4, acc, top0, sum0, top1, sum1);
+    else emit.one(first, acc[0], top0, sum0, top1, sum1);
 }
 
 template <typename T, int D, int NT>
-static ds_status attend(const AttendParams& p, int dev, int64_t units, int64_t out_rows, cudaStream_t stream) {
+static ds_status attend(const AttendParams& p, int dev, int sms, int64_t units, cudaStream_t stream) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
     auto kern = ds_attend_kernel<T, D, NT, PARTS, PARTS>;
     const size_t ring = static_cast<size_t>(kAttWarps) * kAttStages * TileAt<D>::kBytes + D / 16 * 32 * 8 * NT * PARTS;
-    const size_t join = (static_cast<size_t>(kAttWarps) * (D + 4) + D + 2) * 8 * NT * sizeof(float);
+    const size_t join = (static_cast<size_t>(kAttWarps) * (D + 4) + D + 2) * 8 * NT * sizeof(float);  // sm_o, sm_r, sm_j, sm_ml
     const size_t smem = ring > join ? ring : join;
     // the opt-in above 48 KB is a property of the kernel on a device: set once
     static std::atomic<bool> opted[64];
@@ -819,16 +918,20 @@ static ds_status attend(const AttendParams& p, int dev, int64_t units, int64_t o
     const dim3 grid(static_cast<unsigned>(units * p.splits));
     const ds_status st = launch_pdl(kern, grid, kAttWarps * 32, smem, p.cluster ? p.splits : 1, stream, p);
     if (st != DS_OK || p.splits == 1 || p.cluster) return st;
-    int warps = 1;
-    while (warps < 32 && 4 * warps < p.splits) warps <<= 1;
-    return launch_pdl(ds_attend_join_kernel<T, D>, dim3(static_cast<unsigned>(out_rows)), warps * 32, 0, 1, stream, p,
-                      8 * NT);
+    const auto join_by = [&](auto kernel, int fr, int most) {
+        int warps = 1;
+        while (warps < most && 4 * warps < p.splits) warps <<= 1;
+        const size_t bytes = warps > 1 ? static_cast<size_t>(warps) * (fr * 32 * 16 + 32) : 0;
+        return launch_pdl(kernel, dim3(static_cast<unsigned>(units * (NT * D / 16) / fr)), warps * 32, bytes, 1, stream, p);
+    };
+    return units * (NT * D / 64) < 2 * sms ? join_by(ds_attend_join_kernel<T, D, NT, 1>, 1, 32)
+                                           : join_by(ds_attend_join_kernel<T, D, NT, 4>, 4, 16);
 }
 
 template <typename T, int D>
-static ds_status attend_rows(const AttendParams& p, int dev, int nt, int64_t units, int64_t out_rows, cudaStream_t stream) {
-    if (nt == 1) return attend<T, D, 1>(p, dev, units, out_rows, stream);
-    return attend<T, D, 2>(p, dev, units, out_rows, stream);
+static ds_status attend_rows(const AttendParams& p, int dev, int sms, int nt, int64_t units, cudaStream_t stream) {
+    if (nt == 1) return attend<T, D, 1>(p, dev, sms, units, stream);
+    return attend<T, D, 2>(p, dev, sms, units, stream);
 }
 
 }  // namespace dsk
@@ -876,7 +979,8 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
     p.indices = indices;
     p.out = out;
     p.lse = out_lse;
-    p.max_pos = table_width * page;
+    p.max_pos = static_cast<int32_t>(table_width * page);
+    p.span = indices ? K : p.max_pos;
     p.Q = tokens;
     p.K = K;
     p.heads = heads;
@@ -891,15 +995,16 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
     const int nt = rows > 8 ? 2 : 1;
     p.row_groups = (p.rows + 8 * nt - 1) / (8 * nt);
     const int64_t units = (indices ? sequences * tokens : sequences) * heads * p.row_groups;
-    const int64_t out_rows = sequences * tokens * q_heads;
-    // Splits: two CTAs for each place on an SM (what one leaves over at its end another fills;
-    // 4M positions of 16 rows: one 174 us, two 150, three 160, four 170), at least two tiles a warp.
-    const int64_t span = indices ? K : p.max_pos;
+    // Splits.  Few units, so few sequences: as many as fill every place on an SM once (4 contexts of
+    // 1M positions and 16 rows: 131 us; twice 141, three times 150).  Many units: four times, since
+    // their lengths differ and the longest must not be left for the end (48 contexts of up to 8192
+    // positions: once 82 us, twice 81, four times 77).  At least one tile for each warp.
+    const int64_t span = p.span;
     const int64_t unit_tiles = kAttWarps * kAttTile;
     const int64_t places = static_cast<int64_t>(info.sms) *
                            (dtype == DS_BF16 ? att_resident<__nv_bfloat16>(D, nt) : att_resident<float>(D, nt));
-    int64_t splits = (2 * places + units - 1) / units;
-    const int64_t most = (span + 2 * unit_tiles - 1) / (2 * unit_tiles);
+    int64_t splits = ((2 * units < places ? 1 : 4) * places + units - 1) / units;
+    const int64_t most = (span + unit_tiles - 1) / unit_tiles;
     if (splits > most) splits = most;
     if (splits < 1) splits = 1;
     int64_t chunk = (span + splits - 1) / splits;
@@ -909,25 +1014,25 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
     if (splits < 1) splits = 1;
     p.splits = static_cast<int32_t>(splits);
     p.chunk = static_cast<int32_t>(chunk);
-    if (units * splits > 0x7FFFFFFFLL || out_rows > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
+    if (units * splits > 0x7FFFFFFFLL || units * (nt * D / 16) > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
     // Lists have one length: up to 8 splits of one are a cluster and join over its shared memory
-    // (512 positions for 64 rows: 12.7 us, through the workspace 15.0).  Contexts differ in theirs,
+    // (512 positions for 64 rows: 11.4 us, through the workspace 13.6).  Contexts differ in theirs,
     // and a cluster holds its places until the longest split is done (48 contexts of up to 8192
-    // positions: 114 us, through the workspace 90).
+    // positions: 105 us, through the workspace 81).
     p.cluster = indices && splits > 1 && splits <= kAttCluster;
     if (splits > 1 && !p.cluster) {
         const size_t entries = static_cast<size_t>(units) * splits * 8 * nt;
         void* ws = nullptr;
         const ds_status st = library_workspace(dev, kWsAttend, entries * (D + 2) * sizeof(float), stream, &ws);
         if (st != DS_OK) return st;
-        p.ws_o = static_cast<float*>(ws);
-        p.ws_ml = p.ws_o + entries * D;
+        p.ws_o = static_cast<float4*>(ws);
+        p.ws_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) + entries * D);
     }
     if (dtype == DS_BF16)
-        return D == 64 ? attend_rows<__nv_bfloat16, 64>(p, dev, nt, units, out_rows, stream)
-                       : attend_rows<__nv_bfloat16, 128>(p, dev, nt, units, out_rows, stream);
-    return D == 64 ? attend_rows<float, 64>(p, dev, nt, units, out_rows, stream)
-                   : attend_rows<float, 128>(p, dev, nt, units, out_rows, stream);
+        return D == 64 ? attend_rows<__nv_bfloat16, 64>(p, dev, info.sms, nt, units, stream)
+                       : attend_rows<__nv_bfloat16, 128>(p, dev, info.sms, nt, units, stream);
+    return D == 64 ? attend_rows<float, 64>(p, dev, info.sms, nt, units, stream)
+                   : attend_rows<float, 128>(p, dev, info.sms, nt, units, stream);
 }
 
 }  // extern "C"
