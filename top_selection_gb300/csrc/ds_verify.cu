@@ -183,43 +183,78 @@ __device__ __forceinline__ void add_numbers(RowStat& a, const float (&x)[M][N], 
     }
 }
 
-// A thread's statistics of CTA `part`'s slice of a row of V numbers: 16-byte words from the first
-// aligned place on, the numbers before and behind them one each by the first CTA's threads.
-template <typename T, bool GREEDY>
-__device__ __forceinline__ RowStat slice_stats(const T* x, int V, int part, int parts, float c) {
-    constexpr int N = Vec<T>::N, U = 4;
-    RowStat a = {-INFINITY, 0.f, 0x7FFFFFFF};
-    const int tid = threadIdx.x;
-    const int head = min(V, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(x) & 15u)) & 15u) / static_cast<int>(sizeof(T)));
-    const int words = (V - head) / N;
-    const int from = static_cast<int>(static_cast<int64_t>(words) * part / parts);
-    const int to = static_cast<int>(static_cast<int64_t>(words) * (part + 1) / parts);
-    const uint4* w = reinterpret_cast<const uint4*>(x + head);
-    if (part == 0) {
-        const int tail = head + words * N;  // up to 2 (N - 1) numbers outside the words
-        const int place = tid < head ? tid : tail + tid - head;
-        if (place < V) {
-            const float one[1][1] = {{ver_f32(x[place])}};
-            add_numbers<1, 1, GREEDY>(a, one, place, 0, c);
+// CTA `part`'s slice of a row of V numbers: 16-byte words from the first aligned place on; the
+// numbers before and behind the words fall to the first CTA.
+template <typename T>
+struct Slice {
+    static constexpr int N = Vec<T>::N;
+    const T* x;
+    int V, head, words, from, to;
+    __device__ __forceinline__ Slice(const T* x, int V, int part, int parts) : x(x), V(V) {
+        const uint32_t past = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x)) & 15u;
+        head = min(V, static_cast<int>((16u - past) & 15u) / static_cast<int>(sizeof(T)));
+        words = (V - head) / N;
+        from = static_cast<int>(static_cast<int64_t>(words) * part / parts);
+        to = static_cast<int>(static_cast<int64_t>(words) * (part + 1) / parts);
+    }
+    // U words from `at` on, one a thread; -inf behind the slice
+    template <int U>
+    __device__ __forceinline__ void load(int at, uint4 (&q)[U]) const {
+        constexpr uint32_t none = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+        const uint4* w = reinterpret_cast<const uint4*>(x + head);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            q[u] = make_uint4(none, none, none, none);
+            if (at + u * kVerThreads < to) q[u] = w[at + u * kVerThreads];
         }
     }
-    RowStat b = {-INFINITY, 0.f, 0x7FFFFFFF};
-    int i = from + tid;
-    for (; i + (U - 1) * kVerThreads < to; i += U * kVerThreads) {
-        uint4 q[U];
-        float y[U][N];
-#pragma unroll
-        for (int u = 0; u < U; ++u) q[u] = w[i + u * kVerThreads];
-#pragma unroll
-        for (int u = 0; u < U; ++u) Vec<T>::unpack(q[u], y[u]);
-        add_numbers<U, N, GREEDY>(b, y, head + i * N, kVerThreads * N, c);
+    // the number outside the words that is this thread's, if it has one
+    __device__ __forceinline__ int outside() const {
+        const int tid = threadIdx.x, place = tid < head ? tid : head + words * N + tid - head;
+        return place < V ? place : -1;
     }
-    for (; i < to; i += kVerThreads) {
-        float y[1][N];
-        Vec<T>::unpack(w[i], y[0]);
-        add_numbers<1, N, GREEDY>(b, y, head + i * N, 0, c);
+};
+
+// Each warp's statistics of the CTA's slices of `rows` rows, into `out`.  A thread loads the next
+// words, of the same row or the next, while it works on the last.
+template <typename T, bool GREEDY>
+__device__ __forceinline__ void rows_stats(const T* x0, int64_t stride, int rows, int V, int part, int parts, float c,
+                                           RowStat (*out)[kVerWarps]) {
+    constexpr int N = Vec<T>::N, U = sizeof(T) == 4 ? 4 : 2, STEP = U * kVerThreads;
+    const int tid = threadIdx.x;
+    Slice<T> next(x0, V, part, parts);
+    int at = next.from + tid;
+    uint4 q[U];
+    next.load(at, q);
+    for (int i = 0; i < rows; ++i) {
+        const Slice<T> s = next;
+        RowStat a = {-INFINITY, 0.f, 0x7FFFFFFF};
+        // every thread takes the same steps (what lies behind the slice is -inf)
+        for (int base = s.from; base < s.to || base == s.from; base += STEP) {
+            float y[U][N];
+#pragma unroll
+            for (int u = 0; u < U; ++u) Vec<T>::unpack(q[u], y[u]);
+            const int here = base + tid;
+            if (base + STEP < s.to) {
+                s.load(here + STEP, q);
+            } else if (i + 1 < rows) {
+                next = Slice<T>(x0 + (i + 1) * stride, V, part, parts);
+                next.load(next.from + tid, q);
+            }
+            add_numbers<U, N, GREEDY>(a, y, s.head + here * N, kVerThreads * N, c);
+        }
+        if (part == 0) {
+            const int place = s.outside();
+            if (place >= 0) {
+                const float one[1][1] = {{ver_f32(s.x[place])}};
+                RowStat b = {-INFINITY, 0.f, 0x7FFFFFFF};
+                add_numbers<1, 1, GREEDY>(b, one, place, 0, c);
+                a = both_stats(a, b, c);
+            }
+        }
+        a = warp_stats(a, c, GREEDY);
+        if ((tid & 31) == 0) out[i][tid >> 5] = a;
     }
-    return both_stats(a, b, c);
 }
 
 struct Race {
@@ -342,12 +377,9 @@ __global__ void __launch_bounds__(kVerThreads, 2) ds_verify_kernel(const VerifyP
                 if (p.q) qt = p.q[b * p.q_seq + (n + lane) * p.q_row + t];
             }
         }
-        for (int i = 0; i < rows; ++i) {
-            const T* x = seq + (n + i) * p.row_stride;
-            RowStat a = greedy ? slice_stats<T, true>(x, p.V, part, p.C, c) : slice_stats<T, false>(x, p.V, part, p.C, c);
-            a = warp_stats(a, c, greedy);
-            if (lane == 0) sh_warp[i][warp] = a;
-        }
+        const T* x0 = seq + n * p.row_stride;
+        if (greedy) rows_stats<T, true>(x0, p.row_stride, rows, p.V, part, p.C, c, sh_warp);
+        else rows_stats<T, false>(x0, p.row_stride, rows, p.V, part, p.C, c, sh_warp);
         __syncthreads();
         RowStat* mine = sh_cta[round & 1];
         if (warp < rows) {
