@@ -5,10 +5,13 @@
 // ds_cache.cu), so a query row q scores it as
 //     q . (s c + m) = s (q . c) + m (sum q).
 // With weights p and w = f16(p s) (times a power of two), the values add up to
-//     sum p (s c + m) = sum w c  +  sum p (m + 7.5 s)  -  7.5 sum w,
-// the rounding of w meeting centred codes only: were it to meet c itself, errors of one sign
-// (equal weights) would be large against a result that averages out.  sum w comes from the
-// matrix unit as well, against a row of ones.
+//     sum p (s c + m) = sum w (c - 7.5)  +  sum p (m + 7.5 s).
+// The first sum is taken as  sum_even w c - sum_odd w (15 - c) - 7.5 (sum_even w - sum_odd w)  over
+// even and odd positions (complementing a word of codes is one instruction): the running sums stay
+// near zero where weights are alike, and the rounding of w and of the matrix unit's additions
+// (which cut off) then do not pile up against a result that averages out: over 4 x 1M positions the
+// error was 2.5 times bf16's own rounding with plain codes, and is not to be told from it this way.  sum_even w - sum_odd w
+// comes from the matrix unit as well, against a row of ones.
 //
 // The codes never leave registers once they are there: with tokens as the rows of the matrix
 // instruction, the four lanes that share a fragment row read a token's codes as they lie in
@@ -102,13 +105,14 @@ __device__ __forceinline__ void split_f16(float a, float b, uint32_t (&part)[NS]
 }
 
 // Codes `nib` (0 .. 3) of both halves of w (w already moved down by 8 for nib >= 2): two f16
-// numbers c 2^-24, for odd nib 16 c 2^-24.  CENTRE: c - 8 instead of c, exact as well.
+// numbers c 2^-24, for odd nib 16 c 2^-24.  CENTRE: c - 8 and 16 (c - 8), by way of 1024 + c (normal
+// numbers: the matrix unit keeps fewer bits of subnormal ones' products, 9e-6 of an fp32 result).
 template <bool CENTRE>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int nib) {
-    const uint32_t x = w & (nib & 1 ? 0x00F000F0u : 0x000F000Fu);
-    if (!CENTRE) return x;
-    const uint32_t c8 = nib & 1 ? 0x00800080u : 0x00080008u;
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&c8));
+    const uint32_t mask = nib & 1 ? 0x00F000F0u : 0x000F000Fu;
+    if (!CENTRE) return w & mask;
+    const uint32_t x = (w & mask) | 0x64006400u, mid = nib & 1 ? 0x64806480u : 0x64086408u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&mid));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -276,7 +280,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     constexpr int KS = D / 16;       // k-steps of the scores, and row tiles of the output
     constexpr int ROWS = 8 * NT;
     constexpr bool CENTRE = sizeof(T) == 4;
+    // fp32: the matrix unit's additions cut off, so each of its sums starts at zero and is added here
+    constexpr bool EXACT = sizeof(T) == 4;
     constexpr float MID = CENTRE ? 8.f : 7.5f;
+    constexpr float kUnit = CENTRE ? 1.f : 16777216.f;  // an operand's code counts 1 / kUnit
     using At = TileAt<D>;
     extern __shared__ __align__(128) unsigned char smem[];  // the warps' rings; then the join
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -474,7 +481,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
             for (int i = 0; i < QW / 2; ++i)
                 reinterpret_cast<uint2*>(sm_q)[(kk * 32 + lane) * (QW / 2) + i] = make_uint2(w[2 * i], w[2 * i + 1]);
         }
-        fold *= 16777216.f * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        fold *= kUnit * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
     }
 
     __syncthreads();
@@ -495,6 +502,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
         unseen |= (r < p.rows ? 1u : 0u) << (2 * j) | (r + 1 < p.rows ? 2u : 0u) << (2 * j);
     }
     float wmul = 1.2676506e30f;  // kTop / r; 2^100 until a value scale has been seen
+    const float sign = !CENTRE && (g & 1) ? -1.f : 1.f;  // of the weights of this lane's positions
 
     int slot = 0;
     for (; j0 < to; j0 += STRIDE) {
@@ -555,10 +563,17 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
                 const uint32_t a0 = code_pair<CENTRE>(w0, 0), a1 = code_pair<CENTRE>(w1, 0);
                 const uint32_t a2 = code_pair<CENTRE>(w0, 1), a3 = code_pair<CENTRE>(w1, 1);
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int j = 0; j < NT; ++j) {
+                    float step[4] = {0.f, 0.f, 0.f, 0.f};
+                    float(&sum)[4] = EXACT ? step : s[j][i];
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-                        mma_f16(s[j][i], a0, a1, a2, a3, qf[(j * NQ + n) * 2], qf[(j * NQ + n) * 2 + 1]);
+                    for (int n = NQ - 1; n >= 0; --n)
+                        mma_f16(sum, a0, a1, a2, a3, qf[(j * NQ + n) * 2], qf[(j * NQ + n) * 2 + 1]);
+                    if (EXACT) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[j][i][c] += step[c];
+                    }
+                }
             }
         }
         float vs[4], vm[4];
@@ -598,7 +613,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
         // r where a value scale leaves it behind
         float vw[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vw[i] = vs[i] * wmul;
+        for (int i = 0; i < 4; ++i) vw[i] = vs[i] * wmul * sign;
         float2 high[NT];
         float most = -INFINITY;
 #pragma unroll
@@ -607,7 +622,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
             high[j].y = fmaxf(max3(s[j][0][1], s[j][0][3], s[j][1][1]), s[j][1][3]);
             most = max3(most, high[j].x, high[j].y);
         }
-        if (fresh || __any_sync(kAll, most > kRaise || fmaxf(max3(vw[0], vw[1], vw[2]), vw[3]) > kOver)) {
+        if (fresh || __any_sync(kAll, most > kRaise || fmaxf(max3(fabsf(vw[0]), fabsf(vw[1]), fabsf(vw[2])), fabsf(vw[3])) > kOver)) {
             float vtop = 1e-30f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) vtop = fmaxf(vtop, vs[i] < INFINITY ? vs[i] : 0.f);
@@ -618,7 +633,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
                 change = to_mul / wmul;
                 wmul = to_mul;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) vw[i] = vs[i] * wmul;
+                for (int i = 0; i < 4; ++i) vw[i] = vs[i] * (wmul * sign);
             }
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -693,6 +708,10 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
                 } else {
                     v[r][0] = *reinterpret_cast<const uint32_t*>(tile + At::piece(row, 2 + (g >> 2)) + 4 * (g & 3));
                 }
+                if (!CENTRE && (r & 1)) {  // complements at the odd positions
+#pragma unroll
+                    for (int w = 0; w < D / 64; ++w) v[r][w] = ~v[r][w];
+                }
             }
 #pragma unroll
             for (int w = 0; w < D / 64; ++w) {
@@ -704,13 +723,20 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
                     const uint32_t a0 = code_pair<CENTRE>(xl >> sh, nib), a1 = code_pair<CENTRE>(xh >> sh, nib);
                     const uint32_t a2 = code_pair<CENTRE>(yl >> sh, nib), a3 = code_pair<CENTRE>(yh >> sh, nib);
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
+                    for (int j = 0; j < NT; ++j) {
+                        float step[4] = {0.f, 0.f, 0.f, 0.f};
+                        float(&sum)[4] = EXACT ? step : o[j][4 * w + nib];
 #pragma unroll
-                        for (int n = 0; n < NP; ++n)
-                            mma_f16(o[j][4 * w + nib], a0, a1, a2, a3, wf[j][i][0][n], wf[j][i][1][n]);
+                        for (int n = NP - 1; n >= 0; --n)
+                            mma_f16(sum, a0, a1, a2, a3, wf[j][i][0][n], wf[j][i][1][n]);
+                        if (EXACT) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[j][4 * w + nib][c] += step[c];
+                        }
+                    }
                 }
             }
-            if constexpr (!CENTRE) {  // sum of w, against ones
+            if constexpr (!CENTRE) {  // even minus odd w, against ones
                 constexpr uint32_t ONE = 0x3C003C00u;
 #pragma unroll
                 for (int j = 0; j < NT; ++j) mma_f16(ones[j], ONE, ONE, ONE, ONE, wf[j][i][0][0], wf[j][i][1][0]);
@@ -743,7 +769,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
         }
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
-            const float f = mt & 1 ? 1048576.f : 16777216.f;
+            const float f = mt & 1 ? kUnit * 0.0625f : kUnit;
             sm_o[(warp * NF + j * KS + mt) * 32 + lane] = make_float4(o[j][mt][0] * f * back, o[j][mt][1] * f * back,
                                                                       o[j][mt][2] * f * back, o[j][mt][3] * f * back);
         }

@@ -17,7 +17,7 @@
 // warp, D/16 lanes each, 16 numbers a lane (two pieces of 8: 16 bytes of bf16 in, 4 bytes of codes
 // out), so a warp's code stores and loads are whole lines.  A warp takes U turns with all their
 // loads in flight at once.  Heads are the grid's second extent: no index is divided.
-// 16411 tokens of 8 heads in bf16, stored and read back: @@ us; with 8 numbers a lane and plain
+// 16411 tokens of 8 heads in bf16, stored and read back: 36.7 us (4.6 TB/s); with 8 numbers a lane and plain
 // conversions 50 us, bound by instructions (22 a number); one turn at a time 57 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -15,7 +15,7 @@
 // up to 8, by a network on the order-preserving integer key, equal keys by index); selection is
 // then k rounds of: largest head of the warp (redux.sync), lowest lane that has it (ballot), and
 // that lane moves its list up.  (Searching unsorted lanes in every round took 1172 instructions a
-// row of 256 experts, @@ this way.)  Lane j < k keeps the j-th choice, reads its logit again (the
+// row of 256 experts, 996 this way.)  Lane j < k keeps the j-th choice, reads its logit again (the
 // row is in L1) and computes its weight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
