@@ -385,8 +385,8 @@ ds_status ds_cache_load(const void* cache, const void* scales, int64_t pages, in
  *                counts twice
  *   scale        finite;  out  [sequences, tokens, q_heads, D] dtype, 16-byte aligned;  out_lse  [sequences,
  *                tokens, q_heads] floats or NULL
- * Products are exact in the codes; q enters in its own precision, weights in at least 16 bits,
- * all sums in fp32.  Positions are split over CTAs whose partial results lie in a library-owned
+ * q enters in its own precision, scores, softmax sums and outputs are summed in fp32; the weights
+ * that meet the values are rounded to 11 bits for bf16 q and 22 for fp32.  Positions are split over CTAs whose partial results lie in a library-owned
  * workspace of (device, stream), grown with cudaMalloc as ds_topk's is: a call under stream
  * capture that would have to grow it returns DS_ERR_WORKSPACE.  pages * page * heads < 2^32 - 1,
  * table_width * page <= 2^30.

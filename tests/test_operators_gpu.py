@@ -533,6 +533,114 @@ def test_attention_offsets_past_32_bits(ds):
     assert np.array_equal(k.cpu().numpy(), ref.value(codes, s, m).astype(np.float32))
 
 
+def close_in_norm(got, want, dtype):
+    """The error's norm against the result's: bf16's rounding is at most 2^-9 of each element and
+    the weights' (11 bits) adds a random 2^-12 times a few; fp32: sums of n terms in fp32 by
+    lanes, warps and splits, 2^-24 times the root of the additions and a few roundings each."""
+    off = np.linalg.norm(got - want) / np.linalg.norm(want)
+    assert off <= (2.0 ** -8 if dtype == torch.bfloat16 else 3e-6), off
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("same", [False, True])
+def test_attention_equal_weights_over_a_long_context(ds, dtype, same):
+    """Equal weights average values out to 1/sqrt(n) of their size: errors of one sign would show.
+    `same`: every value row has the same scale, so that the weights are rounded alike."""
+    rng = np.random.default_rng(14)
+    n, D = 60000, 64
+    cache, scales, table = filled(ds, rng, 1, 1, D, 128, [n])
+    if same:
+        scales[..., 2] = 0.3359375
+        scales[..., 3] = -2.53125
+    q = torch.zeros(1, 1, 4, D, device="cuda", dtype=dtype)
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    want = ref.attention(host(q), Paged(cache, scales, table), [n])
+    out, lse = ds.cache_attention(q, cache, scales, table, ln)
+    close_in_norm(host(out), want[0], dtype)
+    assert np.all(np.abs(host(lse) - math.log(n)) <= 1e-5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("order", ["up", "down", "spike"])
+def test_attention_running_maximum(ds, dtype, order):
+    """Scores that rise or fall all along the context, or stand out once: the running maximum
+    moves in every step, in none, or once."""
+    rng = np.random.default_rng(15)
+    n, D = 3000, 64
+    cache, scales, table = filled(ds, rng, 1, 1, D, 32, [n])
+    k = rng.standard_normal((n, 1, D)).astype(np.float32) * 0.1
+    k[:, 0, 0] += {"up": np.linspace(-40, 40, n), "down": np.linspace(40, -40, n),
+                   "spike": np.where(np.arange(n) == 1234, 30.0, 0.0)}[order]
+    v = rng.standard_normal((n, 1, D)).astype(np.float32)
+    t = table[0].cpu().numpy()
+    slots = dev((t[np.arange(n) // 32] * 32 + np.arange(n) % 32).astype(np.int32))
+    ds.cache_store(dev(k), dev(v), cache, scales, slots)
+    q = np.zeros((1, 1, 8, D), dtype=np.float32)
+    q[..., 0] = np.linspace(-3, 3, 8)
+    q = dev(q, dtype)
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    want = ref.attention(host(q), Paged(cache, scales, table), [n], scale=1.0)
+    out, lse = ds.cache_attention(q, cache, scales, table, ln, scale=1.0)
+    # scores reach 120: 2^-24 * 120 * log2(e) * 2 of a weight, and as much of lse
+    limit = 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -13 * 5 if dtype == torch.bfloat16 else 1e-4
+    assert np.all(np.abs(host(out) - want[0]) <= limit)
+    assert np.all(np.abs(host(lse) - want[1]) <= 1e-4)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("low,high", [(-30, 30), (30, -30), (-100, -90), (100, 110)])
+def test_attention_values_of_every_size(ds, dtype, low, high):
+    """Value rows whose sizes run from 2^low to 2^high along the context: the weights' common
+    power of two follows the largest."""
+    rng = np.random.default_rng(16)
+    n, D = 700, 64
+    cache, scales, table = filled(ds, rng, 1, 1, D, 32, [n])
+    size = np.exp2(np.linspace(low, high, n)).astype(np.float32)[:, None, None]
+    k = rng.standard_normal((n, 1, D)).astype(np.float32)
+    v = rng.standard_normal((n, 1, D)).astype(np.float32) * size
+    t = table[0].cpu().numpy()
+    slots = dev((t[np.arange(n) // 32] * 32 + np.arange(n) % 32).astype(np.int32))
+    ds.cache_store(dev(k), dev(v), cache, scales, slots)
+    q = dev(rng.standard_normal((1, 1, 16, D)).astype(np.float32), dtype)
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    want = ref.attention(host(q), Paged(cache, scales, table), [n])
+    out, _ = ds.cache_attention(q, cache, scales, table, ln)
+    limit = 2.0 ** -8 * np.abs(want[0]) if dtype == torch.bfloat16 else 0
+    top = (np.abs(want[0]).max(-1, keepdims=True))
+    assert np.all(np.abs(host(out) - want[0]) <= limit + (2.0 ** -10 if dtype == torch.bfloat16 else 3e-5) * top)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [math.inf, math.nan, -math.inf])
+def test_attention_bad_numbers_in_masked_places(ds, dtype, bad):
+    """A later token's scales that are not finite do not reach the tokens that do not see it."""
+    rng = np.random.default_rng(17)
+    n, Q = 70, 3
+    cache, scales, table = filled(ds, rng, 1, 2, 64, 16, [n])
+    q = dev(rng.standard_normal((1, Q, 4, 64)).astype(np.float32), dtype)
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    want = ref.attention(host(q), Paged(cache, scales, table), [n])
+    scales[table[0, (n - 1) // 16].item(), :, (n - 1) % 16] = bad
+    out, lse = ds.cache_attention(q, cache, scales, table, ln)
+    seen = slice(0, Q - 1)
+    check_attention((out[:, seen], lse[:, seen]), (want[0][:, seen], want[1][:, seen]), 5.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_rows_that_see_something_late(ds, dtype):
+    """Lists whose first hundreds of entries are not seen, differently for each token."""
+    rng = np.random.default_rng(18)
+    n, Q, K = 400, 2, 700
+    cache, scales, table = filled(ds, rng, 1, 1, 128, 64, [n])
+    q = dev(rng.standard_normal((1, Q, 16, 128)).astype(np.float32), dtype)
+    idx = np.full((1, Q, K), -1, dtype=np.int32)
+    idx[0, 0, 500:] = rng.integers(n, size=200)
+    idx[0, 1, 131] = n - 1
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    want = ref.attention(host(q), Paged(cache, scales, table), [n], idx)
+    check_attention(ds.cache_attention(q, cache, scales, table, ln, indices=dev(idx)), want, 5.0, dtype)
+
+
 # ------------------------------------------------------------------ streams, graphs --
 
 def test_other_stream_repeat_and_graph(ds):
@@ -583,3 +691,18 @@ def test_attention_workspace_under_capture(ds):
     assert st == 7          # DS_ERR_WORKSPACE
     want = ref.attention(host(q), Paged(cache, scales, table), [4000])
     check_attention(ds.cache_attention(q, cache, scales, table, ln), want, 5.0, torch.bfloat16)
+
+
+def test_decode_step_example():
+    """The example runs the operators together; the same seed gives the same tokens."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decode_step.py")
+    spec = importlib.util.spec_from_file_location("decode_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    emitted, lens = example.main(steps=4, seed=1)
+    assert (emitted >= 4).all() and (emitted <= 4 * (example.DRAFTS + 1)).all()
+    assert torch.equal(lens.long(), example.CONTEXT + emitted)
+    again, _ = example.main(steps=4, seed=1)
+    assert torch.equal(emitted, again)

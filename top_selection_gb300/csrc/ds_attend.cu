@@ -9,17 +9,18 @@
 // The first sum is taken as  sum_even w c - sum_odd w (15 - c) - 7.5 (sum_even w - sum_odd w)  over
 // even and odd positions (complementing a word of codes is one instruction): the running sums stay
 // near zero where weights are alike, and the rounding of w and of the matrix unit's additions
-// (which cut off) then do not pile up against a result that averages out: over 4 x 1M positions the
-// error was 2.5 times bf16's own rounding with plain codes, and is not to be told from it this way.  sum_even w - sum_odd w
-// comes from the matrix unit as well, against a row of ones.
+// (which cut off) then do not pile up against a result that averages out.  Over 4 x 1M positions the
+// error was 2.5 times bf16's own rounding with plain codes; this way it adds nothing to it.
+// sum_even w - sum_odd w comes from the matrix unit as well, against a row of ones.
 //
 // The codes never leave registers once they are there: with tokens as the rows of the matrix
 // instruction, the four lanes that share a fragment row read a token's codes as they lie in
 // memory (any order of the contracted dimension serves, as long as q is read in the same
 // order).  A masked word is the operand: the 16-bit pattern c, or 16 c, is the subnormal f16
-// number c 2^-24, or 16 c 2^-24, which the matrix unit multiplies exactly; the powers of two
-// are taken out of q beforehand and out of the sums at the end.  Eight codes cost five
-// instructions (one shift, four ANDs; value words of two tokens are interleaved first).
+// number c 2^-24, or 16 c 2^-24, and the powers of two are taken out of q beforehand and out of
+// the sums at the end.  Eight codes cost five instructions (one shift, four ANDs; value words of
+// two tokens are interleaved first), against eleven for conversion by an offset.  The matrix unit
+// keeps fewer bits of subnormal products, far below bf16's rounding; fp32 takes normal numbers.
 //
 // m16n8k16 (mma.sync) rather than tcgen05: a step has 8 to 32 query rows per key head, the
 // operand that streams is the cache, and tcgen05 takes it from shared memory only, so each
