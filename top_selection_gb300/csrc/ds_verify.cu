@@ -51,7 +51,6 @@ struct VerifyParams {
     float temperature;
     int32_t S, V;
     int32_t C, R;                    // CTAs of a sequence, rows of a round
-    int32_t race_vec;                // the race's three rows may be read four numbers at a time
     int32_t* tokens;
     int32_t* accepted;
     float* probs;
@@ -220,7 +219,7 @@ struct Slice {
 template <typename T, bool GREEDY>
 __device__ __forceinline__ void rows_stats(const T* x0, int64_t stride, int rows, int V, int part, int parts, float c,
                                            RowStat (*out)[kVerWarps]) {
-    constexpr int N = Vec<T>::N, U = sizeof(T) == 4 ? 4 : 2, STEP = U * kVerThreads;
+    constexpr int N = Vec<T>::N, U = 4, W = 16 / N, STEP = U * kVerThreads;  // W words at a time
     const int tid = threadIdx.x;
     Slice<T> next(x0, V, part, parts);
     int at = next.from + tid;
@@ -231,9 +230,9 @@ __device__ __forceinline__ void rows_stats(const T* x0, int64_t stride, int rows
         RowStat a = {-INFINITY, 0.f, 0x7FFFFFFF};
         // every thread takes the same steps (what lies behind the slice is -inf)
         for (int base = s.from; base < s.to || base == s.from; base += STEP) {
-            float y[U][N];
+            uint4 now[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) Vec<T>::unpack(q[u], y[u]);
+            for (int u = 0; u < U; ++u) now[u] = q[u];
             const int here = base + tid;
             if (base + STEP < s.to) {
                 s.load(here + STEP, q);
@@ -241,7 +240,13 @@ __device__ __forceinline__ void rows_stats(const T* x0, int64_t stride, int rows
                 next = Slice<T>(x0 + (i + 1) * stride, V, part, parts);
                 next.load(next.from + tid, q);
             }
-            add_numbers<U, N, GREEDY>(a, y, s.head + here * N, kVerThreads * N, c);
+#pragma unroll
+            for (int u = 0; u < U; u += W) {
+                float y[W][N];
+#pragma unroll
+                for (int k = 0; k < W; ++k) Vec<T>::unpack(now[u + k], y[k]);
+                add_numbers<W, N, GREEDY>(a, y, s.head + (here + u * kVerThreads) * N, kVerThreads * N, c);
+            }
         }
         if (part == 0) {
             const int place = s.outside();
@@ -268,15 +273,35 @@ __device__ __forceinline__ Race warp_best(Race a) {
     return a;
 }
 
+// Four numbers from place v on, in one load where `vec`.
+__device__ __forceinline__ void four(const float* p, bool vec, float (&x)[4]) {
+    if (vec) {
+        const float4 w = *reinterpret_cast<const float4*>(p);
+        x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = p[i];
+    }
+}
+__device__ __forceinline__ void four(const __nv_bfloat16* p, bool vec, float (&x)[4]) {
+    if (vec) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = ver_f32(p[i]);
+    }
+}
+
 // A thread's best of r / e over CTA `part`'s slice; q null: the draft is one-hot at t (t < 0: r = p).
-template <typename T, int N>
+// Places go in groups of four from the first one where the noise is aligned to 16 bytes; the logits
+// and q, whose rows may lie otherwise, are read four at a time where both are aligned there too.
+template <typename T>
 __device__ __forceinline__ Race slice_race(const T* x, const float* q, int t, const float* e, int V, int part, int parts,
                                            float m, float c, float inv_s) {
     float br = 0.f, be = 1.f;  // the best so far
     int bi = 0x7FFFFFFF;
-    const int groups = V / N;
-    const int from = static_cast<int>(static_cast<int64_t>(groups) * part / parts);
-    const int to = static_cast<int>(static_cast<int64_t>(groups) * (part + 1) / parts);
     // r / e against br / be by cross products: no quotient, no branch (a thread's bests change
     // often while it has seen few places, and some lane's always does)
     const auto one = [&](int v, float xv, float qv, float ev) {
@@ -286,48 +311,42 @@ __device__ __forceinline__ Race slice_race(const T* x, const float* q, int t, co
         be = wins ? ev : be;
         bi = wins ? v : bi;
     };
-    constexpr int U = N == 4 ? 2 : 8;
-    int g = from + static_cast<int>(threadIdx.x);
-    const auto groups_at = [&](int g, auto count) {
+    const int head = min(V, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(e) & 15u)) & 15u) / 4);
+    const int groups = (V - head) / 4;
+    const int from = static_cast<int>(static_cast<int64_t>(groups) * part / parts);
+    const int to = static_cast<int>(static_cast<int64_t>(groups) * (part + 1) / parts);
+    const T* xg = x + head;
+    const float *eg = e + head, *qg = q ? q + head : nullptr;
+    const bool vec = (reinterpret_cast<uintptr_t>(xg) & (4 * sizeof(T) - 1)) == 0 &&
+                     (reinterpret_cast<uintptr_t>(qg) & 15u) == 0;
+    const auto groups_at = [&](int g, auto count, auto wide) {  // loads of `count` groups in flight
         constexpr int M = decltype(count)::value;
-        float xv[M][N], qv[M][N], ev[M][N];
+        float xv[M][4], qv[M][4], ev[M][4];
 #pragma unroll
         for (int k = 0; k < M; ++k) {
-            const int at = g + k * kVerThreads;
-            if constexpr (N == 4) {
-                if constexpr (sizeof(T) == 4) {
-                    const float4 w = reinterpret_cast<const float4*>(x)[at];
-                    xv[k][0] = w.x, xv[k][1] = w.y, xv[k][2] = w.z, xv[k][3] = w.w;
-                } else {
-                    const uint2 w = reinterpret_cast<const uint2*>(x)[at];
-                    xv[k][0] = __uint_as_float(w.x << 16), xv[k][1] = __uint_as_float(w.x & 0xFFFF0000u);
-                    xv[k][2] = __uint_as_float(w.y << 16), xv[k][3] = __uint_as_float(w.y & 0xFFFF0000u);
-                }
-                const float4 we = reinterpret_cast<const float4*>(e)[at];
-                ev[k][0] = we.x, ev[k][1] = we.y, ev[k][2] = we.z, ev[k][3] = we.w;
-                if (q) {
-                    const float4 wq = reinterpret_cast<const float4*>(q)[at];
-                    qv[k][0] = wq.x, qv[k][1] = wq.y, qv[k][2] = wq.z, qv[k][3] = wq.w;
-                }
-            } else {
-                xv[k][0] = ver_f32(x[at]);
-                ev[k][0] = e[at];
-                if (q) qv[k][0] = q[at];
-            }
+            const int at = (g + k * kVerThreads) * 4;
+            four(xg + at, wide.value, xv[k]);
+            four(eg + at, true, ev[k]);
+            if (q) four(qg + at, wide.value, qv[k]);
         }
 #pragma unroll
         for (int k = 0; k < M; ++k)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int v = (g + k * kVerThreads) * N + i;
+            for (int i = 0; i < 4; ++i) {
+                const int v = head + (g + k * kVerThreads) * 4 + i;
                 one(v, xv[k][i], q ? qv[k][i] : v == t ? 1.f : 0.f, ev[k][i]);
             }
     };
-    for (; g + (U - 1) * kVerThreads < to; g += U * kVerThreads) groups_at(g, std::integral_constant<int, U>{});
-    for (; g < to; g += kVerThreads) groups_at(g, std::integral_constant<int, 1>{});
+    int g = from + static_cast<int>(threadIdx.x);
+    const auto all = [&](auto wide) {
+        for (; g + kVerThreads < to; g += 2 * kVerThreads) groups_at(g, std::integral_constant<int, 2>{}, wide);
+        for (; g < to; g += kVerThreads) groups_at(g, std::integral_constant<int, 1>{}, wide);
+    };
+    if (vec) all(std::true_type{});
+    else all(std::false_type{});
     Race a = {br / be, bi};
-    const int v = groups * N + static_cast<int>(threadIdx.x);
-    if (part == 0 && v < V) {  // a thread's places no longer ascend here
+    const int tid = threadIdx.x, v = tid < head ? tid : head + groups * 4 + tid - head;
+    if (part == 0 && v < V) {  // a thread's places do not ascend here
         br = 0.f, be = 1.f, bi = 0x7FFFFFFF;
         one(v, ver_f32(x[v]), q ? q[v] : v == t ? 1.f : 0.f, e[v]);
         best_of(a.v, a.i, br / be, bi);
@@ -432,8 +451,7 @@ __global__ void __launch_bounds__(kVerThreads, 2) ds_verify_kernel(const VerifyP
         int t = refused && !p.q ? p.drafts[b * p.S + n] : -1;
         const float inv_s = 1.f / stop.s;
         for (int attempt = 0; attempt < 2; ++attempt) {  // the second: r was 0 everywhere, so p itself
-            Race a = p.race_vec ? slice_race<T, 4>(x, q, t, e, p.V, part, p.C, stop.m, c, inv_s)
-                                : slice_race<T, 1>(x, q, t, e, p.V, part, p.C, stop.m, c, inv_s);
+            Race a = slice_race(x, q, t, e, p.V, part, p.C, stop.m, c, inv_s);
             a = warp_best(a);
             if (lane == 0) sh_race[warp] = a;
             __syncthreads();
@@ -537,10 +555,6 @@ ds_status ds_verify_drafts(const void* logits, int32_t dtype, int64_t sequences,
     // 16.2 us, with one row to a round 21.5); else two, one of which may be read in vain, for one
     // exchange less (64 sequences: 40.9 us, one 42.0, all 41.8; 200 of 5 short drafts 27.7, 27.8, 34.4)
     p.R = sequences * p.C <= info.sms ? kVerRound : 2;
-    const uintptr_t mask = 4 * es - 1;
-    p.race_vec = (reinterpret_cast<uintptr_t>(logits) & mask) == 0 && (row_stride % 4 == 0 || S == 0) &&
-                 (seq_stride % 4 == 0 || sequences == 1) && aligned16(noise) && (noise_stride % 4 == 0 || sequences == 1) &&
-                 aligned16(draft_probs) && (!draft_probs || (probs_row_stride % 4 == 0 && probs_seq_stride % 4 == 0));
     if (sequences * p.C > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
     return dtype == DS_BF16 ? launch_verify<__nv_bfloat16>(p, dev, sequences, stream)
                             : launch_verify<float>(p, dev, sequences, stream);
