@@ -11,12 +11,13 @@
 //
 // One warp per row, the row in registers: lane l holds n consecutive experts of one group
 // (each group has a power-of-two number of lanes), so lanes ascend with the experts and the
-// lowest lane holding a maximum holds the lowest expert.  Each lane sorts its experts (in lists of
-// up to 8, by a network on the order-preserving integer key, equal keys by index); selection is
-// then k rounds of: largest head of the warp (redux.sync), lowest lane that has it (ballot), and
-// that lane moves its list up.  (Searching unsorted lanes in every round took 1172 instructions a
-// row of 256 experts, 996 this way.)  Lane j < k keeps the j-th choice, reads its logit again (the
-// row is in L1) and computes its weight.
+// lowest lane holding a maximum holds the lowest expert.  Each lane sorts its order-preserving
+// integer keys (lists of up to 8, by a network of minima and maxima); selection is then k rounds
+// of: largest head of the warp (redux.sync), lowest lane that has it (ballot), and that lane moves
+// its list up.  Lane j < k keeps the j-th choice's key and holder, and looks the expert up among
+// the holder's unsorted keys at the end, all choices at once.  (Instructions for a row of 256
+// experts: searching unsorted lanes in every round 1172, sorting pairs of key and place 996, this
+// way 928.)  It reads its expert's logit again (the row is in L1) and computes its weight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -86,13 +87,13 @@ struct RouteParams {
 };
 
 // Sorts L numbers, the largest first (odd-even merge networks).
-__device__ __forceinline__ void order(unsigned long long& a, unsigned long long& b) {
-    const unsigned long long hi = a > b ? a : b, lo = a > b ? b : a;
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
+    const uint32_t hi = max(a, b), lo = min(a, b);
     a = hi;
     b = lo;
 }
 template <int L>
-__device__ __forceinline__ void sort_down(unsigned long long (&x)[L]) {
+__device__ __forceinline__ void sort_down(uint32_t (&x)[L]) {
     if constexpr (L == 2) {
         order(x[0], x[1]);
     } else if constexpr (L == 4) {
@@ -204,45 +205,55 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
         }
     }
 
-    // sorted lists: keys, and the place of each in 4 bits, the head's lowest
+    // each lane's keys in sorted lists; then k rounds of the warp's largest head
     constexpr int L = EPL < 8 ? EPL : 8, NL = EPL / L;
-    uint32_t place[NL];
+    uint32_t list[NL][L];
 #pragma unroll
     for (int n = 0; n < NL; ++n) {
-        unsigned long long item[L];
 #pragma unroll
-        for (int i = 0; i < L; ++i) item[i] = static_cast<unsigned long long>(key[n * L + i]) << 32 | (15 - i);
-        sort_down<L>(item);
-        place[n] = 0u;
-#pragma unroll
-        for (int i = 0; i < L; ++i) {
-            key[n * L + i] = static_cast<uint32_t>(item[i] >> 32);
-            place[n] |= (15u - static_cast<uint32_t>(item[i])) << (4 * i);
-        }
+        for (int i = 0; i < L; ++i) list[n][i] = key[n * L + i];
+        sort_down<L>(list[n]);
     }
-    int mine = 0;  // lane j: the j-th choice
+    // lane j: the j-th choice's key, the lane that holds it, and how many choices in a row before it
+    // had the same key and holder (equal keys come in turn, a holder's all at once)
+    uint32_t won = 0u, last_top = 0u;
+    int holder = lane, before = 0, last_from = -1, run = 0;
     for (int j = 0; j < p.k; ++j) {
-        uint32_t head = key[0];
+        uint32_t head = list[0][0];
 #pragma unroll
-        for (int n = 1; n < NL; ++n) head = max(head, key[n * L]);
+        for (int n = 1; n < NL; ++n) head = max(head, list[n][0]);
         const uint32_t top = __reduce_max_sync(kFull, head);
         const int from = __ffs(__ballot_sync(kFull, head == top)) - 1;
-        int at = 0;
+        run = top == last_top && from == last_from ? run + 1 : 0;
+        last_top = top;
+        last_from = from;
+        if (lane == j) {
+            won = top;
+            holder = from;
+            before = run;
+        }
         bool open = lane == from;
 #pragma unroll
         for (int n = 0; n < NL; ++n) {
-            const bool here = open && (n == NL - 1 || key[n * L] == top);
-            if (here) {
-                at = n * L + static_cast<int>(place[n] & 15u);
-                place[n] >>= 4;
+            const bool here = open && (n == NL - 1 || list[n][0] == top);
 #pragma unroll
-                for (int i = 0; i + 1 < L; ++i) key[n * L + i] = key[n * L + i + 1];
-                key[n * L + L - 1] = 0u;
-                open = false;
-            }
+            for (int i = 0; i + 1 < L; ++i) list[n][i] = here ? list[n][i + 1] : list[n][i];
+            list[n][L - 1] = here ? 0u : list[n][L - 1];
+            open = open && !here;
         }
-        const int e = __shfl_sync(kFull, first + at, from);
-        if (lane == j) mine = e;
+    }
+    // the expert behind each choice: the holder's first place with that key, or one further for each
+    // of those before
+    int mine = __shfl_sync(kFull, first, holder);
+    {
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            const bool hit = __shfl_sync(kFull, key[i], holder) == won;
+            if (hit && before == 0) at = i;
+            before -= hit ? 1 : 0;
+        }
+        mine += at;
     }
     float s = 0.f;
     if (lane < p.k) {
