@@ -145,6 +145,26 @@ def test_route_ties_and_infinities(ds):
     assert torch.isfinite(back).all() and back[3].abs().max() == 0
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shift", [1, 2, 3])
+def test_route_alignment(ds, dtype, shift):
+    """Logits, bias, and the experts' and gradient's rows that start anywhere."""
+    rng = np.random.default_rng(shift)
+    rows, E, k = 5, 256, 8
+    x = dev((1.5 * rng.standard_normal((rows, E))).astype(np.float32), dtype)
+    b = dev((0.1 * rng.standard_normal(E)).astype(np.float32))
+    kw = dict(scoring="sigmoid", groups=8, topk_groups=4, group_score="top2")
+    w, e = ds.route(x, k, bias=b, **kw)
+    wide = torch.zeros(E + 4, device="cuda")[shift:shift + E].copy_(b)
+    w2, e2 = ds.route(x, k, bias=wide, **kw)
+    assert torch.equal(w, w2) and torch.equal(e, e2)
+    xs = torch.zeros(rows, E + 8, device="cuda", dtype=dtype)[:, shift:shift + E].copy_(x)
+    w2, e2 = ds.route(xs, k, bias=wide, **kw)
+    assert torch.equal(w, w2) and torch.equal(e, e2)
+    g = dev(rng.standard_normal((rows, k)).astype(np.float32))
+    assert torch.equal(ds.route_backward(g, xs, e, scoring="sigmoid"), ds.route_backward(g, x, e, scoring="sigmoid"))
+
+
 def test_route_backward_ignores_outside_indices(ds):
     x = torch.randn(3, 20, device="cuda")
     e = torch.tensor([[2, -1, 5], [20, 3, 1 << 30], [-1, -1, -1]], dtype=torch.int32, device="cuda")

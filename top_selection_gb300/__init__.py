@@ -8,6 +8,11 @@ There is no CPU fallback; when the library has not been built every call raises.
 The C ABI (``include/ds_topk.h``) documents the operation, the argument layout, the
 ownership rules and the error codes.  ``topk()`` is a convenience wrapper that takes and
 returns torch tensors (PyTorch supplies device memory and streams only).
+
+The operators around the top-k in a decoding step -- ``route``, ``route_backward``,
+``verify_drafts``, ``cache_store``, ``cache_load``, ``cache_attention`` -- take and return torch
+tensors as well; their checks, outputs and calls run in a compiled binding
+(``csrc/ds_torch.cpp``), since a step makes many small ones.
 """
 from __future__ import annotations
 

@@ -487,9 +487,9 @@ ds_status ds_route(const void* logits, int32_t dtype, int64_t rows, int32_t E, i
     p.scale = scale;
     int epl = 1;
     while (epl < p.n) epl <<= 1;
-    // 16-byte loads when every lane's run starts on 16 bytes; else element by element
+    // 16-byte loads when every lane's run (and its bias) starts on 16 bytes; else element by element
     const bool vec = bits % 16 == 0 && row_stride * es % 16 == 0 && static_cast<int64_t>(p.n) * es % 16 == 0 &&
-                     static_cast<int64_t>(p.size) * es % 16 == 0;
+                     static_cast<int64_t>(p.size) * es % 16 == 0 && aligned16(bias);
     int dev = 0;
     DevInfo info;
     if (cudaGetDevice(&dev) != cudaSuccess || !dev_info(dev, info)) return DS_ERR_CUDA;
