@@ -8,7 +8,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/full.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -108,7 +108,7 @@ cudaStream_t stream_of(PyObject* o, c10::DeviceIndex index) {
 }
 
 at::Tensor make(std::initializer_list<int64_t> shape, at::ScalarType type, const at::Tensor& like) {
-    return at::empty(at::IntArrayRef(shape.begin(), shape.size()), at::TensorOptions().dtype(type).device(like.device()));
+    return at::detail::empty_cuda(at::IntArrayRef(shape.begin(), shape.size()), type, like.device(), std::nullopt);
 }
 
 void check(int status, const char* what) {
