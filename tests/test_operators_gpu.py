@@ -661,6 +661,23 @@ def test_attention_rows_that_see_something_late(ds, dtype):
     check_attention(ds.cache_attention(q, cache, scales, table, ln, indices=dev(idx)), want, 5.0, dtype)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("Q,group,D,K", [(1, 8, 128, 0), (2, 6, 64, 0), (1, 4, 64, 70), (1, 16, 128, 200)])
+def test_attention_many_short(ds, dtype, Q, group, D, K):
+    """Hundreds of contexts of a few pages: a key head's rows are one warp's work, or a few warps'."""
+    rng = np.random.default_rng(19 + K)
+    B, heads = 90, 8
+    lens = rng.integers(0, 300, B)
+    lens[:6] = [0, 1, 31, 32, 33, 299]
+    cache, scales, table = filled(ds, rng, B, heads, D, 16, lens, width=20)
+    q = dev((1.5 * rng.standard_normal((B, Q, heads * group, D))).astype(np.float32), dtype)
+    idx = rng.integers(-1, 300, (B, Q, K), dtype=np.int32) if K else None
+    want = ref.attention(host(q), Paged(cache, scales, table), lens, idx)
+    got = ds.cache_attention(q, cache, scales, table, dev(lens.astype(np.int32)),
+                             indices=None if idx is None else dev(idx))
+    check_attention(got, want, 5.0, dtype)
+
+
 # ------------------------------------------------------------------ streams, graphs --
 
 def test_other_stream_repeat_and_graph(ds):

@@ -48,7 +48,7 @@
 
 namespace dsk {
 
-constexpr int kAttWarps = 4;
+constexpr int kAttWarps = 4;                   // warps of a CTA, or one where there are many units
 constexpr int kAttTile = 32;                   // positions per warp and step
 constexpr int kAttStages = 3;                  // tiles of a warp's ring
 constexpr int kAttCluster = 8;                 // portable cluster size
@@ -267,17 +267,16 @@ struct Emit {
     }
 };
 
-// CTAs per SM that the registers are cut for
-template <typename T>
-constexpr int att_resident(int D, int NT) {
-    return sizeof(T) == 4 ? (NT == 1 ? 3 : 2) : NT == 1 ? 3 : 2;
+// CTAs per SM that the registers are cut for: 8 warps for 16 rows, 12 for 8
+constexpr int att_resident(int NT, int WARPS) {
+    return (NT == 1 ? 12 : 8) / WARPS;
 }
 
 // T: type of q and out.  NQ / NP: f16 parts of q and of the weights.  bf16: one part each (q is
 // exact, a weight keeps 11 bits, and the result's rounding to 8 dominates); fp32: two, 22 bits,
 // and the codes centred, so that sums cancel less.
-template <typename T, int D, int NT, int NQ, int NP>
-__global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_attend_kernel(const AttendParams p) {
+template <typename T, int D, int NT, int NQ, int NP, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend_kernel(const AttendParams p) {
     constexpr int KS = D / 16;       // k-steps of the scores, and row tiles of the output
     constexpr int ROWS = 8 * NT;
     constexpr bool CENTRE = sizeof(T) == 4;
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     const auto is_run = [&](uint32_t entry) { return runs && __all_sync(kAll, entry != kNoEntry); };
 
     // tiles of this warp: two in flight while one is computed
-    constexpr int STRIDE = kAttWarps * kAttTile;
+    constexpr int STRIDE = WARPS * kAttTile;
     int j0 = from + warp * kAttTile;
     int pos[kAttStages];  // the lane's position in each tile: current, in flight, next
     int at_ahead, page_ahead, at_far;
@@ -400,7 +399,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
         return true;
     };
     constexpr int QW = 2 * NT * NQ;  // words of a lane and k-step: kept in shared memory
-    uint32_t* sm_q = reinterpret_cast<uint32_t*>(smem + kAttWarps * kAttStages * At::kBytes);
+    uint32_t* sm_q = reinterpret_cast<uint32_t*>(smem + WARPS * kAttStages * At::kBytes);
     float2 qsum[NT];
     int ends[NT][2];
     int first_end = 0x7FFFFFFF;  // below it no row of the CTA masks anything
@@ -465,7 +464,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
         // each warp writes its share of the k-steps
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
-            if (kk % kAttWarps != warp) continue;
+            if (kk % WARPS != warp) continue;
             uint32_t w[QW];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -752,7 +751,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     // is a run of 512 bytes.
     constexpr int NF = NT * KS;                          // fragments of a warp
     float4* sm_o = reinterpret_cast<float4*>(smem);      // [warps][NF][32]
-    float4* sm_r = sm_o + kAttWarps * NF * 32;           // [warps][ROWS]: maximum, sum of p, of p (m + MID s)
+    float4* sm_r = sm_o + WARPS * NF * 32;           // [warps][ROWS]: maximum, sum of p, of p (m + MID s)
     const float back = 1.f / wmul;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -778,16 +777,16 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     __syncthreads();
     // one warp joins the four fragments of a row tile j and code word w: they hold eight numbers in
     // a row of rows 2t and 2t + 1
-    float4* sm_j = sm_r + kAttWarps * ROWS;              // the CTA's join, for its cluster: [NF][32]
+    float4* sm_j = sm_r + WARPS * ROWS;              // the CTA's join, for its cluster: [NF][32]
     float2* sm_ml = reinterpret_cast<float2*>(sm_j + NF * 32);  // [ROWS]
     constexpr int ITEMS = NF / 4;
     const Emit<T, D> emit = {p, b, h, q0, picked, rg * ROWS, min(ROWS, p.rows - rg * ROWS), g, t};
-    for (int item = warp; item < ITEMS; item += kAttWarps) {
+    for (int item = warp; item < ITEMS; item += WARPS) {
         const int r = 8 * (item / (D / 64)) + 2 * t;
-        float4 a0[kAttWarps], a1[kAttWarps];
+        float4 a0[WARPS], a1[WARPS];
         float top0 = kNone, top1 = kNone, sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             a0[w] = sm_r[w * ROWS + r];
             a1[w] = sm_r[w * ROWS + r + 1];
             top0 = fmaxf(top0, a0[w].x);
@@ -797,7 +796,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
 #pragma unroll
         for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kAttWarps; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const float f0 = exp2_fast(a0[w].x - top0), f1 = exp2_fast(a1[w].x - top1);
             sum0 += f0 * a0[w].y;
             sum1 += f1 * a1[w].y;
@@ -824,7 +823,7 @@ __global__ void __launch_bounds__(kAttWarps * 32, att_resident<T>(D, NT)) ds_att
     if (!p.cluster) return;
     // every CTA of the cluster joins its share of the items from all of them
     cluster_sync_all();
-    for (int item = warp * p.splits + split; item < ITEMS; item += kAttWarps * p.splits) {
+    for (int item = warp * p.splits + split; item < ITEMS; item += WARPS * p.splits) {
         const int r = 8 * (item / (D / 64)) + 2 * t;
         float top0 = kNone, top1 = kNone, sum0 = 0.f, sum1 = 0.f;
         for (int c = 0; c < p.splits; ++c) {
@@ -928,12 +927,12 @@ __global__ void __launch_bounds__(1024) ds_attend_join_kernel(const AttendParams
     else emit.one(first, acc[0], top0, sum0, top1, sum1);
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, int WARPS>
 static ds_status attend(const AttendParams& p, int dev, int sms, int64_t units, cudaStream_t stream) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
-    auto kern = ds_attend_kernel<T, D, NT, PARTS, PARTS>;
-    const size_t ring = static_cast<size_t>(kAttWarps) * kAttStages * TileAt<D>::kBytes + D / 16 * 32 * 8 * NT * PARTS;
-    const size_t join = (static_cast<size_t>(kAttWarps) * (D + 4) + D + 2) * 8 * NT * sizeof(float);  // sm_o, sm_r, sm_j, sm_ml
+    auto kern = ds_attend_kernel<T, D, NT, PARTS, PARTS, WARPS>;
+    const size_t ring = static_cast<size_t>(WARPS) * kAttStages * TileAt<D>::kBytes + D / 16 * 32 * 8 * NT * PARTS;
+    const size_t join = (static_cast<size_t>(WARPS) * (D + 4) + D + 2) * 8 * NT * sizeof(float);  // sm_o, sm_r, sm_j, sm_ml
     const size_t smem = ring > join ? ring : join;
     // the opt-in above 48 KB is a property of the kernel on a device: set once
     static std::atomic<bool> opted[64];
@@ -943,7 +942,7 @@ static ds_status attend(const AttendParams& p, int dev, int sms, int64_t units, 
         opted[dev].store(true, std::memory_order_release);
     }
     const dim3 grid(static_cast<unsigned>(units * p.splits));
-    const ds_status st = launch_pdl(kern, grid, kAttWarps * 32, smem, p.cluster ? p.splits : 1, stream, p);
+    const ds_status st = launch_pdl(kern, grid, WARPS * 32, smem, p.cluster ? p.splits : 1, stream, p);
     if (st != DS_OK || p.splits == 1 || p.cluster) return st;
     const auto join_by = [&](auto kernel, int fr, int most) {
         int warps = 1;
@@ -956,9 +955,12 @@ static ds_status attend(const AttendParams& p, int dev, int sms, int64_t units, 
 }
 
 template <typename T, int D>
-static ds_status attend_rows(const AttendParams& p, int dev, int sms, int nt, int64_t units, cudaStream_t stream) {
-    if (nt == 1) return attend<T, D, 1>(p, dev, sms, units, stream);
-    return attend<T, D, 2>(p, dev, sms, units, stream);
+static ds_status attend_rows(const AttendParams& p, int dev, int sms, int nt, int warps, int64_t units, cudaStream_t stream) {
+    if (nt == 1)
+        return warps == 1 ? attend<T, D, 1, 1>(p, dev, sms, units, stream)
+                          : attend<T, D, 1, kAttWarps>(p, dev, sms, units, stream);
+    return warps == 1 ? attend<T, D, 2, 1>(p, dev, sms, units, stream)
+                      : attend<T, D, 2, kAttWarps>(p, dev, sms, units, stream);
 }
 
 }  // namespace dsk
@@ -1022,17 +1024,29 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
     const int nt = rows > 8 ? 2 : 1;
     p.row_groups = (p.rows + 8 * nt - 1) / (8 * nt);
     const int64_t units = (indices ? sequences * tokens : sequences) * heads * p.row_groups;
-    // Splits.  Few units, so few sequences: as many as fill every place on an SM once (4 contexts of
-    // 1M positions and 16 rows: 131 us; twice 141, three times 150).  Many units: four times, since
-    // their lengths differ and the longest must not be left for the end (48 contexts of up to 8192
-    // positions: once 82 us, twice 81, four times 77).  At least one tile for each warp.
+    // Splits: as many as fill every place on an SM once, down to one tile a warp (4 contexts of 1M
+    // positions and 16 rows: 131 us; twice as many 141, three times 150).  Many units: up to four times
+    // as many, since their lengths differ and the longest must not be left for the end (48 contexts of
+    // up to 8192 positions: once 82.7 us, four times 77.6), but no shorter than 16 tiles a warp: a CTA
+    // costs 7 us beside its tiles (304 units of 512 positions: one CTA each 11.4 us, four 30; 304 of
+    // 2048: 26.6, four each 47.6).
+    // Units that many and that short are one warp's work each, since a CTA of four has little more than
+    // its start and its join to do (2432 units of 512 positions: 53.6 us, with four warps 88.7; 608:
+    // 20.9 and 24.5).  From 1024 positions on four warps win (1216 units: 33.0, one warp 35.5; 2432 of
+    // up to 4096: 140 and 162), and so they do with few units (304 of 512: 11.4 and 15.0).
     const int64_t span = p.span;
-    const int64_t unit_tiles = kAttWarps * kAttTile;
-    const int64_t places = static_cast<int64_t>(info.sms) *
-                           (dtype == DS_BF16 ? att_resident<__nv_bfloat16>(D, nt) : att_resident<float>(D, nt));
-    int64_t splits = ((2 * units < places ? 1 : 4) * places + units - 1) / units;
-    const int64_t most = (span + unit_tiles - 1) / unit_tiles;
-    if (splits > most) splits = most;
+    const int warps = units >= 4LL * info.sms && span <= 4 * kAttWarps * kAttTile ? 1 : kAttWarps;
+    const int64_t unit_tiles = warps * kAttTile;
+    const int64_t places = static_cast<int64_t>(info.sms) * att_resident(nt, warps);
+    const auto at_most = [&](int64_t n, int64_t least) {
+        const int64_t most = (span + least - 1) / least;
+        return n < most ? n : most;
+    };
+    int64_t splits = at_most((places + units - 1) / units, unit_tiles);
+    if (2 * units >= places) {
+        const int64_t many = at_most((4 * places + units - 1) / units, 16 * unit_tiles);
+        if (splits < many) splits = many;
+    }
     if (splits < 1) splits = 1;
     int64_t chunk = (span + splits - 1) / splits;
     chunk = (chunk + unit_tiles - 1) / unit_tiles * unit_tiles;
@@ -1056,10 +1070,10 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
         p.ws_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) + entries * D);
     }
     if (dtype == DS_BF16)
-        return D == 64 ? attend_rows<__nv_bfloat16, 64>(p, dev, info.sms, nt, units, stream)
-                       : attend_rows<__nv_bfloat16, 128>(p, dev, info.sms, nt, units, stream);
-    return D == 64 ? attend_rows<float, 64>(p, dev, info.sms, nt, units, stream)
-                   : attend_rows<float, 128>(p, dev, info.sms, nt, units, stream);
+        return D == 64 ? attend_rows<__nv_bfloat16, 64>(p, dev, info.sms, nt, warps, units, stream)
+                       : attend_rows<__nv_bfloat16, 128>(p, dev, info.sms, nt, warps, units, stream);
+    return D == 64 ? attend_rows<float, 64>(p, dev, info.sms, nt, warps, units, stream)
+                   : attend_rows<float, 128>(p, dev, info.sms, nt, warps, units, stream);
 }
 
 }  // extern "C"
