@@ -14,14 +14,23 @@
 // key m, value s, value m.  Token slot t is place t % page of page t / page.
 //
 // Both kernels move each byte once.  A token's key and value row of one head are neighbours in a
-// warp, D/16 lanes each, 16 numbers a lane (two pieces of 8: 16 bytes of bf16 in, 4 bytes of codes
-// out), so a warp's code stores and loads are whole lines.  A warp takes U turns with all their
-// loads in flight at once.  Heads are the grid's second extent: no index is divided.
-// 16411 tokens of 8 heads in bf16, stored and read back: 36.7 us (4.6 TB/s); with 8 numbers a lane and plain
-// conversions 50 us, bound by instructions (22 a number); one turn at a time 57 us.
+// warp.  Heads are the grid's second extent: no index is divided.
+//
+// Storing is bound by instructions (unpacking, the row's extremes, rounding), and what a row costs
+// whatever its lanes (its places, its scale and their division, the exchanges) counts most: 32
+// numbers a lane in pieces of 8.  16411 tokens of 8 heads in bf16: 15.4 us (5.5 TB/s); with 16
+// numbers a lane 18.6, twice those with their loads in flight at once 20.7 (more registers, fewer
+// warps to compute meanwhile), 64 numbers 15.4 and slower at 4096 tokens (5.1 us for 4.15).
+// From fp32 23.4 us (6.5 TB/s).
+//
+// Loading is bound by its stores: a lane's piece is 16 bytes of numbers, so that a row's lanes write
+// whole sectors side by side (fp32 by pairs of pieces: 37 us for 25), and its words of codes are
+// 32 or 16 bits.  The same tokens: 12.3 us (6.9 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "ds_common.cuh"
 #include "ds_host.cuh"
@@ -29,7 +38,7 @@
 
 namespace dsk {
 
-constexpr int kCacheThreads = 256;
+constexpr int kCacheThreads = 128;
 constexpr uint32_t kWhole = 0x4B000000u;  // 2^23 as fp32: its low bits count ones
 
 struct CacheParams {
@@ -80,7 +89,7 @@ __device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
         x[4 * i] = q.x, x[4 * i + 1] = q.y, x[4 * i + 2] = q.z, x[4 * i + 3] = q.w;
     }
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -89,15 +98,15 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store16(float* p, const float (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
 }
 
-// Where a lane works: `which` row (key 0, value 1), its lane of the row, and the token of turn k.
-template <int D, int U>
+// Where a lane of LPR to a row works: `which` row (key 0, value 1), its lane of the row, and the
+// token of turn k of U.
+template <int LPR, int U>
 struct Place {
-    static constexpr int LPR = D / 16, TPW = 16 / LPR, WARPS = kCacheThreads / 32;  // tokens per warp and turn
+    static constexpr int TPW = 16 / LPR, WARPS = kCacheThreads / 32;  // TPW: tokens per warp and turn
     int which, sub;
     int64_t first;
     __device__ __forceinline__ Place() {
@@ -136,93 +145,89 @@ __device__ __forceinline__ int64_t entry_of_slot(const CacheParams& p, int64_t s
     return ((page * p.heads + head) << p.page_log) + place;
 }
 
-template <typename T, int D, int U>
+template <typename T, int D>
 __global__ void __launch_bounds__(kCacheThreads) ds_cache_store_kernel(const CacheParams p) {
-    constexpr int LPR = D / 16;
+    constexpr int N = 4, LPR = D / (8 * N);  // N pieces of 8 numbers a lane
     pdl_launch_dependents();
     pdl_wait();
-    const Place<D, U> at;
+    const Place<LPR, 1> at;
     const int head = blockIdx.y;
-    const T* src = static_cast<const T*>(at.which ? p.v : p.k) + head * (at.which ? p.v_head : p.k_head) + at.sub * 8;
-    const int64_t stride = at.which ? p.v_token : p.k_token;
-    float x[U][2][8];
-    int64_t slot[U];
+    const int64_t token = at.token(0);
+    const T* src = static_cast<const T*>(at.which ? p.v : p.k) + head * (at.which ? p.v_head : p.k_head) +
+                   token * (at.which ? p.v_token : p.k_token) + at.sub * 8;
+    float x[N][8];
+    int64_t slot = -1;
+    if (token < p.tokens) {
+        slot = p.slots[token];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int64_t token = at.token(k);
-        slot[k] = -1;
-        if (token < p.tokens) {
-            slot[k] = p.slots[token];
-            load8<T>(src + token * stride, x[k][0]);
-            load8<T>(src + token * stride + D / 2, x[k][1]);
-        } else {
+        for (int h = 0; h < N; ++h) load8<T>(src + h * (D / N), x[h]);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[k][0][i] = x[k][1][i] = 0.f;
-        }
+        for (int i = 0; i < 8 * N; ++i) x[i / 8][i % 8] = 0.f;
+    }
+    float lo = fminf(x[0][0], x[0][1]), hi = fmaxf(x[0][0], x[0][1]);
+#pragma unroll
+    for (int i = 2; i < 8 * N; i += 2) {
+        lo = min3(lo, x[i / 8][i % 8], x[i / 8][i % 8 + 1]);
+        hi = max3(hi, x[i / 8][i % 8], x[i / 8][i % 8 + 1]);
     }
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        float lo = fminf(x[k][0][0], x[k][1][0]), hi = fmaxf(x[k][0][0], x[k][1][0]);
-#pragma unroll
-        for (int i = 1; i < 8; ++i) {
-            lo = min3(lo, x[k][0][i], x[k][1][i]);
-            hi = max3(hi, x[k][0][i], x[k][1][i]);
-        }
-#pragma unroll
-        for (int d = LPR / 2; d >= 1; d >>= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, d));
-            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
-        }
-        const uint32_t mb = bf16_bits(lo);
-        const float m = low_bf16(mb);
-        const uint32_t sb = bf16_bits((hi - m) * (1.0f / 15.0f));
-        const float s = low_bf16(sb);
-        const float inv = s >= 1.17549435e-38f ? 1.0f / s : 0.f;
-        // Adding 2^23 rounds 0 .. 15 to a whole number, ties to even, and leaves it in the low bits;
-        // the sum of the shifted words carries eight copies of 2^23's pattern, taken off beforehand.
-        // (x - m) / s is at most 15 (1 + 2^-9) / (1 - 2^-9), which rounds to 15; it falls below 0
-        // where m was rounded up.
-        uint32_t word[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            word[h] = 0u - kWhole * 0x11111111u;
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const float2 c = add_mul2(make_float2(x[k][h][i], x[k][h][i + 1]), -m, inv);
-                word[h] += __float_as_uint(fmaxf(c.x, 0.f) + 8388608.f) << (4 * i);
-                word[h] += __float_as_uint(fmaxf(c.y, 0.f) + 8388608.f) << (4 * i + 4);
-            }
-        }
-        const int64_t entry = entry_of_slot(p, slot[k], head);
-        if (entry < 0) continue;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.cache + entry * D + at.which * (D / 2)) + at.sub;
-        dst[0] = word[0];
-        dst[LPR] = word[1];
-        if (at.sub == 0) p.scales[entry * 2 + at.which] = sb | mb << 16;
+    for (int d = LPR / 2; d >= 1; d >>= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, d));
+        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, d));
     }
+    const uint32_t mb = bf16_bits(lo);
+    const float m = low_bf16(mb);
+    const uint32_t sb = bf16_bits((hi - m) * (1.0f / 15.0f));
+    const float s = low_bf16(sb);
+    const float inv = s >= 1.17549435e-38f ? 1.0f / s : 0.f;
+    // Adding 2^23 rounds 0 .. 15 to a whole number, ties to even, and leaves it in the low bits;
+    // the sum of the shifted words carries eight copies of 2^23's pattern, taken off beforehand.
+    // (x - m) / s is at most 15 (1 + 2^-9) / (1 - 2^-9), which rounds to 15; it falls below 0
+    // where m was rounded up.
+    uint32_t word[N];
+#pragma unroll
+    for (int h = 0; h < N; ++h) {
+        word[h] = 0u - kWhole * 0x11111111u;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float2 c = add_mul2(make_float2(x[h][i], x[h][i + 1]), -m, inv);
+            word[h] += __float_as_uint(fmaxf(c.x, 0.f) + 8388608.f) << (4 * i);
+            word[h] += __float_as_uint(fmaxf(c.y, 0.f) + 8388608.f) << (4 * i + 4);
+        }
+    }
+    const int64_t entry = entry_of_slot(p, slot, head);
+    if (entry < 0) return;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.cache + entry * D + at.which * (D / 2)) + at.sub;
+#pragma unroll
+    for (int h = 0; h < N; ++h) dst[h * LPR] = word[h];
+    if (at.sub == 0) p.scales[entry * 2 + at.which] = sb | mb << 16;
 }
 
 template <typename T, int D, int U>
 __global__ void __launch_bounds__(kCacheThreads) ds_cache_load_kernel(const CacheParams p) {
-    constexpr int LPR = D / 16;
+    using Word = std::conditional_t<sizeof(T) == 2, uint32_t, uint16_t>;  // the codes of a piece
+    constexpr int LPR = D / 16, PER = 16 / sizeof(T), N = 16 / PER;         // N pieces of PER numbers a lane
     pdl_launch_dependents();
     pdl_wait();
-    const Place<D, U> at;
+    const Place<LPR, U> at;
     const int head = blockIdx.y;
-    uint32_t word[U][2], sm[U];
+    uint32_t word[U][N], sm[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         const int64_t token = at.token(k);
         const int64_t entry = token < p.tokens ? entry_of_slot(p, p.slots[token], head) : -1;
-        word[k][0] = word[k][1] = sm[k] = 0u;  // a slot outside the cache: zeros
+        sm[k] = 0u;  // a slot outside the cache: zeros
+#pragma unroll
+        for (int h = 0; h < N; ++h) word[k][h] = 0u;
         if (entry >= 0) {
-            const uint32_t* src = reinterpret_cast<const uint32_t*>(p.cache + entry * D + at.which * (D / 2)) + at.sub;
-            word[k][0] = src[0];
-            word[k][1] = src[LPR];
+            const Word* src = reinterpret_cast<const Word*>(p.cache + entry * D + at.which * (D / 2)) + at.sub;
+#pragma unroll
+            for (int h = 0; h < N; ++h) word[k][h] = src[h * LPR];
             sm[k] = p.scales[entry * 2 + at.which];
         }
     }
-    T* dst = static_cast<T*>(const_cast<void*>(at.which ? p.v : p.k)) + head * (at.which ? p.v_head : p.k_head) + at.sub * 8;
+    T* dst = static_cast<T*>(const_cast<void*>(at.which ? p.v : p.k)) + head * (at.which ? p.v_head : p.k_head) + at.sub * PER;
     const int64_t stride = at.which ? p.v_token : p.k_token;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -233,10 +238,10 @@ __global__ void __launch_bounds__(kCacheThreads) ds_cache_load_kernel(const Cach
         const float s = low_bf16(sm[k]), m = high_bf16(sm[k]);
         const float2 s01 = make_float2(s, s * 0.0625f), s23 = make_float2(s * 0.00390625f, s * 0.000244140625f);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float x[8];
+        for (int h = 0; h < N; ++h) {
+            float x[PER];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < PER / 4; ++q) {
                 const uint32_t w = word[k][h] >> (16 * q);
                 const float2 a = less_mul_add2(make_float2(__uint_as_float((w & 0xFu) | kWhole), __uint_as_float((w & 0xF0u) | kWhole)),
                                                8388608.f, s01, m);
@@ -244,26 +249,29 @@ __global__ void __launch_bounds__(kCacheThreads) ds_cache_load_kernel(const Cach
                                                8388608.f, s23, m);
                 x[4 * q] = a.x, x[4 * q + 1] = a.y, x[4 * q + 2] = b.x, x[4 * q + 3] = b.y;
             }
-            store8(dst + token * stride + h * (D / 2), x);
+            store16(dst + token * stride + h * (D / N), x);
         }
     }
 }
 
-template <typename T, int D, int U>
-static ds_status launch_cache(const CacheParams& p, bool store, cudaStream_t stream) {
-    constexpr int64_t per = kCacheThreads / (D / 8) * U;  // tokens of a CTA
+template <int LPR, int U, typename Kernel>
+static ds_status launch_cache(Kernel kern, const CacheParams& p, cudaStream_t stream) {
+    constexpr int64_t per = kCacheThreads / (2 * LPR) * U;  // tokens of a CTA
     const int64_t ctas = (p.tokens + per - 1) / per;
     if (ctas > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
-    const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(p.heads));
-    return store ? launch_pdl(ds_cache_store_kernel<T, D, U>, grid, kCacheThreads, 0, 1, stream, p)
-                 : launch_pdl(ds_cache_load_kernel<T, D, U>, grid, kCacheThreads, 0, 1, stream, p);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p.heads)), kCacheThreads, 0, 1, stream, p);
 }
 
-// One turn while that gives an SM less than 8 CTAs (latency counts), else two.
+// Loading takes two turns with all their loads in flight at once (16411 tokens: 12.3 us, with one
+// 18.0), but one while that gives an SM less than 8 CTAs, as latency counts then (64 tokens: 1.3 us,
+// with two 1.6).
 template <typename T, int D>
 static ds_status launch_cache(const CacheParams& p, bool store, int sms, cudaStream_t stream) {
-    const int64_t ctas = p.tokens * p.heads / (kCacheThreads / (D / 8));
-    return ctas < 8 * static_cast<int64_t>(sms) ? launch_cache<T, D, 1>(p, store, stream) : launch_cache<T, D, 2>(p, store, stream);
+    if (store) return launch_cache<D / 32, 1>(ds_cache_store_kernel<T, D>, p, stream);
+    constexpr int LPR = D / 16;
+    const int64_t ctas = p.tokens * p.heads / (kCacheThreads / (2 * LPR));
+    return ctas < 8 * static_cast<int64_t>(sms) ? launch_cache<LPR, 1>(ds_cache_load_kernel<T, D, 1>, p, stream)
+                                                : launch_cache<LPR, 2>(ds_cache_load_kernel<T, D, 2>, p, stream);
 }
 
 static ds_status cache_call(bool store, const void* k, const void* v, int32_t dtype, int64_t tokens, int32_t heads,
