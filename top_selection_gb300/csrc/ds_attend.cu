@@ -301,14 +301,8 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     const bool picked = p.indices != nullptr;
     const int b = picked ? bq / p.Q : bq;
     const int q0 = picked ? bq % p.Q : 0;
-    const int len = min(p.lens[b], p.max_pos);
-    // query token i sees positions below len - (Q - 1 - i)
-    const int end_all = max(picked ? len - (p.Q - 1 - q0) : len, 0);
-    const int count = picked ? p.K : end_all;       // positions (or list entries) of this unit
-    const int from = split * p.chunk, to = min(from + p.chunk, count);
-    // without a cluster the join is a kernel, which reads only splits that have work
-    if (!p.cluster && from >= count && split > 0) return;
-
+    const int length = p.lens[b];
+    const int from = split * p.chunk;
     const int32_t* table = p.table + b * p.table_stride;
     const int32_t* list = picked ? p.indices + static_cast<int64_t>(bq) * p.K : nullptr;
     const int page_mask = (1 << p.page_log) - 1;
@@ -321,6 +315,25 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     const auto page_of = [&](int at) -> int {
         return table[(static_cast<uint32_t>(at) < static_cast<uint32_t>(p.max_pos) ? at : 0) >> p.page_log];
     };
+    // tiles of this warp: two in flight while one is computed
+    constexpr int STRIDE = WARPS * kAttTile;
+    int j0 = from + warp * kAttTile;
+    int ahead[kAttStages], page[kAttStages];
+#pragma unroll
+    for (int s = 0; s < kAttStages; ++s) ahead[s] = position_at(j0 + s * STRIDE + lane);
+    int at_far = position_at(j0 + kAttStages * STRIDE + lane);
+#pragma unroll
+    for (int s = 0; s < kAttStages; ++s) page[s] = page_of(ahead[s]);
+
+    // the length comes beside the first pages, not before them
+    const int len = min(length, p.max_pos);
+    // query token i sees positions below len - (Q - 1 - i)
+    const int end_all = max(picked ? len - (p.Q - 1 - q0) : len, 0);
+    const int count = picked ? p.K : end_all;       // positions (or list entries) of this unit
+    const int to = min(from + p.chunk, count);
+    // without a cluster the join is a kernel, which reads only splits that have work
+    if (!p.cluster && from >= count && split > 0) return;
+
     const auto entry_of = [&](int at, int page, int& pos) -> uint32_t {
         const bool seen = at >= 0 && at < end_all && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
         pos = seen ? at : 0x7FFFFFFF;
@@ -363,26 +376,13 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     const bool runs = !picked && p.page_log >= 5;
     const auto is_run = [&](uint32_t entry) { return runs && __all_sync(kAll, entry != kNoEntry); };
 
-    // tiles of this warp: two in flight while one is computed
-    constexpr int STRIDE = WARPS * kAttTile;
-    int j0 = from + warp * kAttTile;
     int pos[kAttStages];  // the lane's position in each tile: current, in flight, next
-    int at_ahead, page_ahead, at_far;
-    {
-        int at[kAttStages], page[kAttStages];
 #pragma unroll
-        for (int s = 0; s < kAttStages; ++s) at[s] = position_at(j0 + s * STRIDE + lane);
-        at_far = position_at(j0 + kAttStages * STRIDE + lane);
-#pragma unroll
-        for (int s = 0; s < kAttStages; ++s) page[s] = page_of(at[s]);
-#pragma unroll
-        for (int s = 0; s + 1 < kAttStages; ++s) {
-            const uint32_t entry = entry_of(at[s], page[s], pos[s]);
-            issue(s, entry, is_run(entry));
-        }
-        at_ahead = at[kAttStages - 1];
-        page_ahead = page[kAttStages - 1];
+    for (int s = 0; s + 1 < kAttStages; ++s) {
+        const uint32_t entry = entry_of(ahead[s], page[s], pos[s]);
+        issue(s, entry, is_run(entry));
     }
+    int at_ahead = ahead[kAttStages - 1], page_ahead = page[kAttStages - 1];
 
     // q as the second operand: row g of each tile, the lane's quarter of the numbers in the
     // order of the codes, times a power of two that brings the largest to 2^13 .. 2^14, and
