@@ -1048,6 +1048,9 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
         if (splits < many) splits = many;
     }
     if (splits < 1) splits = 1;
+    // Short contexts whose splits all run at once are split over a cluster, up to two tiles a warp.
+    const bool few = units * splits <= places && span <= 2 * kAttCluster * unit_tiles;
+    if (few && splits > kAttCluster) splits = kAttCluster;
     int64_t chunk = (span + splits - 1) / splits;
     chunk = (chunk + unit_tiles - 1) / unit_tiles * unit_tiles;
     if (chunk < unit_tiles) chunk = unit_tiles;
@@ -1056,11 +1059,12 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
     p.splits = static_cast<int32_t>(splits);
     p.chunk = static_cast<int32_t>(chunk);
     if (units * splits > 0x7FFFFFFFLL || units * (nt * D / 16) > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
-    // Lists have one length: up to 8 splits of one are a cluster and join over its shared memory
-    // (512 positions for 64 rows: 11.4 us, through the workspace 13.6).  Contexts differ in theirs,
-    // and a cluster holds its places until the longest split is done (48 contexts of up to 8192
-    // positions: 105 us, through the workspace 81).
-    p.cluster = indices && splits > 1 && splits <= kAttCluster;
+    // Up to 8 splits of a list or of few short contexts are a cluster and join over its shared memory
+    // (64 lists of 512 positions: 11.4 us, through the workspace 13.6; 4 contexts of 512, 8 heads: 7.4
+    // and 8.4; one of 2048: 7.8 and 8.1).  Many contexts differ in length, and a cluster holds its
+    // places until the longest split is done (48 of up to 8192 positions: 105 us, through the
+    // workspace 81).
+    p.cluster = (indices || few) && splits > 1 && splits <= kAttCluster;
     if (splits > 1 && !p.cluster) {
         const size_t entries = static_cast<size_t>(units) * splits * 8 * nt;
         void* ws = nullptr;
