@@ -678,6 +678,25 @@ def test_attention_many_short(ds, dtype, Q, group, D, K):
     check_attention(got, want, 5.0, dtype)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens,heads,group,Q,width", [
+    ([9000], 1, 4, 1, 16384),                      # a table much wider than its context
+    ([0, 1, 3000, 0, 7777, 129, 128, 8200], 2, 4, 1, 1024),
+    ([1] * 40 + [6000, 0, 40], 1, 8, 2, 512),      # one context is nearly all of the work
+    ([5000] * 5, 2, 16, 1, 1024),
+    ([0, 0, 0], 2, 4, 1, 2560),
+    ([16384, 16384, 1], 4, 2, 2, 1024),            # whole tables
+])
+def test_attention_splits_by_length(ds, dtype, lens, heads, group, Q, width):
+    """Few contexts in wide tables, cut to splits by their lengths."""
+    rng = np.random.default_rng(sum(lens) + group)
+    cache, scales, table = filled(ds, rng, len(lens), heads, 64, 16, lens, width=width)
+    q = dev((1.5 * rng.standard_normal((len(lens), Q, heads * group, 64))).astype(np.float32), dtype)
+    want = ref.attention(host(q), Paged(cache, scales, table), lens)
+    got = ds.cache_attention(q, cache, scales, table, dev(np.array(lens, dtype=np.int32)))
+    check_attention(got, want, 5.0, dtype)
+
+
 # ------------------------------------------------------------------ streams, graphs --
 
 def test_other_stream_repeat_and_graph(ds):

@@ -39,6 +39,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -73,14 +74,17 @@ struct AttendParams {
     const int32_t* indices;        // [B, Q, K] or null
     void* out;
     float* lse;
-    float4* ws_o;                  // split partials: [unit][split][fragment][lane]
-    float2* ws_ml;                 //                 [unit][split][rows]: maximum, sum of weights
+    float4* ws_o;                  // splits' partial results, one a CTA: [CTA][fragment][lane]
+    float2* ws_ml;                 //                                     [CTA][rows]: maximum, sum of weights
+    int2* ws_cut;                  // fitted splits: each unit's first CTA and number of splits
     int32_t max_pos, span;         // table width * page; max_pos or K
     int32_t Q, K, heads, group, page_log, pages;
     int32_t rows;                  // query rows per unit before tiling
     int32_t row_groups, splits, chunk;
     int32_t q_vec;                 // q rows start on 16 bytes
     int32_t cluster;               // the splits of a unit are one cluster and join in it
+    int32_t sequences;
+    int32_t fit;                   // > 0: splits by length (`fitted`), so many a head and row group
     float scale;
 };
 
@@ -272,6 +276,60 @@ constexpr int att_resident(int NT, int WARPS) {
     return (NT == 1 ? 12 : 8) / WARPS;
 }
 
+// Splits by the contexts' lengths, which the host does not know: all of one size, the smallest of 32
+// for which the places that run at once are enough (p.fit for each head and row group).  Every warp
+// finds its CTA's split by itself, by the same arithmetic.
+struct Fitted {
+    uint32_t unit;
+    int split, splits;  // splits 0: this CTA has none
+    int steps, first;   // of STEP positions in a split; the unit's first CTA
+};
+template <int STEP>
+__device__ __forceinline__ Fitted fitted(const AttendParams& p, int lane) {
+    const auto steps_of = [&](int b) { return (max(min(p.lens[b], p.max_pos), 1) + STEP - 1) / STEP; };
+    // ceil(n / c): the product is at least 1 / 2 c from a whole number, more than its error
+    const auto splits_of = [](int n, float by) { return static_cast<int>((static_cast<float>(n) - 0.5f) * by) + 1; };
+    int64_t sum = 0;
+#pragma unroll 4
+    for (int i = lane; i < p.sequences; i += 32) sum += steps_of(i);
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    // lane l: 1 + l / 16 times the size that fills every place; the last ones' splits always fit, as
+    // half of the places are enough for all sequences' first
+    const int least = static_cast<int>((sum + p.fit - 1) / p.fit);
+    const int mine = least + (least * lane + 15) / 16;
+    float by = 1.f / static_cast<float>(mine);
+    int need = 0;
+#pragma unroll 4
+    for (int i = 0; i < p.sequences; ++i) need += splits_of(steps_of(i), by);
+    const int best = __ffs(__ballot_sync(kAll, need <= p.fit)) - 1;
+    Fitted f = {0u, 0, 0, __shfl_sync(kAll, mine, best), 0};
+    by = __shfl_sync(kAll, by, best);
+    const int per = p.heads * p.row_groups, rank = static_cast<int>(blockIdx.x) / per, place = static_cast<int>(blockIdx.x) - rank * per;
+    int before = 0;
+    for (int i = 0; i < p.sequences; i += 32) {
+        const int n = i + lane < p.sequences ? splits_of(steps_of(i + lane), by) : 0;
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(kAll, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const uint32_t behind = __ballot_sync(kAll, before + upto > rank);
+        if (behind) {
+            const int at = __ffs(behind) - 1;
+            f.splits = __shfl_sync(kAll, n, at);
+            const int start = before + __shfl_sync(kAll, upto, at) - f.splits;
+            f.split = rank - start;
+            f.unit = static_cast<uint32_t>(i + at) * per + place;
+            f.first = start * per + place;
+            break;
+        }
+        before += __shfl_sync(kAll, upto, 31);
+    }
+    return f;
+}
+
 // T: type of q and out.  NQ / NP: f16 parts of q and of the weights.  bf16: one part each (q is
 // exact, a weight keeps 11 bits, and the result's rounding to 8 dominates); fp32: two, 22 bits,
 // and the codes centred, so that sums cancel less.
@@ -292,8 +350,21 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     pdl_wait();
 
     // unit = ((sequence [, query token]) * heads + head) * row_groups + row group
-    const uint32_t unit = blockIdx.x / static_cast<uint32_t>(p.splits);
-    const int split = static_cast<int>(blockIdx.x - unit * p.splits);
+    constexpr int STRIDE = WARPS * kAttTile;
+    uint32_t unit;
+    int split, splits = p.splits, chunk = p.chunk;
+    if (p.fit > 0) {
+        const Fitted f = fitted<STRIDE>(p, lane);
+        if (f.splits == 0) return;
+        if (f.split == 0 && tid == 0) p.ws_cut[f.unit] = make_int2(f.first, f.splits);
+        unit = f.unit;
+        split = f.split;
+        splits = f.splits;
+        chunk = f.steps * STRIDE;
+    } else {
+        unit = blockIdx.x / static_cast<uint32_t>(splits);
+        split = static_cast<int>(blockIdx.x - unit * splits);
+    }
     const uint32_t uh = unit / static_cast<uint32_t>(p.row_groups);
     const int rg = static_cast<int>(unit - uh * p.row_groups);
     const int bq = static_cast<int>(uh / static_cast<uint32_t>(p.heads));
@@ -302,7 +373,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     const int b = picked ? bq / p.Q : bq;
     const int q0 = picked ? bq % p.Q : 0;
     const int length = p.lens[b];
-    const int from = split * p.chunk;
+    const int from = split * chunk;
     const int32_t* table = p.table + b * p.table_stride;
     const int32_t* list = picked ? p.indices + static_cast<int64_t>(bq) * p.K : nullptr;
     const int page_mask = (1 << p.page_log) - 1;
@@ -310,13 +381,12 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     // Entries come in three steps, so that no load waits for another: the position at place j (a
     // list's value), its page, and the entry, each a tile ahead of the next.  Loads are made in
     // range whatever the values are (a list's and a table's are the caller's); the entry decides.
-    const int last = min(from + p.chunk, p.span);
+    const int last = min(from + chunk, p.span);
     const auto position_at = [&](int j) -> int { return j >= last ? -1 : picked ? list[j] : j; };
     const auto page_of = [&](int at) -> int {
         return table[(static_cast<uint32_t>(at) < static_cast<uint32_t>(p.max_pos) ? at : 0) >> p.page_log];
     };
     // tiles of this warp: two in flight while one is computed
-    constexpr int STRIDE = WARPS * kAttTile;
     int j0 = from + warp * kAttTile;
     int ahead[kAttStages], page[kAttStages];
 #pragma unroll
@@ -330,7 +400,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     // query token i sees positions below len - (Q - 1 - i)
     const int end_all = max(picked ? len - (p.Q - 1 - q0) : len, 0);
     const int count = picked ? p.K : end_all;       // positions (or list entries) of this unit
-    const int to = min(from + p.chunk, count);
+    const int to = min(from + chunk, count);
     // without a cluster the join is a kernel, which reads only splits that have work
     if (!p.cluster && from >= count && split > 0) return;
 
@@ -807,12 +877,12 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
                 acc[f].z += f0 * (x.z + a0[w].z), acc[f].w += f1 * (x.w + a1[w].z);
             }
         }
-        if (p.splits == 1) {
+        if (splits == 1) {
             emit.four(item, acc, top0, sum0, top1, sum1);
             continue;
         }
-        float4* to = p.cluster ? sm_j : p.ws_o + (static_cast<int64_t>(unit) * p.splits + split) * (NF * 32);
-        float2* ml = p.cluster ? sm_ml : p.ws_ml + (static_cast<int64_t>(unit) * p.splits + split) * ROWS;
+        float4* to = p.cluster ? sm_j : p.ws_o + static_cast<int64_t>(blockIdx.x) * (NF * 32);
+        float2* ml = p.cluster ? sm_ml : p.ws_ml + static_cast<int64_t>(blockIdx.x) * ROWS;
 #pragma unroll
         for (int f = 0; f < 4; ++f) to[(item * 4 + f) * 32 + lane] = acc[f];
         if (g == 0 && item % (D / 64) == 0) {
@@ -873,15 +943,25 @@ __global__ void __launch_bounds__(1024) ds_attend_join_kernel(const AttendParams
     const int h = static_cast<int>(uh - bq * p.heads);
     const bool picked = p.indices != nullptr;
     const int b = picked ? bq / p.Q : bq, q0 = picked ? bq % p.Q : 0;
-    const int count = picked ? p.K : max(min(p.lens[b], p.max_pos), 0);
-    const int splits = max(1, min(p.splits, (count + p.chunk - 1) / p.chunk));
+    int64_t begin = static_cast<int64_t>(unit) * p.splits, apart = 1;  // its splits' CTAs
+    int splits;
+    if (p.fit > 0) {
+        const int2 cut = p.ws_cut[unit];
+        if (cut.y == 1) return;  // written by its only split
+        begin = cut.x;
+        apart = static_cast<int64_t>(p.heads) * p.row_groups;
+        splits = cut.y;
+    } else {
+        const int count = picked ? p.K : max(min(p.lens[b], p.max_pos), 0);
+        splits = max(1, min(p.splits, (count + p.chunk - 1) / p.chunk));
+    }
     const int r = 8 * (first / KS) + 2 * t;
-    const float4* ml = reinterpret_cast<const float4*>(p.ws_ml + static_cast<int64_t>(unit) * p.splits * ROWS + r);
-    const float4* part = p.ws_o + (static_cast<int64_t>(unit) * p.splits * NF + first) * 32 + lane;
+    const float4* ml = reinterpret_cast<const float4*>(p.ws_ml + begin * ROWS + r);
+    const float4* part = p.ws_o + (begin * NF + first) * 32 + lane;
     float top0 = kNone, top1 = kNone, sum0 = 0.f, sum1 = 0.f;
 #pragma unroll 4
     for (int s = g; s < splits; s += 8) {
-        const float4 x = ml[s * (ROWS / 2)];  // maximum and sum of rows r and r + 1
+        const float4 x = ml[s * apart * (ROWS / 2)];  // maximum and sum of rows r and r + 1
         top0 = fmaxf(top0, x.x);
         top1 = fmaxf(top1, x.z);
     }
@@ -895,13 +975,13 @@ __global__ void __launch_bounds__(1024) ds_attend_join_kernel(const AttendParams
     for (int f = 0; f < FR; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int s = warp; s < splits; s += warps) {
-        const float4 x = ml[s * (ROWS / 2)];
+        const float4 x = ml[s * apart * (ROWS / 2)];
         const float f0 = exp2_fast(x.x - top0), f1 = exp2_fast(x.z - top1);
         sum0 += f0 * x.y;
         sum1 += f1 * x.w;
 #pragma unroll
         for (int f = 0; f < FR; ++f) {
-            const float4 y = part[(static_cast<int64_t>(s) * NF + f) * 32];
+            const float4 y = part[(s * apart * NF + f) * 32];
             acc[f].x += f0 * y.x, acc[f].y += f1 * y.y, acc[f].z += f0 * y.z, acc[f].w += f1 * y.w;
         }
     }
@@ -941,7 +1021,7 @@ static ds_status attend(const AttendParams& p, int dev, int sms, int64_t units, 
             return DS_ERR_CUDA;
         opted[dev].store(true, std::memory_order_release);
     }
-    const dim3 grid(static_cast<unsigned>(units * p.splits));
+    const dim3 grid(static_cast<unsigned>(p.fit ? static_cast<int64_t>(p.fit) * p.heads * p.row_groups : units * p.splits));
     const ds_status st = launch_pdl(kern, grid, WARPS * 32, smem, p.cluster ? p.splits : 1, stream, p);
     if (st != DS_OK || p.splits == 1 || p.cluster) return st;
     const auto join_by = [&](auto kernel, int fr, int most) {
@@ -1024,12 +1104,12 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
     const int nt = rows > 8 ? 2 : 1;
     p.row_groups = (p.rows + 8 * nt - 1) / (8 * nt);
     const int64_t units = (indices ? sequences * tokens : sequences) * heads * p.row_groups;
-    // Splits: as many as fill every place on an SM once, down to one tile a warp (4 contexts of 1M
-    // positions and 16 rows: 131 us; twice as many 141, three times 150).  Many units: up to four times
-    // as many, since their lengths differ and the longest must not be left for the end (48 contexts of
-    // up to 8192 positions: once 82.7 us, four times 77.6), but no shorter than 16 tiles a warp: a CTA
-    // costs 7 us beside its tiles (304 units of 512 positions: one CTA each 11.4 us, four 30; 304 of
-    // 2048: 26.6, four each 47.6).
+    // Splits: as many as find a place on an SM at once, down to one tile a warp (4 contexts of 1M
+    // positions and 16 rows: 131 us, twice as many 141, three times 150; 16 lists of 1024 positions,
+    // 4 heads: 9.4, one more split 14.5).  Many units: up to four times as many, since their lengths
+    // differ and the longest must not be left for the end (48 contexts of up to 8192 positions: once
+    // 82.7 us, four times 77.6), but no shorter than 16 tiles a warp: a CTA costs 7 us beside its tiles
+    // (304 units of 512 positions: one CTA each 11.4 us, four 30; 304 of 2048: 26.6, four each 47.6).
     // Units that many and that short are one warp's work each, since a CTA of four has little more than
     // its start and its join to do (2432 units of 512 positions: 53.6 us, with four warps 88.7; 608:
     // 20.9 and 24.5).  From 1024 positions on four warps win (1216 units: 33.0, one warp 35.5; 2432 of
@@ -1042,7 +1122,7 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
         const int64_t most = (span + least - 1) / least;
         return n < most ? n : most;
     };
-    int64_t splits = at_most((places + units - 1) / units, unit_tiles);
+    int64_t splits = at_most(places / units > 1 ? places / units : 1, unit_tiles);
     if (2 * units >= places) {
         const int64_t many = at_most((4 * places + units - 1) / units, 16 * unit_tiles);
         if (splits < many) splits = many;
@@ -1065,13 +1145,26 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
     // places until the longest split is done (48 of up to 8192 positions: 105 us, through the
     // workspace 81).
     p.cluster = (indices || few) && splits > 1 && splits <= kAttCluster;
+    p.sequences = static_cast<int32_t>(sequences);
     if (splits > 1 && !p.cluster) {
-        const size_t entries = static_cast<size_t>(units) * splits * 8 * nt;
+        // Few units with splits of at least four tiles a warp by the table's width: splits by the
+        // lengths (16 contexts of up to 16384 positions, 8 heads: 40.0 us, by the width 59.7; 12 of up to
+        // 4096: 16.3 and 17.9).  Finding them takes 1 to 1.5 us, which shorter splits or equal lengths
+        // do not give back (16 of 16384: 62.0 and 60.6; one of 4096: 11.2 and 9.7).
+        const int64_t per = units / sequences, steps = (span + unit_tiles - 1) / unit_tiles;
+        int64_t partials = units * splits;
+        if (!indices && 2 * units < places && span / splits >= 4 * unit_tiles && steps < (1 << 20)) {
+            p.fit = static_cast<int32_t>(std::min(places / per, sequences * steps));
+            partials = p.fit * per;
+        }
+        const size_t entries = static_cast<size_t>(partials) * 8 * nt;
+        const size_t bytes = entries * (D + 2) * sizeof(float) + (p.fit ? units * sizeof(int2) : 0);
         void* ws = nullptr;
-        const ds_status st = library_workspace(dev, kWsAttend, entries * (D + 2) * sizeof(float), stream, &ws);
+        const ds_status st = library_workspace(dev, kWsAttend, bytes, stream, &ws);
         if (st != DS_OK) return st;
         p.ws_o = static_cast<float4*>(ws);
         p.ws_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) + entries * D);
+        p.ws_cut = reinterpret_cast<int2*>(p.ws_ml + entries);
     }
     if (dtype == DS_BF16)
         return D == 64 ? attend_rows<__nv_bfloat16, 64>(p, dev, info.sms, nt, warps, units, stream)
