@@ -16,8 +16,9 @@
 // of: largest head of the warp (redux.sync), lowest lane that has it (ballot), and that lane moves
 // its list up.  Lane j < k keeps the j-th choice's key and holder, and looks the expert up among
 // the holder's unsorted keys at the end, all choices at once.  (Instructions for a row of 256
-// experts: searching unsorted lanes in every round 1172, sorting pairs of key and place 996, this
-// way 928.)  It reads its expert's logit again (the row is in L1) and computes its weight.
+// experts: searching unsorted lanes in every round 1172, sorting pairs of key and place 996, keys
+// alone with equal choices counted in every round 928, counted at the end 879.)
+// It reads its expert's logit again (the row is in L1) and computes its weight.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -30,7 +31,14 @@
 namespace dsk {
 
 constexpr int kRouteWarps = 8;     // rows at a time per CTA
-constexpr int kCountWarps = 16;    // the same where choices are counted
+// The same where choices are counted, and such CTAs on an SM.  With 8 or 16 experts a lane 56 registers
+// leave room for 36 warps in three CTAs (16384 rows of 256 in groups, with gradient: 23.8 us, two of 16
+// warps 25.3; 512 experts 42.2 and 44.8); with fewer, two CTAs have their counts cleared and added
+// sooner (8190 rows of 60 experts: 7.1 us, three of 12 warps 8.2).
+template <int EPL>
+constexpr int kCountWarps = EPL == 8 || EPL == 16 ? 12 : 16;
+template <int EPL>
+constexpr int kCountCtas = EPL < 8 ? 2 : EPL < 32 ? 3 : 1;
 constexpr int kRouteMaxE = 512;
 constexpr int kRouteMaxK = 32;     // one lane per choice
 constexpr uint32_t kFull = 0xFFFFFFFFu;
@@ -214,23 +222,18 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
         for (int i = 0; i < L; ++i) list[n][i] = key[n * L + i];
         sort_down<L>(list[n]);
     }
-    // lane j: the j-th choice's key, the lane that holds it, and how many choices in a row before it
-    // had the same key and holder (equal keys come in turn, a holder's all at once)
-    uint32_t won = 0u, last_top = 0u;
-    int holder = lane, before = 0, last_from = -1, run = 0;
+    // lane j: the j-th choice's key and the lane that holds it
+    uint32_t won = 0u;
+    int holder = lane;
     for (int j = 0; j < p.k; ++j) {
         uint32_t head = list[0][0];
 #pragma unroll
         for (int n = 1; n < NL; ++n) head = max(head, list[n][0]);
         const uint32_t top = __reduce_max_sync(kFull, head);
         const int from = __ffs(__ballot_sync(kFull, head == top)) - 1;
-        run = top == last_top && from == last_from ? run + 1 : 0;
-        last_top = top;
-        last_from = from;
         if (lane == j) {
             won = top;
             holder = from;
-            before = run;
         }
         bool open = lane == from;
 #pragma unroll
@@ -243,7 +246,11 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
         }
     }
     // the expert behind each choice: the holder's first place with that key, or one further for each
-    // of those before
+    // choice right before it with the same key and holder (a holder's equal keys come in turn)
+    const uint32_t won_up = __shfl_up_sync(kFull, won, 1);
+    const int holder_up = __shfl_up_sync(kFull, holder, 1);
+    const uint32_t again = __ballot_sync(kFull, lane > 0 && won == won_up && holder == holder_up);
+    int before = lane - (31 - __clz(~again & ((2u << lane) - 1u)));
     int mine = __shfl_sync(kFull, first, holder);
     {
         int at = 0;
@@ -275,8 +282,9 @@ __device__ __forceinline__ void route_row(const RouteParams& p, int64_t row, int
 // Choices are counted in shared memory and added to the caller's counts once per CTA (rows going
 // straight to the counts meet in a few lines of L2: 131072 choices of 256 experts took 8 us).
 template <typename T, int EPL, bool VEC, bool COUNT>
-__global__ void __launch_bounds__((COUNT ? kCountWarps : kRouteWarps) * 32) ds_route_kernel(const RouteParams p) {
-    constexpr int WARPS = COUNT ? kCountWarps : kRouteWarps;
+__global__ void __launch_bounds__((COUNT ? kCountWarps<EPL> : kRouteWarps) * 32, COUNT && kCountCtas<EPL> == 3 ? 3 : 0)
+ds_route_kernel(const RouteParams p) {
+    constexpr int WARPS = COUNT ? kCountWarps<EPL> : kRouteWarps;
     __shared__ int sh_count[COUNT ? kRouteMaxE : 1];
     const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
@@ -408,10 +416,11 @@ static ds_status launch_route_as(const RouteParams& p, int sms, cudaStream_t str
                           stream, p);
     }
     // as many CTAs as fit at once, each for many rows: the counts are added once per CTA
-    int64_t ctas = (p.rows + kCountWarps - 1) / kCountWarps;
-    const int64_t most = static_cast<int64_t>(sms) * (EPL <= 16 ? 2 : 1);
+    constexpr int WARPS = kCountWarps<EPL>;
+    int64_t ctas = (p.rows + WARPS - 1) / WARPS;
+    const int64_t most = static_cast<int64_t>(sms) * kCountCtas<EPL>;
     if (ctas > most) ctas = most;
-    return launch_pdl(ds_route_kernel<T, EPL, VEC, true>, dim3(static_cast<unsigned>(ctas)), kCountWarps * 32, 0, 1, stream, p);
+    return launch_pdl(ds_route_kernel<T, EPL, VEC, true>, dim3(static_cast<unsigned>(ctas)), WARPS * 32, 0, 1, stream, p);
 }
 
 // 16-byte loads exist where a lane's run holds 16 bytes
