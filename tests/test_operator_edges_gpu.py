@@ -1,0 +1,85 @@
+"""The operators around the top-k at the ends of their ranges, on the GPU against their definitions
+in 64 bits: scales below zero, rows and values of very unlike size, lengths and scores at the edge
+of their types."""
+import math
+
+import numpy as np
+import pytest
+
+import operator_ref as ref
+import test_operators_gpu as base
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = base.DTYPES
+dev, host = base.dev, base.host
+
+
+@pytest.fixture(scope="module")
+def ds():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import top_selection_gb300 as m
+    return m
+
+
+def rows_to_cache(ds, k, v, page=16):
+    """A cache of one sequence and key head that holds the fp32 rows k and v, the rest junk."""
+    n, D = k.shape
+    pages = -(-n // page)
+    cache, scales = base.new_cache(pages + 1, 1, page, D)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda") + page
+    ds.cache_store(dev(k[:, None]), dev(v[:, None]), cache, scales, slots)
+    return cache, scales, torch.arange(1, pages + 1, dtype=torch.int32, device="cuda")[None]
+
+
+# ------------------------------------------------------------------ attention -----
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,at,size,spread,below", [
+    (1, slice(None), 0.1, 0.0, True),            # one position
+    (1, slice(None), 1.005, 0.0, True),
+    (50, slice(None), 1.003, 1e-5, False),       # every row's spread is below bf16's rounding
+    (50, slice(None), 1.005, 1e-5, True),
+    (700, slice(32, 64), 0.1, 0.0, True),        # one warp's tile of such rows beside ordinary ones
+    (3000, slice(5, None, 7), -0.3, 1e-6, False),
+    (3000, slice(5, None, 7), -0.301, 1e-6, True),
+])
+def test_attention_constant_values(ds, dtype, n, at, size, spread, below):
+    """An fp32 row of nearly one value has m = bf16(its minimum), which may lie above its maximum
+    (`below`): then s < 0 and the codes are 0, and the row stands for m.  Limits: the operator's
+    (base.check_attention)."""
+    rng = np.random.default_rng(n)
+    k, v = rng.standard_normal((2, n, 64)).astype(np.float32)
+    v[at] = size + spread * rng.standard_normal(v[at].shape)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    codes, s, m = ref.quantise(v)
+    stored = scales[1:].float().cpu().numpy().reshape(-1, 4)[:n]
+    assert np.array_equal(stored[:, 2], s) and np.array_equal(stored[:, 3], m)
+    assert (s[at] < 0).all() == below
+    q = dev((1.5 * rng.standard_normal((1, 1, 4, 64))).astype(np.float32), dtype)
+    want = ref.attention(host(q), base.Paged(cache, scales, table), [n])
+    got = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    base.check_attention(got, want, 5.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("which", [slice(None), slice(0, 1), slice(40, 45)])
+def test_attention_scales_below_zero(ds, dtype, which):
+    """Scales a caller wrote: negative ones, larger in size than the positive, with any codes."""
+    rng = np.random.default_rng(21)
+    n = 300
+    k, v = rng.standard_normal((2, n, 64)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    flat = scales[1:].view(-1, 4)
+    flat[which, 2] *= -1.5
+    flat[which, 0] *= -1
+    q = dev((1.5 * rng.standard_normal((1, 1, 8, 64))).astype(np.float32), dtype)
+    want = ref.attention(host(q), base.Paged(cache, scales, table), [n])
+    got = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    # values of up to 2.5 + 1.5 * 15 * 0.35
+    base.check_attention(got, want, 12.0, dtype)

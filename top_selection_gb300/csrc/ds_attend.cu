@@ -63,7 +63,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;                // running maximum of a row that has seen nothing
 // Weights as f16: p is at most 2^kRaise, and w = p s kTop / r, r a power of two near the largest
-// value scale s seen and never below an eighth of one.  The largest w is 16 * 8 * 256 = 2^15
+// value scale |s| seen and never below an eighth of one (a row whose minimum bf16 rounds up past its
+// maximum has s < 0).  The largest |w| is 16 * 8 * 256 = 2^15
 // (f16 ends at 2^16), and the heaviest position's is about 2^8, 22 binades above the subnormals.
 constexpr float kRaise = 4.0f, kTop = 256.0f, kOver = 2048.0f;
 
@@ -699,7 +700,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
         if (fresh || __any_sync(kAll, most > kRaise || fmaxf(max3(fabsf(vw[0]), fabsf(vw[1]), fabsf(vw[2])), fabsf(vw[3])) > kOver)) {
             float vtop = 1e-30f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vtop = fmaxf(vtop, vs[i] < INFINITY ? vs[i] : 0.f);
+            for (int i = 0; i < 4; ++i) vtop = fmaxf(vtop, fabsf(vs[i]) < INFINITY ? fabsf(vs[i]) : 0.f);
             const uint32_t vbits = __reduce_max_sync(kAll, __float_as_uint(vtop));
             float change = 1.f;
             if (__uint_as_float(vbits) * wmul > kOver) {  // r = the power of two at or below vtop
