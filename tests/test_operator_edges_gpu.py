@@ -83,3 +83,21 @@ def test_attention_scales_below_zero(ds, dtype, which):
     got = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
     # values of up to 2.5 + 1.5 * 15 * 0.35
     base.check_attention(got, want, 12.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads,large", [(8, 2.0 ** 22), (16, 2.0 ** 25), (16, 1e8), (8, 1e10), (16, 1e30)])
+def test_attention_query_rows_of_unlike_size(ds, dtype, heads, large):
+    """A query row of any size leaves the rows beside it as they are."""
+    rng = np.random.default_rng(22)
+    n, D = 4096, 128
+    k, v = rng.standard_normal((2, n, D)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v, 64)
+    x = (1.5 * rng.standard_normal((1, 1, heads, D))).astype(np.float32)
+    x[0, 0, [1, heads - 2]] *= np.float32(large)
+    q = dev(x, dtype)
+    plain = [i for i in range(heads) if i not in (1, heads - 2)]
+    want = ref.attention(host(q), base.Paged(cache, scales, table), [n])
+    out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    base.check_attention((out[:, :, plain], lse[:, :, plain]), (want[0][:, :, plain], want[1][:, :, plain]), 5.0, dtype)
+    assert torch.isfinite(out.float()).all()

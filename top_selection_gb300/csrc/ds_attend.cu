@@ -460,8 +460,10 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     int at_ahead = ahead[kAttStages - 1], page_ahead = page[kAttStages - 1];
 
     // q as the second operand: row g of each tile, the lane's quarter of the numbers in the
-    // order of the codes, times a power of two that brings the largest to 2^13 .. 2^14, and
-    // another 1/16 against codes that count 16-fold
+    // order of the codes, times a power of two that brings the row's largest to 2^13 .. 2^14, and
+    // another 1/16 against codes that count 16-fold.  Each row has its own: under one for all of them
+    // a row 2^22 below the largest loses bits to f16's range, and a padded token's row may hold
+    // anything.
     const auto row_query = [&](int r, int64_t& off, int& end) -> bool {  // row r of the unit
         if (r >= p.rows) {
             end = 0;
@@ -478,10 +480,9 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     float2 qsum[NT];
     int ends[NT][2];
     int first_end = 0x7FFFFFFF;  // below it no row of the CTA masks anything
-    float fold;
+    float2 fold[NT];  // what a score of codes and operand counts, of rows 2t and 2t + 1
     {
-        float x[NT][D / 4];
-        float top = 0.f;
+        float x[NT][D / 4], by[NT];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             int64_t off = 0;
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
 #pragma unroll
                 for (int i = 0; i < D / 4; ++i) x[j][i] = on ? static_cast<float>(q[i]) : 0.f;
             }
-            float sum = 0.f;
+            float sum = 0.f, top = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 4; ++i) {
                 sum += x[j][i];
@@ -517,8 +518,16 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
             }
             sum += __shfl_xor_sync(kAll, sum, 1);
             sum += __shfl_xor_sync(kAll, sum, 2);
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+            const int e = static_cast<int>(__float_as_uint(top) >> 23);  // biased exponent
+            const int up = e == 0 ? 0 : min(max(13 - (e - 127), -100), 100);
+            by[j] = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+            const float down = p.scale * kLog2e * kUnit * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            sum *= p.scale * kLog2e;
             // rows 2t + c sit in lanes 4 (2t + c)
             qsum[j] = make_float2(__shfl_sync(kAll, sum, 8 * t), __shfl_sync(kAll, sum, 8 * t + 4));
+            fold[j] = make_float2(__shfl_sync(kAll, down, 8 * t), __shfl_sync(kAll, down, 8 * t + 4));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 int64_t o2;
@@ -527,15 +536,6 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
             }
         }
         first_end = __reduce_min_sync(kAll, first_end);
-        const uint32_t e = __reduce_max_sync(kAll, __float_as_uint(top)) >> 23;  // biased exponent
-        const int up = e == 0u ? 0 : min(max(13 - (static_cast<int>(e) - 127), -100), 100);
-        const float by = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
-        fold = p.scale * kLog2e;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            qsum[j].x *= fold;
-            qsum[j].y *= fold;
-        }
         // each warp writes its share of the k-steps
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int d = 8 * (kk / 2) + 2 * (kk % 2) + half;
-                    const float f = half ? by * 0.0625f : by;
+                    const float f = half ? by[j] * 0.0625f : by[j];
                     uint32_t part[NQ];
                     split_f16<NQ>(x[j][d] * f, x[j][d + 4] * f, part);
 #pragma unroll
@@ -556,7 +556,6 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
             for (int i = 0; i < QW / 2; ++i)
                 reinterpret_cast<uint2*>(sm_q)[(kk * 32 + lane) * (QW / 2) + i] = make_uint2(w[2 * i], w[2 * i + 1]);
         }
-        fold *= kUnit * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
     }
 
     __syncthreads();
@@ -659,11 +658,11 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
             const float ks = __uint_as_float(sc.x << 16), km = __uint_as_float(sc.x & 0xFFFF0000u);
             vs[i] = __uint_as_float(sc.y << 16);
             vm[i] = fmaf(MID, vs[i], __uint_as_float(sc.y & 0xFFFF0000u));
-            const float2 f = both(ks * fold), base = both(CENTRE ? fmaf(8.f, ks, km) : km);
+            const float2 ks2 = both(ks), base = both(CENTRE ? fmaf(8.f, ks, km) : km);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {  // relative to the running maximum
                 float* x = &s[j][i / 2][2 * (i & 1)];
-                const float2 y = fma2(make_float2(x[0], x[1]), f, fma2(base, qsum[j], neg_m[j]));
+                const float2 y = fma2(make_float2(x[0], x[1]), mul2(ks2, fold[j]), fma2(base, qsum[j], neg_m[j]));
                 x[0] = y.x;
                 x[1] = y.y;
             }
