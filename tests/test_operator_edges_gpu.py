@@ -101,3 +101,21 @@ def test_attention_query_rows_of_unlike_size(ds, dtype, heads, large):
     out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
     base.check_attention((out[:, :, plain], lse[:, :, plain]), (want[0][:, :, plain], want[1][:, :, plain]), 5.0, dtype)
     assert torch.isfinite(out.float()).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("large", [2.0 ** 14, 1e6, 1e15, 1e30])
+@pytest.mark.parametrize("n,Q", [(70, 3), (33, 2), (1000, 5), (20, 2)])
+def test_attention_large_numbers_in_masked_places(ds, dtype, large, n, Q):
+    """A later token's scales of any size do not reach the tokens that do not see it (an unwritten
+    slot behind a padded draft)."""
+    rng = np.random.default_rng(n)
+    k, v = rng.standard_normal((2, n, 64)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    q = dev((1.5 * rng.standard_normal((1, Q, 4, 64))).astype(np.float32), dtype)
+    scales[1:].view(-1, 4)[n - 1, 2] = large
+    scales[1:].view(-1, 4)[n - 1, 3] = -large
+    want = ref.attention(host(q), base.Paged(cache, scales, table), [n])
+    out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    seen = slice(0, Q - 1)
+    base.check_attention((out[:, seen], lse[:, seen]), (want[0][:, seen], want[1][:, seen]), 5.0, dtype)

@@ -63,8 +63,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1e30f;                // running maximum of a row that has seen nothing
 // Weights as f16: p is at most 2^kRaise, and w = p s kTop / r, r a power of two near the largest
-// value scale |s| seen and never below an eighth of one (a row whose minimum bf16 rounds up past its
-// maximum has s < 0).  The largest |w| is 16 * 8 * 256 = 2^15
+// value scale |s| that the row has seen and never below an eighth of one (a row of values whose
+// minimum bf16 rounds up past its maximum has s < 0).  The largest |w| is 16 * 8 * 256 = 2^15
 // (f16 ends at 2^16), and the heaviest position's is about 2^8, 22 binades above the subnormals.
 constexpr float kRaise = 4.0f, kTop = 256.0f, kOver = 2048.0f;
 
@@ -575,11 +575,20 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
         const int r = rg * ROWS + 8 * j + 2 * t;
         unseen |= (r < p.rows ? 1u : 0u) << (2 * j) | (r + 1 < p.rows ? 2u : 0u) << (2 * j);
     }
-    float wmul = 1.2676506e30f;  // kTop / r; 2^100 until a value scale has been seen
+    // kTop / r of each row; 2^100 until a value scale has been seen.  A row's r goes by the positions
+    // that it sees: a later token's scale (an unwritten slot behind a padded draft) may be anything.
+    // Rows differ only once such a scale has come (`unlike`), in a warp's last tiles; till then wmul is
+    // every row's, and what lies in shared memory is not read.
+    float2* wrow = reinterpret_cast<float2*>(smem + WARPS * kAttStages * At::kBytes + KS * 32 * QW * 4) + warp * (ROWS / 2) + t;
+    float wmul = 1.2676506e30f;  // the largest of them
+    bool unlike = false;
     const float sign = !CENTRE && (g & 1) ? -1.f : 1.f;  // of the weights of this lane's positions
 
-    int slot = 0;
-    for (; j0 < to; j0 += STRIDE) {
+    int slot = 0, here = 0;
+    const unsigned char* tile = ring;
+    // Waits for the next tile and starts the copies of the one two behind it; whether the tile holds
+    // positions that some row does not see.
+    const auto advance = [&]() -> bool {
         copies_wait<kAttStages - 2>();
         __syncwarp();
         {
@@ -588,15 +597,22 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
             const uint32_t entry = entry_of(at_ahead, page_ahead, pos[kAttStages - 1]);
             issue(next, entry, is_run(entry));
         }
-        const int here = pos[0];
+        here = pos[0];
 #pragma unroll
         for (int i = 0; i + 1 < kAttStages; ++i) pos[i] = pos[i + 1];
         at_ahead = at_far;
         page_ahead = page_of(at_ahead);
         at_far = position_at(j0 + (kAttStages + 1) * STRIDE + lane);
-        const unsigned char* tile = ring + slot * At::kBytes;
+        tile = ring + slot * At::kBytes;
         if (++slot == kAttStages) slot = 0;
-
+        return __any_sync(kAll, here >= first_end);
+    };
+    // Works through a tile.  by_rows: the first one with positions that some row does not see, and those
+    // behind it.  The others have a loop of their own, since the row by row code slows theirs (4 x 1M
+    // positions: 133.4 us, in one loop 138.5).
+    bool masks = false;
+    const auto step = [&](auto by_rows_c) {
+        constexpr bool by_rows = by_rows_c.value;
         // scores of 32 positions: rows of tile i are positions 16 i + {g, g + 8}
         float s[NT][2][4];
 #pragma unroll
@@ -670,7 +686,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
         // positions that some row does not see: their scores become -inf and their weights 0.
         // A scale that is not finite would still make NaN of a weight of 0 (`odd`).
         bool odd = false;
-        if (__any_sync(kAll, here >= first_end)) {
+        if (by_rows && masks) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 at[i] = __shfl_sync(kAll, here, 8 * i + g);
@@ -682,6 +698,53 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
                         if (at[i] >= ends[j][c]) s[j][i / 2][2 * (i & 1) + c] = -INFINITY;
             }
             odd = __any_sync(kAll, odd);
+        }
+        // where rows see different positions, their r are raised row by row
+        if (by_rows) {
+            float vtop = 1e-30f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vtop = fmaxf(vtop, fabsf(vs[i]) < INFINITY ? fabsf(vs[i]) : 0.f);
+            const uint32_t vbits = __reduce_max_sync(kAll, __float_as_uint(vtop));
+            if (__uint_as_float(vbits) * wmul > kOver) {
+                const float to_mul = kTop / __uint_as_float(vbits & 0x7F800000u);
+                float most_mul = 0.f, least_mul = INFINITY;
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float2 mul = unlike ? wrow[4 * j] : both(wmul), change = both(1.f);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float own = 0.f;  // the largest scale of a position that the row sees
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((!masks || at[i] < ends[j][c]) && fabsf(vs[i]) < INFINITY) own = fmaxf(own, fabsf(vs[i]));
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) own = fmaxf(own, __shfl_xor_sync(kAll, own, d));
+                        float& m = c ? mul.y : mul.x;
+                        const bool none = unseen >> (2 * j + c) & 1u || rg * ROWS + 8 * j + 2 * t + c >= p.rows;
+                        if (own * m > kOver || none) {
+                            // the common one where it is at most 8 times too small, or meets nothing
+                            const float to = own == 0.f || 8.f * own * to_mul >= kTop
+                                                 ? to_mul
+                                                 : kTop / __uint_as_float(__float_as_uint(fmaxf(own, 1e-30f)) & 0x7F800000u);
+                            (c ? change.y : change.x) = to / m;
+                            m = to;
+                        }
+                        most_mul = fmaxf(most_mul, m);
+                        least_mul = fminf(least_mul, m);
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < KS; ++mt) {
+                        o[j][mt][0] *= change.x, o[j][mt][1] *= change.y;
+                        o[j][mt][2] *= change.x, o[j][mt][3] *= change.y;
+                    }
+                    ones[j][0] *= change.x, ones[j][1] *= change.y;
+                    __syncwarp();  // the other lanes have read it
+                    if (g == 0) wrow[4 * j] = mul;
+                }
+                wmul = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_mul)));
+                unlike = __any_sync(kAll, least_mul < wmul);
+                __syncwarp();
+            }
         }
         // raise the running maxima where a score passes one by 2^kRaise (or is the first), and
         // r where a value scale leaves it behind
@@ -702,7 +765,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
             for (int i = 0; i < 4; ++i) vtop = fmaxf(vtop, fabsf(vs[i]) < INFINITY ? fabsf(vs[i]) : 0.f);
             const uint32_t vbits = __reduce_max_sync(kAll, __float_as_uint(vtop));
             float change = 1.f;
-            if (__uint_as_float(vbits) * wmul > kOver) {  // r = the power of two at or below vtop
+            if (!by_rows && __uint_as_float(vbits) * wmul > kOver) {  // r = the power of two at or below vtop
                 const float to_mul = kTop / __uint_as_float(vbits & 0x7F800000u);
                 change = to_mul / wmul;
                 wmul = to_mul;
@@ -745,30 +808,29 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
         }
         // weights p, their sums, and w as the second operand
         uint32_t wf[NT][2][2][NP];  // [row tile][16 positions][first or second 8][part]
-        const auto weigh = [&](auto masked) {
+        float2 mul[NT];  // by rows: vs times wmul, of a row that does not see it, could be infinite
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 vw2 = both(vw[i]), vm2 = both(vm[i]);
+        for (int j = 0; j < NT; ++j) mul[j] = by_rows && unlike ? wrow[4 * j] : both(wmul);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const float* x = &s[j][i / 2][2 * (i & 1)];
-                    const float2 e = make_float2(exp2_fast(x[0]), exp2_fast(x[1]));
-                    l[j] = add2(l[j], e);
-                    float2 w = mul2(e, vw2), zn = fma2(e, vm2, z[j]);
-                    if (masked.value) {
-                        if (at[i] >= ends[j][0]) w.x = 0.f, zn.x = z[j].x;
-                        if (at[i] >= ends[j][1]) w.y = 0.f, zn.y = z[j].y;
-                    }
-                    z[j] = zn;
-                    uint32_t part[NP];
-                    split_f16<NP>(w.x, w.y, part);
+        for (int i = 0; i < 4; ++i) {
+            const float2 vw2 = both(by_rows ? vs[i] * sign : vw[i]), vm2 = both(vm[i]);
 #pragma unroll
-                    for (int n = 0; n < NP; ++n) wf[j][i / 2][i & 1][n] = transpose8x8(part[n]);
+            for (int j = 0; j < NT; ++j) {
+                const float* x = &s[j][i / 2][2 * (i & 1)];
+                const float2 e = make_float2(exp2_fast(x[0]), exp2_fast(x[1]));
+                l[j] = add2(l[j], e);
+                float2 w = mul2(by_rows ? mul2(e, mul[j]) : e, vw2), zn = fma2(e, vm2, z[j]);
+                if (by_rows && odd) {
+                    if (at[i] >= ends[j][0]) w.x = 0.f, zn.x = z[j].x;
+                    if (at[i] >= ends[j][1]) w.y = 0.f, zn.y = z[j].y;
                 }
+                z[j] = zn;
+                uint32_t part[NP];
+                split_f16<NP>(w.x, w.y, part);
+#pragma unroll
+                for (int n = 0; n < NP; ++n) wf[j][i / 2][i & 1][n] = transpose8x8(part[n]);
             }
-        };
-        if (!odd) weigh(std::false_type{});
-        else weigh(std::true_type{});
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             // value words of positions 16 i + {2t, 2t + 1, 2t + 8, 2t + 9}, the lane's eighth
@@ -816,8 +878,21 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
                 for (int j = 0; j < NT; ++j) mma_f16(ones[j], ONE, ONE, ONE, ONE, wf[j][i][0][0], wf[j][i][1][0]);
             }
         }
+    };
+    for (; j0 < to; j0 += STRIDE) {
+        masks = advance();
+        if (masks) break;
+        step(std::false_type{});
+    }
+    while (j0 < to) {
+        step(std::true_type{});
+        j0 += STRIDE;
+        if (j0 < to) masks = advance();
     }
     copies_wait<0>();
+    float2 mul[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) mul[j] = unlike ? wrow[4 * j] : both(wmul);
     __syncthreads();  // every warp is done with its ring
 
     // Join the warps: sums over the lanes of a row, then shared memory.  Output fragments stay as the
@@ -826,9 +901,9 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     constexpr int NF = NT * KS;                          // fragments of a warp
     float4* sm_o = reinterpret_cast<float4*>(smem);      // [warps][NF][32]
     float4* sm_r = sm_o + WARPS * NF * 32;           // [warps][ROWS]: maximum, sum of p, of p (m + MID s)
-    const float back = 1.f / wmul;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
+        const float back[2] = {1.f / mul[j].x, 1.f / mul[j].y};
         float ls[2] = {l[j].x, l[j].y}, zs[2] = {z[j].x, z[j].y};
         const float ms[2] = {unseen >> (2 * j) & 1u ? kNone : -neg_m[j].x, unseen >> (2 * j) & 2u ? kNone : -neg_m[j].y};
 #pragma unroll
@@ -838,14 +913,14 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
                 ls[c] += __shfl_xor_sync(kAll, ls[c], d);
                 zs[c] += __shfl_xor_sync(kAll, zs[c], d);
             }
-            if (!CENTRE) zs[c] -= 7.5f * ones[j][c] * back;
+            if (!CENTRE) zs[c] -= 7.5f * ones[j][c] * back[c];
             if (g == 0) sm_r[warp * ROWS + 8 * j + 2 * t + c] = make_float4(ms[c], ls[c], zs[c], 0.f);
         }
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
             const float f = mt & 1 ? kUnit * 0.0625f : kUnit;
-            sm_o[(warp * NF + j * KS + mt) * 32 + lane] = make_float4(o[j][mt][0] * f * back, o[j][mt][1] * f * back,
-                                                                      o[j][mt][2] * f * back, o[j][mt][3] * f * back);
+            sm_o[(warp * NF + j * KS + mt) * 32 + lane] = make_float4(o[j][mt][0] * f * back[0], o[j][mt][1] * f * back[1],
+                                                                      o[j][mt][2] * f * back[0], o[j][mt][3] * f * back[1]);
         }
     }
     __syncthreads();
@@ -1015,7 +1090,8 @@ template <typename T, int D, int NT, int WARPS>
 static ds_status attend(const AttendParams& p, int dev, int sms, int64_t units, cudaStream_t stream) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
     auto kern = ds_attend_kernel<T, D, NT, PARTS, PARTS, WARPS>;
-    const size_t ring = static_cast<size_t>(WARPS) * kAttStages * TileAt<D>::kBytes + D / 16 * 32 * 8 * NT * PARTS;
+    const size_t ring = static_cast<size_t>(WARPS) * kAttStages * TileAt<D>::kBytes + D / 16 * 32 * 8 * NT * PARTS +
+                        WARPS * 8 * NT * sizeof(float);
     const size_t join = (static_cast<size_t>(WARPS) * (D + 4) + D + 2) * 8 * NT * sizeof(float);  // sm_o, sm_r, sm_j, sm_ml
     const size_t smem = ring > join ? ring : join;
     // the opt-in above 48 KB is a property of the kernel on a device: set once
