@@ -119,3 +119,15 @@ def test_attention_large_numbers_in_masked_places(ds, dtype, large, n, Q):
     out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
     seen = slice(0, Q - 1)
     base.check_attention((out[:, seen], lse[:, seen]), (want[0][:, seen], want[1][:, seen]), 5.0, dtype)
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 31), -(1 << 31) + 1])
+@pytest.mark.parametrize("picked", [False, True])
+def test_attention_lengths_below_zero(ds, length, picked):
+    """A length below zero counts as zero, however far below."""
+    k, v = np.random.default_rng(23).standard_normal((2, 40, 64)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    q = torch.randn(1, 4, 8, 64, device="cuda").bfloat16()
+    idx = torch.arange(20, dtype=torch.int32, device="cuda").expand(1, 4, 20).contiguous() if picked else None
+    out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([length], dtype=torch.int32, device="cuda"), indices=idx)
+    assert out.abs().max() == 0 and torch.isneginf(lse).all()

@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     for (int s = 0; s < kAttStages; ++s) page[s] = page_of(ahead[s]);
 
     // the length comes beside the first pages, not before them
-    const int len = min(length, p.max_pos);
+    const int len = max(min(length, p.max_pos), 0);
     // query token i sees positions below len - (Q - 1 - i)
     const int end_all = max(picked ? len - (p.Q - 1 - q0) : len, 0);
     const int count = picked ? p.K : end_all;       // positions (or list entries) of this unit
