@@ -131,3 +131,20 @@ def test_attention_lengths_below_zero(ds, length, picked):
     idx = torch.arange(20, dtype=torch.int32, device="cuda").expand(1, 4, 20).contiguous() if picked else None
     out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([length], dtype=torch.int32, device="cuda"), indices=idx)
     assert out.abs().max() == 0 and torch.isneginf(lse).all()
+
+
+# ------------------------------------------------------------------ gate ---------
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_gradient_of_vanishing_scores(ds, scoring):
+    """Logistic scores near fp32's smallest numbers: the weights are of the order 1, and so is their
+    gradient.  Limits as for ordinary scores (1e-5 of scale * |g|); a score below 2^-126 keeps
+    2^-149, 3e-7 of it."""
+    x = np.array([[-88.0, -88.2, -200.0, -88.5, -300.0], [-85.0, -87.5, -88.5, -86.0, -88.0]], dtype=np.float32)
+    w, e = ds.route(dev(x), 2, scoring=scoring, scale=2.5)
+    g = np.array([[3.0, -3.0], [-5.0, 2.0]], dtype=np.float32)
+    eh = host(e).astype(np.int64)
+    assert np.allclose(host(w), ref.route_weights(x, eh, scoring, True, 2.5), rtol=base.GATE_REL)
+    got = host(ds.route_backward(dev(g), dev(x), e, scoring=scoring, scale=2.5))
+    want = ref.route_gradient(g, x, eh, scoring, True, 2.5)
+    assert np.all(np.abs(got - want) <= 1e-5 * 2.5 * np.abs(g).max())

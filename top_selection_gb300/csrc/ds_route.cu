@@ -381,15 +381,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) ds_route_backward_kernel(con
     const float t = on ? to_f32(x[e]) : -INFINITY;
     if (!WHOLE && !p.sigmoid) mx = row_max(part_max<LPR>(t));
     const float s = !on ? 0.f : p.sigmoid ? logistic(t) : expf(t - mx) / total;
-    float d = p.scale * g, back = 0.f;
+    // d w is s ds without 1 / D by itself: logistic scores may be so small that it is infinite
+    float d = p.scale * g, back = 0.f, w = s;
     if (p.renormalise) {
         const float sum = part_sum<LPR>(s);
-        const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-        const float mean = part_sum<LPR>(g * s * inv);
-        d = on ? p.scale * (g - mean) * inv : 0.f;
+        w = sum > 0.f ? s / sum : 0.f;
+        d = p.scale * (g - part_sum<LPR>(g * w));
     }
     if (WHOLE) back = part_sum<LPR>(d * s);
-    const float dx = p.sigmoid ? d * s * (1.0f - s) : s * (d - back);
+    const float dx = p.sigmoid ? d * w * (1.0f - s) : w * (d - back);
     if (live) {
         if (WHOLE) {
             const float f = -back / total;
