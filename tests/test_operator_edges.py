@@ -1,0 +1,37 @@
+"""Checks of the operators around the top-k that need no GPU: sizes whose products pass 32 or 64 bits
+are refused before anything is launched."""
+import pytest
+
+P = 1 << 20   # a 16-byte aligned address that is never read: the checks run first
+UNSUPPORTED = 3
+
+
+@pytest.fixture(scope="module")
+def ds():
+    from top_selection_gb300 import build
+    build.build()
+    import top_selection_gb300 as m
+    m.load()
+    return m
+
+
+@pytest.mark.parametrize("change", [
+    dict(indices=P, K=(1 << 30) + 1),                                   # places of a list
+    dict(indices=P, K=(1 << 31) - 1),
+    dict(pages=1 << 30, page=1 << 30, heads=16, q_heads=16, table_width=1, table_stride=1),   # 2^64 entries
+    dict(pages=(1 << 31) - 1, page=1 << 30, heads=(1 << 31) - 1, q_heads=(1 << 31) - 1, table_width=1, table_stride=1),
+])
+def test_cache_attention_refuses_sizes(ds, change):
+    a = dict(q=P, dtype=0, sequences=2, tokens=1, q_heads=8, D=128, q_seq_stride=1024, q_token_stride=1024,
+             q_head_stride=128, cache=P, scales=P, pages=8, heads=2, page=16, table=P, table_width=4, table_stride=4,
+             lens=P, indices=0, K=0, scale=0.1, out=P)
+    a.update(change)
+    assert ds.ds_cache_attention(**a) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("change", [dict(pages=1 << 40, page=1 << 30), dict(pages=1 << 62, page=2)])
+def test_cache_store_refuses_sizes(ds, change):
+    a = dict(k=P, v=P, dtype=0, tokens=3, heads=2, D=128, k_token_stride=256, k_head_stride=128, v_token_stride=256,
+             v_head_stride=128, cache=P, scales=P, pages=4, page=16, slots=P)
+    a.update(change)
+    assert ds.ds_cache_store(**a) == UNSUPPORTED

@@ -1140,7 +1140,9 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
         return DS_ERR_INVALID_ARG;
     if (q_seq_stride < 0 || q_token_stride < 0 || q_head_stride < 0 || !isfinite(scale)) return DS_ERR_INVALID_ARG;
     if ((D != 64 && D != 128) || (page & (page - 1)) != 0) return DS_ERR_UNSUPPORTED;
-    if (pages * page * heads >= 0xFFFFFFFFLL || pages > 0x7FFFFFFFLL || table_width > (int64_t(1) << 30) / page)
+    // entries count in 32 bits, positions and places of a list in 31
+    constexpr int64_t kMost = int64_t(1) << 30;
+    if (pages > 0x7FFFFFFFLL || pages > 0xFFFFFFFELL / heads / page || table_width > kMost / page || K > kMost)
         return DS_ERR_UNSUPPORTED;
     if (sequences == 0) return DS_OK;
     if (!q || !cache || !scales || !table || !lens || !out || (K > 0 && !indices)) return DS_ERR_INVALID_ARG;

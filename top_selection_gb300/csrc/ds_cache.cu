@@ -279,7 +279,8 @@ static ds_status cache_call(bool store, const void* k, const void* v, int32_t dt
                             void* scales, int64_t pages, int32_t page, const int32_t* slots, cudaStream_t stream) {
     if ((dtype != DS_BF16 && dtype != DS_FP32) || tokens < 0 || heads < 1 || pages < 0 || page < 1)
         return DS_ERR_INVALID_ARG;
-    if ((page & (page - 1)) != 0 || (D != 64 && D != 128) || heads > 65535) return DS_ERR_UNSUPPORTED;
+    if ((page & (page - 1)) != 0 || (D != 64 && D != 128) || heads > 65535 || pages > INT64_MAX / page / heads / D)
+        return DS_ERR_UNSUPPORTED;
     if (k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0) return DS_ERR_INVALID_ARG;
     if (tokens == 0) return DS_OK;
     if (!k || !v || !slots || (pages > 0 && (!cache || !scales))) return DS_ERR_INVALID_ARG;
