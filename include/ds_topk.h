@@ -263,7 +263,8 @@ size_t ds_noalloc_scratch_bytes(void);
  * drafted tokens, and a key/value cache in 4 bits with the attention that reads it.
  *
  * As above: calls are asynchronous on `stream`, errors found on the host are returned before
- * anything is launched, inputs and outputs are caller-owned device memory, and a call may be
+ * anything is launched, inputs and outputs are caller-owned memory of the current device, which
+ * `stream` belongs to (the Python functions make their tensors' device current), and a call may be
  * captured in a graph (ds_cache_attention once it has run on that stream with arguments that
  * need as much workspace, see there).  Launches are programmatic dependent ones: a kernel
  * touches memory only once the kernel before it on the stream has completed.

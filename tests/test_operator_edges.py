@@ -1,5 +1,7 @@
 """Checks of the operators around the top-k that need no GPU: sizes whose products pass 32 or 64 bits
-are refused before anything is launched."""
+are refused before anything is launched, and a call is made on its tensors' device."""
+import warnings
+
 import pytest
 
 P = 1 << 20   # a 16-byte aligned address that is never read: the checks run first
@@ -35,3 +37,20 @@ def test_cache_store_refuses_sizes(ds, change):
              v_head_stride=128, cache=P, scales=P, pages=4, page=16, slots=P)
     a.update(change)
     assert ds.ds_cache_store(**a) == UNSUPPORTED
+
+
+def test_a_call_is_made_on_its_tensors_device(ds):
+    """Tensors of a device that does not exist, and no tokens: the call has to fail in making that
+    device current, where on the current device it would return with nothing to do."""
+    torch = pytest.importorskip("torch")
+    fake = pytest.importorskip("torch._subclasses.fake_tensor")
+    at = f"cuda:{torch.cuda.device_count() + 1}"
+    with fake.FakeTensorMode():
+        kv = torch.empty(0, 2, 64, device=at, dtype=torch.bfloat16)
+        cache = torch.empty(2, 2, 16, 2, 32, device=at, dtype=torch.uint8)
+        scales = torch.empty(2, 2, 16, 4, device=at, dtype=torch.bfloat16)
+        slots = torch.empty(0, device=at, dtype=torch.int32)
+    with warnings.catch_warnings():
+        warnings.simplefilter("ignore")     # of reading a fake tensor's address
+        with pytest.raises(RuntimeError):
+            ds.cache_store(kv, kv, cache, scales, slots, stream=0)

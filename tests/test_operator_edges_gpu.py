@@ -148,3 +148,16 @@ def test_route_gradient_of_vanishing_scores(ds, scoring):
     got = host(ds.route_backward(dev(g), dev(x), e, scoring=scoring, scale=2.5))
     want = ref.route_gradient(g, x, eh, scoring, True, 2.5)
     assert np.all(np.abs(got - want) <= 1e-5 * 2.5 * np.abs(g).max())
+
+
+# ------------------------------------------------------------------ devices and streams --
+
+def test_tensors_of_another_device(ds):
+    """The tensors' device need not be the current one."""
+    if torch.cuda.device_count() < 2:
+        pytest.skip("needs two GPUs")
+    x = torch.randn(9, 64, device="cuda:0")
+    w, e = ds.route(x, 4)
+    w1, e1 = ds.route(x.to("cuda:1"), 4)
+    assert w1.device.index == 1 and torch.cuda.current_device() == 0
+    assert torch.equal(w.cpu(), w1.cpu()) and torch.equal(e.cpu(), e1.cpu())

@@ -3,13 +3,15 @@
 // call of the C ABI.  A call costs the host one pass through this file (4.4 us for the gate; the
 // same steps in Python with ctypes took 14), which is what a decoding step's small calls wait for.
 // Every function here takes its arguments by position from the documented Python function of the
-// same name.
+// same name.  The tensors' device is current for the length of a call, whichever was before: the C ABI
+// launches on the current one.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/full.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -167,6 +169,7 @@ PyObject* route(PyObject*, Args a, Py_ssize_t n) {
         const int32_t code = float_code(x, "logits"), k = integer32(a[1], "k");
         const int64_t rows = x.size(0), E = x.size(1);
         const auto index = x.get_device();
+        const c10::cuda::CUDAGuard current(index);
         const float* bias = a[3] == Py_None ? nullptr : data<float>(want(a[3], "bias", {E}, at::kFloat, index));
         int32_t* counts = a[9] == Py_None ? nullptr : data<int32_t>(want(a[9], "counts", {E}, at::kInt, index));
         if (E > 0x7FFFFFFF) refuse("logits has too many columns");
@@ -186,6 +189,7 @@ PyObject* route_backward(PyObject*, Args a, Py_ssize_t n) {
         const int32_t code = float_code(x, "logits");
         const int64_t rows = x.size(0), E = x.size(1);
         const auto index = x.get_device();
+        const c10::cuda::CUDAGuard current(index);
         const at::Tensor& chosen = tensor(a[2], "experts");
         const int64_t k = chosen.dim() > 0 ? chosen.size(-1) : 0;
         const at::Tensor& experts = want(a[2], "experts", {rows, k}, at::kInt, index);
@@ -208,6 +212,7 @@ PyObject* verify_drafts(PyObject*, Args a, Py_ssize_t n) {
         if (S < 0) refuse("logits must have at least one row per sequence");
         if (S > 0x7FFFFFFE) refuse("logits has too many rows per sequence");
         const auto index = x.get_device();
+        const c10::cuda::CUDAGuard current(index);
         const at::Tensor& drafts = want(a[1], "drafts", {B, S}, at::kInt, index);
         const at::Tensor& uniforms = want(a[2], "uniforms", {B, S}, at::kFloat, index);
         const at::Tensor& noise = want(a[3], "noise", {B, V}, at::kFloat, index, true);
@@ -258,6 +263,7 @@ struct Cache {
 PyObject* cache_store(PyObject*, Args a, Py_ssize_t n) {
     return guarded(n, 6, [&]() -> PyObject* {
         const Cache c(a[2], a[3]);
+        const c10::cuda::CUDAGuard current(c.index);
         const at::Tensor& k = leading(a[0], "k", 3);
         const int32_t code = float_code(k, "k");
         const int64_t T = k.size(0);
@@ -276,6 +282,7 @@ PyObject* cache_store(PyObject*, Args a, Py_ssize_t n) {
 PyObject* cache_load(PyObject*, Args a, Py_ssize_t n) {
     return guarded(n, 5, [&]() -> PyObject* {
         const Cache c(a[0], a[1]);
+        const c10::cuda::CUDAGuard current(c.index);
         const at::Tensor& s = tensor(a[2], "slots");
         const int64_t T = s.dim() > 0 ? s.size(0) : 0;
         const at::Tensor& slots = want(a[2], "slots", {T}, at::kInt, c.index);
@@ -292,6 +299,7 @@ PyObject* cache_load(PyObject*, Args a, Py_ssize_t n) {
 PyObject* cache_attention(PyObject*, Args a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject* {
         const Cache c(a[1], a[2]);
+        const c10::cuda::CUDAGuard current(c.index);
         const at::Tensor& q = leading(a[0], "q", 4);
         const int32_t code = float_code(q, "q");
         const int64_t B = q.size(0), Q = q.size(1), hq = q.size(2);
