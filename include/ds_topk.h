@@ -383,7 +383,8 @@ ds_status ds_cache_load(const void* cache, const void* scales, int64_t pages, in
  *   lens         [sequences] int32, clamped to 0 .. table_width * page
  *   indices      [sequences, tokens, K] int32 positions (as ds_topk returns them), or NULL; one
  *                outside the visible positions (-1 as padding) is not seen, one listed twice
- *                counts twice
+ *                counts twice; K = 0 with any non-null pointer is a list of nothing, of which
+ *                nothing is read
  *   scale        finite;  out  [sequences, tokens, q_heads, D] dtype, 16-byte aligned;  out_lse  [sequences,
  *                tokens, q_heads] floats or NULL
  * q enters in its own precision, scores, softmax sums and outputs are summed in fp32; the weights

@@ -161,3 +161,27 @@ def test_tensors_of_another_device(ds):
     w1, e1 = ds.route(x.to("cuda:1"), 4)
     assert w1.device.index == 1 and torch.cuda.current_device() == 0
     assert torch.equal(w.cpu(), w1.cpu()) and torch.equal(e.cpu(), e1.cpu())
+
+
+def busy(milliseconds=30):
+    """Keeps the current stream at work for a while."""
+    torch.cuda._sleep(int(milliseconds * 2e6))
+
+
+def test_attention_of_an_empty_list_on_another_stream(ds):
+    """No position is seen, whatever the current stream still has to do and the memory holds."""
+    k, v = np.random.default_rng(24).standard_normal((2, 40, 64)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    q = torch.randn(1, 4, 8, 64, device="cuda").bfloat16()
+    ln = torch.tensor([40], dtype=torch.int32, device="cuda")
+    none = torch.empty(1, 4, 0, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        zeros = torch.zeros(1, 4, 1, dtype=torch.int32, device="cuda")  # a list of position 0, left behind
+        del zeros
+        busy()
+        out, lse = ds.cache_attention(q, cache, scales, table, ln, indices=none, stream=side.cuda_stream)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert out.abs().max() == 0 and torch.isneginf(lse).all()

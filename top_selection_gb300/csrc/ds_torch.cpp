@@ -10,7 +10,6 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
-#include <ATen/ops/full.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -310,24 +309,21 @@ PyObject* cache_attention(PyObject*, Args a, Py_ssize_t n) {
         const int64_t width = pages.size(1);
         const at::Tensor& table = want(a[3], "table", {B, width}, at::kInt, c.index, true);
         const at::Tensor& lens = want(a[4], "lens", {B}, at::kInt, c.index);
-        at::Tensor indices;
+        const int32_t* indices = nullptr;
         int64_t K = 0;
         if (a[5] != Py_None) {
             const at::Tensor& t = tensor(a[5], "indices");
             K = t.dim() > 0 ? t.size(-1) : 0;
-            indices = want(a[5], "indices", {B, Q, K}, at::kInt, c.index);
+            indices = data<int32_t>(want(a[5], "indices", {B, Q, K}, at::kInt, c.index));
             if (K > 0x7FFFFFFF) refuse("indices has too many columns");
-            if (K == 0) {  // a list of nothing: one entry that is not seen
-                indices = at::full({B, Q, 1}, -1, indices.options());
-                K = 1;
-            }
+            if (K == 0) indices = data<int32_t>(lens);  // a list of nothing has no memory; none of it is read
         }
         const float scale = a[6] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.D))) : real(a[6]);
         const at::Tensor out = make({B, Q, hq, c.D}, q.scalar_type(), q), lse = make({B, Q, hq}, at::kFloat, q);
         check(ds_cache_attention(q.data_ptr(), code, B, static_cast<int32_t>(Q), static_cast<int32_t>(hq), c.D, q.stride(0),
                                  q.stride(1), q.stride(2), c.codes->data_ptr(), c.scales->data_ptr(), c.pages, c.heads,
                                  c.page, data<int32_t>(table), width, B > 1 ? table.stride(0) : width, data<int32_t>(lens),
-                                 indices.defined() ? data<int32_t>(indices) : nullptr, static_cast<int32_t>(K), scale,
+                                 indices, static_cast<int32_t>(K), scale,
                                  out.data_ptr(), data<float>(lse), stream_of(a[7], c.index)), "ds_cache_attention");
         return tuple_of({out, lse});
     });
