@@ -185,3 +185,51 @@ def test_attention_of_an_empty_list_on_another_stream(ds):
         side.synchronize()
         torch.cuda.synchronize()
         assert out.abs().max() == 0 and torch.isneginf(lse).all()
+
+
+def test_outputs_on_another_stream(ds):
+    """Outputs of a call on another stream than the current one are not in memory that the current
+    stream, behind in its work, still writes, and outlive their tensors on either."""
+    rng = np.random.default_rng(25)
+    k, v = rng.standard_normal((2, 300, 64)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    q = torch.randn(1, 2, 16, 64, device="cuda")
+    ln = torch.tensor([300], dtype=torch.int32, device="cuda")
+    x = torch.randn(70, 256, device="cuda")
+    logits = 3 * torch.randn(4, 3, 5000, device="cuda")
+    drafts = logits[:, :2].argmax(-1).int()
+    u, noise = torch.rand(4, 2, device="cuda"), torch.empty(4, 5000, device="cuda").exponential_()
+    experts = ds.route(x, 8)[1]
+    g = torch.randn(70, 8, device="cuda")
+    slots = torch.arange(16, 316, dtype=torch.int32, device="cuda")
+
+    def all_(stream=None):
+        return (*ds.cache_attention(q, cache, scales, table, ln, stream=stream), *ds.route(x, 8, stream=stream),
+                ds.route_backward(g, x, experts, stream=stream), *ds.verify_drafts(logits, drafts, u, noise, stream=stream),
+                *ds.cache_load(cache, scales, slots, stream=stream))
+    want = all_()
+    sizes = [t.numel() * t.element_size() for t in want]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        busy()
+        for size in sizes:  # memory that is free for the host, and still to be written
+            t = torch.empty(size, dtype=torch.uint8, device="cuda")
+            t.fill_(77)
+            del t
+        got = all_(side.cuda_stream)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        # the current stream works on them, they are dropped, and the other stream calls again
+        busy()
+        sums = [t.double().abs().nan_to_num(posinf=1.0).sum() for t in got]
+        del got
+        again = all_(side.cuda_stream)
+        for t in again:
+            with torch.cuda.stream(side):
+                t.zero_()
+        torch.cuda.synchronize()
+        assert [float(t) for t in sums] == [float(t.double().abs().nan_to_num(posinf=1.0).sum()) for t in want]
+    torch.cuda.current_stream().synchronize()
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()

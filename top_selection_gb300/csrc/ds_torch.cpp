@@ -17,6 +17,7 @@
 
 #include <cmath>
 #include <initializer_list>
+#include <optional>
 #include <string>
 
 #include "ds_topk.h"
@@ -101,16 +102,33 @@ const at::Tensor& want(PyObject* o, const char* what, std::initializer_list<int6
     return t;
 }
 
-cudaStream_t stream_of(PyObject* o, c10::DeviceIndex index) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(index).stream();
-    void* p = PyLong_AsVoidPtr(o);
-    if (!p && PyErr_Occurred()) throw PythonError{};
-    return static_cast<cudaStream_t>(p);
-}
+// Where a call runs: the tensors' device, made current, and its current stream or the caller's.  Another
+// stream than the current one is torch's current stream for the length of the call, so that outputs
+// come from its memory: what the current stream still has to do with memory that it has freed does
+// not meet them.  Outputs count as used on the current stream as well, where the caller goes on.
+class Place {
+    c10::cuda::CUDAGuard device_;
+    c10::cuda::CUDAStream here_;
+    std::optional<c10::cuda::CUDAStreamGuard> other_;
+    cudaStream_t stream_;
 
-at::Tensor make(std::initializer_list<int64_t> shape, at::ScalarType type, const at::Tensor& like) {
-    return at::detail::empty_cuda(at::IntArrayRef(shape.begin(), shape.size()), type, like.device(), std::nullopt);
-}
+   public:
+    Place(PyObject* o, c10::DeviceIndex index)
+        : device_(index), here_(c10::cuda::getCurrentCUDAStream(index)), stream_(here_.stream()) {
+        if (o == Py_None) return;
+        void* p = PyLong_AsVoidPtr(o);
+        if (!p && PyErr_Occurred()) throw PythonError{};
+        if (p == stream_) return;
+        stream_ = static_cast<cudaStream_t>(p);
+        other_.emplace(c10::cuda::getStreamFromExternal(stream_, index));
+    }
+    cudaStream_t stream() const { return stream_; }
+    at::Tensor make(std::initializer_list<int64_t> shape, at::ScalarType type) const {
+        at::Tensor t = at::detail::empty_cuda(at::IntArrayRef(shape.begin(), shape.size()), type, here_.device(), std::nullopt);
+        if (other_) t.record_stream(here_);
+        return t;
+    }
+};
 
 void check(int status, const char* what) {
     if (status != DS_OK) throw Failed{status, what};
@@ -168,16 +186,16 @@ PyObject* route(PyObject*, Args a, Py_ssize_t n) {
         const int32_t code = float_code(x, "logits"), k = integer32(a[1], "k");
         const int64_t rows = x.size(0), E = x.size(1);
         const auto index = x.get_device();
-        const c10::cuda::CUDAGuard current(index);
+        const Place place(a[10], index);
         const float* bias = a[3] == Py_None ? nullptr : data<float>(want(a[3], "bias", {E}, at::kFloat, index));
         int32_t* counts = a[9] == Py_None ? nullptr : data<int32_t>(want(a[9], "counts", {E}, at::kInt, index));
         if (E > 0x7FFFFFFF) refuse("logits has too many columns");
         const int64_t width = k > 0 ? k : 0;
-        const at::Tensor w = make({rows, width}, at::kFloat, x), e = make({rows, width}, at::kInt, x);
+        const at::Tensor w = place.make({rows, width}, at::kFloat), e = place.make({rows, width}, at::kInt);
         check(ds_route(x.data_ptr(), code, rows, static_cast<int32_t>(E), rows > 1 ? x.stride(0) : E, k,
                        integer32(a[2], "scoring"), bias, integer32(a[4], "groups"), integer32(a[5], "topk_groups"),
                        integer32(a[6], "group_score"), truth(a[7]), real(a[8]), data<float>(w), data<int32_t>(e), counts,
-                       stream_of(a[10], index)), "ds_route");
+                       place.stream()), "ds_route");
         return tuple_of({w, e});
     });
 }
@@ -188,17 +206,17 @@ PyObject* route_backward(PyObject*, Args a, Py_ssize_t n) {
         const int32_t code = float_code(x, "logits");
         const int64_t rows = x.size(0), E = x.size(1);
         const auto index = x.get_device();
-        const c10::cuda::CUDAGuard current(index);
+        const Place place(a[6], index);
         const at::Tensor& chosen = tensor(a[2], "experts");
         const int64_t k = chosen.dim() > 0 ? chosen.size(-1) : 0;
         const at::Tensor& experts = want(a[2], "experts", {rows, k}, at::kInt, index);
         const at::Tensor& grad = want(a[0], "grad_weights", {rows, k}, at::kFloat, index);
         if (E > 0x7FFFFFFF || k > 0x7FFFFFFF) refuse("logits or experts has too many columns");
-        const at::Tensor out = make({rows, E}, x.scalar_type(), x);
+        const at::Tensor out = place.make({rows, E}, x.scalar_type());
         check(ds_route_backward(data<float>(grad), x.data_ptr(), code, rows, static_cast<int32_t>(E),
                                 rows > 1 ? x.stride(0) : E, static_cast<int32_t>(k), data<int32_t>(experts),
                                 integer32(a[3], "scoring"), truth(a[4]), real(a[5]), out.data_ptr(), E,
-                                stream_of(a[6], index)), "ds_route_backward");
+                                place.stream()), "ds_route_backward");
         return THPVariable_Wrap(out);
     });
 }
@@ -211,7 +229,7 @@ PyObject* verify_drafts(PyObject*, Args a, Py_ssize_t n) {
         if (S < 0) refuse("logits must have at least one row per sequence");
         if (S > 0x7FFFFFFE) refuse("logits has too many rows per sequence");
         const auto index = x.get_device();
-        const c10::cuda::CUDAGuard current(index);
+        const Place place(a[7], index);
         const at::Tensor& drafts = want(a[1], "drafts", {B, S}, at::kInt, index);
         const at::Tensor& uniforms = want(a[2], "uniforms", {B, S}, at::kFloat, index);
         const at::Tensor& noise = want(a[3], "noise", {B, V}, at::kFloat, index, true);
@@ -228,12 +246,12 @@ PyObject* verify_drafts(PyObject*, Args a, Py_ssize_t n) {
         float temperature = 0.f;
         if (THPVariable_Check(a[6])) temps = data<float>(want(a[6], "temperature", {B}, at::kFloat, index));
         else temperature = real(a[6]);
-        const at::Tensor tokens = make({B, rows}, at::kInt, x), accepted = make({B}, at::kInt, x),
-                         probs = make({B, rows}, at::kFloat, x);
+        const at::Tensor tokens = place.make({B, rows}, at::kInt), accepted = place.make({B}, at::kInt),
+                         probs = place.make({B, rows}, at::kFloat);
         check(ds_verify_drafts(x.data_ptr(), code, B, static_cast<int32_t>(S), V, x.stride(0), rows > 1 ? x.stride(1) : V,
                                data<int32_t>(drafts), lens, q, q_seq, q_row, data<float>(uniforms), data<float>(noise),
                                B > 1 ? noise.stride(0) : V, temps, temperature, data<int32_t>(tokens),
-                               data<int32_t>(accepted), data<float>(probs), stream_of(a[7], index)), "ds_verify_drafts");
+                               data<int32_t>(accepted), data<float>(probs), place.stream()), "ds_verify_drafts");
         return tuple_of({tokens, accepted, probs});
     });
 }
@@ -262,7 +280,7 @@ struct Cache {
 PyObject* cache_store(PyObject*, Args a, Py_ssize_t n) {
     return guarded(n, 6, [&]() -> PyObject* {
         const Cache c(a[2], a[3]);
-        const c10::cuda::CUDAGuard current(c.index);
+        const Place place(a[5], c.index);
         const at::Tensor& k = leading(a[0], "k", 3);
         const int32_t code = float_code(k, "k");
         const int64_t T = k.size(0);
@@ -273,7 +291,7 @@ PyObject* cache_store(PyObject*, Args a, Py_ssize_t n) {
         const auto stride = [](const at::Tensor& t, int d) { return t.size(d) > 1 ? t.stride(d) : 0; };
         check(ds_cache_store(k.data_ptr(), v.data_ptr(), code, T, c.heads, c.D, stride(k, 0), stride(k, 1), stride(v, 0),
                              stride(v, 1), c.codes->data_ptr(), c.scales->data_ptr(), c.pages, c.page,
-                             data<int32_t>(slots), stream_of(a[5], c.index)), "ds_cache_store");
+                             data<int32_t>(slots), place.stream()), "ds_cache_store");
         Py_RETURN_NONE;
     });
 }
@@ -281,15 +299,15 @@ PyObject* cache_store(PyObject*, Args a, Py_ssize_t n) {
 PyObject* cache_load(PyObject*, Args a, Py_ssize_t n) {
     return guarded(n, 5, [&]() -> PyObject* {
         const Cache c(a[0], a[1]);
-        const c10::cuda::CUDAGuard current(c.index);
+        const Place place(a[4], c.index);
         const at::Tensor& s = tensor(a[2], "slots");
         const int64_t T = s.dim() > 0 ? s.size(0) : 0;
         const at::Tensor& slots = want(a[2], "slots", {T}, at::kInt, c.index);
         const bool wide = truth(a[3]);
         const at::ScalarType type = wide ? at::kFloat : at::kBFloat16;
-        const at::Tensor k = make({T, c.heads, c.D}, type, s), v = make({T, c.heads, c.D}, type, s);
+        const at::Tensor k = place.make({T, c.heads, c.D}, type), v = place.make({T, c.heads, c.D}, type);
         check(ds_cache_load(c.codes->data_ptr(), c.scales->data_ptr(), c.pages, c.page, data<int32_t>(slots), T, c.heads,
-                            c.D, wide ? DS_FP32 : DS_BF16, k.data_ptr(), v.data_ptr(), stream_of(a[4], c.index)),
+                            c.D, wide ? DS_FP32 : DS_BF16, k.data_ptr(), v.data_ptr(), place.stream()),
               "ds_cache_load");
         return tuple_of({k, v});
     });
@@ -298,7 +316,7 @@ PyObject* cache_load(PyObject*, Args a, Py_ssize_t n) {
 PyObject* cache_attention(PyObject*, Args a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject* {
         const Cache c(a[1], a[2]);
-        const c10::cuda::CUDAGuard current(c.index);
+        const Place place(a[7], c.index);
         const at::Tensor& q = leading(a[0], "q", 4);
         const int32_t code = float_code(q, "q");
         const int64_t B = q.size(0), Q = q.size(1), hq = q.size(2);
@@ -319,12 +337,12 @@ PyObject* cache_attention(PyObject*, Args a, Py_ssize_t n) {
             if (K == 0) indices = data<int32_t>(lens);  // a list of nothing has no memory; none of it is read
         }
         const float scale = a[6] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.D))) : real(a[6]);
-        const at::Tensor out = make({B, Q, hq, c.D}, q.scalar_type(), q), lse = make({B, Q, hq}, at::kFloat, q);
+        const at::Tensor out = place.make({B, Q, hq, c.D}, q.scalar_type()), lse = place.make({B, Q, hq}, at::kFloat);
         check(ds_cache_attention(q.data_ptr(), code, B, static_cast<int32_t>(Q), static_cast<int32_t>(hq), c.D, q.stride(0),
                                  q.stride(1), q.stride(2), c.codes->data_ptr(), c.scales->data_ptr(), c.pages, c.heads,
                                  c.page, data<int32_t>(table), width, B > 1 ? table.stride(0) : width, data<int32_t>(lens),
                                  indices, static_cast<int32_t>(K), scale,
-                                 out.data_ptr(), data<float>(lse), stream_of(a[7], c.index)), "ds_cache_attention");
+                                 out.data_ptr(), data<float>(lse), place.stream()), "ds_cache_attention");
         return tuple_of({out, lse});
     });
 }
