@@ -265,8 +265,8 @@ size_t ds_noalloc_scratch_bytes(void);
  * As above: calls are asynchronous on `stream`, errors found on the host are returned before
  * anything is launched, inputs and outputs are caller-owned memory of the current device, which
  * `stream` belongs to (the Python functions make their tensors' device current), and a call may be
- * captured in a graph (ds_cache_attention once it has run on that stream with arguments that
- * need as much workspace, see there).  Launches are programmatic dependent ones: a kernel
+ * captured in a graph (ds_cache_attention with the library's workspace once it has run on that
+ * stream with arguments that need as much, see there).  Launches are programmatic dependent ones: a kernel
  * touches memory only once the kernel before it on the stream has completed.
  * Pointers are aligned to their element unless a call says otherwise (DS_ERR_ALIGNMENT).
  * Logits, keys, values and queries are expected finite, -inf in logits excepted; other values
@@ -388,9 +388,11 @@ ds_status ds_cache_load(const void* cache, const void* scales, int64_t pages, in
  *   scale        finite;  out  [sequences, tokens, q_heads, D] dtype, 16-byte aligned;  out_lse  [sequences,
  *                tokens, q_heads] floats or NULL
  * q enters in its own precision, scores, softmax sums and outputs are summed in fp32; the weights
- * that meet the values are rounded to 11 bits for bf16 q and 22 for fp32.  Positions are split over CTAs whose partial results lie in a library-owned
- * workspace of (device, stream), grown with cudaMalloc as ds_topk's is: a call under stream
- * capture that would have to grow it returns DS_ERR_WORKSPACE.  pages * page * heads < 2^32 - 1,
+ * that meet the values are rounded to 11 bits for bf16 q and 22 for fp32.  Positions are split
+ * over CTAs whose partial results lie in a library-owned workspace of (device, stream), grown with
+ * cudaMalloc as ds_topk's is: a call under stream capture that would have to grow it returns
+ * DS_ERR_WORKSPACE, and graphs captured on one stream share it, so that they must not run at the same
+ * time.  ds_cache_attention_ex takes the caller's workspace instead.  pages * page * heads < 2^32 - 1,
  * table_width * page <= 2^30, K <= 2^30.
  */
 ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads,
@@ -399,6 +401,24 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
                              const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lens,
                              const int32_t* indices, int32_t K, float scale, void* out, float* out_lse,
                              cudaStream_t stream);
+
+/*
+ * ds_cache_attention_ex -- ds_cache_attention with the caller's workspace: device memory, 16-byte
+ * aligned, of at least ds_cache_attention_workspace_bytes() bytes (else DS_ERR_WORKSPACE), with any
+ * content, not used by anything else until the call's work is done.  NULL: the library's.  (The
+ * Python function takes it from torch's allocator.)
+ * ds_cache_attention_workspace_bytes -- the bytes a call of these sizes needs on the current device,
+ * 0 for none; picked: whether it has a list.
+ */
+ds_status ds_cache_attention_ex(const void* q, int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads,
+                                int32_t D, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+                                const void* cache, const void* scales, int64_t pages, int32_t heads, int32_t page,
+                                const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lens,
+                                const int32_t* indices, int32_t K, float scale, void* out, float* out_lse,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream);
+ds_status ds_cache_attention_workspace_bytes(int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads, int32_t D,
+                                             int32_t heads, int32_t page, int64_t table_width, int32_t picked, int32_t K,
+                                             size_t* bytes);
 
 #ifdef __cplusplus
 }

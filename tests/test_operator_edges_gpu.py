@@ -233,3 +233,76 @@ def test_outputs_on_another_stream(ds):
         assert [float(t) for t in sums] == [float(t.double().abs().nan_to_num(posinf=1.0).sum()) for t in want]
     torch.cuda.current_stream().synchronize()
     assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+def long_context(ds, seed, n=6000):
+    rng = np.random.default_rng(seed)
+    k, v = rng.standard_normal((2, n, 64)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v, 64)
+    q = dev(rng.standard_normal((1, 1, 8, 64)).astype(np.float32), torch.bfloat16)
+    ln = torch.tensor([n], dtype=torch.int32, device="cuda")
+    return q, cache, scales, table, ln
+
+
+def test_attention_captured_without_a_warm_up(ds):
+    """A graph has a workspace of its own, whatever its stream has run before."""
+    args = long_context(ds, 26)
+    assert ds.ds_cache_attention_workspace_bytes(ds.DS_BF16, 1, 1, 8, 64, 1, 64, args[3].shape[1]) > 0
+    want = ds.cache_attention(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        got = ds.cache_attention(*args)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_attention_graphs_of_one_stream_at_the_same_time(ds):
+    """Graphs captured on one stream and replayed side by side do not share a workspace."""
+    capture, args = torch.cuda.Stream(), [long_context(ds, 27), long_context(ds, 28)]
+    want, graphs, outs, sides = [], [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for a in args:
+        want.append(ds.cache_attention(*a))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=capture):
+            for _ in range(20):
+                out = ds.cache_attention(*a)
+        graphs.append(graph)
+        outs.append(out)
+    for _ in range(10):
+        for graph, side in zip(graphs, sides):
+            with torch.cuda.stream(side):
+                graph.replay()
+        torch.cuda.synchronize()
+        for got, expect in zip(outs, want):
+            assert torch.equal(got[0], expect[0]) and torch.equal(got[1], expect[1])
+
+
+def test_attention_with_a_workspace_of_the_caller(ds):
+    q, cache, scales, table, ln = long_context(ds, 29)
+    need = ds.ds_cache_attention_workspace_bytes(ds.DS_BF16, 1, 1, 8, 64, 1, 64, table.shape[1])
+    want = ds.cache_attention(q, cache, scales, table, ln)
+    buf = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")   # NaN wherever it is read before it is written
+    out, lse = torch.empty_like(q), torch.empty(1, 1, 8, device="cuda")
+
+    def call(ws, size):
+        return ds.ds_cache_attention_ex(q.data_ptr(), ds.DS_BF16, 1, 1, 8, 64, 512, 512, 64, cache.data_ptr(),
+                                        scales.data_ptr(), cache.shape[0], 1, 64, table.data_ptr(), table.shape[1],
+                                        table.shape[1], ln.data_ptr(), 0, 0, 0.125, out.data_ptr(), lse.data_ptr(), ws,
+                                        size, torch.cuda.current_stream().cuda_stream)
+    assert call(buf.data_ptr(), need - 1) == 7      # DS_ERR_WORKSPACE
+    assert call(buf.data_ptr() + 8, need) == 2      # DS_ERR_ALIGNMENT
+    assert call(buf.data_ptr(), need) == 0
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert (buf[need:] == 255).all()
+    assert call(0, 0) == 0                          # the library's
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    # a list that one cluster takes needs none
+    assert ds.ds_cache_attention_workspace_bytes(ds.DS_BF16, 64, 1, 32, 128, 2, 64, 2048, picked=True, K=512) == 0
+    with pytest.raises(ds.DSError):
+        ds.ds_cache_attention_workspace_bytes(ds.DS_BF16, 1, 1, 8, 96, 1, 64, 4)

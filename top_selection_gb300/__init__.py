@@ -28,6 +28,7 @@ __all__ = [
     "library_path", "load",
     "DS_SOFTMAX", "DS_SIGMOID", "DS_GROUP_MAX", "DS_GROUP_TOP2", "ds_topk_sample", "topk_sample",
     "ds_route", "ds_route_backward", "ds_verify_drafts", "ds_cache_store", "ds_cache_load", "ds_cache_attention",
+    "ds_cache_attention_ex", "ds_cache_attention_workspace_bytes",
     "route", "route_backward", "verify_drafts", "cache_store", "cache_load", "cache_attention",
 ]
 
@@ -136,6 +137,11 @@ def load():
         lib.ds_cache_attention.argtypes = [vp, i32, i64, i32, i32, i32, i64, i64, i64, vp, vp, i64, i32, i32, vp, i64,
                                            i64, vp, vp, i32, f32, vp, vp, vp]
         lib.ds_cache_attention.restype = ctypes.c_int
+        lib.ds_cache_attention_ex.argtypes = [*lib.ds_cache_attention.argtypes[:-1], vp, ctypes.c_size_t, vp]
+        lib.ds_cache_attention_ex.restype = ctypes.c_int
+        lib.ds_cache_attention_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32, i32, i64, i32, i32,
+                                                           ctypes.POINTER(ctypes.c_size_t)]
+        lib.ds_cache_attention_workspace_bytes.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -358,6 +364,27 @@ def ds_cache_attention(q, dtype, sequences, tokens, q_heads, D, q_seq_stride, q_
                                      heads, page, int(table) or None, table_width, table_stride, int(lens) or None,
                                      int(indices) or None, K, float(scale), int(out) or None, int(out_lse) or None,
                                      int(stream) or None)
+
+
+def ds_cache_attention_ex(q, dtype, sequences, tokens, q_heads, D, q_seq_stride, q_token_stride, q_head_stride, cache,
+                          scales, pages, heads, page, table, table_width, table_stride, lens, indices, K, scale, out,
+                          out_lse=0, workspace=0, workspace_bytes=0, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_cache_attention_ex(int(q) or None, dtype, sequences, tokens, q_heads, D, q_seq_stride,
+                                        q_token_stride, q_head_stride, int(cache) or None, int(scales) or None, pages,
+                                        heads, page, int(table) or None, table_width, table_stride, int(lens) or None,
+                                        int(indices) or None, K, float(scale), int(out) or None, int(out_lse) or None,
+                                        int(workspace) or None, workspace_bytes, int(stream) or None)
+
+
+def ds_cache_attention_workspace_bytes(dtype, sequences, tokens, q_heads, D, heads, page, table_width, picked=False,
+                                       K=0) -> int:
+    out = ctypes.c_size_t(0)
+    st = load().ds_cache_attention_workspace_bytes(dtype, sequences, tokens, q_heads, D, heads, page, table_width,
+                                                   int(bool(picked)), K, ctypes.byref(out))
+    if st != 0:
+        raise DSError(st, "ds_cache_attention_workspace_bytes")
+    return int(out.value)
 
 
 class _Names(dict):

@@ -1123,27 +1123,110 @@ static ds_status attend_rows(const AttendParams& p, int dev, int sms, int nt, in
                       : attend<T, D, 2, kAttWarps>(p, dev, sms, units, stream);
 }
 
+// How a call is cut up, and the workspace that takes.
+struct AttendPlan {
+    int64_t units;
+    int32_t rows, nt, row_groups, warps, splits, chunk, cluster, fit;
+    size_t entries, bytes;  // rows of partial results; 0 bytes: no workspace
+};
+
+// span: the table's positions, or the list's length where `picked`
+static ds_status attend_plan(int64_t sequences, int32_t tokens, int32_t q_heads, int32_t heads, int32_t D, bool picked,
+                             int64_t span, int sms, AttendPlan& a) {
+    const int64_t group = q_heads / heads, rows = picked ? group : group * tokens;
+    if (rows > (1 << 20)) return DS_ERR_UNSUPPORTED;
+    a.rows = static_cast<int32_t>(rows);
+    a.nt = rows > 8 ? 2 : 1;
+    a.row_groups = (a.rows + 8 * a.nt - 1) / (8 * a.nt);
+    a.units = (picked ? sequences * tokens : sequences) * heads * a.row_groups;
+    // Splits: as many as find a place on an SM at once, down to one tile a warp (4 contexts of 1M
+    // positions and 16 rows: 131 us, twice as many 141, three times 150; 16 lists of 1024 positions,
+    // 4 heads: 9.4, one more split 14.5).  Many units: up to four times as many, since their lengths
+    // differ and the longest must not be left for the end (48 contexts of up to 8192 positions: once
+    // 82.7 us, four times 77.6), but no shorter than 16 tiles a warp: a CTA costs 7 us beside its tiles
+    // (304 units of 512 positions: one CTA each 11.4 us, four 30; 304 of 2048: 26.6, four each 47.6).
+    // Units that many and that short are one warp's work each, since a CTA of four has little more than
+    // its start and its join to do (2432 units of 512 positions: 53.6 us, with four warps 88.7; 608:
+    // 20.9 and 24.5).  From 1024 positions on four warps win (1216 units: 33.0, one warp 35.5; 2432 of
+    // up to 4096: 140 and 162), and so they do with few units (304 of 512: 11.4 and 15.0).
+    a.warps = a.units >= 4LL * sms && span <= 4 * kAttWarps * kAttTile ? 1 : kAttWarps;
+    const int64_t unit_tiles = a.warps * kAttTile;
+    const int64_t places = static_cast<int64_t>(sms) * att_resident(a.nt, a.warps);
+    const auto at_most = [&](int64_t n, int64_t least) {
+        const int64_t most = (span + least - 1) / least;
+        return n < most ? n : most;
+    };
+    int64_t splits = at_most(places / a.units > 1 ? places / a.units : 1, unit_tiles);
+    if (2 * a.units >= places) {
+        const int64_t many = at_most((4 * places + a.units - 1) / a.units, 16 * unit_tiles);
+        if (splits < many) splits = many;
+    }
+    if (splits < 1) splits = 1;
+    // Short contexts whose splits all run at once are split over a cluster, up to two tiles a warp.
+    const bool few = a.units * splits <= places && span <= 2 * kAttCluster * unit_tiles;
+    if (few && splits > kAttCluster) splits = kAttCluster;
+    int64_t chunk = (span + splits - 1) / splits;
+    chunk = (chunk + unit_tiles - 1) / unit_tiles * unit_tiles;
+    if (chunk < unit_tiles) chunk = unit_tiles;
+    splits = (span + chunk - 1) / chunk;
+    if (splits < 1) splits = 1;
+    a.splits = static_cast<int32_t>(splits);
+    a.chunk = static_cast<int32_t>(chunk);
+    if (a.units * splits > 0x7FFFFFFFLL || a.units * (a.nt * D / 16) > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
+    // Up to 8 splits of a list or of few short contexts are a cluster and join over its shared memory
+    // (64 lists of 512 positions: 11.4 us, through the workspace 13.6; 4 contexts of 512, 8 heads: 7.4
+    // and 8.4; one of 2048: 7.8 and 8.1).  Many contexts differ in length, and a cluster holds its
+    // places until the longest split is done (48 of up to 8192 positions: 105 us, through the
+    // workspace 81).
+    a.cluster = (picked || few) && splits > 1 && splits <= kAttCluster;
+    a.fit = 0;
+    a.entries = a.bytes = 0;
+    if (splits > 1 && !a.cluster) {
+        // Few units with splits of at least four tiles a warp by the table's width: splits by the
+        // lengths (16 contexts of up to 16384 positions, 8 heads: 40.0 us, by the width 59.7; 12 of up to
+        // 4096: 16.3 and 17.9).  Finding them takes 1 to 1.5 us, which shorter splits or equal lengths
+        // do not give back (16 of 16384: 62.0 and 60.6; one of 4096: 11.2 and 9.7).
+        const int64_t per = a.units / sequences, steps = (span + unit_tiles - 1) / unit_tiles;
+        int64_t partials = a.units * splits;
+        if (!picked && 2 * a.units < places && span / splits >= 4 * unit_tiles && steps < (1 << 20)) {
+            a.fit = static_cast<int32_t>(std::min(places / per, sequences * steps));
+            partials = a.fit * per;
+        }
+        a.entries = static_cast<size_t>(partials) * 8 * a.nt;
+        a.bytes = a.entries * (D + 2) * sizeof(float) + (a.fit ? a.units * sizeof(int2) : 0);
+    }
+    return DS_OK;
+}
+
+// What a call's sizes have to be, whatever its pointers.
+static ds_status attend_sizes(int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads, int32_t D, int32_t heads,
+                              int32_t page, int64_t table_width, int32_t K) {
+    if ((dtype != DS_BF16 && dtype != DS_FP32) || sequences < 0 || tokens < 1 || q_heads < 1 || heads < 1 ||
+        q_heads % heads != 0 || page < 1 || table_width < 1 || K < 0)
+        return DS_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128) || (page & (page - 1)) != 0) return DS_ERR_UNSUPPORTED;
+    // positions and places of a list count in 31 bits
+    constexpr int64_t kMost = int64_t(1) << 30;
+    return table_width > kMost / page || K > kMost ? DS_ERR_UNSUPPORTED : DS_OK;
+}
+
 }  // namespace dsk
 
 using namespace dsk;
 
 extern "C" {
 
-ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads,
-                             int32_t D, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
-                             const void* cache, const void* scales, int64_t pages, int32_t heads, int32_t page,
-                             const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lens,
-                             const int32_t* indices, int32_t K, float scale, void* out, float* out_lse,
-                             cudaStream_t stream) {
-    if ((dtype != DS_BF16 && dtype != DS_FP32) || sequences < 0 || tokens < 1 || q_heads < 1 || heads < 1 ||
-        q_heads % heads != 0 || pages < 1 || page < 1 || table_width < 1 || table_stride < table_width || K < 0)
+ds_status ds_cache_attention_ex(const void* q, int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads,
+                                int32_t D, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+                                const void* cache, const void* scales, int64_t pages, int32_t heads, int32_t page,
+                                const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lens,
+                                const int32_t* indices, int32_t K, float scale, void* out, float* out_lse,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    if (pages < 1 || table_stride < table_width || q_seq_stride < 0 || q_token_stride < 0 || q_head_stride < 0 || !isfinite(scale))
         return DS_ERR_INVALID_ARG;
-    if (q_seq_stride < 0 || q_token_stride < 0 || q_head_stride < 0 || !isfinite(scale)) return DS_ERR_INVALID_ARG;
-    if ((D != 64 && D != 128) || (page & (page - 1)) != 0) return DS_ERR_UNSUPPORTED;
-    // entries count in 32 bits, positions and places of a list in 31
-    constexpr int64_t kMost = int64_t(1) << 30;
-    if (pages > 0x7FFFFFFFLL || pages > 0xFFFFFFFELL / heads / page || table_width > kMost / page || K > kMost)
-        return DS_ERR_UNSUPPORTED;
+    const ds_status sizes = attend_sizes(dtype, sequences, tokens, q_heads, D, heads, page, table_width, K);
+    if (sizes != DS_OK) return sizes;
+    if (pages > 0x7FFFFFFFLL || pages > 0xFFFFFFFELL / heads / page) return DS_ERR_UNSUPPORTED;  // 32 bits count entries
     if (sequences == 0) return DS_OK;
     if (!q || !cache || !scales || !table || !lens || !out || (K > 0 && !indices)) return DS_ERR_INVALID_ARG;
     const int es = dtype == DS_BF16 ? 2 : 4;
@@ -1180,79 +1263,62 @@ ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, in
     p.pages = static_cast<int32_t>(pages);
     p.scale = scale;
     p.q_vec = aligned16(q) && q_seq_stride * es % 16 == 0 && q_token_stride * es % 16 == 0 && q_head_stride * es % 16 == 0;
-    const int64_t rows = indices ? p.group : static_cast<int64_t>(p.group) * tokens;
-    if (rows > (1 << 20)) return DS_ERR_UNSUPPORTED;
-    p.rows = static_cast<int32_t>(rows);
-    const int nt = rows > 8 ? 2 : 1;
-    p.row_groups = (p.rows + 8 * nt - 1) / (8 * nt);
-    const int64_t units = (indices ? sequences * tokens : sequences) * heads * p.row_groups;
-    // Splits: as many as find a place on an SM at once, down to one tile a warp (4 contexts of 1M
-    // positions and 16 rows: 131 us, twice as many 141, three times 150; 16 lists of 1024 positions,
-    // 4 heads: 9.4, one more split 14.5).  Many units: up to four times as many, since their lengths
-    // differ and the longest must not be left for the end (48 contexts of up to 8192 positions: once
-    // 82.7 us, four times 77.6), but no shorter than 16 tiles a warp: a CTA costs 7 us beside its tiles
-    // (304 units of 512 positions: one CTA each 11.4 us, four 30; 304 of 2048: 26.6, four each 47.6).
-    // Units that many and that short are one warp's work each, since a CTA of four has little more than
-    // its start and its join to do (2432 units of 512 positions: 53.6 us, with four warps 88.7; 608:
-    // 20.9 and 24.5).  From 1024 positions on four warps win (1216 units: 33.0, one warp 35.5; 2432 of
-    // up to 4096: 140 and 162), and so they do with few units (304 of 512: 11.4 and 15.0).
-    const int64_t span = p.span;
-    const int warps = units >= 4LL * info.sms && span <= 4 * kAttWarps * kAttTile ? 1 : kAttWarps;
-    const int64_t unit_tiles = warps * kAttTile;
-    const int64_t places = static_cast<int64_t>(info.sms) * att_resident(nt, warps);
-    const auto at_most = [&](int64_t n, int64_t least) {
-        const int64_t most = (span + least - 1) / least;
-        return n < most ? n : most;
-    };
-    int64_t splits = at_most(places / units > 1 ? places / units : 1, unit_tiles);
-    if (2 * units >= places) {
-        const int64_t many = at_most((4 * places + units - 1) / units, 16 * unit_tiles);
-        if (splits < many) splits = many;
-    }
-    if (splits < 1) splits = 1;
-    // Short contexts whose splits all run at once are split over a cluster, up to two tiles a warp.
-    const bool few = units * splits <= places && span <= 2 * kAttCluster * unit_tiles;
-    if (few && splits > kAttCluster) splits = kAttCluster;
-    int64_t chunk = (span + splits - 1) / splits;
-    chunk = (chunk + unit_tiles - 1) / unit_tiles * unit_tiles;
-    if (chunk < unit_tiles) chunk = unit_tiles;
-    splits = (span + chunk - 1) / chunk;
-    if (splits < 1) splits = 1;
-    p.splits = static_cast<int32_t>(splits);
-    p.chunk = static_cast<int32_t>(chunk);
-    if (units * splits > 0x7FFFFFFFLL || units * (nt * D / 16) > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
-    // Up to 8 splits of a list or of few short contexts are a cluster and join over its shared memory
-    // (64 lists of 512 positions: 11.4 us, through the workspace 13.6; 4 contexts of 512, 8 heads: 7.4
-    // and 8.4; one of 2048: 7.8 and 8.1).  Many contexts differ in length, and a cluster holds its
-    // places until the longest split is done (48 of up to 8192 positions: 105 us, through the
-    // workspace 81).
-    p.cluster = (indices || few) && splits > 1 && splits <= kAttCluster;
+    AttendPlan a;
+    const ds_status planned = attend_plan(sequences, tokens, q_heads, heads, D, indices != nullptr, p.span, info.sms, a);
+    if (planned != DS_OK) return planned;
+    p.rows = a.rows;
+    p.row_groups = a.row_groups;
+    p.splits = a.splits;
+    p.chunk = a.chunk;
+    p.cluster = a.cluster;
+    p.fit = a.fit;
     p.sequences = static_cast<int32_t>(sequences);
-    if (splits > 1 && !p.cluster) {
-        // Few units with splits of at least four tiles a warp by the table's width: splits by the
-        // lengths (16 contexts of up to 16384 positions, 8 heads: 40.0 us, by the width 59.7; 12 of up to
-        // 4096: 16.3 and 17.9).  Finding them takes 1 to 1.5 us, which shorter splits or equal lengths
-        // do not give back (16 of 16384: 62.0 and 60.6; one of 4096: 11.2 and 9.7).
-        const int64_t per = units / sequences, steps = (span + unit_tiles - 1) / unit_tiles;
-        int64_t partials = units * splits;
-        if (!indices && 2 * units < places && span / splits >= 4 * unit_tiles && steps < (1 << 20)) {
-            p.fit = static_cast<int32_t>(std::min(places / per, sequences * steps));
-            partials = p.fit * per;
+    if (a.bytes > 0) {
+        void* ws = workspace;
+        if (!ws) {
+            const ds_status st = library_workspace(dev, kWsAttend, a.bytes, stream, &ws);
+            if (st != DS_OK) return st;
+        } else if (workspace_bytes < a.bytes) {
+            return DS_ERR_WORKSPACE;
+        } else if (!aligned16(ws)) {
+            return DS_ERR_ALIGNMENT;
         }
-        const size_t entries = static_cast<size_t>(partials) * 8 * nt;
-        const size_t bytes = entries * (D + 2) * sizeof(float) + (p.fit ? units * sizeof(int2) : 0);
-        void* ws = nullptr;
-        const ds_status st = library_workspace(dev, kWsAttend, bytes, stream, &ws);
-        if (st != DS_OK) return st;
         p.ws_o = static_cast<float4*>(ws);
-        p.ws_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) + entries * D);
-        p.ws_cut = reinterpret_cast<int2*>(p.ws_ml + entries);
+        p.ws_ml = reinterpret_cast<float2*>(static_cast<float*>(ws) + a.entries * D);
+        p.ws_cut = reinterpret_cast<int2*>(p.ws_ml + a.entries);
     }
     if (dtype == DS_BF16)
-        return D == 64 ? attend_rows<__nv_bfloat16, 64>(p, dev, info.sms, nt, warps, units, stream)
-                       : attend_rows<__nv_bfloat16, 128>(p, dev, info.sms, nt, warps, units, stream);
-    return D == 64 ? attend_rows<float, 64>(p, dev, info.sms, nt, warps, units, stream)
-                   : attend_rows<float, 128>(p, dev, info.sms, nt, warps, units, stream);
+        return D == 64 ? attend_rows<__nv_bfloat16, 64>(p, dev, info.sms, a.nt, a.warps, a.units, stream)
+                       : attend_rows<__nv_bfloat16, 128>(p, dev, info.sms, a.nt, a.warps, a.units, stream);
+    return D == 64 ? attend_rows<float, 64>(p, dev, info.sms, a.nt, a.warps, a.units, stream)
+                   : attend_rows<float, 128>(p, dev, info.sms, a.nt, a.warps, a.units, stream);
+}
+
+ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads,
+                             int32_t D, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,
+                             const void* cache, const void* scales, int64_t pages, int32_t heads, int32_t page,
+                             const int32_t* table, int64_t table_width, int64_t table_stride, const int32_t* lens,
+                             const int32_t* indices, int32_t K, float scale, void* out, float* out_lse,
+                             cudaStream_t stream) {
+    return ds_cache_attention_ex(q, dtype, sequences, tokens, q_heads, D, q_seq_stride, q_token_stride, q_head_stride,
+                                 cache, scales, pages, heads, page, table, table_width, table_stride, lens, indices, K,
+                                 scale, out, out_lse, nullptr, 0, stream);
+}
+
+ds_status ds_cache_attention_workspace_bytes(int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads, int32_t D,
+                                             int32_t heads, int32_t page, int64_t table_width, int32_t picked, int32_t K,
+                                             size_t* bytes) {
+    if (!bytes) return DS_ERR_INVALID_ARG;
+    *bytes = 0;
+    const ds_status sizes = attend_sizes(dtype, sequences, tokens, q_heads, D, heads, page, table_width, K);
+    if (sizes != DS_OK || sequences == 0) return sizes;
+    int dev = 0;
+    DevInfo info;
+    if (cudaGetDevice(&dev) != cudaSuccess || !dev_info(dev, info)) return DS_ERR_CUDA;
+    AttendPlan a;
+    const ds_status st = attend_plan(sequences, tokens, q_heads, heads, D, picked != 0, picked ? K : table_width * page, info.sms, a);
+    if (st == DS_OK) *bytes = a.bytes;
+    return st;
 }
 
 }  // extern "C"

@@ -128,6 +128,11 @@ class Place {
         if (other_) t.record_stream(here_);
         return t;
     }
+    // bytes that only the call itself uses: a graph that is being captured gets its own
+    at::Tensor scratch(size_t bytes) const {
+        if (bytes == 0) return {};
+        return at::detail::empty_cuda(static_cast<int64_t>(bytes), at::kByte, here_.device(), std::nullopt);
+    }
 };
 
 void check(int status, const char* what) {
@@ -338,11 +343,16 @@ PyObject* cache_attention(PyObject*, Args a, Py_ssize_t n) {
         }
         const float scale = a[6] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(c.D))) : real(a[6]);
         const at::Tensor out = place.make({B, Q, hq, c.D}, q.scalar_type()), lse = place.make({B, Q, hq}, at::kFloat);
-        check(ds_cache_attention(q.data_ptr(), code, B, static_cast<int32_t>(Q), static_cast<int32_t>(hq), c.D, q.stride(0),
-                                 q.stride(1), q.stride(2), c.codes->data_ptr(), c.scales->data_ptr(), c.pages, c.heads,
-                                 c.page, data<int32_t>(table), width, B > 1 ? table.stride(0) : width, data<int32_t>(lens),
-                                 indices, static_cast<int32_t>(K), scale,
-                                 out.data_ptr(), data<float>(lse), place.stream()), "ds_cache_attention");
+        const int32_t tokens = static_cast<int32_t>(Q), heads = static_cast<int32_t>(hq), list = static_cast<int32_t>(K);
+        size_t bytes = 0;
+        check(ds_cache_attention_workspace_bytes(code, B, tokens, heads, c.D, c.heads, c.page, width, indices != nullptr,
+                                                 list, &bytes), "ds_cache_attention");
+        const at::Tensor ws = place.scratch(bytes);
+        check(ds_cache_attention_ex(q.data_ptr(), code, B, tokens, heads, c.D, q.stride(0), q.stride(1), q.stride(2),
+                                    c.codes->data_ptr(), c.scales->data_ptr(), c.pages, c.heads, c.page,
+                                    data<int32_t>(table), width, B > 1 ? table.stride(0) : width, data<int32_t>(lens),
+                                    indices, list, scale, out.data_ptr(), data<float>(lse),
+                                    bytes ? ws.data_ptr() : nullptr, bytes, place.stream()), "ds_cache_attention");
         return tuple_of({out, lse});
     });
 }
