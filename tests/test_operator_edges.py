@@ -22,6 +22,9 @@ def ds():
     dict(indices=P, K=(1 << 31) - 1),
     dict(pages=1 << 30, page=1 << 30, heads=16, q_heads=16, table_width=1, table_stride=1),   # 2^64 entries
     dict(pages=(1 << 31) - 1, page=1 << 30, heads=(1 << 31) - 1, q_heads=(1 << 31) - 1, table_width=1, table_stride=1),
+    dict(sequences=1 << 40, tokens=1 << 30, heads=8, indices=P, K=1),                          # 2^73 lists
+    dict(sequences=1 << 62, heads=4),                                                          # 2^64 units
+    dict(sequences=1 << 32),
 ])
 def test_cache_attention_refuses_sizes(ds, change):
     a = dict(q=P, dtype=0, sequences=2, tokens=1, q_heads=8, D=128, q_seq_stride=1024, q_token_stride=1024,
@@ -37,6 +40,14 @@ def test_cache_store_refuses_sizes(ds, change):
              v_head_stride=128, cache=P, scales=P, pages=4, page=16, slots=P)
     a.update(change)
     assert ds.ds_cache_store(**a) == UNSUPPORTED
+
+
+def test_route_refuses_sizes(ds):
+    rows = (1 << 63) - 1
+    assert ds.ds_route(logits=P, dtype=1, rows=rows, E=64, row_stride=64, k=4, scoring=0, bias=0, groups=1, topk_groups=1,
+                       group_score=0, renormalise=True, scale=1.0, out_weights=P, out_experts=P) == UNSUPPORTED
+    assert ds.ds_route_backward(grad_weights=P, logits=P, dtype=1, rows=rows, E=64, row_stride=64, k=4, experts=P,
+                                scoring=0, renormalise=True, scale=1.0, grad_logits=P, grad_stride=64) == UNSUPPORTED
 
 
 def test_a_call_is_made_on_its_tensors_device(ds):

@@ -1123,6 +1123,29 @@ static ds_status attend_rows(const AttendParams& p, int dev, int sms, int nt, in
                       : attend<T, D, 2, kAttWarps>(p, dev, sms, units, stream);
 }
 
+// Query rows of a unit: the heads of a group, and for whole contexts the step's tokens as well.
+static int64_t attend_unit_rows(int32_t tokens, int32_t q_heads, int32_t heads, bool picked) {
+    return static_cast<int64_t>(q_heads / heads) * (picked ? 1 : tokens);
+}
+static int attend_row_tiles(int64_t rows) { return rows > 8 ? 2 : 1; }
+
+// What a call's sizes have to be, whatever its pointers.
+static ds_status attend_sizes(int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads, int32_t D, int32_t heads,
+                              int32_t page, int64_t table_width, bool picked, int32_t K) {
+    if ((dtype != DS_BF16 && dtype != DS_FP32) || sequences < 0 || tokens < 1 || q_heads < 1 || heads < 1 ||
+        q_heads % heads != 0 || page < 1 || table_width < 1 || K < 0)
+        return DS_ERR_INVALID_ARG;
+    if ((D != 64 && D != 128) || (page & (page - 1)) != 0) return DS_ERR_UNSUPPORTED;
+    // positions and places of a list count in 31 bits
+    constexpr int64_t kMost = int64_t(1) << 30;
+    if (table_width > kMost / page || K > kMost) return DS_ERR_UNSUPPORTED;
+    // units are blocks of a grid, 31 bits as well
+    const int64_t rows = attend_unit_rows(tokens, q_heads, heads, picked), tile = 8 * attend_row_tiles(rows);
+    if (rows > (1 << 20) || sequences > 0x7FFFFFFFLL / (picked ? tokens : 1) / heads / ((rows + tile - 1) / tile))
+        return DS_ERR_UNSUPPORTED;
+    return DS_OK;
+}
+
 // How a call is cut up, and the workspace that takes.
 struct AttendPlan {
     int64_t units;
@@ -1133,12 +1156,10 @@ struct AttendPlan {
 // span: the table's positions, or the list's length where `picked`
 static ds_status attend_plan(int64_t sequences, int32_t tokens, int32_t q_heads, int32_t heads, int32_t D, bool picked,
                              int64_t span, int sms, AttendPlan& a) {
-    const int64_t group = q_heads / heads, rows = picked ? group : group * tokens;
-    if (rows > (1 << 20)) return DS_ERR_UNSUPPORTED;
-    a.rows = static_cast<int32_t>(rows);
-    a.nt = rows > 8 ? 2 : 1;
+    a.rows = static_cast<int32_t>(attend_unit_rows(tokens, q_heads, heads, picked));
+    a.nt = attend_row_tiles(a.rows);
     a.row_groups = (a.rows + 8 * a.nt - 1) / (8 * a.nt);
-    a.units = (picked ? sequences * tokens : sequences) * heads * a.row_groups;
+    a.units = sequences * (picked ? tokens : 1) * heads * a.row_groups;
     // Splits: as many as find a place on an SM at once, down to one tile a warp (4 contexts of 1M
     // positions and 16 rows: 131 us, twice as many 141, three times 150; 16 lists of 1024 positions,
     // 4 heads: 9.4, one more split 14.5).  Many units: up to four times as many, since their lengths
@@ -1198,18 +1219,6 @@ static ds_status attend_plan(int64_t sequences, int32_t tokens, int32_t q_heads,
     return DS_OK;
 }
 
-// What a call's sizes have to be, whatever its pointers.
-static ds_status attend_sizes(int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads, int32_t D, int32_t heads,
-                              int32_t page, int64_t table_width, int32_t K) {
-    if ((dtype != DS_BF16 && dtype != DS_FP32) || sequences < 0 || tokens < 1 || q_heads < 1 || heads < 1 ||
-        q_heads % heads != 0 || page < 1 || table_width < 1 || K < 0)
-        return DS_ERR_INVALID_ARG;
-    if ((D != 64 && D != 128) || (page & (page - 1)) != 0) return DS_ERR_UNSUPPORTED;
-    // positions and places of a list count in 31 bits
-    constexpr int64_t kMost = int64_t(1) << 30;
-    return table_width > kMost / page || K > kMost ? DS_ERR_UNSUPPORTED : DS_OK;
-}
-
 }  // namespace dsk
 
 using namespace dsk;
@@ -1224,7 +1233,7 @@ ds_status ds_cache_attention_ex(const void* q, int32_t dtype, int64_t sequences,
                                 void* workspace, size_t workspace_bytes, cudaStream_t stream) {
     if (pages < 1 || table_stride < table_width || q_seq_stride < 0 || q_token_stride < 0 || q_head_stride < 0 || !isfinite(scale))
         return DS_ERR_INVALID_ARG;
-    const ds_status sizes = attend_sizes(dtype, sequences, tokens, q_heads, D, heads, page, table_width, K);
+    const ds_status sizes = attend_sizes(dtype, sequences, tokens, q_heads, D, heads, page, table_width, indices != nullptr, K);
     if (sizes != DS_OK) return sizes;
     if (pages > 0x7FFFFFFFLL || pages > 0xFFFFFFFELL / heads / page) return DS_ERR_UNSUPPORTED;  // 32 bits count entries
     if (sequences == 0) return DS_OK;
@@ -1310,7 +1319,7 @@ ds_status ds_cache_attention_workspace_bytes(int32_t dtype, int64_t sequences, i
                                              size_t* bytes) {
     if (!bytes) return DS_ERR_INVALID_ARG;
     *bytes = 0;
-    const ds_status sizes = attend_sizes(dtype, sequences, tokens, q_heads, D, heads, page, table_width, K);
+    const ds_status sizes = attend_sizes(dtype, sequences, tokens, q_heads, D, heads, page, table_width, picked != 0, K);
     if (sizes != DS_OK || sequences == 0) return sizes;
     int dev = 0;
     DevInfo info;

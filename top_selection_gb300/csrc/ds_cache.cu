@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(kCacheThreads) ds_cache_load_kernel(const Cach
 template <int LPR, int U, typename Kernel>
 static ds_status launch_cache(Kernel kern, const CacheParams& p, cudaStream_t stream) {
     constexpr int64_t per = kCacheThreads / (2 * LPR) * U;  // tokens of a CTA
+    if (p.tokens > 0x7FFFFFFFLL * per) return DS_ERR_UNSUPPORTED;
     const int64_t ctas = (p.tokens + per - 1) / per;
-    if (ctas > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
     return launch_pdl(kern, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(p.heads)), kCacheThreads, 0, 1, stream, p);
 }
 

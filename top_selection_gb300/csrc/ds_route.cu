@@ -467,7 +467,7 @@ ds_status ds_route(const void* logits, int32_t dtype, int64_t rows, int32_t E, i
     if (groups < 1 || E % groups != 0 || topk_groups < 1 || topk_groups > groups) return DS_ERR_INVALID_ARG;
     if (k > static_cast<int64_t>(E / groups) * topk_groups || !isfinite(scale)) return DS_ERR_INVALID_ARG;
     if (E > kRouteMaxE || k > kRouteMaxK || groups > 32) return DS_ERR_UNSUPPORTED;
-    if ((rows + kRouteWarps - 1) / kRouteWarps > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
+    if (rows > 0x7FFFFFFFLL * kRouteWarps) return DS_ERR_UNSUPPORTED;
     if (rows == 0) return DS_OK;
     if (!logits || !out_weights || !out_experts) return DS_ERR_INVALID_ARG;
     const int es = dtype == DS_BF16 ? 2 : 4;
@@ -514,7 +514,7 @@ ds_status ds_route_backward(const float* grad_weights, const void* logits, int32
         return DS_ERR_INVALID_ARG;
     if ((scoring != DS_SOFTMAX && scoring != DS_SIGMOID) || !isfinite(scale)) return DS_ERR_INVALID_ARG;
     if (E > kRouteMaxE || k > kRouteMaxK) return DS_ERR_UNSUPPORTED;
-    if ((rows + kRouteWarps - 1) / kRouteWarps > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
+    if (rows > 0x7FFFFFFFLL * kRouteWarps) return DS_ERR_UNSUPPORTED;
     if (rows == 0) return DS_OK;
     if (!grad_weights || !logits || !experts || !grad_logits) return DS_ERR_INVALID_ARG;
     const int es = dtype == DS_BF16 ? 2 : 4;
