@@ -121,6 +121,18 @@ def test_attention_large_numbers_in_masked_places(ds, dtype, large, n, Q):
     base.check_attention((out[:, seen], lse[:, seen]), (want[0][:, seen], want[1][:, seen]), 5.0, dtype)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_strides_of_one(ds, dtype):
+    """The stride of an extent of 1 is never used, whatever it is."""
+    k, v = np.random.default_rng(30).standard_normal((2, 200, 64)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    q = torch.randn(1, 1, 1, 64, device="cuda").to(dtype)
+    ln = torch.tensor([200], dtype=torch.int32, device="cuda")
+    want = ds.cache_attention(q, cache, scales, table, ln)
+    got = ds.cache_attention(q.as_strided((1, 1, 1, 64), (3, 77, 5, 1)), cache, scales, table, ln)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("length", [-1, -(1 << 31), -(1 << 31) + 1])
 @pytest.mark.parametrize("picked", [False, True])
 def test_attention_lengths_below_zero(ds, length, picked):

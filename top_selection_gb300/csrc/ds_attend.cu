@@ -1271,7 +1271,9 @@ ds_status ds_cache_attention_ex(const void* q, int32_t dtype, int64_t sequences,
     while ((1 << p.page_log) < page) ++p.page_log;
     p.pages = static_cast<int32_t>(pages);
     p.scale = scale;
-    p.q_vec = aligned16(q) && q_seq_stride * es % 16 == 0 && q_token_stride * es % 16 == 0 && q_head_stride * es % 16 == 0;
+    // the stride of an extent of 1 is never used
+    p.q_vec = aligned16(q) && (sequences == 1 || q_seq_stride * es % 16 == 0) &&
+              (tokens == 1 || q_token_stride * es % 16 == 0) && (q_heads == 1 || q_head_stride * es % 16 == 0);
     AttendPlan a;
     const ds_status planned = attend_plan(sequences, tokens, q_heads, heads, D, indices != nullptr, p.span, info.sms, a);
     if (planned != DS_OK) return planned;
