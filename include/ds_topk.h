@@ -346,8 +346,9 @@ ds_status ds_verify_drafts(const void* logits, int32_t dtype, int64_t sequences,
 /*
  * The 4-bit cache.  A key or value row of D numbers x is held as D codes c in 0 .. 15 and a
  * pair (s, m) of bf16, standing for s * c + m:  m = bf16(min x), s = bf16((max x - m) / 15),
- * c = clamp(rint((x - m) / s), 0, 15) (0 where s < 2^-126), the quotients as fp32 products with
- * 1/15 and 1/s.  Layout, caller-owned:
+ * c = clamp(rint((x - m) / s), 0, 15) (0 where s < 2^-126, negative s included: a row so narrow that
+ * m was rounded up past its maximum), the quotients as fp32 products with 1/15 and 1/s.  Numbers up to
+ * 2^126 in size come back finite.  Layout, caller-owned:
  *   cache   [pages][heads][page][2][D / 2] bytes, 16-byte aligned: key, then value; number 2 j
  *           in the low half of byte j, 2 j + 1 in the high half
  *   scales  [pages][heads][page][4] bf16, 8-byte aligned: key s, key m, value s, value m
@@ -387,6 +388,8 @@ ds_status ds_cache_load(const void* cache, const void* scales, int64_t pages, in
  *                nothing is read
  *   scale        finite;  out  [sequences, tokens, q_heads, D] dtype, 16-byte aligned;  out_lse  [sequences,
  *                tokens, q_heads] floats or NULL
+ * Results are finite for |q| < 2^113, |v| <= 2^90 and products scale q_d k_d up to 2^100; any number
+ * elsewhere affects only the rows that see it.
  * q enters in its own precision, scores, softmax sums and outputs are summed in fp32; the weights
  * that meet the values are rounded to 11 bits for bf16 q and 22 for fp32.  Positions are split
  * over CTAs whose partial results lie in a library-owned workspace of (device, stream), grown with

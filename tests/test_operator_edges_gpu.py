@@ -122,6 +122,20 @@ def test_attention_large_numbers_in_masked_places(ds, dtype, large, n, Q):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_at_the_ends_of_the_range(ds, dtype):
+    """Values of 2^90 and keys whose products with the query are ordinary but whose own size is not.
+    Limits as for ordinary values (base.check_attention), relative to their size."""
+    rng = np.random.default_rng(31)
+    k, v = rng.standard_normal((2, 2500, 64)).astype(np.float32)
+    big = np.float32(2.0 ** 90) / np.abs(v).max()
+    cache, scales, table = rows_to_cache(ds, k * np.float32(2.0 ** 60), v * big)
+    q = dev((rng.standard_normal((1, 1, 8, 64)) * 2.0 ** -60).astype(np.float32), dtype)
+    want = ref.attention(host(q), base.Paged(cache, scales, table), [2500])
+    out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([2500], dtype=torch.int32, device="cuda"))
+    base.check_attention((out.double() / float(big), lse), (want[0] / float(big), want[1]), 5.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_attention_strides_of_one(ds, dtype):
     """The stride of an extent of 1 is never used, whatever it is."""
     k, v = np.random.default_rng(30).standard_normal((2, 200, 64)).astype(np.float32)
@@ -143,6 +157,27 @@ def test_attention_lengths_below_zero(ds, length, picked):
     idx = torch.arange(20, dtype=torch.int32, device="cuda").expand(1, 4, 20).contiguous() if picked else None
     out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([length], dtype=torch.int32, device="cuda"), indices=idx)
     assert out.abs().max() == 0 and torch.isneginf(lse).all()
+
+
+# ------------------------------------------------------------------ 4-bit cache ---
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [2.0 ** 126, 2.0 ** -126])
+def test_cache_at_the_ends_of_the_range(ds, dtype, size):
+    """Rows of 2^126 come back finite, and those near fp32's smallest numbers by the format's rules;
+    the bits are the format's."""
+    rng = np.random.default_rng(32)
+    x = rng.uniform(-1, 1, (40, 64)).astype(np.float32)
+    x[:, 0], x[:, 1] = -1, 1
+    x = dev(x * np.float32(size), dtype)
+    cache, scales, table = rows_to_cache(ds, x.float().cpu().numpy(), -x.float().cpu().numpy())
+    codes, s, m = ref.quantise(x.float().cpu().numpy())
+    flat = scales[1:].float().cpu().numpy().reshape(-1, 4)[:40]
+    assert np.array_equal(cache[1:, 0, :, 0].cpu().numpy().reshape(-1, 32)[:40], ref.pack(codes))
+    assert np.array_equal(flat[:, 0], s) and np.array_equal(flat[:, 1], m)
+    k, v = ds.cache_load(cache, scales, torch.arange(16, 56, dtype=torch.int32, device="cuda"), dtype=torch.float32)
+    assert torch.isfinite(k).all() and torch.isfinite(v).all()
+    assert np.array_equal(k[:, 0].cpu().numpy(), ref.value(codes, s, m).astype(np.float32))
 
 
 # ------------------------------------------------------------------ gate ---------

@@ -4,9 +4,10 @@
 // A row (one token's key or value of one head, D numbers x) is held as D codes c in 0..15 and
 // a bf16 pair (s, m), standing for s * c + m:
 //   m = bf16(min x),  s = bf16((max x - m) / 15),  c = clamp(rint((x - m) / s), 0, 15).
-// m and s are rounded before the codes are computed, so the codes make up for their rounding;
-// bf16 has fp32's range, so no input of the supported types overflows them.  A row whose s is
-// below 2^-126 (a constant row) has codes 0.
+// m and s are rounded before the codes are computed, so the codes make up for their rounding.
+// Numbers up to 2^126 in size keep max - m and 15 s within fp32; beyond that s, or the value on
+// loading, may be infinite.  A row whose s is below 2^-126 has codes 0 and stands for m: a constant
+// row, and an fp32 row so narrow that m was rounded up past its maximum, whose s is negative.
 //
 // Layout: cache [pages][heads][page][2][D/2] bytes, key then value of a token side by side (at
 // D = 128 one 128-byte line, so attention over scattered positions reads whole lines), two
