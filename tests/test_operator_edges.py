@@ -65,3 +65,15 @@ def test_a_call_is_made_on_its_tensors_device(ds):
         warnings.simplefilter("ignore")     # of reading a fake tensor's address
         with pytest.raises(RuntimeError):
             ds.cache_store(kv, kv, cache, scales, slots, stream=0)
+
+
+def test_binding_of_another_torch(ds, monkeypatch):
+    """A binding built against another torch is built anew, and not loaded."""
+    pytest.importorskip("torch")
+    from top_selection_gb300 import build
+    assert build.up_to_date() and build.binding_matches()
+    monkeypatch.setattr(build, "_torch_version", lambda: "0.1+other", raising=False)
+    assert not build.up_to_date()
+    monkeypatch.setattr(ds, "_binding", None)
+    with pytest.raises(RuntimeError, match="another torch"):
+        ds.route(None, 1)

@@ -406,11 +406,15 @@ def _load_binding():
     with _lock:
         if _binding is None:
             import torch  # noqa: F401  (the binding's own libraries)
+            from . import build
+            missing = ("the tensor binding is missing or was built for another torch: build it with "
+                       "`python -m top_selection_gb300.build`")
+            if not build.binding_matches():
+                raise RuntimeError(missing)
             try:
                 ops = importlib.import_module("._ops", __name__)
             except ImportError as e:
-                raise RuntimeError("the tensor binding is missing or was built for another torch: build it with "
-                                   "`python -m top_selection_gb300.build`") from e
+                raise RuntimeError(missing) from e
             ops.set_error(DSError)
             _binding = ops
     return _binding

@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -16,6 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libds_topk.so")
 BINDING = os.path.join(HERE, "_ops.so")
+BUILT_FOR = os.path.join(HERE, "_ops.built_for")  # the torch and Python that BINDING was built against
 BINDING_SOURCE = os.path.join(CSRC, "ds_torch.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("ds_topk.cu", "ds_route.cu", "ds_verify.cu", "ds_cache.cu",
                                            "ds_attend.cu")]
@@ -47,12 +49,27 @@ def _torch_dir():
     return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
+def _torch_version() -> str:
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return re.search(r"^__version__ *(?::[^=]*)?= *['\"]([^'\"]+)", f.read(), flags=re.M).group(1)
+
+
+def binding_matches() -> bool:
+    """Whether the binding was built against this torch and Python: it uses the C++ interface of one
+    torch release, which another need not keep."""
+    try:
+        with open(BUILT_FOR) as f:
+            return f.read() == f"{_torch_version()} {sys.implementation.cache_tag}"
+    except OSError:
+        return False
+
+
 def _outputs() -> list:
     return [LIB, BINDING] if _torch_dir() else [LIB]
 
 
 def up_to_date() -> bool:
-    if not all(os.path.exists(o) for o in _outputs()):
+    if not all(os.path.exists(o) for o in _outputs()) or (_torch_dir() and not binding_matches()):
         return False
     t = min(os.path.getmtime(o) for o in _outputs())
     return all(os.path.getmtime(d) <= t for d in deps())
@@ -88,7 +105,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             subprocess.run(["g++", "-shared", "-o", BINDING + suffix, binding, "-L" + os.path.join(torch, "lib"),
                             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + HERE,
                             "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"], check=True)
+            if os.path.exists(BUILT_FOR):
+                os.remove(BUILT_FOR)
             os.replace(BINDING + suffix, BINDING)
+            with open(BUILT_FOR + suffix, "w") as f:
+                f.write(f"{_torch_version()} {sys.implementation.cache_tag}")
+            os.replace(BUILT_FOR + suffix, BUILT_FOR)
     return LIB
 
 
