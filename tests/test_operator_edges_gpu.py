@@ -136,6 +136,22 @@ def test_attention_at_the_ends_of_the_range(ds, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [40, 200])
+def test_attention_scores_far_below_zero(ds, dtype, n):
+    """Scores of -1e31 and below, and warps that have no position: the best one wins all the same.
+    The scores' errors, 1e-6 of them, are far below their gaps, so the weights are 0 and 1."""
+    rng = np.random.default_rng(33)
+    k = (1.0 + rng.random((n, 64))).astype(np.float32)
+    v = rng.standard_normal((n, 64)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    q = dev(np.full((1, 1, 4, 64), -1e31, dtype=np.float32) * np.array([1, 2, 3, 4], dtype=np.float32)[:, None], dtype)
+    want = ref.attention(host(q), base.Paged(cache, scales, table), [n])
+    out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    assert np.all(np.abs(host(out) - want[0]) <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -13 * 5)
+    assert np.allclose(host(lse), want[1], rtol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_attention_strides_of_one(ds, dtype):
     """The stride of an extent of 1 is never used, whatever it is."""
     k, v = np.random.default_rng(30).standard_normal((2, 200, 64)).astype(np.float32)

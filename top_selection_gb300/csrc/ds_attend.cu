@@ -61,7 +61,7 @@ constexpr uint32_t kNoEntry = 0xFFFFFFFFu;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNone = -1e30f;                // running maximum of a row that has seen nothing
+constexpr float kNone = -3e38f;                // below any score: running maximum of a row that has seen nothing
 // Weights as f16: p is at most 2^kRaise, and w = p s kTop / r, r a power of two near the largest
 // value scale |s| that the row has seen and never below an eighth of one (a row of values whose
 // minimum bf16 rounds up past its maximum has s < 0).  The largest |w| is 16 * 8 * 256 = 2^15
