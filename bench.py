@@ -104,11 +104,16 @@ def _peak():
         return FALLBACK_HBM_GBS, "fallback"
 
 
+# sources compiled by themselves that hold none of the top-k's kernels
+OTHER_OPERATORS = ("ds_route.cu", "ds_verify.cu", "ds_cache.cu", "ds_attend.cu")
+
+
 def _source_digest() -> str:
+    """Ties a capture of the top-k's kernels to the sources that they are built from."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "top_selection_gb300", "csrc")
     for name in sorted(os.listdir(csrc)):
-        if name.endswith((".cu", ".cuh")):
+        if name.endswith((".cu", ".cuh")) and name not in OTHER_OPERATORS:
             with open(os.path.join(csrc, name), "rb") as f:
                 h.update(name.encode())
                 h.update(f.read())

@@ -77,3 +77,26 @@ def test_binding_of_another_torch(ds, monkeypatch):
     monkeypatch.setattr(ds, "_binding", None)
     with pytest.raises(RuntimeError, match="another torch"):
         ds.route(None, 1)
+
+
+def test_captures_of_the_topk_outlive_the_other_operators(tmp_path, monkeypatch):
+    """An edit of another operator's source, which includes none of the top-k's kernels, leaves the
+    digest of its captures as it is; an edit of a shared header does not."""
+    import os
+    import bench
+    csrc = os.path.join(os.path.dirname(os.path.abspath(bench.__file__)), "top_selection_gb300", "csrc")
+    kernels = ("ds_split.cuh", "ds_select.cuh")
+    for name in bench.OTHER_OPERATORS:
+        text = open(os.path.join(csrc, name)).read()
+        assert not any(f'#include "{k}"' in text for k in kernels)
+    tree = tmp_path / "top_selection_gb300" / "csrc"
+    tree.mkdir(parents=True)
+    for name in ("ds_topk.cu", "ds_common.cuh", *bench.OTHER_OPERATORS):
+        (tree / name).write_text(name)
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    digest = bench._source_digest()
+    for name in bench.OTHER_OPERATORS:
+        (tree / name).write_text("edited")
+    assert bench._source_digest() == digest
+    (tree / "ds_common.cuh").write_text("edited")
+    assert bench._source_digest() != digest
