@@ -285,7 +285,8 @@ typedef enum { DS_GROUP_MAX = 0, DS_GROUP_TOP2 = 1 } ds_group_score;
  * experts of the topk_groups best runs are eligible.  The k eligible experts of the largest
  * choice values are returned in descending order; every tie, of experts or groups, goes to the
  * lower index, and -0 equals +0.  weight_j = scale * s_j / (renormalise ? sum of the k s : 1);
- * a sum of 0 gives weights of 0.  The bias moves the choice only.
+ * a sum of 0 gives weights of 0.  The bias moves the choice only.  The softmax's sum takes
+ * exponentials that are off by 2^-22 of each; the chosen scores themselves go by expf.
  *   logits, dtype   row r starts at element r * row_stride (any stride >= E)
  *   rows            >= 0
  *   E, k            1 <= k <= min(E / groups * topk_groups, 32); E <= 512, groups <= 32
@@ -320,7 +321,8 @@ ds_status ds_route_backward(const float* grad_weights, const void* logits, int32
  * sequence's last draft, one more token is emitted: argmax_v r_v / noise[b, v], with
  * r = max(p_i - q_i, 0) at a refused draft (p_i if that is 0 everywhere) and r = p_i after the
  * last; ties to the lowest v.  With exponential noise the tokens are distributed as samples
- * of the target.
+ * of the target.  Sums and the race take exponentials that are off by 2^-22 of each (probabilities of
+ * 129280 logits come out within 2.4e-7).
  *   logits, dtype    place i of sequence b starts at element b * seq_stride + i * row_stride;
  *                    -inf excludes a token.  A row of -inf alone: refused, token -1, probability 0
  *   sequences        >= 0; drafts_per_sequence S >= 0 (<= 1024); 1 <= V <= 2^30
@@ -331,7 +333,7 @@ ds_status ds_route_backward(const float* grad_weights, const void* logits, int32
  *   uniforms         [sequences, S] floats in [0, 1)
  *   noise            [sequences, V] positive floats, sequence b at b * noise_stride: independent
  *                    draws of the exponential distribution
- *   temperatures     [sequences] floats, or NULL: `temperature` (>= 0, finite) for all
+ *   temperatures     [sequences] finite floats, or NULL: `temperature` (>= 0, finite) for all
  *   out_tokens       [sequences, S + 1] int32: the accepted drafts, the emitted token, then -1
  *   out_accepted     [sequences] int32: the number of accepted drafts
  *   out_probs        [sequences, S + 1] floats or NULL: p_i of each token, 0 after the last

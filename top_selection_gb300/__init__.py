@@ -12,7 +12,9 @@ returns torch tensors (PyTorch supplies device memory and streams only).
 The operators around the top-k in a decoding step -- ``route``, ``route_backward``,
 ``verify_drafts``, ``cache_store``, ``cache_load``, ``cache_attention`` -- take and return torch
 tensors as well; their checks, outputs and calls run in a compiled binding
-(``csrc/ds_torch.cpp``), since a step makes many small ones.
+(``csrc/ds_torch.cpp``), since a step makes many small ones.  They run on their tensors' device, on
+its current stream or on ``stream`` (a raw handle): then inputs have to be ready there and stay until
+the call's work is done, and outputs come from that stream's memory.
 """
 from __future__ import annotations
 
@@ -430,7 +432,7 @@ def route(logits, k: int, scoring: str = "softmax", bias=None, groups: int = 1, 
     ``scale`` times the scores, divided by their sum over the chosen with ``renormalise``.
     ``counts`` (E,) int32, if given, is added the number of rows that chose each expert.
     Returns (weights (rows, k) float32, experts (rows, k) int32), best first, ties to the lower
-    index."""
+    index.  The weights carry no autograd history: ``route_backward`` gives their gradient."""
     return (_binding or _load_binding()).route(logits, k, _SCORING[scoring], bias, groups, topk_groups,
                                                  _GROUP_SCORE[group_score], renormalise, scale, counts, stream)
 

@@ -22,10 +22,12 @@
 // two tokens are interleaved first), against eleven for conversion by an offset.  The matrix unit
 // keeps fewer bits of subnormal products, far below bf16's rounding; fp32 takes normal numbers.
 //
-// m16n8k16 (mma.sync) rather than tcgen05: a step has 8 to 32 query rows per key head, the
-// operand that streams is the cache, and tcgen05 takes it from shared memory only, so each
-// tile would be expanded to four times its bytes, stored and read back.  Here the cache's
-// bytes are the operand.
+// m16n8k16 (mma.sync) rather than tcgen05: with up to 16 query rows per key head the operand that
+// streams is the cache, and tcgen05 takes it from shared memory only, so each tile would be
+// expanded to twice its bytes or more, stored and read back.  Here the cache's bytes are the
+// operand.  More rows go in groups of 16, each of which reads and masks the cache again: 4 x 1M positions
+// with 16 rows 132 us, with 64 rows 476 (fp32 242 and 912).  There one expansion for all rows would
+// serve tcgen05, which has not been tried.
 //
 // Rows: the query rows that share a key head (heads of a group, and for whole contexts the
 // tokens of the step as well) in tiles of 8; a CTA takes up to 8 * NT of them and one split of
@@ -36,7 +38,8 @@
 //
 // 16 rows are bound by the matrix, ALU and FMA pipes together (4 x 1M positions, 570 MB: 132 us, 4.3
 // TB/s, matrix pipe 48 %), 8 rows nearly by memory (97 us, 5.9 TB/s), short contexts by the chain from
-// lengths over pages and codes to the join (one of 4096 positions, 8 heads: 9.7 us).
+// lengths over pages and codes to the join (one of 4096 positions, 8 heads: 9.8 us).  fp32 queries take
+// twice the matrix instructions, and each sum's additions outside of them (16 rows 242 us, 8 rows 165).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

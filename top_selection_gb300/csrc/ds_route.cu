@@ -31,9 +31,9 @@
 namespace dsk {
 
 constexpr int kRouteWarps = 8;     // rows at a time per CTA
-// The same where choices are counted, and such CTAs on an SM.  With 8 or 16 experts a lane 56 registers
-// leave room for 36 warps in three CTAs (16384 rows of 256 in groups, with gradient: 23.8 us, two of 16
-// warps 25.3; 512 experts 42.2 and 44.8); with fewer, two CTAs have their counts cleared and added
+// The same where choices are counted, and such CTAs on an SM.  With 8 or 16 experts a lane, cut to 56
+// registers, 36 warps find room in three CTAs (16384 rows of 256 in groups, with gradient: 23.8 us, two
+// of 16 warps 25.3; 512 experts, which spill 32 to 44 bytes a thread then, 42.2 and 44.8); with fewer, two CTAs have their counts cleared and added
 // sooner (8190 rows of 60 experts: 7.1 us, three of 12 warps 8.2).
 template <int EPL>
 constexpr int kCountWarps = EPL == 8 || EPL == 16 ? 12 : 16;

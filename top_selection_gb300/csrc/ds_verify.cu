@@ -548,12 +548,12 @@ ds_status ds_verify_drafts(const void* logits, int32_t dtype, int64_t sequences,
     p.accepted = out_accepted;
     p.probs = out_probs;
     // CTAs of a sequence: as many as fit the GPU at once (two to an SM) with slices of at least 2048
-    // numbers.  64 sequences of 129280 logits: 1 CTA each 81 us, 2 54, 4 42, 8 (two waves) 61.
+    // numbers.  64 sequences of 129280 logits: 1 CTA each 78.7 us, 2 51.0, 4 37.4, 8 (two waves) 48.1.
     p.C = 1;
     while (p.C < kVerCluster && sequences * p.C * 2 <= 2 * info.sms && V / (p.C * 2) >= 2048) p.C *= 2;
-    // rows of a round: all where CTAs are few and latency counts (one sequence of 4 drafts, 8 CTAs:
-    // 16.2 us, with one row to a round 21.5); else two, one of which may be read in vain, for one
-    // exchange less (64 sequences: 40.9 us, one 42.0, all 41.8; 200 of 5 short drafts 27.7, 27.8, 34.4)
+    // rows of a round: all where CTAs are few and latency counts (one sequence of 4 drafts, 16 CTAs:
+    // 13.4 us, with one row to a round 21.3); else two, one of which may be read in vain, for one
+    // exchange less (64 sequences: 37.1 us, one 39.0, all 38.0; 200 of 5 short drafts 25.2, 26.0, 33.0)
     p.R = sequences * p.C <= info.sms ? kVerRound : 2;
     if (sequences * p.C > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
     return dtype == DS_BF16 ? launch_verify<__nv_bfloat16>(p, dev, sequences, stream)
