@@ -136,6 +136,33 @@ def test_attention_at_the_ends_of_the_range(ds, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+@pytest.mark.parametrize("n,Q,heads,D", [(4, 5, 4, 64), (20, 6, 1, 64), (32, 5, 2, 128), (33, 5, 4, 64), (34, 8, 1, 64),
+                                         (66, 5, 8, 128), (70, 3, 4, 64), (1000, 6, 4, 64), (5000, 5, 4, 128), (5121, 4, 16, 64)])
+def test_attention_new_tokens_of_unlike_size(ds, dtype, order, n, Q, heads, D):
+    """The step's own tokens have values of very unlike size, each seen by its token and the later
+    ones: every row keeps its bits, relative to the largest value that it sees.  Limits: the operator's
+    (base.check_attention), with that value."""
+    rng = np.random.default_rng(n + Q)
+    k, v = rng.standard_normal((2, n, D)).astype(np.float32)
+    cache, scales, table = rows_to_cache(ds, k, v)
+    sizes = 10.0 ** np.array([3, 9, 1, 20, 14, 25, 30, 28][:Q])
+    sizes = {"up": np.sort(sizes), "down": np.sort(sizes)[::-1], "mixed": sizes}[order]
+    for i in range(min(Q, n)):  # the new tokens, the last one last
+        scales[1:].view(-1, 4)[n - 1 - i, 2:] *= float(sizes[Q - 1 - i])
+    q = dev((1.5 * rng.standard_normal((1, Q, heads, D))).astype(np.float32), dtype)
+    want = ref.attention(host(q), base.Paged(cache, scales, table), [n])
+    out, lse = ds.cache_attention(q, cache, scales, table, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    sc = scales[1:].view(-1, 4)[:n].double().cpu().numpy()
+    most = np.maximum(np.abs(sc[:, 3]), np.abs(15 * sc[:, 2] + sc[:, 3]))
+    for i in range(Q):
+        end = n - (Q - 1 - i)
+        size = most[:end].max() / 5.0 if end > 0 else 1.0
+        base.check_attention((out[:, i:i + 1].double() / size, lse[:, i:i + 1]),
+                             (want[0][:, i:i + 1] / size, want[1][:, i:i + 1]), 5.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n", [40, 200])
 def test_attention_scores_far_below_zero(ds, dtype, n):
     """Scores of -1e31 and below, and warps that have no position: the best one wins all the same.

@@ -61,13 +61,14 @@ constexpr int kAttTile = 32;                   // positions per warp and step
 constexpr int kAttStages = 3;                  // tiles of a warp's ring
 constexpr int kAttCluster = 8;                 // portable cluster size
 constexpr uint32_t kNoEntry = 0xFFFFFFFFu;
+constexpr int kNoPosition = 0x7FFFFFFF;        // of a place without an entry
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3e38f;                // below any score: running maximum of a row that has seen nothing
 // Weights as f16: p is at most 2^kRaise, and w = p s kTop / r, r a power of two near the largest
-// value scale |s| that the row has seen and never below an eighth of one (a row of values whose
-// minimum bf16 rounds up past its maximum has s < 0).  The largest |w| is 16 * 8 * 256 = 2^15
+// value scale |s| seen and never below an eighth of one (a row of values whose minimum bf16 rounds up
+// past its maximum has s < 0).  The largest |w| is 16 * 8 * 256 = 2^15
 // (f16 ends at 2^16), and the heaviest position's is about 2^8, 22 binades above the subnormals.
 constexpr float kRaise = 4.0f, kTop = 256.0f, kOver = 2048.0f;
 
@@ -341,7 +342,8 @@ __device__ __forceinline__ Fitted fitted(const AttendParams& p, int lane) {
 // T: type of q and out.  NQ / NP: f16 parts of q and of the weights.  bf16: one part each (q is
 // exact, a weight keeps 11 bits, and the result's rounding to 8 dominates); fp32: two, 22 bits,
 // and the codes centred, so that sums cancel less.
-template <typename T, int D, int NT, int NQ, int NP, int WARPS>
+// TOKENS: the rows are of several tokens, which see different positions.
+template <typename T, int D, int NT, int NQ, int NP, int WARPS, bool TOKENS>
 __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend_kernel(const AttendParams p) {
     constexpr int KS = D / 16;       // k-steps of the scores, and row tiles of the output
     constexpr int ROWS = 8 * NT;
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
 
     const auto entry_of = [&](int at, int page, int& pos) -> uint32_t {
         const bool seen = at >= 0 && at < end_all && static_cast<uint32_t>(page) < static_cast<uint32_t>(p.pages);
-        pos = seen ? at : 0x7FFFFFFF;
+        pos = seen ? at : kNoPosition;
         return seen ? ((static_cast<uint32_t>(page) * p.heads + h) << p.page_log) + (at & page_mask) : kNoEntry;
     };
     unsigned char* ring = smem + warp * (kAttStages * At::kBytes);
@@ -578,324 +580,324 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
         const int r = rg * ROWS + 8 * j + 2 * t;
         unseen |= (r < p.rows ? 1u : 0u) << (2 * j) | (r + 1 < p.rows ? 2u : 0u) << (2 * j);
     }
-    // kTop / r of each row; 2^100 until a value scale has been seen.  A row's r goes by the positions
-    // that it sees: a later token's scale (an unwritten slot behind a padded draft) may be anything.
-    // Rows differ only once such a scale has come (`unlike`), in a warp's last tiles; till then wmul is
-    // every row's, and what lies in shared memory is not read.
-    float2* wrow = reinterpret_cast<float2*>(smem + WARPS * kAttStages * At::kBytes + KS * 32 * QW * 4) + warp * (ROWS / 2) + t;
-    float wmul = 1.2676506e30f;  // the largest of them
-    bool unlike = false;
+    float wmul = 1.2676506e30f;  // kTop / r; 2^100 until a value scale has been seen
     const float sign = !CENTRE && (g & 1) ? -1.f : 1.f;  // of the weights of this lane's positions
 
-    int slot = 0, here = 0;
-    const unsigned char* tile = ring;
-    // Waits for the next tile and starts the copies of the one two behind it; whether the tile holds
-    // positions that some row does not see.
-    const auto advance = [&]() -> bool {
-        copies_wait<kAttStages - 2>();
-        __syncwarp();
-        {
-            int next = slot + kAttStages - 1;
-            if (next >= kAttStages) next -= kAttStages;
-            const uint32_t entry = entry_of(at_ahead, page_ahead, pos[kAttStages - 1]);
-            issue(next, entry, is_run(entry));
-        }
-        here = pos[0];
-#pragma unroll
-        for (int i = 0; i + 1 < kAttStages; ++i) pos[i] = pos[i + 1];
-        at_ahead = at_far;
-        page_ahead = page_of(at_ahead);
-        at_far = position_at(j0 + (kAttStages + 1) * STRIDE + lane);
-        tile = ring + slot * At::kBytes;
-        if (++slot == kAttStages) slot = 0;
-        return __any_sync(kAll, here >= first_end);
-    };
-    // Works through a tile.  by_rows: the first one with positions that some row does not see, and those
-    // behind it.  The others have a loop of their own, since the row by row code slows theirs (4 x 1M
-    // positions: 133.4 us, in one loop 138.5).
-    bool masks = false;
-    const auto step = [&](auto by_rows_c) {
-        constexpr bool by_rows = by_rows_c.value;
-        // scores of 32 positions: rows of tile i are positions 16 i + {g, g + 8}
-        float s[NT][2][4];
+    int slot = 0;
+    // the least end behind position x, and the last
+    const auto end_past = [&](int x) -> int {
+        int e = kNoPosition;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int c = 0; c < 2; ++c)
+                if (ends[j][c] > x) e = min(e, ends[j][c]);
+        return __reduce_min_sync(kAll, e);
+    };
+    const auto last_end = [&]() -> int {
+        int e = 0;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) s[j][i][c] = 0.f;
-        uint32_t kw[4][D / 32];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 8 * r + g;
-            if constexpr (D == 128) {
-                const uint4 w = *reinterpret_cast<const uint4*>(tile + At::piece(row, t));
-                kw[r][0] = w.x, kw[r][1] = w.y, kw[r][2] = w.z, kw[r][3] = w.w;
-            } else {
-                const uint2 w = *reinterpret_cast<const uint2*>(tile + At::piece(row, t >> 1) + 8 * (t & 1));
-                kw[r][0] = w.x, kw[r][1] = w.y;
+        for (int j = 0; j < NT; ++j) e = max(e, max(ends[j][0], ends[j][1]));
+        return __reduce_max_sync(kAll, e);
+    };
+    // The tiles in turn, in one run as a rule.  TOKENS: a scale that some row does not see (an unwritten slot
+    // behind a padded draft may hold anything) must not set r while that row's weights are rounded.
+    // A tile where it is more than 8 times the largest that the tile's rows all see ends the run: it
+    // is worked through for the positions that they all see, then again for each further one, upwards.  Rows
+    // that do not see it have no weights left then, and what they have summed moves by a power of two
+    // and back.  The state of such turns lies in shared memory, since registers are short: the first
+    // position behind the present one, 0 for an ordinary run, and the end of the split.  (Rows of one token
+    // have a kernel without all this, which takes 2 % of a long context's time, 5 % for fp32.)
+    volatile int* turn = reinterpret_cast<int*>(smem + WARPS * kAttStages * At::kBytes + KS * 32 * QW * 4) + 2 * warp;
+    if (TOKENS && lane == 0) turn[0] = 0;
+    int upto = to;
+    while (true) {
+        for (; j0 < upto; j0 += STRIDE) {
+            copies_wait<kAttStages - 2>();
+            __syncwarp();
+            {
+                int next = slot + kAttStages - 1;
+                if (next >= kAttStages) next -= kAttStages;
+                const uint32_t entry = entry_of(at_ahead, page_ahead, pos[kAttStages - 1]);
+                issue(next, entry, is_run(entry));
             }
-        }
+            int here = pos[0];
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-            const int sh = 8 * (kk & 1);
-            uint32_t qf[QW];
-            if constexpr (QW == 2) {
-                const uint2 w = reinterpret_cast<const uint2*>(sm_q)[kk * 32 + lane];
-                qf[0] = w.x, qf[1] = w.y;
-            } else {
+            for (int i = 0; i + 1 < kAttStages; ++i) pos[i] = pos[i + 1];
+            at_ahead = at_far;
+            page_ahead = page_of(at_ahead);
+            at_far = position_at(j0 + (kAttStages + 1) * STRIDE + lane);
+            const unsigned char* tile = ring + slot * At::kBytes;
+            if (++slot == kAttStages) slot = 0;
+
+            // scores of 32 positions: rows of tile i are positions 16 i + {g, g + 8}
+            float s[NT][2][4];
 #pragma unroll
-                for (int i = 0; i < QW / 4; ++i) {
-                    const uint4 w = reinterpret_cast<const uint4*>(sm_q)[(kk * 32 + lane) * (QW / 4) + i];
-                    qf[4 * i] = w.x, qf[4 * i + 1] = w.y, qf[4 * i + 2] = w.z, qf[4 * i + 3] = w.w;
-                }
-            }
+            for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t w0 = kw[2 * i][kk / 2] >> sh, w1 = kw[2 * i + 1][kk / 2] >> sh;
-                const uint32_t a0 = code_pair<CENTRE>(w0, 0), a1 = code_pair<CENTRE>(w1, 0);
-                const uint32_t a2 = code_pair<CENTRE>(w0, 1), a3 = code_pair<CENTRE>(w1, 1);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float step[4] = {0.f, 0.f, 0.f, 0.f};
-                    float(&sum)[4] = EXACT ? step : s[j][i];
-#pragma unroll
-                    for (int n = NQ - 1; n >= 0; --n)
-                        mma_f16(sum, a0, a1, a2, a3, qf[(j * NQ + n) * 2], qf[(j * NQ + n) * 2 + 1]);
-                    if (EXACT) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) s[j][i][c] += step[c];
-                    }
-                }
-            }
-        }
-        float vs[4], vm[4];
-        int at[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint2 sc = *reinterpret_cast<const uint2*>(tile + At::kScaleAt + (8 * i + g) * 8);
-            const float ks = __uint_as_float(sc.x << 16), km = __uint_as_float(sc.x & 0xFFFF0000u);
-            vs[i] = __uint_as_float(sc.y << 16);
-            vm[i] = fmaf(MID, vs[i], __uint_as_float(sc.y & 0xFFFF0000u));
-            const float2 ks2 = both(ks), base = both(CENTRE ? fmaf(8.f, ks, km) : km);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {  // relative to the running maximum
-                float* x = &s[j][i / 2][2 * (i & 1)];
-                const float2 y = fma2(make_float2(x[0], x[1]), mul2(ks2, fold[j]), fma2(base, qsum[j], neg_m[j]));
-                x[0] = y.x;
-                x[1] = y.y;
-            }
-        }
-        // positions that some row does not see: their scores become -inf and their weights 0.
-        // A scale that is not finite would still make NaN of a weight of 0 (`odd`).
-        bool odd = false;
-        if (by_rows && masks) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                at[i] = __shfl_sync(kAll, here, 8 * i + g);
-                odd |= !(fabsf(vs[i]) < INFINITY && fabsf(vm[i]) < INFINITY);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        if (at[i] >= ends[j][c]) s[j][i / 2][2 * (i & 1) + c] = -INFINITY;
-            }
-            odd = __any_sync(kAll, odd);
-        }
-        // where rows see different positions, their r are raised row by row
-        if (by_rows) {
-            float vtop = 1e-30f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vtop = fmaxf(vtop, fabsf(vs[i]) < INFINITY ? fabsf(vs[i]) : 0.f);
-            const uint32_t vbits = __reduce_max_sync(kAll, __float_as_uint(vtop));
-            if (__uint_as_float(vbits) * wmul > kOver) {
-                const float to_mul = kTop / __uint_as_float(vbits & 0x7F800000u);
-                float most_mul = 0.f, least_mul = INFINITY;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float2 mul = unlike ? wrow[4 * j] : both(wmul), change = both(1.f);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float own = 0.f;  // the largest scale of a position that the row sees
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if ((!masks || at[i] < ends[j][c]) && fabsf(vs[i]) < INFINITY) own = fmaxf(own, fabsf(vs[i]));
-#pragma unroll
-                        for (int d = 4; d <= 16; d <<= 1) own = fmaxf(own, __shfl_xor_sync(kAll, own, d));
-                        float& m = c ? mul.y : mul.x;
-                        const bool none = unseen >> (2 * j + c) & 1u || rg * ROWS + 8 * j + 2 * t + c >= p.rows;
-                        if (own * m > kOver || none) {
-                            // the common one where it is at most 8 times too small, or meets nothing
-                            const float to = own == 0.f || 8.f * own * to_mul >= kTop
-                                                 ? to_mul
-                                                 : kTop / __uint_as_float(__float_as_uint(fmaxf(own, 1e-30f)) & 0x7F800000u);
-                            (c ? change.y : change.x) = to / m;
-                            m = to;
-                        }
-                        most_mul = fmaxf(most_mul, m);
-                        least_mul = fminf(least_mul, m);
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < KS; ++mt) {
-                        o[j][mt][0] *= change.x, o[j][mt][1] *= change.y;
-                        o[j][mt][2] *= change.x, o[j][mt][3] *= change.y;
-                    }
-                    ones[j][0] *= change.x, ones[j][1] *= change.y;
-                    __syncwarp();  // the other lanes have read it
-                    if (g == 0) wrow[4 * j] = mul;
-                }
-                wmul = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_mul)));
-                unlike = __any_sync(kAll, least_mul < wmul);
-                __syncwarp();
-            }
-        }
-        // raise the running maxima where a score passes one by 2^kRaise (or is the first), and
-        // r where a value scale leaves it behind
-        float vw[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vw[i] = vs[i] * wmul * sign;
-        float2 high[NT];
-        float most = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            high[j].x = fmaxf(max3(s[j][0][0], s[j][0][2], s[j][1][0]), s[j][1][2]);
-            high[j].y = fmaxf(max3(s[j][0][1], s[j][0][3], s[j][1][1]), s[j][1][3]);
-            most = max3(most, high[j].x, high[j].y);
-        }
-        if (fresh || __any_sync(kAll, most > kRaise || fmaxf(max3(fabsf(vw[0]), fabsf(vw[1]), fabsf(vw[2])), fabsf(vw[3])) > kOver)) {
-            float vtop = 1e-30f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vtop = fmaxf(vtop, fabsf(vs[i]) < INFINITY ? fabsf(vs[i]) : 0.f);
-            const uint32_t vbits = __reduce_max_sync(kAll, __float_as_uint(vtop));
-            float change = 1.f;
-            if (!by_rows && __uint_as_float(vbits) * wmul > kOver) {  // r = the power of two at or below vtop
-                const float to_mul = kTop / __uint_as_float(vbits & 0x7F800000u);
-                change = to_mul / wmul;
-                wmul = to_mul;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) vw[i] = vs[i] * (wmul * sign);
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                float2 x = high[j];
-#pragma unroll
-                for (int d = 4; d <= 16; d <<= 1) {
-                    x.x = fmaxf(x.x, __shfl_xor_sync(kAll, x.x, d));
-                    x.y = fmaxf(x.y, __shfl_xor_sync(kAll, x.y, d));
-                }
-                // a row's first score sets its maximum, up or down; nothing is summed yet
-                float2 by = make_float2(1.f, 1.f);
-                if (unseen >> (2 * j) & 1u) { if (x.x > -INFINITY) unseen &= ~(1u << (2 * j)); else x.x = 0.f; }
-                else { x.x = fmaxf(x.x, 0.f); by.x = exp2_fast(-x.x); }
-                if (unseen >> (2 * j + 1) & 1u) { if (x.y > -INFINITY) unseen &= ~(2u << (2 * j)); else x.y = 0.f; }
-                else { x.y = fmaxf(x.y, 0.f); by.y = exp2_fast(-x.y); }
-                const float2 down = make_float2(-x.x, -x.y);
-                neg_m[j] = add2(neg_m[j], down);
-                l[j] = mul2(l[j], by);
-                z[j] = mul2(z[j], by);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float* y = &s[j][i / 2][2 * (i & 1)];
-                    y[0] += down.x;
-                    y[1] += down.y;
-                }
-                const float2 all = mul2(by, both(change));
-#pragma unroll
-                for (int mt = 0; mt < KS; ++mt) {
-                    o[j][mt][0] *= all.x, o[j][mt][1] *= all.y;
-                    o[j][mt][2] *= all.x, o[j][mt][3] *= all.y;
-                }
-                ones[j][0] *= all.x, ones[j][1] *= all.y;
-            }
-            fresh = __any_sync(kAll, unseen != 0u);
-        }
-        // weights p, their sums, and w as the second operand
-        uint32_t wf[NT][2][2][NP];  // [row tile][16 positions][first or second 8][part]
-        float2 mul[NT];  // by rows: vs times wmul, of a row that does not see it, could be infinite
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mul[j] = by_rows && unlike ? wrow[4 * j] : both(wmul);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 vw2 = both(by_rows ? vs[i] * sign : vw[i]), vm2 = both(vm[i]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const float* x = &s[j][i / 2][2 * (i & 1)];
-                const float2 e = make_float2(exp2_fast(x[0]), exp2_fast(x[1]));
-                l[j] = add2(l[j], e);
-                float2 w = mul2(by_rows ? mul2(e, mul[j]) : e, vw2), zn = fma2(e, vm2, z[j]);
-                if (by_rows && odd) {
-                    if (at[i] >= ends[j][0]) w.x = 0.f, zn.x = z[j].x;
-                    if (at[i] >= ends[j][1]) w.y = 0.f, zn.y = z[j].y;
-                }
-                z[j] = zn;
-                uint32_t part[NP];
-                split_f16<NP>(w.x, w.y, part);
-#pragma unroll
-                for (int n = 0; n < NP; ++n) wf[j][i / 2][i & 1][n] = transpose8x8(part[n]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            // value words of positions 16 i + {2t, 2t + 1, 2t + 8, 2t + 9}, the lane's eighth
-            uint32_t v[4][D / 64];
+                    for (int c = 0; c < 4; ++c) s[j][i][c] = 0.f;
+            uint32_t kw[4][D / 32];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = 16 * i + 8 * (r >> 1) + 2 * t + (r & 1);
+                const int row = 8 * r + g;
                 if constexpr (D == 128) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(tile + At::piece(row, 4 + (g >> 1)) + 8 * (g & 1));
-                    v[r][0] = w.x, v[r][1] = w.y;
+                    const uint4 w = *reinterpret_cast<const uint4*>(tile + At::piece(row, t));
+                    kw[r][0] = w.x, kw[r][1] = w.y, kw[r][2] = w.z, kw[r][3] = w.w;
                 } else {
-                    v[r][0] = *reinterpret_cast<const uint32_t*>(tile + At::piece(row, 2 + (g >> 2)) + 4 * (g & 3));
-                }
-                if (!CENTRE && (r & 1)) {  // complements at the odd positions
-#pragma unroll
-                    for (int w = 0; w < D / 64; ++w) v[r][w] = ~v[r][w];
+                    const uint2 w = *reinterpret_cast<const uint2*>(tile + At::piece(row, t >> 1) + 8 * (t & 1));
+                    kw[r][0] = w.x, kw[r][1] = w.y;
                 }
             }
 #pragma unroll
-            for (int w = 0; w < D / 64; ++w) {
-                const uint32_t xl = __byte_perm(v[0][w], v[1][w], 0x5410), xh = __byte_perm(v[0][w], v[1][w], 0x7632);
-                const uint32_t yl = __byte_perm(v[2][w], v[3][w], 0x5410), yh = __byte_perm(v[2][w], v[3][w], 0x7632);
+            for (int kk = 0; kk < KS; ++kk) {
+                const int sh = 8 * (kk & 1);
+                uint32_t qf[QW];
+                if constexpr (QW == 2) {
+                    const uint2 w = reinterpret_cast<const uint2*>(sm_q)[kk * 32 + lane];
+                    qf[0] = w.x, qf[1] = w.y;
+                } else {
 #pragma unroll
-                for (int nib = 0; nib < 4; ++nib) {
-                    const int sh = nib >= 2 ? 8 : 0;
-                    const uint32_t a0 = code_pair<CENTRE>(xl >> sh, nib), a1 = code_pair<CENTRE>(xh >> sh, nib);
-                    const uint32_t a2 = code_pair<CENTRE>(yl >> sh, nib), a3 = code_pair<CENTRE>(yh >> sh, nib);
+                    for (int i = 0; i < QW / 4; ++i) {
+                        const uint4 w = reinterpret_cast<const uint4*>(sm_q)[(kk * 32 + lane) * (QW / 4) + i];
+                        qf[4 * i] = w.x, qf[4 * i + 1] = w.y, qf[4 * i + 2] = w.z, qf[4 * i + 3] = w.w;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w0 = kw[2 * i][kk / 2] >> sh, w1 = kw[2 * i + 1][kk / 2] >> sh;
+                    const uint32_t a0 = code_pair<CENTRE>(w0, 0), a1 = code_pair<CENTRE>(w1, 0);
+                    const uint32_t a2 = code_pair<CENTRE>(w0, 1), a3 = code_pair<CENTRE>(w1, 1);
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         float step[4] = {0.f, 0.f, 0.f, 0.f};
-                        float(&sum)[4] = EXACT ? step : o[j][4 * w + nib];
+                        float(&sum)[4] = EXACT ? step : s[j][i];
 #pragma unroll
-                        for (int n = NP - 1; n >= 0; --n)
-                            mma_f16(sum, a0, a1, a2, a3, wf[j][i][0][n], wf[j][i][1][n]);
+                        for (int n = NQ - 1; n >= 0; --n)
+                            mma_f16(sum, a0, a1, a2, a3, qf[(j * NQ + n) * 2], qf[(j * NQ + n) * 2 + 1]);
                         if (EXACT) {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) o[j][4 * w + nib][c] += step[c];
+                            for (int c = 0; c < 4; ++c) s[j][i][c] += step[c];
                         }
                     }
                 }
             }
-            if constexpr (!CENTRE) {  // even minus odd w, against ones
-                constexpr uint32_t ONE = 0x3C003C00u;
+            float vs[4], vm[4];
+            int at[4];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma_f16(ones[j], ONE, ONE, ONE, ONE, wf[j][i][0][0], wf[j][i][1][0]);
+            for (int i = 0; i < 4; ++i) {
+                const uint2 sc = *reinterpret_cast<const uint2*>(tile + At::kScaleAt + (8 * i + g) * 8);
+                const float ks = __uint_as_float(sc.x << 16), km = __uint_as_float(sc.x & 0xFFFF0000u);
+                vs[i] = __uint_as_float(sc.y << 16);
+                vm[i] = fmaf(MID, vs[i], __uint_as_float(sc.y & 0xFFFF0000u));
+                const float2 ks2 = both(ks), base = both(CENTRE ? fmaf(8.f, ks, km) : km);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {  // relative to the running maximum
+                    float* x = &s[j][i / 2][2 * (i & 1)];
+                    const float2 y = fma2(make_float2(x[0], x[1]), mul2(ks2, fold[j]), fma2(base, qsum[j], neg_m[j]));
+                    x[0] = y.x;
+                    x[1] = y.y;
+                }
+            }
+            // positions that some row does not see: their scores become -inf and their weights 0.
+            // A scale that is not finite would still make NaN of a weight of 0 (`odd`).
+            bool odd = false;
+            if (__any_sync(kAll, here >= first_end)) {
+                if constexpr (TOKENS) {
+                    const float v = fabsf(__uint_as_float(reinterpret_cast<const uint2*>(tile + At::kScaleAt)[lane].y << 16));
+                    const uint32_t mine = __float_as_uint(v < INFINITY ? v : 0.f);
+                    const float all = __uint_as_float(__reduce_max_sync(kAll, mine));
+                    if (all * wmul > kOver && all > 8.f * __uint_as_float(__reduce_max_sync(kAll, here < first_end ? mine : 0u))) {
+                        const int e = end_past(__reduce_min_sync(kAll, here));  // of the rows that see something here
+                        if (all > 8.f * __uint_as_float(__reduce_max_sync(kAll, here < e ? mine : 0u))) {
+                            if (lane == 0) {
+                                turn[0] = e;
+                                turn[1] = upto;
+                            }
+                            if (here >= e) here = kNoPosition;
+                            upto = j0 + 1;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    at[i] = __shfl_sync(kAll, here, 8 * i + g);
+                    if (TOKENS && at[i] == kNoPosition) vs[i] = vm[i] = 0.f;  // in another turn
+                    odd |= !(fabsf(vs[i]) < INFINITY && fabsf(vm[i]) < INFINITY);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            if (at[i] >= ends[j][c]) s[j][i / 2][2 * (i & 1) + c] = -INFINITY;
+                }
+                odd = __any_sync(kAll, odd);
+            }
+            // raise the running maxima where a score passes one by 2^kRaise (or is the first), and
+            // r where a value scale leaves it behind
+            float vw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vw[i] = vs[i] * wmul * sign;
+            float2 high[NT];
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                high[j].x = fmaxf(max3(s[j][0][0], s[j][0][2], s[j][1][0]), s[j][1][2]);
+                high[j].y = fmaxf(max3(s[j][0][1], s[j][0][3], s[j][1][1]), s[j][1][3]);
+                most = max3(most, high[j].x, high[j].y);
+            }
+            if (fresh || __any_sync(kAll, most > kRaise || fmaxf(max3(fabsf(vw[0]), fabsf(vw[1]), fabsf(vw[2])), fabsf(vw[3])) > kOver)) {
+                float vtop = 1e-30f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vtop = fmaxf(vtop, fabsf(vs[i]) < INFINITY ? fabsf(vs[i]) : 0.f);
+                const uint32_t vbits = __reduce_max_sync(kAll, __float_as_uint(vtop));
+                float change = 1.f;
+                if (__uint_as_float(vbits) * wmul > kOver) {  // r = the power of two at or below vtop
+                    const float to_mul = kTop / __uint_as_float(vbits & 0x7F800000u);
+                    change = to_mul / wmul;
+                    wmul = to_mul;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vw[i] = vs[i] * (wmul * sign);
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float2 x = high[j];
+#pragma unroll
+                    for (int d = 4; d <= 16; d <<= 1) {
+                        x.x = fmaxf(x.x, __shfl_xor_sync(kAll, x.x, d));
+                        x.y = fmaxf(x.y, __shfl_xor_sync(kAll, x.y, d));
+                    }
+                    // a row's first score sets its maximum, up or down; nothing is summed yet
+                    float2 by = make_float2(1.f, 1.f);
+                    if (unseen >> (2 * j) & 1u) { if (x.x > -INFINITY) unseen &= ~(1u << (2 * j)); else x.x = 0.f; }
+                    else { x.x = fmaxf(x.x, 0.f); by.x = exp2_fast(-x.x); }
+                    if (unseen >> (2 * j + 1) & 1u) { if (x.y > -INFINITY) unseen &= ~(2u << (2 * j)); else x.y = 0.f; }
+                    else { x.y = fmaxf(x.y, 0.f); by.y = exp2_fast(-x.y); }
+                    const float2 down = make_float2(-x.x, -x.y);
+                    neg_m[j] = add2(neg_m[j], down);
+                    l[j] = mul2(l[j], by);
+                    z[j] = mul2(z[j], by);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float* y = &s[j][i / 2][2 * (i & 1)];
+                        y[0] += down.x;
+                        y[1] += down.y;
+                    }
+                    const float2 all = mul2(by, both(change));
+#pragma unroll
+                    for (int mt = 0; mt < KS; ++mt) {
+                        o[j][mt][0] *= all.x, o[j][mt][1] *= all.y;
+                        o[j][mt][2] *= all.x, o[j][mt][3] *= all.y;
+                    }
+                    ones[j][0] *= all.x, ones[j][1] *= all.y;
+                }
+                fresh = __any_sync(kAll, unseen != 0u);
+            }
+            // weights p, their sums, and w as the second operand
+            uint32_t wf[NT][2][2][NP];  // [row tile][16 positions][first or second 8][part]
+            const auto weigh = [&](auto zeros) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 vw2 = both(vw[i]), vm2 = both(vm[i]);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const float* x = &s[j][i / 2][2 * (i & 1)];
+                        const float2 e = make_float2(exp2_fast(x[0]), exp2_fast(x[1]));
+                        l[j] = add2(l[j], e);
+                        float2 w = mul2(e, vw2), zn = fma2(e, vm2, z[j]);
+                        if (zeros.value) {
+                            if (at[i] >= ends[j][0]) w.x = 0.f, zn.x = z[j].x;
+                            if (at[i] >= ends[j][1]) w.y = 0.f, zn.y = z[j].y;
+                        }
+                        z[j] = zn;
+                        uint32_t part[NP];
+                        split_f16<NP>(w.x, w.y, part);
+#pragma unroll
+                        for (int n = 0; n < NP; ++n) wf[j][i / 2][i & 1][n] = transpose8x8(part[n]);
+                    }
+                }
+            };
+            if (!odd) weigh(std::false_type{});
+            else weigh(std::true_type{});
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // value words of positions 16 i + {2t, 2t + 1, 2t + 8, 2t + 9}, the lane's eighth
+                uint32_t v[4][D / 64];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * i + 8 * (r >> 1) + 2 * t + (r & 1);
+                    if constexpr (D == 128) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(tile + At::piece(row, 4 + (g >> 1)) + 8 * (g & 1));
+                        v[r][0] = w.x, v[r][1] = w.y;
+                    } else {
+                        v[r][0] = *reinterpret_cast<const uint32_t*>(tile + At::piece(row, 2 + (g >> 2)) + 4 * (g & 3));
+                    }
+                    if (!CENTRE && (r & 1)) {  // complements at the odd positions
+#pragma unroll
+                        for (int w = 0; w < D / 64; ++w) v[r][w] = ~v[r][w];
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < D / 64; ++w) {
+                    const uint32_t xl = __byte_perm(v[0][w], v[1][w], 0x5410), xh = __byte_perm(v[0][w], v[1][w], 0x7632);
+                    const uint32_t yl = __byte_perm(v[2][w], v[3][w], 0x5410), yh = __byte_perm(v[2][w], v[3][w], 0x7632);
+#pragma unroll
+                    for (int nib = 0; nib < 4; ++nib) {
+                        const int sh = nib >= 2 ? 8 : 0;
+                        const uint32_t a0 = code_pair<CENTRE>(xl >> sh, nib), a1 = code_pair<CENTRE>(xh >> sh, nib);
+                        const uint32_t a2 = code_pair<CENTRE>(yl >> sh, nib), a3 = code_pair<CENTRE>(yh >> sh, nib);
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            float step[4] = {0.f, 0.f, 0.f, 0.f};
+                            float(&sum)[4] = EXACT ? step : o[j][4 * w + nib];
+#pragma unroll
+                            for (int n = NP - 1; n >= 0; --n)
+                                mma_f16(sum, a0, a1, a2, a3, wf[j][i][0][n], wf[j][i][1][n]);
+                            if (EXACT) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) o[j][4 * w + nib][c] += step[c];
+                            }
+                        }
+                    }
+                }
+                if constexpr (!CENTRE) {  // even minus odd w, against ones
+                    constexpr uint32_t ONE = 0x3C003C00u;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) mma_f16(ones[j], ONE, ONE, ONE, ONE, wf[j][i][0][0], wf[j][i][1][0]);
+                }
             }
         }
-    };
-    for (; j0 < to; j0 += STRIDE) {
-        masks = advance();
-        if (masks) break;
-        step(std::false_type{});
-    }
-    while (j0 < to) {
-        step(std::true_type{});
-        j0 += STRIDE;
-        if (j0 < to) masks = advance();
+        if constexpr (!TOKENS) break;
+        __syncwarp();
+        int past = turn[0];
+        if (past == 0) break;
+        // again the tile that was the last, for its next position, or on behind it
+        int begin = past++;
+        j0 -= STRIDE;
+        if (begin >= min(j0 + kAttTile, last_end())) {
+            j0 += STRIDE;
+            begin = past = 0;
+        }
+        upto = past > 0 ? j0 + 1 : turn[1];
+        copies_wait<0>();
+        __syncwarp();
+        if (lane == 0) turn[0] = past;
+#pragma unroll
+        for (int i = 0; i < kAttStages; ++i) ahead[i] = position_at(j0 + i * STRIDE + lane);
+        at_far = position_at(j0 + kAttStages * STRIDE + lane);
+        if (past > 0 && (ahead[0] < begin || ahead[0] >= past)) ahead[0] = -1;
+#pragma unroll
+        for (int i = 0; i < kAttStages; ++i) page[i] = page_of(ahead[i]);
+#pragma unroll
+        for (int i = 0; i + 1 < kAttStages; ++i) {
+            const uint32_t entry = entry_of(ahead[i], page[i], pos[i]);
+            issue(i, entry, is_run(entry));
+        }
+        at_ahead = ahead[kAttStages - 1];
+        page_ahead = page[kAttStages - 1];
+        slot = 0;
     }
     copies_wait<0>();
-    float2 mul[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) mul[j] = unlike ? wrow[4 * j] : both(wmul);
     __syncthreads();  // every warp is done with its ring
 
     // Join the warps: sums over the lanes of a row, then shared memory.  Output fragments stay as the
@@ -904,9 +906,9 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
     constexpr int NF = NT * KS;                          // fragments of a warp
     float4* sm_o = reinterpret_cast<float4*>(smem);      // [warps][NF][32]
     float4* sm_r = sm_o + WARPS * NF * 32;           // [warps][ROWS]: maximum, sum of p, of p (m + MID s)
+    const float back = 1.f / wmul;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const float back[2] = {1.f / mul[j].x, 1.f / mul[j].y};
         float ls[2] = {l[j].x, l[j].y}, zs[2] = {z[j].x, z[j].y};
         const float ms[2] = {unseen >> (2 * j) & 1u ? kNone : -neg_m[j].x, unseen >> (2 * j) & 2u ? kNone : -neg_m[j].y};
 #pragma unroll
@@ -916,14 +918,14 @@ __global__ void __launch_bounds__(WARPS * 32, att_resident(NT, WARPS)) ds_attend
                 ls[c] += __shfl_xor_sync(kAll, ls[c], d);
                 zs[c] += __shfl_xor_sync(kAll, zs[c], d);
             }
-            if (!CENTRE) zs[c] -= 7.5f * ones[j][c] * back[c];
+            if (!CENTRE) zs[c] -= 7.5f * ones[j][c] * back;
             if (g == 0) sm_r[warp * ROWS + 8 * j + 2 * t + c] = make_float4(ms[c], ls[c], zs[c], 0.f);
         }
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
             const float f = mt & 1 ? kUnit * 0.0625f : kUnit;
-            sm_o[(warp * NF + j * KS + mt) * 32 + lane] = make_float4(o[j][mt][0] * f * back[0], o[j][mt][1] * f * back[1],
-                                                                      o[j][mt][2] * f * back[0], o[j][mt][3] * f * back[1]);
+            sm_o[(warp * NF + j * KS + mt) * 32 + lane] = make_float4(o[j][mt][0] * f * back, o[j][mt][1] * f * back,
+                                                                      o[j][mt][2] * f * back, o[j][mt][3] * f * back);
         }
     }
     __syncthreads();
@@ -1089,12 +1091,11 @@ __global__ void __launch_bounds__(1024) ds_attend_join_kernel(const AttendParams
     else emit.one(first, acc[0], top0, sum0, top1, sum1);
 }
 
-template <typename T, int D, int NT, int WARPS>
+template <typename T, int D, int NT, int WARPS, bool TOKENS>
 static ds_status attend(const AttendParams& p, int dev, int sms, int64_t units, cudaStream_t stream) {
     constexpr int PARTS = sizeof(T) == 2 ? 1 : 2;
-    auto kern = ds_attend_kernel<T, D, NT, PARTS, PARTS, WARPS>;
-    const size_t ring = static_cast<size_t>(WARPS) * kAttStages * TileAt<D>::kBytes + D / 16 * 32 * 8 * NT * PARTS +
-                        WARPS * 8 * NT * sizeof(float);
+    auto kern = ds_attend_kernel<T, D, NT, PARTS, PARTS, WARPS, TOKENS>;
+    const size_t ring = static_cast<size_t>(WARPS) * kAttStages * TileAt<D>::kBytes + D / 16 * 32 * 8 * NT * PARTS + WARPS * 8;
     const size_t join = (static_cast<size_t>(WARPS) * (D + 4) + D + 2) * 8 * NT * sizeof(float);  // sm_o, sm_r, sm_j, sm_ml
     const size_t smem = ring > join ? ring : join;
     // the opt-in above 48 KB is a property of the kernel on a device: set once
@@ -1119,11 +1120,16 @@ static ds_status attend(const AttendParams& p, int dev, int sms, int64_t units, 
 
 template <typename T, int D>
 static ds_status attend_rows(const AttendParams& p, int dev, int sms, int nt, int warps, int64_t units, cudaStream_t stream) {
-    if (nt == 1)
-        return warps == 1 ? attend<T, D, 1, 1>(p, dev, sms, units, stream)
-                          : attend<T, D, 1, kAttWarps>(p, dev, sms, units, stream);
-    return warps == 1 ? attend<T, D, 2, 1>(p, dev, sms, units, stream)
-                      : attend<T, D, 2, kAttWarps>(p, dev, sms, units, stream);
+    const auto by = [&](auto tiles, auto size) {
+        constexpr int NT = decltype(tiles)::value, WARPS = decltype(size)::value;
+        return p.Q > 1 && !p.indices ? attend<T, D, NT, WARPS, true>(p, dev, sms, units, stream)
+                                     : attend<T, D, NT, WARPS, false>(p, dev, sms, units, stream);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    using Warps = std::integral_constant<int, kAttWarps>;
+    if (nt == 1) return warps == 1 ? by(One{}, One{}) : by(One{}, Warps{});
+    return warps == 1 ? by(Two{}, One{}) : by(Two{}, Warps{});
 }
 
 // Query rows of a unit: the heads of a group, and for whole contexts the step's tokens as well.
