@@ -26,7 +26,7 @@
 // streams is the cache, and tcgen05 takes it from shared memory only, so each tile would be
 // expanded to twice its bytes or more, stored and read back.  Here the cache's bytes are the
 // operand.  More rows go in groups of 16, each of which reads and masks the cache again: 4 x 1M positions
-// with 16 rows 132 us, with 64 rows 476 (fp32 242 and 912).  There one expansion for all rows would
+// with 16 rows 132 us, with 64 rows 476 (fp32 235 and 883).  There one expansion for all rows would
 // serve tcgen05, which has not been tried.
 //
 // Rows: the query rows that share a key head (heads of a group, and for whole contexts the
@@ -37,9 +37,9 @@
 // over a cluster's or by a second kernel.
 //
 // 16 rows are bound by the matrix, ALU and FMA pipes together (4 x 1M positions, 570 MB: 132 us, 4.3
-// TB/s, matrix pipe 48 %), 8 rows nearly by memory (97 us, 5.9 TB/s), short contexts by the chain from
+// TB/s, matrix pipe 48 %), 8 rows nearly by memory (100 us, 5.7 TB/s), short contexts by the chain from
 // lengths over pages and codes to the join (one of 4096 positions, 8 heads: 9.8 us).  fp32 queries take
-// twice the matrix instructions, and each sum's additions outside of them (16 rows 242 us, 8 rows 165).
+// twice the matrix instructions, and each sum's additions outside of them (16 rows 235 us, 8 rows 164).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
