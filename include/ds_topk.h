@@ -397,8 +397,8 @@ ds_status ds_cache_load(const void* cache, const void* scales, int64_t pages, in
  * over CTAs whose partial results lie in a library-owned workspace of (device, stream), grown with
  * cudaMalloc as ds_topk's is: a call under stream capture that would have to grow it returns
  * DS_ERR_WORKSPACE, and graphs captured on one stream share it, so that they must not run at the same
- * time.  ds_cache_attention_ex takes the caller's workspace instead.  pages * page * heads < 2^32 - 1,
- * table_width * page <= 2^30, K <= 2^30.
+ * time.  ds_cache_attention_ex takes the caller's workspace instead.  pages >= 1, table_width >= 1,
+ * pages * page * heads < 2^32 - 1, table_width * page <= 2^30, K <= 2^30.
  */
 ds_status ds_cache_attention(const void* q, int32_t dtype, int64_t sequences, int32_t tokens, int32_t q_heads,
                              int32_t D, int64_t q_seq_stride, int64_t q_token_stride, int64_t q_head_stride,

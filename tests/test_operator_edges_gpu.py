@@ -163,6 +163,25 @@ def test_attention_new_tokens_of_unlike_size(ds, dtype, order, n, Q, heads, D):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", ["many", "few", "wide"])
+def test_attention_large_numbers_in_batches(ds, dtype, case):
+    """The same in every sequence of a batch: hundreds of short contexts (one warp's work each), a few
+    that are split by their lengths, and 40 rows on a key head."""
+    rng = np.random.default_rng(34)
+    B, Q, heads, group, D, width = {"many": (90, 2, 8, 4, 64, 20), "few": (4, 3, 2, 4, 64, 1024), "wide": (3, 5, 1, 8, 128, 64)}[case]
+    lens = rng.integers(Q, 300, B) if case == "many" else np.array([3000, Q, 7777, 8161])[:B] if case == "few" else np.array([33, 900, 64])
+    cache, scales, table = base.filled(ds, rng, B, heads, D, 16, lens, width=width)
+    q = dev((1.5 * rng.standard_normal((B, Q, heads * group, D))).astype(np.float32), dtype)
+    want = ref.attention(host(q), base.Paged(cache, scales, table), lens)
+    for b in range(B):  # the last token's, seen by itself alone
+        page = int(table[b, (lens[b] - 1) // 16])
+        scales[page, :, (lens[b] - 1) % 16, 2:] = float(10.0 ** rng.uniform(3, 35))
+    out, lse = ds.cache_attention(q, cache, scales, table, dev(lens.astype(np.int32)))
+    seen = slice(0, Q - 1)
+    base.check_attention((out[:, seen], lse[:, seen]), (want[0][:, seen], want[1][:, seen]), 5.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("n", [40, 200])
 def test_attention_scores_far_below_zero(ds, dtype, n):
     """Scores of -1e31 and below, and warps that have no position: the best one wins all the same.
