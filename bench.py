@@ -105,7 +105,8 @@ def _peak():
 
 
 # sources compiled by themselves that hold none of the top-k's kernels
-OTHER_OPERATORS = ("ds_route.cu", "ds_verify.cu", "ds_cache.cu", "ds_attend.cu")
+OTHER_OPERATORS = ("ds_route.cu", "ds_verify.cu", "ds_cache.cu", "ds_attend.cu", "ds_experts.cu", "ds_logprobs.cu",
+                   "ds_quantise.cu", "ds_product.cu", "ds_rows.cuh")
 
 
 def _source_digest() -> str:

@@ -425,6 +425,120 @@ ds_status ds_cache_attention_workspace_bytes(int32_t dtype, int64_t sequences, i
                                              int32_t heads, int32_t page, int64_t table_width, int32_t picked, int32_t K,
                                              size_t* bytes);
 
+/* ======================================================================================
+ * What follows the selections: log probabilities of chosen tokens, the exchange of tokens with
+ * their chosen experts, and the experts' products in 8 bits.  Rules as for the operators above.
+ * ==================================================================================== */
+
+/*
+ * ds_token_logprobs -- per row x of V logits: lse = log sum exp(x), the given token's log
+ * probability x_t - lse, the entropy -sum p log p of p = softmax(x), and the `top` largest
+ * logits' tokens with their log probabilities, in descending order, equal logits by the lower
+ * index (-0 equals +0).
+ *   logits, dtype   row r starts at element r * row_stride (any stride >= V); -inf excludes a
+ *                   token, whose log probability is -inf
+ *   rows            0 .. 2^31 - 1;  1 <= V <= 2^30;  0 <= top <= min(V, 32)
+ *   tokens          [rows] int32; outside [0, V): none is given, log probability 0
+ *   out_logprobs, out_lse, out_entropy   [rows] floats
+ *   out_top_logprobs, out_top_tokens     [rows, top] floats and int32 (unused with top = 0)
+ * A row of -inf alone: lse and log probabilities -inf, entropy 0, its first tokens as the top.  Sums
+ * are fp32, of exponentials off by 2^-22 of each; x is taken relative to the row's largest
+ * before anything is rounded.
+ */
+ds_status ds_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int64_t V, int64_t row_stride,
+                            const int32_t* tokens, int32_t top, float* out_logprobs, float* out_lse, float* out_entropy,
+                            float* out_top_logprobs, int32_t* out_top_tokens, cudaStream_t stream);
+
+/*
+ * ds_token_logprobs_backward -- the gradient of the given tokens' log probabilities and of the
+ * entropies with respect to the logits:
+ *   dx_v = g ([v = t] - p_v) - h p_v (log p_v + entropy),  p = exp(x - lse).
+ *   grad_logprobs g [rows];  grad_entropy h [rows] or NULL (0)
+ *   lse, entropy    as ds_token_logprobs gave them (entropy may be NULL where grad_entropy is)
+ *   grad_logits     rows of V elements of dtype, row r at element r * grad_stride (>= V); every
+ *                   element is written; must not overlap logits
+ * A row without a given token has the entropy's part alone, a row of -inf alone zeros.  The top tokens'
+ * log probabilities have no gradient here.  lse is rounded to fp32, which moves a row's p by 2^-24 |lse|
+ * of themselves.
+ */
+ds_status ds_token_logprobs_backward(const float* grad_logprobs, const void* logits, int32_t dtype, int64_t rows,
+                                     int64_t V, int64_t row_stride, const int32_t* tokens, const float* lse,
+                                     const float* grad_entropy, const float* entropy, void* grad_logits,
+                                     int64_t grad_stride, cudaStream_t stream);
+
+/*
+ * The experts' exchange.  Slot t * k + i is token t's i-th choice (ds_route's experts).
+ *
+ * ds_expert_sort ranks the slots by expert, equal experts by slot:
+ *   experts   [tokens, k] int32; one outside [0, E) is no choice (a padded token's)
+ *   places    [tokens, k] int32: the slot's rank, -1 for no choice
+ *   offsets   [E + 1] int32: the first rank of each expert, then the number of choices
+ * ds_expert_gather writes row t of x to row places[t, i] of out for each i, and zeros to the rows
+ * of out ([tokens * k, D], dtype) behind the last choice.
+ * ds_expert_combine: out[t] = sum_i weights[t, i] * y[places[t, i]], over the places in
+ * [0, rows); sums in fp32, in order of i.  weights NULL: 1 (the gradient of ds_expert_gather).
+ * ds_expert_combine_backward, for the gradient `grad` of out and y [tokens * k, D]:
+ *   grad_y[places[t, i]] = weights[t, i] * grad[t] (rows behind the last choice: zeros),
+ *   grad_weights[t, i] = grad[t] . y[places[t, i]] (0 for no choice); sums in fp32.
+ * tokens >= 0, 1 <= k <= 32, tokens * k < 2^31, E <= 512, D >= 1; x, y and grad take a row stride >= D
+ * in elements, outputs are contiguous and overlap no input.  places and offsets are those of one
+ * ds_expert_sort (places outside the rows are left out whatever they hold).
+ */
+ds_status ds_expert_sort(const int32_t* experts, int64_t tokens, int32_t k, int32_t E, int32_t* places,
+                         int32_t* offsets, cudaStream_t stream);
+ds_status ds_expert_gather(const void* x, int32_t dtype, int64_t tokens, int32_t D, int64_t row_stride,
+                           const int32_t* places, int32_t k, const int32_t* offsets, int32_t E, void* out,
+                           cudaStream_t stream);
+ds_status ds_expert_combine(const void* y, int32_t dtype, int64_t rows, int32_t D, int64_t row_stride,
+                            const int32_t* places, int64_t tokens, int32_t k, const float* weights, void* out,
+                            cudaStream_t stream);
+ds_status ds_expert_combine_backward(const void* grad, int64_t grad_stride, const void* y, int32_t dtype, int32_t D,
+                                     int64_t row_stride, const int32_t* places, int64_t tokens, int32_t k,
+                                     const int32_t* offsets, int32_t E, const float* weights, void* grad_y,
+                                     float* grad_weights, cudaStream_t stream);
+
+/*
+ * The 8-bit form: codes of e4m3 and an fp32 scale for each block of 128 numbers of a row, or of
+ * 128 x 128 numbers of a matrix; blocks at the edges are smaller.  A code c of a block with scale s
+ * stands for c * s.
+ *
+ * ds_quantise_blocks: s is the least power of two >= 2^-126 with max |x| <= 448 s, c = e4m3(x / s),
+ * rounded to nearest, ties to even (x / s is exact).
+ *   x, dtype    row r of matrix m at element m * matrix_stride + r * row_stride, K numbers
+ *   block_rows  1 or 128
+ *   codes       [matrices, rows, K] bytes;  scales [matrices, ceil(rows / block_rows),
+ *               ceil(K / 128)] floats
+ * ds_expert_gather_quantised is ds_expert_gather with rows in that form: codes [tokens * k, D] bytes,
+ * scales [tokens * k, ceil(D / 128)]; rows behind the last choice are the form of zeros.
+ */
+ds_status ds_quantise_blocks(const void* x, int32_t dtype, int64_t matrices, int64_t rows, int32_t K,
+                             int64_t matrix_stride, int64_t row_stride, int32_t block_rows, void* codes, float* scales,
+                             cudaStream_t stream);
+ds_status ds_expert_gather_quantised(const void* x, int32_t dtype, int64_t tokens, int32_t D, int64_t row_stride,
+                                     const int32_t* places, int32_t k, const int32_t* offsets, int32_t E, void* codes,
+                                     float* scales, cudaStream_t stream);
+
+/*
+ * ds_expert_product -- rows sorted by expert times each expert's weights, both in 8 bits:
+ *   out[r, n] = sum_b x_scales[r, b] * w_scales[e, n / 128, b] * sum_{j in block b} x[r, j] w[e, n, j]
+ * for the rows r in [offsets[e], offsets[e + 1]) of each expert e.  Products of codes are exact, a
+ * block's are summed by the tensor cores and the blocks' sums in fp32.  Rows outside
+ * [offsets[0], offsets[E]) are zeros.
+ *   x           [rows, K] e4m3 codes, row r at byte r * x_stride;  x_scales [rows, ceil(K / 128)]
+ *   w           [E, N, K] e4m3 codes, row n of expert e at byte e * w_matrix_stride + n *
+ *               w_row_stride;  w_scales [E, ceil(N / 128), ceil(K / 128)], any fp32 scales
+ *   offsets     [E + 1] int32, ascending, or NULL: one expert (E = 1) has all rows
+ *   dtype, out  [rows, N] bf16 or fp32
+ * K is a multiple of 16, x, w and their strides are 16-byte aligned; 0 <= rows <= 2^30, E <= 512, N and
+ * K <= 2^24.  Scales whose product leaves fp32's range do not give finite numbers.  A wait inside the
+ * kernel that runs out (about a second) is recorded for ds_get_device_status, and the outputs are then
+ * undefined.
+ */
+ds_status ds_expert_product(const void* x, const float* x_scales, int64_t rows, int32_t K, int64_t x_stride,
+                            const void* w, const float* w_scales, int32_t E, int32_t N, int64_t w_row_stride,
+                            int64_t w_matrix_stride, const int32_t* offsets, int32_t dtype, void* out,
+                            cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

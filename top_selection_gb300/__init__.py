@@ -10,8 +10,10 @@ ownership rules and the error codes.  ``topk()`` is a convenience wrapper that t
 returns torch tensors (PyTorch supplies device memory and streams only).
 
 The operators around the top-k in a decoding step -- ``route``, ``route_backward``,
-``verify_drafts``, ``cache_store``, ``cache_load``, ``cache_attention`` -- take and return torch
-tensors as well; their checks, outputs and calls run in a compiled binding
+``verify_drafts``, ``cache_store``, ``cache_load``, ``cache_attention`` -- and what follows the
+selections -- ``token_logprobs`` and ``token_logprobs_backward``; ``expert_sort``, ``expert_gather``,
+``expert_combine`` and ``expert_combine_backward``; ``quantise_blocks`` and ``expert_product`` -- take and
+return torch tensors as well; their checks, outputs and calls run in a compiled binding
 (``csrc/ds_torch.cpp``), since a step makes many small ones.  They run on their tensors' device, on
 its current stream or on ``stream`` (a raw handle): then inputs have to be ready there and stay until
 the call's work is done, and outputs come from that stream's memory.
@@ -32,6 +34,10 @@ __all__ = [
     "ds_route", "ds_route_backward", "ds_verify_drafts", "ds_cache_store", "ds_cache_load", "ds_cache_attention",
     "ds_cache_attention_ex", "ds_cache_attention_workspace_bytes",
     "route", "route_backward", "verify_drafts", "cache_store", "cache_load", "cache_attention",
+    "ds_token_logprobs", "ds_token_logprobs_backward", "ds_expert_sort", "ds_expert_gather", "ds_expert_combine",
+    "ds_expert_combine_backward", "ds_quantise_blocks", "ds_expert_gather_quantised", "ds_expert_product",
+    "token_logprobs", "token_logprobs_backward", "expert_sort", "expert_gather", "expert_combine",
+    "expert_combine_backward", "quantise_blocks", "expert_product",
 ]
 
 DS_BF16 = 0
@@ -144,6 +150,24 @@ def load():
         lib.ds_cache_attention_workspace_bytes.argtypes = [i32, i64, i32, i32, i32, i32, i32, i64, i32, i32,
                                                            ctypes.POINTER(ctypes.c_size_t)]
         lib.ds_cache_attention_workspace_bytes.restype = ctypes.c_int
+        lib.ds_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, vp, vp]
+        lib.ds_token_logprobs.restype = ctypes.c_int
+        lib.ds_token_logprobs_backward.argtypes = [vp, vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, i64, vp]
+        lib.ds_token_logprobs_backward.restype = ctypes.c_int
+        lib.ds_expert_sort.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+        lib.ds_expert_sort.restype = ctypes.c_int
+        lib.ds_expert_gather.argtypes = [vp, i32, i64, i32, i64, vp, i32, vp, i32, vp, vp]
+        lib.ds_expert_gather.restype = ctypes.c_int
+        lib.ds_expert_combine.argtypes = [vp, i32, i64, i32, i64, vp, i64, i32, vp, vp, vp]
+        lib.ds_expert_combine.restype = ctypes.c_int
+        lib.ds_expert_combine_backward.argtypes = [vp, i64, vp, i32, i32, i64, vp, i64, i32, vp, i32, vp, vp, vp, vp]
+        lib.ds_expert_combine_backward.restype = ctypes.c_int
+        lib.ds_quantise_blocks.argtypes = [vp, i32, i64, i64, i32, i64, i64, i32, vp, vp, vp]
+        lib.ds_quantise_blocks.restype = ctypes.c_int
+        lib.ds_expert_gather_quantised.argtypes = [vp, i32, i64, i32, i64, vp, i32, vp, i32, vp, vp, vp]
+        lib.ds_expert_gather_quantised.restype = ctypes.c_int
+        lib.ds_expert_product.argtypes = [vp, vp, i64, i32, i64, vp, vp, i32, i32, i64, i64, vp, i32, vp, vp]
+        lib.ds_expert_product.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -389,6 +413,72 @@ def ds_cache_attention_workspace_bytes(dtype, sequences, tokens, q_heads, D, hea
     return int(out.value)
 
 
+def ds_token_logprobs(logits, dtype, rows, V, row_stride, tokens, top, out_logprobs, out_lse, out_entropy,
+                      out_top_logprobs=0, out_top_tokens=0, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_token_logprobs(int(logits) or None, dtype, rows, V, row_stride, int(tokens) or None, top,
+                                    int(out_logprobs) or None, int(out_lse) or None, int(out_entropy) or None,
+                                    int(out_top_logprobs) or None, int(out_top_tokens) or None, int(stream) or None)
+
+
+def ds_token_logprobs_backward(grad_logprobs, logits, dtype, rows, V, row_stride, tokens, lse, grad_entropy, entropy,
+                               grad_logits, grad_stride, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_token_logprobs_backward(int(grad_logprobs) or None, int(logits) or None, dtype, rows, V, row_stride,
+                                             int(tokens) or None, int(lse) or None, int(grad_entropy) or None,
+                                             int(entropy) or None, int(grad_logits) or None, grad_stride,
+                                             int(stream) or None)
+
+
+def ds_expert_sort(experts, tokens, k, E, places, offsets, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_expert_sort(int(experts) or None, tokens, k, E, int(places) or None, int(offsets) or None,
+                                 int(stream) or None)
+
+
+def ds_expert_gather(x, dtype, tokens, D, row_stride, places, k, offsets, E, out, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_expert_gather(int(x) or None, dtype, tokens, D, row_stride, int(places) or None, k,
+                                   int(offsets) or None, E, int(out) or None, int(stream) or None)
+
+
+def ds_expert_combine(y, dtype, rows, D, row_stride, places, tokens, k, weights, out, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_expert_combine(int(y) or None, dtype, rows, D, row_stride, int(places) or None, tokens, k,
+                                    int(weights) or None, int(out) or None, int(stream) or None)
+
+
+def ds_expert_combine_backward(grad, grad_stride, y, dtype, D, row_stride, places, tokens, k, offsets, E, weights,
+                               grad_y, grad_weights, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_expert_combine_backward(int(grad) or None, grad_stride, int(y) or None, dtype, D, row_stride,
+                                             int(places) or None, tokens, k, int(offsets) or None, E,
+                                             int(weights) or None, int(grad_y) or None, int(grad_weights) or None,
+                                             int(stream) or None)
+
+
+def ds_quantise_blocks(x, dtype, matrices, rows, K, matrix_stride, row_stride, block_rows, codes, scales,
+                       stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_quantise_blocks(int(x) or None, dtype, matrices, rows, K, matrix_stride, row_stride, block_rows,
+                                     int(codes) or None, int(scales) or None, int(stream) or None)
+
+
+def ds_expert_gather_quantised(x, dtype, tokens, D, row_stride, places, k, offsets, E, codes, scales, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_expert_gather_quantised(int(x) or None, dtype, tokens, D, row_stride, int(places) or None, k,
+                                             int(offsets) or None, E, int(codes) or None, int(scales) or None,
+                                             int(stream) or None)
+
+
+def ds_expert_product(x, x_scales, rows, K, x_stride, w, w_scales, E, N, w_row_stride, w_matrix_stride, offsets, dtype,
+                      out, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_expert_product(int(x) or None, int(x_scales) or None, rows, K, x_stride, int(w) or None,
+                                    int(w_scales) or None, E, N, w_row_stride, w_matrix_stride, int(offsets) or None,
+                                    dtype, int(out) or None, int(stream) or None)
+
+
 class _Names(dict):
     """Values by name; a name that is none of them is refused."""
 
@@ -484,3 +574,78 @@ def cache_attention(q, cache, scales, table, lens, indices=None, scale=None, str
     is 1 / sqrt(D) by default.  Returns (out (B, Q, query heads, D) in q's dtype, lse (B, Q, query
     heads) float32); a token that sees nothing gives 0 and -inf."""
     return (_binding or _load_binding()).cache_attention(q, cache, scales, table, lens, indices, scale, stream)
+
+
+# --------------------------------------------- behind the selections ----------------
+
+def token_logprobs(logits, tokens, top: int = 0, stream=None):
+    """The log probability of each row's given token under the softmax of ``logits`` (rows, V), with
+    the distribution's entropy and its ``top`` likeliest tokens.
+
+    ``tokens`` (rows,) int32; one outside [0, V) stands for none: 0, without a gradient.  Returns
+    (logprobs (rows,), lse (rows,), entropy (rows,), top_logprobs (rows, top), top_tokens (rows, top)
+    int32), float32, the likeliest first, ties to the lower token; ``top`` is at most 32.  The
+    results carry no autograd history: ``token_logprobs_backward`` gives their gradient."""
+    return (_binding or _load_binding()).token_logprobs(logits, tokens, top, stream)
+
+
+def token_logprobs_backward(grad_logprobs, logits, tokens, lse, grad_entropy=None, entropy=None, stream=None):
+    """The gradient of ``token_logprobs``' log probabilities, and of its entropies with
+    ``grad_entropy`` (rows,) and the ``entropy`` it gave, with respect to its ``logits``: (rows, V) in
+    the logits' dtype.  ``lse`` is the one it gave."""
+    return (_binding or _load_binding()).token_logprobs_backward(grad_logprobs, logits, tokens, lse, grad_entropy, entropy,
+                                                                 stream)
+
+
+def expert_sort(experts, E: int, stream=None):
+    """Ranks the choices ``experts`` (tokens, k) int32 of a gate of ``E`` experts (``route``'s) by
+    expert, equal ones by token and choice; one outside [0, E) is no choice (a padded token).
+
+    Returns (places (tokens, k) int32 -- each choice's rank, -1 for none -- and offsets (E + 1,)
+    int32: each expert's first rank, then the number of choices)."""
+    return (_binding or _load_binding()).expert_sort(experts, E, stream)
+
+
+def expert_gather(x, places, offsets, quantise: bool = False, stream=None):
+    """The rows of ``x`` (tokens, D) in the order of the experts: row ``places[t, i]`` of the result
+    (tokens * k, D) is row t; rows behind the last choice are zeros.  Its gradient is
+    ``expert_combine`` without weights.  With ``quantise`` the rows come in 8 bits, as
+    ``quantise_blocks`` gives them: (codes, scales)."""
+    return (_binding or _load_binding()).expert_gather(x, places, offsets, quantise, stream)
+
+
+def expert_combine(y, places, weights=None, stream=None):
+    """The experts' outputs ``y`` (tokens * k, D) back at their tokens: (tokens, D) sums of
+    ``weights[t, i] * y[places[t, i]]`` (weights (tokens, k) float32, None: 1), in y's dtype.  Its
+    gradient is ``expert_combine_backward``."""
+    return (_binding or _load_binding()).expert_combine(y, places, weights, stream)
+
+
+def expert_combine_backward(grad, y, places, offsets, weights, stream=None):
+    """The gradients of ``expert_combine``'s result with respect to ``y`` and ``weights``, for its
+    gradient ``grad`` (tokens, D): ((tokens * k, D) in y's dtype, zeros behind the last choice, and
+    (tokens, k) float32)."""
+    return (_binding or _load_binding()).expert_combine_backward(grad, y, places, offsets, weights, stream)
+
+
+def quantise_blocks(x, block_rows: int = 1, stream=None):
+    """``x`` (rows, K) or (matrices, rows, K) in 8 bits: (codes float8_e4m3fn of x's shape, scales
+    float32), a scale for each ``block_rows`` (1 or 128) x 128 numbers, the least power of two that
+    brings their largest to 448 or below.  A code stands for code * scale."""
+    return (_binding or _load_binding()).quantise_blocks(x, block_rows, stream)
+
+
+def expert_product(x, x_scales, w, w_scales, offsets=None, dtype=None, stream=None):
+    """Rows sorted by expert times each expert's weights, both in 8 bits.
+
+    ``x`` (rows, K) float8_e4m3fn and ``x_scales`` (rows, ceil(K / 128)) as ``expert_gather`` or
+    ``quantise_blocks`` give them; ``w`` (experts, N, K) float8_e4m3fn with ``w_scales`` (experts,
+    ceil(N / 128), ceil(K / 128)), any float32 scales; ``offsets`` (experts + 1,) int32, ``expert_sort``'s
+    -- None, with w (N, K) or one expert, for all rows.  K is a multiple of 16.  Returns (rows, N) in
+    ``dtype`` (bfloat16, the default, or float32); rows outside the offsets are zeros.  The weights
+    are constants: the gradient with respect to x is the same product of the outputs' gradient with
+    w transposed, whose 128 x 128 blocks' scales are the transposed ones."""
+    ops = _binding or _load_binding()
+    if dtype is not None and str(dtype) not in ("torch.bfloat16", "torch.float32"):
+        raise TypeError(f"dtype: unsupported dtype {dtype}: bfloat16 and float32 only")
+    return ops.expert_product(x, x_scales, w, w_scales, offsets, str(dtype) == "torch.float32", stream)

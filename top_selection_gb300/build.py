@@ -20,7 +20,8 @@ BINDING = os.path.join(HERE, "_ops.so")
 BUILT_FOR = os.path.join(HERE, "_ops.built_for")  # the torch and Python that BINDING was built against
 BINDING_SOURCE = os.path.join(CSRC, "ds_torch.cpp")
 SOURCES = [os.path.join(CSRC, f) for f in ("ds_topk.cu", "ds_route.cu", "ds_verify.cu", "ds_cache.cu",
-                                           "ds_attend.cu")]
+                                           "ds_attend.cu", "ds_experts.cu", "ds_logprobs.cu", "ds_quantise.cu",
+                                           "ds_product.cu")]
 
 
 def deps() -> list:

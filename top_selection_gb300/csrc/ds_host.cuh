@@ -26,6 +26,10 @@ bool dev_info(int dev, DevInfo& out);
 enum WsKind : int { kWsTopk = 0, kWsAttend = 1 };
 ds_status library_workspace(int dev, WsKind kind, size_t bytes, cudaStream_t stream, void** out);
 
+// The current device's status word, for kernels that record a wait that ran out (defined in
+// ds_topk.cu); null on a CUDA error.
+uint32_t* status_word();
+
 // Launches `kern` so that it may begin while the stream's previous kernel ends
 // (programmatic dependent launch): the kernel waits for its predecessor (pdl_wait) before
 // it touches global memory.  `cluster` > 1 sets the thread-block cluster's size.

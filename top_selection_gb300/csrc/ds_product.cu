@@ -1,0 +1,546 @@
+// ds_product.cu -- the experts' products in 8 bits (ds_expert_product): rows sorted by expert times
+// each expert's weights, both e4m3 with an fp32 scale for each block of 128.
+//
+//   out[r, n] = sum_b xs[r, b] ws[e, n / 128, b] sum_{k in block b} x[r, k] w[e, n, k]
+//
+// tcgen05 (kind::f8f6f4, M = 128 rows, N = BN weights' rows, K = 32 an instruction) sums one block of
+// 128 along k from shared memory into tensor memory; the scales of a block differ from row to row, so
+// each block's sums are read back, multiplied by their row's scale and added up in registers in
+// fp32, while the next blocks are being multiplied (512 / BN buffers in tensor memory).
+//
+// Warps 0 to 7 add up and store, warp 8 loads (TMA, 128-byte swizzle), warp 9 issues the products.
+// A tile is up to 128 rows of one expert by BN outputs; CTAs take tiles in turn.  Rows of a
+// tile that lie behind the expert's last are computed from whatever is in shared memory and not
+// stored (no row's sums meet another's); of the rows only 32 at a time as needed are loaded.
+// Few tiles: the CTAs of a cluster split a tile's blocks, and add their sums over distributed shared
+// memory in a fixed order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "ds_common.cuh"
+#include "ds_host.cuh"
+#include "ds_rows.cuh"
+#include "ds_topk.h"
+
+namespace dsk {
+
+constexpr int kProdRows = 128;                   // rows of a tile
+constexpr int kProdBlock = 128;                  // numbers along k of a block, bytes of a swizzled row
+constexpr int kProdSumWarps = 8;
+constexpr int kProdThreads = (kProdSumWarps + 2) * 32;
+constexpr int kProdMaxE = 512;
+constexpr int kProdBox = 32;                     // rows of x to a copy
+constexpr int kProdMaxSplit = 8;
+
+template <int BN>
+struct ProdShape {
+    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int BUFS = 512 / BN;
+    static constexpr int A_BYTES = kProdRows * kProdBlock, B_BYTES = BN * kProdBlock;
+    static constexpr int STAGE = A_BYTES + B_BYTES;
+    static constexpr int COLS = BN / 2;           // a warp's outputs of a row
+    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + 1024;
+};
+
+struct ProdParams {
+    const float* x_scales;
+    const float* w_scales;
+    const int32_t* offsets;
+    void* out;
+    uint32_t* status;
+    int64_t rows;
+    int32_t K, blocks;    // blocks of 128 along k
+    int32_t N, n_blocks;  // blocks of 128 outputs
+    int32_t n_tiles;      // tiles of BN outputs
+    int32_t E;
+    int32_t vec;          // rows of out start on 32 bytes
+};
+
+struct ProdShared {
+    uint64_t full[8], empty[8], sums[8], taken[8];
+    int64_t tiles[kProdMaxE + 1];  // row tiles before each expert's
+    int32_t first[kProdMaxE + 1];  // rows before each expert's
+    int64_t scan[kProdThreads / 32];
+    uint32_t tmem;
+    int failed;
+};
+
+// ---------------------------------------------------------------- PTX ---------------
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t columns) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+// 32 columns of the warp's 32 lanes
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Shared-memory descriptor of a K-major operand in rows of 128 bytes, 128-byte swizzle: groups of 8
+// rows 1024 bytes apart.  Steps along k within the row move the address by their bytes.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t at) {
+    return static_cast<uint64_t>((at >> 4) & 0x3FFFu) | 1ull << 16 | static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 |
+           2ull << 61;
+}
+// e4m3 by e4m3 into fp32, both K-major, M = 128, N = n
+__host__ __device__ constexpr uint32_t instruction_desc(uint32_t n) { return 1u << 4 | (n >> 3) << 17 | (128u >> 4) << 24; }
+
+// Waits for a phase, about a second at most; then (or when another wait of the CTA has run out) false.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed) {
+    for (int i = 0; i < 8; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait_sleep(bar, parity, 1000u)) {
+        if (*failed || clock64() - t0 > kSpinLimit) {
+            *failed = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ unsigned long long pair_of(float a, float b) {
+    return static_cast<unsigned long long>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float pair_get(unsigned long long p, int i) {
+    return __uint_as_float(static_cast<uint32_t>(i ? p >> 32 : p));
+}
+
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// Which tile is number t: expert, first row, rows, first output.  False behind the last.
+struct Tile {
+    int e, rows, n0;
+    int64_t row0;
+};
+template <int BN>
+__device__ __forceinline__ bool tile_at(const ProdShared& sh, const ProdParams& p, int64_t t, Tile& out) {
+    if (t >= sh.tiles[p.E] * p.n_tiles) return false;
+    int lo = 0, hi = p.E;  // the last expert whose tiles start at t or before
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (sh.tiles[mid] * p.n_tiles <= t) lo = mid;
+        else hi = mid;
+    }
+    const int64_t high = sh.tiles[lo + 1] - sh.tiles[lo], at = t - sh.tiles[lo] * p.n_tiles;
+    const int64_t m = at % high;  // tiles that run at once share weights first
+    out.e = lo;
+    out.n0 = static_cast<int>(at / high) * BN;
+    out.row0 = sh.first[lo] + m * kProdRows;
+    const int64_t left = sh.first[lo + 1] - out.row0;
+    out.rows = static_cast<int>(left < kProdRows ? left : kProdRows);
+    return true;
+}
+
+template <typename O>
+__device__ __forceinline__ void put_out(O* p, float v) { row_put(p, v); }
+
+template <int BN, typename O, bool SPLIT>
+__global__ void __launch_bounds__(kProdThreads, 1)
+ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const ProdParams p) {
+    using S = ProdShape<BN>;
+    extern __shared__ uint8_t sh_raw[];
+    __shared__ ProdShared sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t stage0 = (smem_u32(sh_raw) + 1023u) & ~1023u;
+    volatile int* failed = &sh.failed;
+
+    if (tid == 0) {
+        for (int i = 0; i < S::STAGES; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < S::BUFS; ++i) mbar_init(&sh.sums[i], 1), mbar_init(&sh.taken[i], kProdSumWarps);
+        sh.failed = 0;
+        fence_mbar_init();
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
+    }
+    if (warp == kProdSumWarps + 1) tmem_alloc(&sh.tmem, 512);
+    pdl_launch_dependents();
+    pdl_wait();
+    // rows of each expert, ends in ascending order and within the rows whatever the offsets say;
+    // E <= 512: up to two experts to a thread
+    if (p.offsets) {
+        if (tid <= p.E || tid + kProdThreads <= p.E)
+            for (int e = tid; e <= p.E; e += kProdThreads) {
+                const int64_t v = p.offsets[e];
+                sh.first[e] = static_cast<int32_t>(v < 0 ? 0 : v > p.rows ? p.rows : v);
+            }
+    } else if (tid == 0) {
+        sh.first[0] = 0;
+        sh.first[1] = static_cast<int32_t>(p.rows);
+    }
+    __syncthreads();
+    {
+        int64_t mine[2], sum = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = tid * 2 + i;
+            const int n = e < p.E ? sh.first[e + 1] - sh.first[e] : 0;
+            mine[i] = sum;
+            sum += n > 0 ? (n + kProdRows - 1) / kProdRows : 0;
+        }
+        int64_t upto = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        if (lane == 31) sh.scan[warp] = upto;
+        __syncthreads();
+        int64_t before = upto - sum;
+        for (int w = 0; w < warp; ++w) before += sh.scan[w];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (tid * 2 + i < p.E) sh.tiles[tid * 2 + i] = before + mine[i];
+        if (tid == kProdThreads - 1) sh.tiles[p.E] = before + sum;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+
+    uint32_t splits = 1, split = 0;
+    if constexpr (SPLIT) {
+        asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
+        split = cluster_ctarank();
+    }
+    const int per = (p.blocks + static_cast<int>(splits) - 1) / static_cast<int>(splits);
+    const int b0 = min(p.blocks, static_cast<int>(split) * per), b1 = min(p.blocks, b0 + per);
+    // a cluster that splits tiles takes one; else tiles in turn
+    const int64_t tile0 = blockIdx.x / splits, step = SPLIT ? (1LL << 40) : gridDim.x;
+
+    if (warp == kProdSumWarps) {
+        if (lane == 0) {
+            uint32_t n = 0;  // blocks loaded so far
+            Tile t;
+            bool ok = true;
+            for (int64_t i = tile0; ok && tile_at<BN>(sh, p, i, t); i += step) {
+                const int boxes = (t.rows + kProdBox - 1) / kProdBox;
+                for (int b = b0; b < b1; ++b, ++n) {
+                    const uint32_t s = n % S::STAGES;
+                    if (!(ok = wait_phase(&sh.empty[s], (n / S::STAGES + 1) & 1, failed))) break;
+                    const uint32_t a = stage0 + s * S::STAGE;
+                    mbar_arrive_expect_tx(&sh.full[s], boxes * kProdBox * kProdBlock + S::B_BYTES);
+                    tma_load_3d(a + S::A_BYTES, &map_w, b * kProdBlock, t.n0, t.e, &sh.full[s]);
+                    for (int x = 0; x < boxes; ++x)
+                        tma_load_2d(a + x * kProdBox * kProdBlock, &map_x, b * kProdBlock,
+                                    static_cast<int>(t.row0) + x * kProdBox, &sh.full[s]);
+                }
+            }
+            if (!ok)  // copies in flight land before the CTA leaves
+                for (uint32_t j = n > S::STAGES ? n - S::STAGES : 0; j < n; ++j) {
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait_sleep(&sh.full[j % S::STAGES], (j / S::STAGES) & 1, 1000u) && clock64() - t0 < kSpinLimit) {}
+                }
+        }
+        __syncwarp();
+    } else if (warp == kProdSumWarps + 1) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            Tile t;
+            bool ok = true;
+            for (int64_t i = tile0; ok && tile_at<BN>(sh, p, i, t); i += step) {
+                for (int b = b0; b < b1; ++b, ++n) {
+                    const uint32_t s = n % S::STAGES, d = n % S::BUFS;
+                    ok = wait_phase(&sh.taken[d], (n / S::BUFS + 1) & 1, failed) && wait_phase(&sh.full[s], (n / S::STAGES) & 1, failed);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = stage0 + s * S::STAGE;
+                    const uint64_t da = operand_desc(a), db = operand_desc(a + S::A_BYTES);
+#pragma unroll
+                    for (int k = 0; k < kProdBlock / 32; ++k)  // 32 bytes along k: 2 in the descriptors' units
+                        tc_mma_f8(tmem + d * BN, da + 2 * k, db + 2 * k, instruction_desc(BN), k > 0);
+                    tc_commit(&sh.empty[s]);
+                    tc_commit(&sh.sums[d]);
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quarter = warp & 3, side = warp >> 2;
+        uint32_t n = 0;
+        Tile t;
+        bool ok = true;
+        for (int64_t i = tile0; ok && tile_at<BN>(sh, p, i, t); i += step) {
+            const int r = quarter * 32 + lane;             // the thread's row of the tile
+            const bool some = quarter * 32 < t.rows;       // the warp has a row to add up
+            const float* xs = p.x_scales + (t.row0 + (r < t.rows ? r : 0)) * p.blocks;
+            const int nb = min((t.n0 + side * S::COLS) / 128, p.n_blocks - 1);
+            const float* ws = p.w_scales + (static_cast<int64_t>(t.e) * p.n_blocks + nb) * p.blocks;
+            unsigned long long acc[S::COLS / 2];
+#pragma unroll
+            for (int c = 0; c < S::COLS / 2; ++c) acc[c] = 0ull;
+            float f = some && b0 < b1 ? xs[b0] * ws[b0] : 0.f;
+            for (int b = b0; b < b1; ++b, ++n) {
+                const uint32_t d = n % S::BUFS;
+                const float next = some && b + 1 < b1 ? xs[b + 1] * ws[b + 1] : 0.f;
+                ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[d], (n / S::BUFS) & 1, failed));
+                if (!ok) break;
+                tc_fence_after();
+                if (some) {
+                    const unsigned long long ff = pair_of(f, f);
+                    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + d * BN + side * S::COLS;
+#pragma unroll
+                    for (int c = 0; c < S::COLS / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_load32(at + c * 32, v);
+                        tmem_wait_load();
+                        if (c == S::COLS / 32 - 1) {
+                            tc_fence_before();
+                            if (lane == 0) mbar_arrive(&sh.taken[d]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            acc[c * 16 + j] = fma_pair(
+                                static_cast<unsigned long long>(v[2 * j + 1]) << 32 | v[2 * j], ff, acc[c * 16 + j]);
+                    }
+                } else if (lane == 0) {
+                    mbar_arrive(&sh.taken[d]);
+                }
+                f = next;
+            }
+            if (!ok) break;
+            if constexpr (SPLIT) {
+                // sums to the stages' memory (all products have read it), rows 16 bytes apart in their banks
+                if (some) {
+                    const uint32_t at = stage0 + (r * (BN + 4) + side * S::COLS) * 4;
+#pragma unroll
+                    for (int c = 0; c < S::COLS / 4; ++c)
+                        asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + c * 16), "l"(acc[2 * c]), "l"(acc[2 * c + 1])
+                                     : "memory");
+                }
+            } else if (r < t.rows) {
+                const int c0 = t.n0 + side * S::COLS;
+                O* out = static_cast<O*>(p.out) + (t.row0 + r) * p.N + c0;
+                if (p.vec && c0 + S::COLS <= p.N) {
+                    constexpr int W = 32 / static_cast<int>(sizeof(O));  // outputs to a store
+#pragma unroll
+                    for (int c = 0; c < S::COLS / W; ++c) {
+                        uint32_t w[8];
+                        if constexpr (sizeof(O) == 2) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(pair_get(acc[c * 8 + j], 0), pair_get(acc[c * 8 + j], 1));
+                                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(pair_get(acc[c * 4 + j / 2], j & 1));
+                        }
+                        store32(out + c * W, w);
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < S::COLS; ++c)
+                        if (c0 + c < p.N) put_out(out + c, pair_get(acc[c / 2], c & 1));
+                }
+            }
+        }
+        __syncwarp();
+    }
+
+    if constexpr (SPLIT) {
+        cluster_sync_all();
+        Tile t;
+        if (tile_at<BN>(sh, p, tile0, t)) {
+            // the cluster's sums of the tile, four outputs at a time; each CTA takes a share of them
+            const int units = t.rows * (BN / 4), share = (units + static_cast<int>(splits) - 1) / static_cast<int>(splits);
+            const int end = min(units, share * (static_cast<int>(split) + 1));
+            for (int u = share * static_cast<int>(split) + tid; u < end; u += kProdThreads) {
+                const int r = u / (BN / 4), c = u % (BN / 4) * 4;
+                float sum[4] = {};
+                for (uint32_t s = 0; s < splits; ++s) {
+                    uint32_t from;
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(stage0 + (r * (BN + 4) + c) * 4), "r"(s));
+                    const uint4 v = ld_cluster_v4(from);
+                    sum[0] += __uint_as_float(v.x), sum[1] += __uint_as_float(v.y);
+                    sum[2] += __uint_as_float(v.z), sum[3] += __uint_as_float(v.w);
+                }
+                O* out = static_cast<O*>(p.out) + (t.row0 + r) * p.N + t.n0 + c;
+                if (p.vec && t.n0 + c + 4 <= p.N) {
+                    if constexpr (sizeof(O) == 2) {
+                        const __nv_bfloat162 a = __floats2bfloat162_rn(sum[0], sum[1]), b = __floats2bfloat162_rn(sum[2], sum[3]);
+                        *reinterpret_cast<uint2*>(out) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+                    } else {
+                        *reinterpret_cast<float4*>(out) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (t.n0 + c + j < p.N) put_out(out + j, sum[j]);
+                }
+            }
+        }
+        cluster_sync_all();  // no CTA leaves while its sums are read
+    }
+    // rows that belong to no expert: zeros
+    {
+        O* out = static_cast<O*>(p.out);
+        const int64_t head = static_cast<int64_t>(sh.first[0]) * p.N, tail = static_cast<int64_t>(sh.first[p.E]) * p.N;
+        const int64_t all = p.rows * p.N, at = static_cast<int64_t>(blockIdx.x) * kProdThreads + tid;
+        const int64_t stride = static_cast<int64_t>(gridDim.x) * kProdThreads;
+        for (int64_t j = at; j < head; j += stride) put_out(out + j, 0.f);
+        for (int64_t j = tail + at; j < all; j += stride) put_out(out + j, 0.f);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kProdSumWarps + 1) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
+    }
+    if (tid == 0 && sh.failed) atomicOr(p.status, kErrTimeout);
+}
+
+// ---------------------------------------------------------------- host --------------
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's encoder of tensor maps, looked up once for the process.
+static EncodeTiled encoder() {
+    static std::atomic<EncodeTiled> found{nullptr};
+    EncodeTiled f = found.load(std::memory_order_acquire);
+    if (!f) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            return nullptr;
+        f = reinterpret_cast<EncodeTiled>(p);
+        found.store(f, std::memory_order_release);
+    }
+    return f;
+}
+
+// Bytes in rows of K, `box` rows of 128 bytes to a copy, 128-byte swizzle; what lies outside reads as zero.
+static bool byte_map(CUtensorMap& map, const void* base, int dims, int64_t K, int64_t rows, int64_t matrices, int64_t stride,
+                     int64_t matrix_stride, int box) {
+    const EncodeTiled encode = encoder();
+    if (!encode) return false;
+    const cuuint64_t size[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(matrices)};
+    const cuuint64_t pitch[2] = {static_cast<cuuint64_t>(stride), static_cast<cuuint64_t>(matrix_stride)};
+    const cuuint32_t extent[3] = {kProdBlock, static_cast<cuuint32_t>(box), 1}, step[3] = {1, 1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(dims), const_cast<void*>(base), size, pitch,
+                  extent, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN, typename O, bool SPLIT>
+static ds_status launch_product(const CUtensorMap& mx, const CUtensorMap& mw, const ProdParams& p, int64_t ctas, int splits,
+                                cudaStream_t stream) {
+    const auto kern = ds_expert_product_kernel<BN, O, SPLIT>;
+    const size_t smem = ProdShape<BN>::SMEM;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return DS_ERR_CUDA;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kProdThreads, smem, splits, stream, mx, mw, p);
+}
+
+}  // namespace dsk
+
+using namespace dsk;
+
+extern "C" ds_status ds_expert_product(const void* x, const float* x_scales, int64_t rows, int32_t K, int64_t x_stride,
+                                       const void* w, const float* w_scales, int32_t E, int32_t N, int64_t w_row_stride,
+                                       int64_t w_matrix_stride, const int32_t* offsets, int32_t dtype, void* out,
+                                       cudaStream_t stream) {
+    if ((dtype != DS_BF16 && dtype != DS_FP32) || rows < 0 || K < 1 || N < 1 || E < 1 || x_stride < K || w_row_stride < K ||
+        w_matrix_stride < 0 || (!offsets && E != 1))
+        return DS_ERR_INVALID_ARG;
+    if (K % 16 != 0 || E > kProdMaxE || rows > (1LL << 30) || K > (1 << 24) || N > (1 << 24)) return DS_ERR_UNSUPPORTED;
+    if (x_stride >= (1LL << 36) || w_row_stride >= (1LL << 36) || w_matrix_stride >= (1LL << 39)) return DS_ERR_UNSUPPORTED;
+    if (rows == 0) return DS_OK;
+    if (!x || !x_scales || !w || !w_scales || !out) return DS_ERR_INVALID_ARG;
+    const int es = dtype == DS_BF16 ? 2 : 4;
+    const auto off_by = [](const void* q, int bytes) { return reinterpret_cast<uintptr_t>(q) % bytes != 0; };
+    if (!aligned16(x) || !aligned16(w) || x_stride % 16 || w_row_stride % 16 || (E > 1 && w_matrix_stride % 16) ||
+        off_by(x_scales, 4) || off_by(w_scales, 4) || off_by(offsets, 4) || off_by(out, es))
+        return DS_ERR_ALIGNMENT;
+    int dev = 0;
+    DevInfo info;
+    ProdParams p = {};
+    if (cudaGetDevice(&dev) != cudaSuccess || !dev_info(dev, info) || !(p.status = status_word())) return DS_ERR_CUDA;
+    p.x_scales = x_scales;
+    p.w_scales = w_scales;
+    p.offsets = offsets;
+    p.out = out;
+    p.rows = rows;
+    p.K = K;
+    p.blocks = (K + 127) / 128;
+    p.N = N;
+    p.n_blocks = (N + 127) / 128;
+    p.E = E;
+    p.vec = !off_by(out, 32) && static_cast<int64_t>(N) * es % 32 == 0;
+    // 256 outputs to a tile where experts have rows enough that the products bound it; 128 where the
+    // weights' bytes do, so that there are more tiles to share out
+    const bool wide = rows >= 64LL * E && N > 128;
+    const int bn = wide ? 256 : 128;
+    p.n_tiles = (N + bn - 1) / bn;
+    const int64_t tall = rows / kProdRows + (rows < E ? rows : E);  // row tiles at most (one more for each expert's end)
+    const int64_t tiles = tall * p.n_tiles;
+    int splits = 1;
+    if (!wide)
+        while (splits < kProdMaxSplit && tiles * splits * 2 <= info.sms && p.blocks >= splits * 4) splits *= 2;
+    CUtensorMap mx, mw;
+    if (!byte_map(mx, x, 2, K, rows, 1, x_stride, 0, kProdBox) ||
+        !byte_map(mw, w, 3, K, N, E, w_row_stride, E > 1 ? w_matrix_stride : w_row_stride, bn))
+        return DS_ERR_CUDA;
+    const int64_t ctas = splits > 1 ? tiles * splits : tiles < info.sms ? tiles : info.sms;
+    if (wide)
+        return dtype == DS_BF16 ? launch_product<256, __nv_bfloat16, false>(mx, mw, p, ctas, 1, stream)
+                                : launch_product<256, float, false>(mx, mw, p, ctas, 1, stream);
+    if (splits > 1)
+        return dtype == DS_BF16 ? launch_product<128, __nv_bfloat16, true>(mx, mw, p, ctas, splits, stream)
+                                : launch_product<128, float, true>(mx, mw, p, ctas, splits, stream);
+    return dtype == DS_BF16 ? launch_product<128, __nv_bfloat16, false>(mx, mw, p, ctas, 1, stream)
+                            : launch_product<128, float, false>(mx, mw, p, ctas, 1, stream);
+}

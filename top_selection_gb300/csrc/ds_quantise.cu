@@ -1,0 +1,236 @@
+// ds_quantise.cu -- rows and weights in 8 bits with a scale for each block of 128
+// (ds_quantise_blocks), and the experts' gather that gives its rows in that form
+// (ds_expert_gather_quantised).
+//
+// A block of numbers (128 of a row, or 128 x 128 of a matrix) has the scale s, the least power of
+// two that brings its largest number to e4m3's 448 or below, and codes e4m3(x / s).  The division by
+// a power of two is exact, so a code is x / s rounded once: half a step, 2^-4 of the number (or
+// 2^-10 s below 2^-6 s).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ds_common.cuh"
+#include "ds_host.cuh"
+#include "ds_rows.cuh"
+#include "ds_topk.h"
+
+namespace dsk {
+
+constexpr int kQuantThreads = 256;
+constexpr int kQuantMaxE = 512, kQuantMaxK = 32;
+
+struct QuantParams {
+    const void* x;
+    uint8_t* codes;
+    float* scales;
+    int64_t matrices, rows, matrix_stride, stride;  // rows of each matrix
+    int32_t K, blocks;                              // numbers of a row, blocks of 128 in it
+    // the gather: k places of each row, and the rows behind the last place
+    const int32_t* places;
+    const int32_t* offsets;
+    int32_t k, E;
+};
+
+// A lane's 8 numbers of a block of 128, 16 lanes to the block: 8 in a run (VEC), or every 16th one.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_eight(const T* row, int first, int K, int sub, float (&v)[8]) {
+    if constexpr (VEC) {
+        const int at = first + sub * 8;
+        if (at >= K) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        } else if constexpr (sizeof(T) == 2) {
+            unpack16(*reinterpret_cast<const uint4*>(row + at), v);
+        } else {
+            float a[4], b[4];
+            unpack16(reinterpret_cast<const uint4*>(row + at)[0], a);
+            unpack16(reinterpret_cast<const uint4*>(row + at)[1], b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = a[j], v[j + 4] = b[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int at = first + sub + 16 * j;
+            v[j] = at < K ? row_f32(row[at]) : 0.f;
+        }
+    }
+}
+__device__ __forceinline__ float eight_max(const float (&v)[8]) {
+    float m = fabsf(v[0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+    return m;
+}
+__device__ __forceinline__ uint2 eight_codes(const float (&v)[8], float inv) {
+    return make_uint2(e4m3_four(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                      e4m3_four(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+template <bool VEC>
+__device__ __forceinline__ void store_eight(uint8_t* row, int first, int K, int sub, uint2 c) {
+    if constexpr (VEC) {
+        if (first + sub * 8 < K) *reinterpret_cast<uint2*>(row + first + sub * 8) = c;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int at = first + sub + 16 * j;
+            if (at < K) row[at] = static_cast<uint8_t>((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+        }
+    }
+}
+
+// Blocks of one row: 16 lanes to a block, kQuantUnits blocks to a lane, all loaded before the first is used.
+constexpr int kQuantUnits = 4;
+
+template <typename T, bool VEC, bool GATHER>
+__global__ void __launch_bounds__(kQuantThreads) ds_quantise_rows_kernel(const QuantParams p) {
+    const int sub = threadIdx.x & 15;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t total = p.matrices * p.rows * p.blocks;
+    constexpr int UNITS = GATHER ? 1 : kQuantUnits, HALVES = kQuantThreads / 16;
+    const int64_t unit0 = static_cast<int64_t>(blockIdx.x) * (HALVES * UNITS) + threadIdx.x / 16;
+    float v[UNITS][8];
+    int64_t row[UNITS];
+    int block[UNITS];
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+        const int64_t unit = min(unit0 + i * HALVES, total - 1);
+        row[i] = unit / p.blocks;
+        block[i] = static_cast<int>(unit - row[i] * p.blocks);
+        const int64_t m = p.matrices == 1 ? 0 : row[i] / p.rows;
+        const T* src = static_cast<const T*>(p.x) + m * p.matrix_stride + (row[i] - m * p.rows) * p.stride;
+        load_eight<T, VEC>(src, block[i] * 128, p.K, sub, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < UNITS; ++i) {
+        const float s = block_scale(lanes_max<16>(eight_max(v[i])));
+        const uint2 c = eight_codes(v[i], block_inverse(s));
+        if constexpr (!GATHER) {
+            if (unit0 + i * HALVES >= total) continue;  // (the warp stays whole for its shuffles)
+            store_eight<VEC>(p.codes + row[i] * p.K, block[i] * 128, p.K, sub, c);
+            if (sub == 0) p.scales[row[i] * p.blocks + block[i]] = s;
+        } else {
+            if (unit0 >= total) return;
+            const int64_t slots = p.rows * p.k, first = row[i] * p.k;
+            for (int j = 0; j < p.k; ++j) {
+                const int64_t at = p.places[first + j];
+                if (at < 0 || at >= slots) continue;
+                store_eight<VEC>(p.codes + at * p.K, block[i] * 128, p.K, sub, c);
+                if (sub == 0) p.scales[at * p.blocks + block[i]] = s;
+            }
+            const int64_t filled = p.offsets[p.E];
+            for (int64_t at = max(filled, first); at < first + p.k; ++at) {  // a row of zeros
+                store_eight<VEC>(p.codes + at * p.K, block[i] * 128, p.K, sub, make_uint2(0u, 0u));
+                if (sub == 0) p.scales[at * p.blocks + block[i]] = block_scale(0.f);
+            }
+        }
+    }
+}
+
+// Blocks of 128 x 128: a CTA holds one in registers, 16 lanes to a row, 8 rows to a lane.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kQuantThreads) ds_quantise_tiles_kernel(const QuantParams p) {
+    constexpr int HALVES = kQuantThreads / 16, R = 128 / HALVES;
+    __shared__ float sh_max[kQuantThreads / 32];
+    const int sub = threadIdx.x & 15, half = threadIdx.x >> 4;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t tall = (p.rows + 127) / 128;
+    const int64_t strip = blockIdx.x / p.blocks, m = strip / tall;
+    const int block = static_cast<int>(blockIdx.x - strip * p.blocks);
+    const int64_t row0 = (strip - m * tall) * 128;
+    const T* x = static_cast<const T*>(p.x) + m * p.matrix_stride;
+    float v[R][8];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = row0 + half + i * HALVES;
+        if (r < p.rows) load_eight<T, VEC>(x + r * p.stride, block * 128, p.K, sub, v[i]);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) top = fmaxf(top, eight_max(v[i]));
+    top = lanes_max<32>(top);
+    if (threadIdx.x % 32 == 0) sh_max[threadIdx.x / 32] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQuantThreads / 32; ++w) top = fmaxf(top, sh_max[w]);
+    const float s = block_scale(top), inv = block_inverse(s);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t r = row0 + half + i * HALVES;
+        if (r < p.rows) store_eight<VEC>(p.codes + (m * p.rows + r) * p.K, block * 128, p.K, sub, eight_codes(v[i], inv));
+    }
+    if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
+}
+
+// ---------------------------------------------------------------- host --------------
+template <typename T>
+static ds_status launch_quantise(const QuantParams& p, int block_rows, bool vec, bool gather, cudaStream_t stream) {
+    const auto go = [&](auto kern, int64_t ctas) {
+        if (ctas > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
+        return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kQuantThreads, 0, 1, stream, p);
+    };
+    if (block_rows == 128) {
+        const int64_t ctas = p.matrices * ((p.rows + 127) / 128) * p.blocks;
+        return vec ? go(ds_quantise_tiles_kernel<T, true>, ctas) : go(ds_quantise_tiles_kernel<T, false>, ctas);
+    }
+    const int64_t units = p.matrices * p.rows * p.blocks, per = kQuantThreads / 16 * (gather ? 1 : kQuantUnits);
+    const int64_t ctas = (units + per - 1) / per;
+    if (gather) return vec ? go(ds_quantise_rows_kernel<T, true, true>, ctas) : go(ds_quantise_rows_kernel<T, false, true>, ctas);
+    return vec ? go(ds_quantise_rows_kernel<T, true, false>, ctas) : go(ds_quantise_rows_kernel<T, false, false>, ctas);
+}
+
+static bool not_on(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
+
+}  // namespace dsk
+
+using namespace dsk;
+
+extern "C" {
+
+ds_status ds_quantise_blocks(const void* x, int32_t dtype, int64_t matrices, int64_t rows, int32_t K,
+                             int64_t matrix_stride, int64_t row_stride, int32_t block_rows, void* codes, float* scales,
+                             cudaStream_t stream) {
+    if ((dtype != DS_BF16 && dtype != DS_FP32) || matrices < 0 || rows < 0 || K < 1 || row_stride < K || matrix_stride < 0 ||
+        (block_rows != 1 && block_rows != 128))
+        return DS_ERR_INVALID_ARG;
+    const int64_t limit = 1LL << 40;  // numbers in all, and their reach in x
+    if (rows > limit / K || (rows > 0 && matrices > limit / K / rows) || (rows > 0 && row_stride > (limit << 8) / rows) ||
+        (matrices > 0 && matrix_stride > (limit << 8) / matrices))
+        return DS_ERR_UNSUPPORTED;
+    if (matrices == 0 || rows == 0) return DS_OK;
+    if (!x || !codes || !scales) return DS_ERR_INVALID_ARG;
+    const int es = dtype == DS_BF16 ? 2 : 4;
+    if (not_on(x, es) || not_on(scales, 4)) return DS_ERR_ALIGNMENT;
+    QuantParams p = {x, static_cast<uint8_t*>(codes), scales, matrices, rows, matrix_stride, row_stride, K, (K + 127) / 128,
+                     nullptr, nullptr, 0, 0};
+    if (block_rows == 1 && (matrices == 1 || matrix_stride == rows * row_stride)) p.rows = matrices * rows, p.matrices = 1;
+    const bool vec = K % 8 == 0 && aligned16(x) && !not_on(codes, 8) && row_stride * es % 16 == 0 &&
+                     (matrices == 1 || matrix_stride * es % 16 == 0);
+    return dtype == DS_BF16 ? launch_quantise<__nv_bfloat16>(p, block_rows, vec, false, stream)
+                            : launch_quantise<float>(p, block_rows, vec, false, stream);
+}
+
+ds_status ds_expert_gather_quantised(const void* x, int32_t dtype, int64_t tokens, int32_t D, int64_t row_stride,
+                                     const int32_t* places, int32_t k, const int32_t* offsets, int32_t E, void* codes,
+                                     float* scales, cudaStream_t stream) {
+    if ((dtype != DS_BF16 && dtype != DS_FP32) || tokens < 0 || D < 1 || k < 1 || row_stride < D || E < 1)
+        return DS_ERR_INVALID_ARG;
+    if (k > kQuantMaxK || E > kQuantMaxE || tokens > 0x7FFFFFFFLL / k) return DS_ERR_UNSUPPORTED;
+    if (tokens == 0) return DS_OK;
+    if (!x || !places || !offsets || !codes || !scales) return DS_ERR_INVALID_ARG;
+    const int es = dtype == DS_BF16 ? 2 : 4;
+    if (not_on(x, es) || not_on(scales, 4) || not_on(places, 4) || not_on(offsets, 4)) return DS_ERR_ALIGNMENT;
+    const QuantParams p = {x, static_cast<uint8_t*>(codes), scales, 1, tokens, 0, row_stride, D, (D + 127) / 128,
+                           places, offsets, k, E};
+    const bool vec = D % 8 == 0 && aligned16(x) && !not_on(codes, 8) && row_stride * es % 16 == 0;
+    return dtype == DS_BF16 ? launch_quantise<__nv_bfloat16>(p, 1, vec, true, stream)
+                            : launch_quantise<float>(p, 1, vec, true, stream);
+}
+
+}  // extern "C"

@@ -1367,6 +1367,11 @@ ds_status library_workspace(int dev, WsKind kind, size_t bytes, cudaStream_t str
     return DS_OK;
 }
 
+uint32_t* status_word() {
+    void* at = nullptr;
+    return cudaGetSymbolAddress(&at, g_ds_status) == cudaSuccess ? static_cast<uint32_t*>(at) : nullptr;
+}
+
 }  // namespace dsk
 
 using namespace dsk;

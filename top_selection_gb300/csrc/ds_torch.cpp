@@ -357,6 +357,199 @@ PyObject* cache_attention(PyObject*, Args a, Py_ssize_t n) {
     });
 }
 
+PyObject* token_logprobs(PyObject*, Args a, Py_ssize_t n) {
+    return guarded(n, 4, [&]() -> PyObject* {
+        const at::Tensor& x = leading(a[0], "logits", 2);
+        const int32_t code = float_code(x, "logits"), top = integer32(a[2], "top");
+        const int64_t rows = x.size(0), V = x.size(1);
+        const auto index = x.get_device();
+        const Place place(a[3], index);
+        const at::Tensor& tokens = want(a[1], "tokens", {rows}, at::kInt, index);
+        const int64_t width = top > 0 ? top : 0;
+        if (width > V) refuse("top is larger than the number of logits");
+        const at::Tensor logprobs = place.make({rows}, at::kFloat), lse = place.make({rows}, at::kFloat),
+                         entropy = place.make({rows}, at::kFloat), top_logprobs = place.make({rows, width}, at::kFloat),
+                         top_tokens = place.make({rows, width}, at::kInt);
+        check(ds_token_logprobs(x.data_ptr(), code, rows, V, rows > 1 ? x.stride(0) : V, data<int32_t>(tokens), top,
+                                data<float>(logprobs), data<float>(lse), data<float>(entropy), data<float>(top_logprobs),
+                                data<int32_t>(top_tokens), place.stream()), "ds_token_logprobs");
+        return tuple_of({logprobs, lse, entropy, top_logprobs, top_tokens});
+    });
+}
+
+PyObject* token_logprobs_backward(PyObject*, Args a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject* {
+        const at::Tensor& x = leading(a[1], "logits", 2);
+        const int32_t code = float_code(x, "logits");
+        const int64_t rows = x.size(0), V = x.size(1);
+        const auto index = x.get_device();
+        const Place place(a[6], index);
+        const at::Tensor& grad = want(a[0], "grad_logprobs", {rows}, at::kFloat, index);
+        const at::Tensor& tokens = want(a[2], "tokens", {rows}, at::kInt, index);
+        const at::Tensor& lse = want(a[3], "lse", {rows}, at::kFloat, index);
+        const float *grad_entropy = nullptr, *entropy = nullptr;
+        if (a[4] != Py_None) {
+            if (a[5] == Py_None) refuse("grad_entropy needs entropy");
+            grad_entropy = data<float>(want(a[4], "grad_entropy", {rows}, at::kFloat, index));
+        }
+        if (a[5] != Py_None) entropy = data<float>(want(a[5], "entropy", {rows}, at::kFloat, index));
+        const at::Tensor out = place.make({rows, V}, x.scalar_type());
+        check(ds_token_logprobs_backward(data<float>(grad), x.data_ptr(), code, rows, V, rows > 1 ? x.stride(0) : V,
+                                         data<int32_t>(tokens), data<float>(lse), grad_entropy, entropy, out.data_ptr(), V,
+                                         place.stream()), "ds_token_logprobs_backward");
+        return THPVariable_Wrap(out);
+    });
+}
+
+// A token's choices: (tokens, k) int32.
+const at::Tensor& choices(PyObject* o, const char* what) {
+    const at::Tensor& t = leading(o, what, 2);
+    want(o, what, {t.size(0), t.size(1)}, at::kInt, t.get_device());
+    if (t.size(1) > 0x7FFFFFFF) refuse(std::string(what) + " has too many columns");
+    return t;
+}
+// The first row of each expert, and behind the last: (experts + 1,) int32.
+int32_t experts_of(PyObject* o, c10::DeviceIndex index) {
+    const at::Tensor& t = tensor(o, "offsets");
+    const int64_t size = t.dim() > 0 ? t.size(0) : 0;
+    if (size < 2 || size > 0x7FFFFFFF) refuse("offsets must have one number more than there are experts");
+    want(o, "offsets", {size}, at::kInt, index);
+    return static_cast<int32_t>(size - 1);
+}
+int32_t width_of(const at::Tensor& t, const char* what) {
+    if (t.size(-1) > 0x7FFFFFFF) refuse(std::string(what) + " has too many columns");
+    return static_cast<int32_t>(t.size(-1));
+}
+
+PyObject* expert_sort(PyObject*, Args a, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        const at::Tensor& experts = choices(a[0], "experts");
+        const int32_t E = integer32(a[1], "E");
+        const Place place(a[2], experts.get_device());
+        const at::Tensor places = place.make({experts.size(0), experts.size(1)}, at::kInt),
+                         offsets = place.make({(E > 0 ? static_cast<int64_t>(E) : 0) + 1}, at::kInt);
+        check(ds_expert_sort(data<int32_t>(experts), experts.size(0), static_cast<int32_t>(experts.size(1)), E,
+                             data<int32_t>(places), data<int32_t>(offsets), place.stream()), "ds_expert_sort");
+        return tuple_of({places, offsets});
+    });
+}
+
+PyObject* expert_gather(PyObject*, Args a, Py_ssize_t n) {
+    return guarded(n, 5, [&]() -> PyObject* {
+        const at::Tensor& x = leading(a[0], "x", 2);
+        const int32_t code = float_code(x, "x"), D = width_of(x, "x");
+        const int64_t T = x.size(0);
+        const auto index = x.get_device();
+        const Place place(a[4], index);
+        const at::Tensor& places = choices(a[1], "places");
+        const int64_t k = places.size(1);
+        want(a[1], "places", {T, k}, at::kInt, index);
+        const int32_t E = experts_of(a[2], index);
+        const int32_t* offsets = data<int32_t>(tensor(a[2], "offsets"));
+        const int64_t stride = T > 1 ? x.stride(0) : D;
+        if (truth(a[3])) {
+            const at::Tensor codes = place.make({T * k, D}, at::kFloat8_e4m3fn),
+                             scales = place.make({T * k, (static_cast<int64_t>(D) + 127) / 128}, at::kFloat);
+            check(ds_expert_gather_quantised(x.data_ptr(), code, T, D, stride, data<int32_t>(places), static_cast<int32_t>(k),
+                                             offsets, E, codes.data_ptr(), data<float>(scales), place.stream()),
+                  "ds_expert_gather_quantised");
+            return tuple_of({codes, scales});
+        }
+        const at::Tensor out = place.make({T * k, D}, x.scalar_type());
+        check(ds_expert_gather(x.data_ptr(), code, T, D, stride, data<int32_t>(places), static_cast<int32_t>(k), offsets, E,
+                               out.data_ptr(), place.stream()), "ds_expert_gather");
+        return THPVariable_Wrap(out);
+    });
+}
+
+PyObject* expert_combine(PyObject*, Args a, Py_ssize_t n) {
+    return guarded(n, 4, [&]() -> PyObject* {
+        const at::Tensor& y = leading(a[0], "y", 2);
+        const int32_t code = float_code(y, "y"), D = width_of(y, "y");
+        const auto index = y.get_device();
+        const Place place(a[3], index);
+        const at::Tensor& places = choices(a[1], "places");
+        const int64_t T = places.size(0), k = places.size(1);
+        want(a[1], "places", {T, k}, at::kInt, index);
+        const float* weights = a[2] == Py_None ? nullptr : data<float>(want(a[2], "weights", {T, k}, at::kFloat, index));
+        const at::Tensor out = place.make({T, D}, y.scalar_type());
+        check(ds_expert_combine(y.data_ptr(), code, y.size(0), D, y.size(0) > 1 ? y.stride(0) : D, data<int32_t>(places), T,
+                                static_cast<int32_t>(k), weights, out.data_ptr(), place.stream()), "ds_expert_combine");
+        return THPVariable_Wrap(out);
+    });
+}
+
+PyObject* expert_combine_backward(PyObject*, Args a, Py_ssize_t n) {
+    return guarded(n, 6, [&]() -> PyObject* {
+        const at::Tensor& grad = leading(a[0], "grad", 2);
+        const int32_t code = float_code(grad, "grad"), D = width_of(grad, "grad");
+        const int64_t T = grad.size(0);
+        const auto index = grad.get_device();
+        const Place place(a[5], index);
+        const at::Tensor& places = choices(a[2], "places");
+        const int64_t k = places.size(1);
+        want(a[2], "places", {T, k}, at::kInt, index);
+        const at::Tensor& y = want(a[1], "y", {T * k, D}, grad.scalar_type(), index, true);
+        const int32_t E = experts_of(a[3], index);
+        const at::Tensor& weights = want(a[4], "weights", {T, k}, at::kFloat, index);
+        const at::Tensor grad_y = place.make({T * k, D}, grad.scalar_type()), grad_weights = place.make({T, k}, at::kFloat);
+        check(ds_expert_combine_backward(grad.data_ptr(), T > 1 ? grad.stride(0) : D, y.data_ptr(), code, D,
+                                         T * k > 1 ? y.stride(0) : D, data<int32_t>(places), T, static_cast<int32_t>(k),
+                                         data<int32_t>(tensor(a[3], "offsets")), E, data<float>(weights), grad_y.data_ptr(),
+                                         data<float>(grad_weights), place.stream()), "ds_expert_combine_backward");
+        return tuple_of({grad_y, grad_weights});
+    });
+}
+
+PyObject* quantise_blocks(PyObject*, Args a, Py_ssize_t n) {
+    return guarded(n, 3, [&]() -> PyObject* {
+        const at::Tensor& t = tensor(a[0], "x");
+        const bool many = t.dim() == 3;
+        const at::Tensor& x = leading(a[0], "x", many ? 3 : 2);
+        const int32_t code = float_code(x, "x"), K = width_of(x, "x"), block = integer32(a[1], "block_rows");
+        if (block != 1 && block != 128) refuse("block_rows must be 1 or 128");
+        const Place place(a[2], x.get_device());
+        const int64_t E = many ? x.size(0) : 1, N = x.size(-2), n_scales = (N + block - 1) / block,
+                      k_scales = (static_cast<int64_t>(K) + 127) / 128;
+        const int64_t row_stride = N > 1 ? x.stride(-2) : K, matrix_stride = E > 1 ? x.stride(0) : N * row_stride;
+        const at::Tensor codes = many ? place.make({E, N, K}, at::kFloat8_e4m3fn) : place.make({N, K}, at::kFloat8_e4m3fn),
+                         scales = many ? place.make({E, n_scales, k_scales}, at::kFloat) : place.make({n_scales, k_scales}, at::kFloat);
+        check(ds_quantise_blocks(x.data_ptr(), code, E, N, K, matrix_stride, row_stride, block, codes.data_ptr(),
+                                 data<float>(scales), place.stream()), "ds_quantise_blocks");
+        return tuple_of({codes, scales});
+    });
+}
+
+PyObject* expert_product(PyObject*, Args a, Py_ssize_t n) {
+    return guarded(n, 7, [&]() -> PyObject* {
+        const at::Tensor& x = leading(a[0], "x", 2);
+        const int64_t T = x.size(0), blocks = (x.size(1) + 127) / 128;
+        const int32_t K = width_of(x, "x");
+        const auto index = x.get_device();
+        const Place place(a[6], index);
+        want(a[0], "x", {T, K}, at::kFloat8_e4m3fn, index, true);
+        const at::Tensor& xs = want(a[1], "x_scales", {T, blocks}, at::kFloat, index);
+        const bool many = tensor(a[2], "w").dim() == 3;  // one expert's may come as a matrix
+        const at::Tensor& w = leading(a[2], "w", many ? 3 : 2);
+        const int64_t E = many ? w.size(0) : 1, N = w.size(-2), n_blocks = (N + 127) / 128;
+        if (many) want(a[2], "w", {E, N, K}, at::kFloat8_e4m3fn, index, true);
+        else want(a[2], "w", {N, K}, at::kFloat8_e4m3fn, index, true);
+        const at::Tensor& ws = many ? want(a[3], "w_scales", {E, n_blocks, blocks}, at::kFloat, index)
+                                    : want(a[3], "w_scales", {n_blocks, blocks}, at::kFloat, index);
+        if (E > 0x7FFFFFFE || N > 0x7FFFFFFF) refuse("w has too many experts or rows");
+        const int32_t* offsets = nullptr;
+        if (a[4] != Py_None) offsets = data<int32_t>(want(a[4], "offsets", {E + 1}, at::kInt, index));
+        else if (E != 1) refuse("w of several experts needs offsets");
+        const bool wide = truth(a[5]);
+        const at::Tensor out = place.make({T, N}, wide ? at::kFloat : at::kBFloat16);
+        const int64_t w_row = N > 1 ? w.stride(-2) : K;
+        check(ds_expert_product(x.data_ptr(), data<float>(xs), T, K, T > 1 ? x.stride(0) : K, w.data_ptr(), data<float>(ws),
+                                static_cast<int32_t>(E), static_cast<int32_t>(N), w_row, E > 1 ? w.stride(0) : N * w_row,
+                                offsets, wide ? DS_FP32 : DS_BF16, out.data_ptr(), place.stream()), "ds_expert_product");
+        return THPVariable_Wrap(out);
+    });
+}
+
 PyObject* set_error(PyObject*, PyObject* type) {
     Py_INCREF(type);
     Py_XDECREF(g_error);
@@ -366,7 +559,9 @@ PyObject* set_error(PyObject*, PyObject* type) {
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(route), FAST(route_backward), FAST(verify_drafts), FAST(cache_store), FAST(cache_load),
-                         FAST(cache_attention), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+                         FAST(cache_attention), FAST(token_logprobs), FAST(token_logprobs_backward), FAST(expert_sort),
+                         FAST(expert_gather), FAST(expert_combine), FAST(expert_combine_backward), FAST(quantise_blocks),
+                         FAST(expert_product), {"set_error", set_error, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
