@@ -14,6 +14,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "ds_common.cuh"
 #include "ds_host.cuh"
 #include "ds_rows.cuh"
@@ -119,15 +121,80 @@ __global__ void __launch_bounds__(kSortWarps * 32) ds_expert_sort_kernel(const S
 }
 
 // ---------------------------------------------------------------- rows --------------
-// WPR warps to a token's row, 8 warps to a CTA; a thread takes 16 bytes at a time (VEC), or one
-// number where rows do not start on 16 bytes.  Lane i of each warp keeps the token's i-th place.
+// WPR warps to a token's row, 8 warps to a CTA.  A thread takes words of WB bytes, the largest of 16, 4 and
+// 2 that every row starts on, UC of them at a time from each of KC choices.  The choices' rows are
+// looked up once for the whole row (MANY, k > 8: 8 at a time for each stretch of it): with a look-up by
+// shuffles at each word the sums of 4093 x 4 rows of 1001 fp32 numbers took 40 us, issue 90 %.
 constexpr int kRowWarps = 8;
 
-// The place of the lane's choice, -1 for none.
-__device__ __forceinline__ int64_t place_of(const int32_t* places, int64_t token, int k, int lane, int64_t rows) {
+template <int WB>
+struct WordOf;
+template <>
+struct WordOf<16> { using type = uint4; };
+template <>
+struct WordOf<4> { using type = uint32_t; };
+template <>
+struct WordOf<2> { using type = uint16_t; };
+template <int WB>
+using Word = typename WordOf<WB>::type;
+
+template <typename T, int WB>
+constexpr int kNumbers = WB / static_cast<int>(sizeof(T));
+
+template <typename T, int WB>
+__device__ __forceinline__ void numbers(const Word<WB>& q, float (&v)[kNumbers<T, WB>]) {
+    if constexpr (WB == 16) {
+        unpack16(q, v);
+    } else if constexpr (sizeof(T) == 4) {
+        v[0] = __uint_as_float(q);
+    } else {
+        v[0] = __uint_as_float(static_cast<uint32_t>(q) << 16);
+        if constexpr (WB == 4) v[1] = __uint_as_float(q & 0xFFFF0000u);
+    }
+}
+template <typename T, int WB>
+__device__ __forceinline__ Word<WB> word(const float (&v)[kNumbers<T, WB>]) {
+    if constexpr (WB == 16) {
+        return pack16(v);
+    } else if constexpr (sizeof(T) == 4) {
+        return __float_as_uint(v[0]);
+    } else if constexpr (WB == 4) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[0], v[1]);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        return __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+    }
+}
+template <int WB>
+__device__ __forceinline__ Word<WB> zero_word() {
+    if constexpr (WB == 16) return make_uint4(0u, 0u, 0u, 0u);
+    else return 0;
+}
+
+// Lane i's choice of a token: its place, -1 for none.
+__device__ __forceinline__ int place_of(const int32_t* places, int64_t token, int k, int lane, int64_t rows) {
     if (lane >= k) return -1;
-    const int64_t at = places[token * k + lane];
+    const int at = places[token * k + lane];
     return at < rows ? at : -1;
+}
+
+// The rows of choices i0 .. i0 + KC - 1 in a buffer of rows; null for none.
+template <typename T, int KC>
+__device__ __forceinline__ void rows_of(T* base, int64_t stride, int place, int i0, T* (&row)[KC]) {
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+        const int at = __shfl_sync(kEvery, place, (i0 + i) & 31);
+        row[i] = i0 + i < 32 && at >= 0 ? base + at * stride : nullptr;
+    }
+}
+
+// The rows of a buffer behind the last choice, as many as slots are without an expert: zeros.
+template <typename T, int WPR, int WB>
+__device__ __forceinline__ void clear_behind(T* base, int64_t D, int n, int64_t filled, int64_t token, int k) {
+    for (int64_t r = max(filled, token * k); r < (token + 1) * k; ++r) {
+        Word<WB>* dst = reinterpret_cast<Word<WB>*>(base + r * D);
+        for (int c = threadIdx.x % (WPR * 32); c < n; c += WPR * 32) dst[c] = zero_word<WB>();
+    }
 }
 
 struct GatherParams {
@@ -139,43 +206,40 @@ struct GatherParams {
     int32_t D, k, E;
 };
 
-template <typename T, int WPR, bool VEC>
+template <typename T, int WPR, int WB, int KC, bool MANY>
 __global__ void __launch_bounds__(kRowWarps * 32) ds_expert_gather_kernel(const GatherParams p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int STEP = WPR * 32, UC = 4;
+    const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRowWarps / WPR) + warp / WPR;
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRowWarps / WPR) + threadIdx.x / STEP;
     if (token >= p.tokens) return;
-    const int64_t rows = p.tokens * p.k;
-    const int64_t place = place_of(p.places, token, p.k, lane, rows);
+    const int place = place_of(p.places, token, p.k, lane, p.tokens * p.k);
     const int64_t filled = p.offsets[p.E];
-    using Word = typename std::conditional<VEC, uint4, T>::type;
-    const int n = VEC ? p.D / kPer<T> : p.D;
-    const Word* src = reinterpret_cast<const Word*>(static_cast<const T*>(p.x) + token * p.stride);
+    const int n = p.D / kNumbers<T, WB>;
+    const Word<WB>* src = reinterpret_cast<const Word<WB>*>(static_cast<const T*>(p.x) + token * p.stride);
     T* out = static_cast<T*>(p.out);
-    constexpr int STEP = WPR * 32, U = 4;
-    for (int c = (warp % WPR) * 32 + lane; __any_sync(kEvery, c < n); c += STEP * U) {
-        Word v[U];
+    T* row[KC];
+    if (!MANY) rows_of(out, p.D, place, 0, row);
+    for (int c0 = threadIdx.x % STEP - lane; c0 < n; c0 += STEP * UC) {  // the warp's words
+        const int c = c0 + lane;
+        Word<WB> v[UC];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < UC; ++u)
             if (c + u * STEP < n) v[u] = src[c + u * STEP];
-        for (int i = 0; i < p.k; ++i) {
-            const int64_t at = __shfl_sync(kEvery, place, i);
-            if (at < 0) continue;
-            Word* dst = reinterpret_cast<Word*>(out + at * p.D);
+        for (int i0 = 0; i0 < (MANY ? p.k : 1); i0 += KC) {
+            if (MANY) rows_of(out, p.D, place, i0, row);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (c + u * STEP < n) dst[c + u * STEP] = v[u];
+            for (int i = 0; i < KC; ++i) {
+                if (!row[i]) continue;
+                Word<WB>* dst = reinterpret_cast<Word<WB>*>(row[i]) + c;
+#pragma unroll
+                for (int u = 0; u < UC; ++u)
+                    if (c + u * STEP < n) dst[u * STEP] = v[u];
+            }
         }
     }
-    // rows behind the last expert's: zeros, as many as slots are without an expert
-    for (int64_t r = max(filled, token * p.k); r < (token + 1) * p.k; ++r) {
-        Word* dst = reinterpret_cast<Word*>(out + r * p.D);
-        for (int c = (warp % WPR) * 32 + lane; c < n; c += STEP) {
-            if constexpr (VEC) dst[c] = make_uint4(0u, 0u, 0u, 0u);
-            else row_put(dst + c, 0.f);
-        }
-    }
+    clear_behind<T, WPR, WB>(out, p.D, n, filled, token, p.k);
 }
 
 struct CombineParams {
@@ -187,63 +251,53 @@ struct CombineParams {
     int32_t D, k;
 };
 
-template <typename T, int WPR, bool VEC>
+template <typename T, int WPR, int WB, int KC, bool MANY>
 __global__ void __launch_bounds__(kRowWarps * 32) ds_expert_combine_kernel(const CombineParams p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int STEP = WPR * 32, N = kNumbers<T, WB>, UC = WB == 16 ? (KC < 8 ? 2 : 1) : 4;
+    const int lane = threadIdx.x & 31;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRowWarps / WPR) + warp / WPR;
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRowWarps / WPR) + threadIdx.x / STEP;
     if (token >= p.tokens) return;
-    const int64_t place = place_of(p.places, token, p.k, lane, p.rows);
-    float weight = 1.f;
-    if (p.weights && lane < p.k) weight = p.weights[token * p.k + lane];
+    const int place = place_of(p.places, token, p.k, lane, p.rows);
+    const float weight = lane < p.k ? (p.weights ? p.weights[token * p.k + lane] : 1.f) : 0.f;
     const T* y = static_cast<const T*>(p.y);
-    T* out = static_cast<T*>(p.out) + token * p.D;
-    constexpr int STEP = WPR * 32, U = 8, PER = VEC ? kPer<T> : 1;  // U rows at a time
-    const int n = p.D / PER;
-    for (int c = (warp % WPR) * 32 + lane; __any_sync(kEvery, c < n); c += STEP) {
-        const bool in = c < n;
-        float sum[PER] = {};
-        for (int i0 = 0; i0 < p.k; i0 += U) {
-            if constexpr (VEC) {
-                uint4 v[U];
+    Word<WB>* out = reinterpret_cast<Word<WB>*>(static_cast<T*>(p.out) + token * p.D);
+    const int n = p.D / N;
+    const T* row[KC];
+    float w[KC];
+    const auto look_up = [&](int i0) {
+        rows_of(y, p.stride, place, i0, row);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int64_t at = __shfl_sync(kEvery, place, (i0 + u) & 31);
-                    v[u] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in && i0 + u < p.k && at >= 0) v[u] = reinterpret_cast<const uint4*>(y + at * p.stride)[c];
-                }
+        for (int i = 0; i < KC; ++i) w[i] = __shfl_sync(kEvery, weight, (i0 + i) & 31);
+    };
+    if (!MANY) look_up(0);
+    for (int c0 = threadIdx.x % STEP - lane; c0 < n; c0 += STEP * UC) {
+        const int c = c0 + lane;
+        float sum[UC][N] = {};
+        for (int i0 = 0; i0 < (MANY ? p.k : 1); i0 += KC) {
+            if (MANY) look_up(i0);
+            Word<WB> v[KC][UC];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float w = __shfl_sync(kEvery, weight, (i0 + u) & 31);
-                    const int64_t at = __shfl_sync(kEvery, place, (i0 + u) & 31);
-                    if (i0 + u < p.k && at >= 0) {
-                        float f[PER];
-                        unpack16(v[u], f);
+            for (int i = 0; i < KC; ++i)
 #pragma unroll
-                        for (int j = 0; j < PER; ++j) sum[j] = fmaf(w, f[j], sum[j]);
-                    }
-                }
-            } else {
-                float v[U];
+                for (int u = 0; u < UC; ++u)
+                    if (row[i] && c + u * STEP < n) v[i][u] = reinterpret_cast<const Word<WB>*>(row[i])[c + u * STEP];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int64_t at = __shfl_sync(kEvery, place, (i0 + u) & 31);
-                    v[u] = 0.f;
-                    if (in && i0 + u < p.k && at >= 0) v[u] = row_f32(y[at * p.stride + c]);
-                }
+            for (int i = 0; i < KC; ++i) {
+                if (!row[i]) continue;  // what no choice holds has no part, whatever its weight
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float w = __shfl_sync(kEvery, weight, (i0 + u) & 31);
-                    const int64_t at = __shfl_sync(kEvery, place, (i0 + u) & 31);
-                    if (i0 + u < p.k && at >= 0) sum[0] = fmaf(w, v[u], sum[0]);
+                for (int u = 0; u < UC; ++u) {
+                    float f[N];
+                    numbers<T, WB>(v[i][u], f);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) sum[u][j] = fmaf(w[i], f[j], sum[u][j]);
                 }
             }
         }
-        if (in) {
-            if constexpr (VEC) reinterpret_cast<uint4*>(out)[c] = pack16(sum);
-            else row_put(out + c, sum[0]);
-        }
+#pragma unroll
+        for (int u = 0; u < UC; ++u)
+            if (c + u * STEP < n) out[c + u * STEP] = word<T, WB>(sum[u]);
     }
 }
 
@@ -259,92 +313,84 @@ struct CombineBackParams {
     int32_t D, k, E;
 };
 
-// KC: the most choices; a lane sums its part of each choice's product over the whole row, and the
-// lanes' (and warps') parts are added at the end, in a fixed order.
-template <typename T, int WPR, int KC, bool VEC>
+// KC choices at a time over the whole row (with more of them the gradient's row is read again, from L1): a
+// lane sums its part of each choice's product, and the lanes' (and warps') parts are added in a fixed
+// order.
+template <typename T, int WPR, int WB, int KC>
 __global__ void __launch_bounds__(kRowWarps * 32) ds_expert_combine_backward_kernel(const CombineBackParams p) {
+    constexpr int STEP = WPR * 32, N = kNumbers<T, WB>, UC = WB == 16 ? 1 : 4;
     __shared__ float sh_part[kRowWarps][KC];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRowWarps / WPR) + warp / WPR;
-    if (WPR == 1 && token >= p.tokens) return;  // (a whole CTA has one token otherwise)
-    const int64_t rows = p.tokens * p.k;
-    const int64_t place = place_of(p.places, token, p.k, lane, rows);
+    const int64_t token = static_cast<int64_t>(blockIdx.x) * (kRowWarps / WPR) + threadIdx.x / STEP;
+    if (token >= p.tokens) return;  // (never one of a CTA that has a token to itself)
+    const int place = place_of(p.places, token, p.k, lane, p.tokens * p.k);
     const int64_t filled = p.offsets[p.E];
     const float weight = lane < p.k ? p.weights[token * p.k + lane] : 0.f;
-    const T* g = static_cast<const T*>(p.grad) + token * p.grad_stride;
-    const T* y = static_cast<const T*>(p.y);
-    T* gy = static_cast<T*>(p.grad_y);
-    constexpr int STEP = WPR * 32, PER = VEC ? kPer<T> : 1;
-    const int n = p.D / PER;
-    float dot[KC] = {};
-    for (int c = (warp % WPR) * 32 + lane; __any_sync(kEvery, c < n); c += STEP) {
-        const bool in = c < n;
-        float gv[PER];
-        if constexpr (VEC) unpack16(in ? reinterpret_cast<const uint4*>(g)[c] : make_uint4(0u, 0u, 0u, 0u), gv);
-        else gv[0] = in ? row_f32(g[c]) : 0.f;
-        constexpr int U = KC < 8 ? KC : 8;
+    const Word<WB>* g = reinterpret_cast<const Word<WB>*>(static_cast<const T*>(p.grad) + token * p.grad_stride);
+    const int n = p.D / N;
+    for (int i0 = 0; i0 < p.k; i0 += KC) {
+        const T* row[KC];
+        T* out[KC];
+        float w[KC], dot[KC] = {};
+        rows_of(static_cast<const T*>(p.y), p.stride, place, i0, row);
+        rows_of(static_cast<T*>(p.grad_y), static_cast<int64_t>(p.D), place, i0, out);
 #pragma unroll
-        for (int i0 = 0; i0 < KC; i0 += U) {
-            if (i0 >= p.k) break;
-            uint4 v[U];
-            float f[U];
+        for (int i = 0; i < KC; ++i) w[i] = __shfl_sync(kEvery, weight, (i0 + i) & 31);
+        for (int c = threadIdx.x % STEP; c < n; c += STEP * UC) {
+            Word<WB> gw[UC], v[KC][UC];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t at = __shfl_sync(kEvery, place, i0 + u);
-                v[u] = make_uint4(0u, 0u, 0u, 0u), f[u] = 0.f;
-                if (in && at >= 0) {
-                    if constexpr (VEC) v[u] = reinterpret_cast<const uint4*>(y + at * p.stride)[c];
-                    else f[u] = row_f32(y[at * p.stride + c]);
-                }
-            }
+            for (int u = 0; u < UC; ++u)
+                if (c + u * STEP < n) gw[u] = g[c + u * STEP];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t at = __shfl_sync(kEvery, place, i0 + u);
-                const float w = __shfl_sync(kEvery, weight, i0 + u);
-                if (!in || at < 0) continue;
-                if constexpr (VEC) {
-                    float yv[PER], out[PER];
-                    unpack16(v[u], yv);
+            for (int i = 0; i < KC; ++i)
 #pragma unroll
-                    for (int j = 0; j < PER; ++j) {
-                        dot[i0 + u] = fmaf(gv[j], yv[j], dot[i0 + u]);
-                        out[j] = w * gv[j];
+                for (int u = 0; u < UC; ++u)
+                    if (row[i] && c + u * STEP < n) v[i][u] = reinterpret_cast<const Word<WB>*>(row[i])[c + u * STEP];
+#pragma unroll
+            for (int u = 0; u < UC; ++u) {
+                if (c + u * STEP >= n) break;
+                float gv[N];
+                numbers<T, WB>(gw[u], gv);
+#pragma unroll
+                for (int i = 0; i < KC; ++i) {
+                    if (!row[i]) continue;
+                    float yv[N], d[N];
+                    numbers<T, WB>(v[i][u], yv);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        dot[i] = fmaf(gv[j], yv[j], dot[i]);
+                        d[j] = w[i] * gv[j];
                     }
-                    reinterpret_cast<uint4*>(gy + at * p.D)[c] = pack16(out);
-                } else {
-                    dot[i0 + u] = fmaf(gv[0], f[u], dot[i0 + u]);
-                    row_put(gy + at * p.D + c, w * gv[0]);
+                    reinterpret_cast<Word<WB>*>(out[i])[c + u * STEP] = word<T, WB>(d);
                 }
             }
         }
-    }
-    for (int64_t r = max(filled, token * p.k); r < (token + 1) * p.k; ++r)
-        for (int c = (warp % WPR) * 32 + lane; c < n; c += STEP) {
-            if constexpr (VEC) reinterpret_cast<uint4*>(gy + r * p.D)[c] = make_uint4(0u, 0u, 0u, 0u);
-            else row_put(gy + r * p.D + c, 0.f);
-        }
-    float mine = 0.f;
+        float mine = 0.f;
 #pragma unroll
-    for (int i = 0; i < KC; ++i) {
-        const float s = lanes_sum<32>(dot[i]);
-        if (lane == i) mine = s;
+        for (int i = 0; i < KC; ++i) {
+            const float s = lanes_sum<32>(dot[i]);
+            if (lane == i) mine = s;
+        }
+        if (WPR > 1) {
+            if (lane < KC) sh_part[warp][lane] = mine;
+            __syncthreads();
+            mine = 0.f;
+            if (warp == 0 && lane < KC)
+                for (int v = 0; v < WPR; ++v) mine += sh_part[v][lane];
+            __syncthreads();
+        }
+        if ((WPR == 1 || warp == 0) && lane < KC && i0 + lane < p.k) p.grad_weights[token * p.k + i0 + lane] = mine;
     }
-    if (WPR > 1) {
-        if (lane < KC) sh_part[warp][lane] = mine;
-        __syncthreads();
-        if (warp > 0) return;
-        mine = 0.f;
-        if (lane < KC)
-            for (int w = 0; w < WPR; ++w) mine += sh_part[w][lane];
-    }
-    if (lane < p.k) p.grad_weights[token * p.k + lane] = place >= 0 ? mine : 0.f;
+    clear_behind<T, WPR, WB>(static_cast<T*>(p.grad_y), p.D, n, filled, token, p.k);
 }
 
 // ---------------------------------------------------------------- host --------------
-static bool aligned_rows(const void* p, int64_t stride, int64_t D, int es) {
-    return aligned16(p) && stride * es % 16 == 0 && D * es % 16 == 0;
+// The bytes of a word that all rows of a buffer start on and D numbers are a multiple of.
+static int word_bytes(const void* p, int64_t stride, int64_t D, int es) {
+    const uint64_t all = reinterpret_cast<uintptr_t>(p) | static_cast<uint64_t>(stride * es) | static_cast<uint64_t>(D * es);
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
 }
 
 // One warp to a row where tokens are many (fewer sums over lanes), eight where they would leave most of
@@ -360,32 +406,31 @@ static ds_status launch_rows(const P& p, int64_t tokens, int sms, cudaStream_t s
                  : launch_pdl(one, grid, kRowWarps * 32, 0, 1, stream, p);
 }
 
-template <typename T>
-static ds_status launch_gather(const GatherParams& p, bool vec, int sms, cudaStream_t s) {
-    return vec ? launch_rows(p, p.tokens, sms, s, ds_expert_gather_kernel<T, 1, true>, ds_expert_gather_kernel<T, 8, true>)
-               : launch_rows(p, p.tokens, sms, s, ds_expert_gather_kernel<T, 1, false>, ds_expert_gather_kernel<T, 8, false>);
+template <typename T, int WB, int KC, bool MANY>
+static ds_status launch_as(const GatherParams& p, int sms, cudaStream_t s) {
+    return launch_rows(p, p.tokens, sms, s, ds_expert_gather_kernel<T, 1, WB, KC, MANY>, ds_expert_gather_kernel<T, 8, WB, KC, MANY>);
+}
+template <typename T, int WB, int KC, bool MANY>
+static ds_status launch_as(const CombineParams& p, int sms, cudaStream_t s) {
+    return launch_rows(p, p.tokens, sms, s, ds_expert_combine_kernel<T, 1, WB, KC, MANY>, ds_expert_combine_kernel<T, 8, WB, KC, MANY>);
+}
+template <typename T, int WB, int KC, bool MANY>
+static ds_status launch_as(const CombineBackParams& p, int sms, cudaStream_t s) {
+    return launch_rows(p, p.tokens, sms, s, ds_expert_combine_backward_kernel<T, 1, WB, KC>,
+                       ds_expert_combine_backward_kernel<T, 8, WB, KC>);
 }
 
-template <typename T>
-static ds_status launch_combine(const CombineParams& p, bool vec, int sms, cudaStream_t s) {
-    return vec ? launch_rows(p, p.tokens, sms, s, ds_expert_combine_kernel<T, 1, true>, ds_expert_combine_kernel<T, 8, true>)
-               : launch_rows(p, p.tokens, sms, s, ds_expert_combine_kernel<T, 1, false>, ds_expert_combine_kernel<T, 8, false>);
+template <typename T, int WB, typename P>
+static ds_status launch_choices(const P& p, int sms, cudaStream_t s) {
+    if (p.k <= 2) return launch_as<T, WB, 2, false>(p, sms, s);
+    if (p.k <= 4) return launch_as<T, WB, 4, false>(p, sms, s);
+    return p.k <= 8 ? launch_as<T, WB, 8, false>(p, sms, s) : launch_as<T, WB, 8, true>(p, sms, s);
 }
-
-template <typename T, int KC>
-static ds_status launch_combine_backward_as(const CombineBackParams& p, bool vec, int sms, cudaStream_t s) {
-    return vec ? launch_rows(p, p.tokens, sms, s, ds_expert_combine_backward_kernel<T, 1, KC, true>,
-                             ds_expert_combine_backward_kernel<T, 8, KC, true>)
-               : launch_rows(p, p.tokens, sms, s, ds_expert_combine_backward_kernel<T, 1, KC, false>,
-                             ds_expert_combine_backward_kernel<T, 8, KC, false>);
-}
-
-template <typename T>
-static ds_status launch_combine_backward(const CombineBackParams& p, bool vec, int sms, cudaStream_t s) {
-    if (p.k <= 2) return launch_combine_backward_as<T, 2>(p, vec, sms, s);
-    if (p.k <= 4) return launch_combine_backward_as<T, 4>(p, vec, sms, s);
-    if (p.k <= 8) return launch_combine_backward_as<T, 8>(p, vec, sms, s);
-    return launch_combine_backward_as<T, 32>(p, vec, sms, s);
+template <typename P>
+static ds_status launch_exchange(const P& p, int32_t dtype, int bytes, int sms, cudaStream_t s) {
+    if (dtype == DS_FP32) return bytes == 16 ? launch_choices<float, 16>(p, sms, s) : launch_choices<float, 4>(p, sms, s);
+    if (bytes == 16) return launch_choices<__nv_bfloat16, 16>(p, sms, s);
+    return bytes == 4 ? launch_choices<__nv_bfloat16, 4>(p, sms, s) : launch_choices<__nv_bfloat16, 2>(p, sms, s);
 }
 
 static ds_status device_sms(int& sms) {
@@ -434,7 +479,9 @@ ds_status ds_expert_sort(const int32_t* experts, int64_t tokens, int32_t k, int3
                              kSortWarps * kSortMaxE * static_cast<int>(sizeof(int32_t))) != cudaSuccess ||
         cudaFuncSetAttribute(ds_expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return DS_ERR_CUDA;
-    return launch_pdl(ds_expert_sort_kernel, dim3(ctas), kSortWarps * 32, smem, ctas, stream, p);
+    // a thread for each expert, a warp for each that has slots
+    const int threads = std::max((E + 31) / 32, std::max(p.warps, 1)) * 32;
+    return launch_pdl(ds_expert_sort_kernel, dim3(ctas), threads, smem, ctas, stream, p);
 }
 
 ds_status ds_expert_gather(const void* x, int32_t dtype, int64_t tokens, int32_t D, int64_t row_stride,
@@ -448,10 +495,10 @@ ds_status ds_expert_gather(const void* x, int32_t dtype, int64_t tokens, int32_t
     const int es = dtype == DS_BF16 ? 2 : 4;
     if (off(x, es) || off(out, es) || off(places, 4) || off(offsets, 4)) return DS_ERR_ALIGNMENT;
     const GatherParams p = {x, places, offsets, out, tokens, row_stride, D, k, E};
-    const bool vec = aligned_rows(x, row_stride, D, es) && aligned16(out);
+    const int bytes = std::min(word_bytes(x, row_stride, D, es), word_bytes(out, D, D, es));
     int sms = 0;
     if (const ds_status st = device_sms(sms)) return st;
-    return dtype == DS_BF16 ? launch_gather<__nv_bfloat16>(p, vec, sms, stream) : launch_gather<float>(p, vec, sms, stream);
+    return launch_exchange(p, dtype, bytes, sms, stream);
 }
 
 ds_status ds_expert_combine(const void* y, int32_t dtype, int64_t rows, int32_t D, int64_t row_stride,
@@ -464,10 +511,10 @@ ds_status ds_expert_combine(const void* y, int32_t dtype, int64_t rows, int32_t 
     const int es = dtype == DS_BF16 ? 2 : 4;
     if (off(y, es) || off(out, es) || off(places, 4) || off(weights, 4)) return DS_ERR_ALIGNMENT;
     const CombineParams p = {y, places, weights, out, tokens, rows, row_stride, D, k};
-    const bool vec = aligned_rows(y, row_stride, D, es) && aligned16(out);
+    const int bytes = std::min(word_bytes(y, row_stride, D, es), word_bytes(out, D, D, es));
     int sms = 0;
     if (const ds_status st = device_sms(sms)) return st;
-    return dtype == DS_BF16 ? launch_combine<__nv_bfloat16>(p, vec, sms, stream) : launch_combine<float>(p, vec, sms, stream);
+    return launch_exchange(p, dtype, bytes, sms, stream);
 }
 
 ds_status ds_expert_combine_backward(const void* grad, int64_t grad_stride, const void* y, int32_t dtype, int32_t D,
@@ -485,11 +532,10 @@ ds_status ds_expert_combine_backward(const void* grad, int64_t grad_stride, cons
         return DS_ERR_ALIGNMENT;
     const CombineBackParams p = {grad, y, places, offsets, weights, grad_y, grad_weights, tokens, grad_stride, row_stride,
                                  D, k, E};
-    const bool vec = aligned_rows(grad, grad_stride, D, es) && aligned_rows(y, row_stride, D, es) && aligned16(grad_y);
+    const int bytes = std::min({word_bytes(grad, grad_stride, D, es), word_bytes(y, row_stride, D, es), word_bytes(grad_y, D, D, es)});
     int sms = 0;
     if (const ds_status st = device_sms(sms)) return st;
-    return dtype == DS_BF16 ? launch_combine_backward<__nv_bfloat16>(p, vec, sms, stream)
-                            : launch_combine_backward<float>(p, vec, sms, stream);
+    return launch_exchange(p, dtype, bytes, sms, stream);
 }
 
 }  // extern "C"

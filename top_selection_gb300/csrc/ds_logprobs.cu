@@ -17,6 +17,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ds_common.cuh"
 #include "ds_host.cuh"
 #include "ds_rows.cuh"
@@ -30,7 +32,6 @@ constexpr int kLogCluster = 16;      // most CTAs to a row
 constexpr int kLogMaxTop = 32;
 constexpr int kLogGroups = 64;       // groups of threads whose maxima give the first threshold
 constexpr int kLogList = 512;        // places of a CTA's list (and of the join: 16 x 32)
-constexpr int kLogRoom = 128;        // a list this much over `top` is cut back
 constexpr int kLogHeld = 32;         // numbers a thread holds at a time
 constexpr uint32_t kLanes = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -55,26 +56,45 @@ struct LogParams {
     int32_t per_cta;  // 16-byte words of a row to a CTA
 };
 
-// m, s, w of a part of a row, w in units of ln 2: sums of 2^y and 2^y y with y = (x - m) log2 e.
+// Sums over a part of a row whose largest number is m, relative to 2^r with r = m log2 e as fp32 rounds it: s
+// of 2^y and w of 2^y y, with y = x log2 e - r, one rounding (fma).  Every term and every result is
+// taken relative to the same r, so its rounding cancels.
 struct Part {
     float m, s, w;
 };
+
+// Numbers beyond this leave fp32's range when they are multiplied by log2 e, or their differences do.  fp32's
+// steps are 10^30 there: beside a part's largest number of that size only its equals count.
+constexpr float kFar = 1e37f;
+__device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar; }
+// r of a part: never contracted with what follows, so that it is the same number everywhere
+__device__ __forceinline__ float reference(float m) { return __fmul_rn(m, kLog2e); }
+
 __device__ __forceinline__ void rise(Part& a, float m) {  // to a larger m
     if (m > a.m) {
         if (a.s > 0.f) {
-            const float d = fmaxf((a.m - m) * kLog2e, -150.f), f = exp2_term(d);
+            const float d = is_far(m) || is_far(a.m) ? -150.f : fmaxf(reference(a.m) - reference(m), -150.f), f = exp2_term(d);
             a.w = f * fmaf(a.s, d, a.w);
             a.s *= f;
         }
         a.m = m;
     }
 }
-__device__ __forceinline__ void join(Part& a, Part b) {
-    const float m = fmaxf(a.m, b.m);
-    rise(a, m);
-    rise(b, m);
-    a.s += b.s;
-    a.w += b.w;
+using Two = unsigned long long;  // two fp32 numbers, for the packed instructions
+__device__ __forceinline__ Two two(float a, float b) {
+    return static_cast<Two>(__float_as_uint(b)) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float lower(Two a) { return __uint_as_float(static_cast<uint32_t>(a)); }
+__device__ __forceinline__ float upper(Two a) { return __uint_as_float(static_cast<uint32_t>(a >> 32)); }
+__device__ __forceinline__ Two fma_two(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Two add_two(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 // 16 bytes of the row, word g of it counted from the 16-byte boundary at or below its start
@@ -116,11 +136,33 @@ __device__ __forceinline__ float word_max(const uint4& q) {
     }
 }
 
+// the two halves of a cluster barrier: the arrivals tell that the CTAs run
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_u32(uint32_t at, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ uint64_t order_key(float v, int at) {
     return static_cast<uint64_t>(key_f32(__float_as_uint(v + 0.f))) << 32 | static_cast<uint32_t>(~at);  // -0 equals +0
 }
 __device__ __forceinline__ float key_value(uint64_t k) { return __uint_as_float(unkey_f32(static_cast<uint32_t>(k >> 32))); }
 __device__ __forceinline__ int key_at(uint64_t k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
+
+// A word's numbers, none below -10 kFar: beside a larger one those have no part in the sums.
+__device__ __forceinline__ void bounded(const uint4& q, float (&v)[4]) {
+    unpack16(q, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = fmaxf(v[j], -10.f * kFar);
+}
+__device__ __forceinline__ void bounded(uint4 q, float (&v)[8]) {
+    const __nv_bfloat162 least = __float2bfloat162_rn(-10.f * kFar);
+    const auto raise = [&](uint32_t u) {
+        const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&u), least);
+        return *reinterpret_cast<const uint32_t*>(&m);
+    };
+    unpack16(make_uint4(raise(q.x), raise(q.y), raise(q.z), raise(q.w)), v);
+}
 
 struct LogShared {
     uint64_t list[kLogList];
@@ -128,28 +170,137 @@ struct LogShared {
     float group[kLogGroups];
     uint64_t reduce[kLogWarps];
     Part parts[kLogWarps];
-    Part part;                  // the CTA's
     float edge;
     int count, kept;
+    // the row's first CTA: what every CTA of the cluster found, written by them
+    Part all_parts[kLogCluster];
+    int all_kept[kLogCluster];
+    uint64_t all_best[kLogCluster * kLogMaxTop];
 };
 
-// The `top` largest of list[0 .. count), in order, to best[]: each entry's rank is the number of
-// larger ones.  Called by all threads; list and count are complete, best is afterwards.
-__device__ __forceinline__ void cut_list(LogShared& sh, int count, int top) {
+// The `top` largest of list[0 .. count), in order, to best[] and the list's begin: each entry's rank is
+// the number of larger ones.  Called by all threads; list and count are complete.  Returns what all
+// later numbers have to exceed.
+__device__ __forceinline__ float cut_list(LogShared& sh, int count, int top) {
     for (int i = threadIdx.x; i < count; i += kLogThreads) {
         const uint64_t k = sh.list[i];
         int above = 0;
+#pragma unroll 4
         for (int j = 0; j < count; ++j) above += sh.list[j] > k ? 1 : 0;
         if (above < top) sh.best[above] = k;
     }
-    if (threadIdx.x == 0) sh.kept = min(count, top);
+    const int kept = min(count, top);
+    if (threadIdx.x == 0) sh.kept = sh.count = kept;
     __syncthreads();
+    if (threadIdx.x < kept) sh.list[threadIdx.x] = sh.best[threadIdx.x];
+    const float edge = kept == top ? key_value(sh.best[top - 1]) : -INFINITY;
+    __syncthreads();
+    return edge;
+}
+
+// A number that at least `top` of the CTA's present numbers reach, from the maxima of groups of
+// threads (each thread's is `most`): the largest group maximum that `top` of them reach, -inf where
+// there are too few.
+__device__ __forceinline__ float group_edge(LogShared& sh, float most, int top) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    constexpr int GROUP = kLogThreads / kLogGroups;
+    const float g = lanes_max<GROUP>(most);
+    if (lane % GROUP == 0) sh.group[tid / GROUP] = g;
+    __syncthreads();
+    if (tid < 32) {
+        const float a = sh.group[lane], b = sh.group[lane + 32];
+        int na = 0, nb = 0;
+#pragma unroll
+        for (int j = 0; j < kLogGroups / 4; ++j) {
+            const float4 o = reinterpret_cast<const float4*>(sh.group)[j];
+            na += (o.x >= a) + (o.y >= a) + (o.z >= a) + (o.w >= a);
+            nb += (o.x >= b) + (o.y >= b) + (o.z >= b) + (o.w >= b);
+        }
+        const float c = lanes_max<32>(fmaxf(na >= top ? a : -INFINITY, nb >= top ? b : -INFINITY));
+        if (lane == 0) sh.edge = c;
+    }
+    __syncthreads();
+    return sh.edge;
+}
+
+// The `top` largest of words [first, last) of a row, to best[]: for rows where the short list did not do
+// (rising ones, or thousands of equal numbers).  Chunk by chunk: an edge from the chunk's maxima first;
+// where even that leaves too many, one number at a time.
+template <typename T>
+__device__ __noinline__ void largest_slowly(LogShared& sh, const T* x, int first, int last, int shift, int V, int top) {
+    constexpr int PER = kPer<T>, U = kLogHeld / PER;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float edge = -INFINITY;
+    __syncthreads();
+    if (tid == 0) sh.count = sh.kept = 0;
+    __syncthreads();
+    for (int g0 = first; g0 < last; g0 += kLogThreads * U) {
+        float most = -INFINITY;
+#pragma unroll 1
+        for (int u = 0; u < U; ++u) {
+            const int g = g0 + u * kLogThreads + tid;
+            if (g < last) most = fmaxf(most, word_max<T>(row_word(x, g, shift, V)));
+        }
+        // numbers at the edge of earlier chunks lose to those, at this chunk's they may win
+        const float e = fmaxf(edge, group_edge(sh, most, top));
+        const bool equal = e > edge;
+        if (equal ? most >= e : most > e) {
+#pragma unroll 1
+            for (int u = 0; u < U; ++u) {
+                const int g = g0 + u * kLogThreads + tid, at = g * PER - shift;
+                float v[PER];
+                unpack16(g < last ? row_word(x, g, shift, V) : no_word<T>(), v);
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (equal ? v[j] >= e : v[j] > e) {
+                        const int n = atomicAdd(&sh.count, 1);
+                        if (n < kLogList) sh.list[n] = order_key(v[j], at + j);
+                    }
+            }
+        }
+        __syncthreads();
+        int count = sh.count;
+        if (count > kLogList) {
+            uint64_t below = ~0ull;
+            count = sh.kept;
+            for (int i = 0; i < top; ++i) {
+                uint64_t k = 0;
+#pragma unroll 1
+                for (int u = 0; u < U; ++u) {
+                    const int g = g0 + u * kLogThreads + tid, at = g * PER - shift;
+                    float v[PER];
+                    unpack16(g < last ? row_word(x, g, shift, V) : no_word<T>(), v);
+#pragma unroll
+                    for (int j = 0; j < PER; ++j) {
+                        const uint64_t c = v[j] > edge ? order_key(v[j], at + j) : 0;
+                        k = c < below && c > k ? c : k;
+                    }
+                }
+#pragma unroll
+                for (int d = 16; d >= 1; d >>= 1) {
+                    const uint64_t o = __shfl_xor_sync(kLanes, k, d);
+                    k = o > k ? o : k;
+                }
+                if (lane == 0) sh.reduce[warp] = k;
+                __syncthreads();
+                k = 0;
+                for (int w = 0; w < kLogWarps; ++w) k = sh.reduce[w] > k ? sh.reduce[w] : k;
+                __syncthreads();
+                if (k == 0) break;
+                if (tid == 0) sh.list[count] = k;
+                ++count;
+                below = k;
+            }
+        }
+        __syncthreads();
+        edge = cut_list(sh, count, top);
+    }
 }
 
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const LogParams p) {
-    constexpr int PER = kPer<T>, U = kLogHeld / PER;
-    __shared__ LogShared sh;
+    constexpr int PER = kPer<T>, U = kLogHeld / PER, CHUNK = kLogThreads * U;
+    __shared__ __align__(16) LogShared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ctas = gridDim.x, rank = blockIdx.x;  // of the row
     const int64_t row = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
@@ -160,64 +311,67 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
     const int words = (p.V + shift + PER - 1) / PER;
     const int first = min(words, static_cast<int>(rank) * p.per_cta), last = min(words, first + p.per_cta);
+    const int whole = min(last, (p.V + shift) / PER);  // words that end within the row
+    if (ctas > 1) cluster_arrive();
     if (TOP) __syncthreads();
     pdl_wait();
 
     Part a = {-INFINITY, 0.f, 0.f};
-    float edge = -INFINITY;  // at least `top` numbers of earlier chunks reach it (or it is -inf)
-    for (int g0 = first; g0 < last; g0 += kLogThreads * U) {
+    float edge = -INFINITY;  // at least `top` numbers seen reach it (or it is -inf): later ones have to exceed it
+    bool slow = false;       // the list was too short
+    int chunk = 0, cut_at = 4;
+    for (int g0 = first; g0 < last; g0 += CHUNK, ++chunk) {
         uint4 q[U];
+        if (g0 > 0 && g0 + CHUNK <= whole) {
+            const T* at = x + (static_cast<int64_t>(g0 + tid) * PER - shift);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int g = g0 + u * kLogThreads + tid;
-            q[u] = g < last ? row_word(x, g, shift, p.V) : no_word<T>();
+            for (int u = 0; u < U; ++u) q[u] = *reinterpret_cast<const uint4*>(at + u * kLogThreads * PER);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int g = g0 + u * kLogThreads + tid;
+                q[u] = g < last ? row_word(x, g, shift, p.V) : no_word<T>();
+            }
         }
         float most = word_max<T>(q[0]);
 #pragma unroll
         for (int u = 1; u < U; ++u) most = fmaxf(most, word_max<T>(q[u]));
         rise(a, most);
-        const float m = a.m == -INFINITY ? 0.f : a.m;
+        if (!is_far(a.m)) {
+            const float r = reference(a.m);
+            const Two nr = two(-r, -r), l2e = two(kLog2e, kLog2e);
+            Two s = 0, w = 0;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float v[PER];
-            unpack16(q[u], v);
+            for (int u = 0; u < U; ++u) {
+                float v[PER];
+                bounded(q[u], v);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) {
-                const float y = fmaxf((v[j] - m) * kLog2e, -150.f), e = exp2_term(y);
-                a.s += e;
-                a.w = fmaf(e, y, a.w);
+                for (int j = 0; j < PER; j += 2) {
+                    const Two y = fma_two(two(v[j], v[j + 1]), l2e, nr);
+                    const Two e = two(exp2_term(lower(y)), exp2_term(upper(y)));
+                    s = add_two(s, e);
+                    w = fma_two(e, y, w);
+                }
+            }
+            a.s += lower(s) + upper(s);
+            a.w += lower(w) + upper(w);
+        } else if (a.m > -INFINITY) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float v[PER];
+                unpack16(q[u], v);
+#pragma unroll
+                for (int j = 0; j < PER; ++j) a.s += v[j] == a.m ? 1.f : 0.f;
             }
         }
         if constexpr (TOP) {
-            // a way of finding what may be among the largest: 0, numbers above the edge so far (their
-            // indices are all higher, so equal ones lose); 1, an edge from this chunk as well, which
-            // equal numbers reach; 2, in turn, one number at a time, where thousands are equal
-            bool fits = false;
-            int count = 0;
-            for (int way = g0 == first ? 1 : 0; way < 2 && !fits; ++way) {
+            if (!slow) {
+                bool equal = false;
                 float e = edge;
-                if (way == 1) {
-                    const float g = lanes_max<4>(most);
-                    if (lane % 4 == 0) sh.group[tid / 4] = g;
-                    if (tid == 0) sh.count = sh.kept;
-                    __syncthreads();
-                    if (warp == 0) {  // the largest group maximum that `top` of them reach
-                        const float g0v = sh.group[lane], g1v = sh.group[lane + 32];
-                        int n0 = 0, n1 = 0;
-#pragma unroll 8
-                        for (int j = 0; j < kLogGroups; ++j) {
-                            const float o = sh.group[j];
-                            n0 += o >= g0v ? 1 : 0;
-                            n1 += o >= g1v ? 1 : 0;
-                        }
-                        const float c = lanes_max<32>(fmaxf(n0 >= p.top ? g0v : -INFINITY, n1 >= p.top ? g1v : -INFINITY));
-                        if (lane == 0) sh.edge = c;
-                    }
-                    __syncthreads();
-                    e = fmaxf(edge, sh.edge);
+                if (chunk == 0) {
+                    e = group_edge(sh, most, p.top);
+                    equal = e > -INFINITY;
                 }
-                // numbers at the edge of earlier chunks lose to those, at this chunk's they may win
-                const bool equal = e > edge;
                 if (equal ? most >= e : most > e) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
@@ -234,121 +388,94 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
                             }
                     }
                 }
-                __syncthreads();
-                count = sh.count;
-                fits = count <= kLogList;
-                __syncthreads();  // the next append comes after everyone's look at the count
-            }
-            if (!fits) {
-                uint64_t below = ~0ull;
-                int found = sh.kept;
-                for (int i = 0; i < p.top; ++i) {
-                    uint64_t k = 0;
-#pragma unroll 1
-                    for (int u = 0; u < U; ++u) {  // (read again: rare, and the registers are dear)
-                        const int g = g0 + u * kLogThreads + tid, at = g * PER - shift;
-                        float v[PER];
-                        unpack16(g < last ? row_word(x, g, shift, p.V) : no_word<T>(), v);
-#pragma unroll
-                        for (int j = 0; j < PER; ++j) {
-                            const uint64_t c = v[j] > edge ? order_key(v[j], at + j) : 0;
-                            k = c < below && c > k ? c : k;
-                        }
-                    }
-#pragma unroll
-                    for (int d = 16; d >= 1; d >>= 1) {
-                        const uint64_t o = __shfl_xor_sync(kLanes, k, d);
-                        k = o > k ? o : k;
-                    }
-                    if (lane == 0) sh.reduce[warp] = k;
+                // cut after 1, 4, 16 .. chunks and at the end: in between the list grows by a few times `top`
+                // where numbers come in no order
+                if (chunk == 0 || chunk + 1 == cut_at || g0 + CHUNK >= last) {
+                    if (chunk + 1 == cut_at) cut_at *= 4;
                     __syncthreads();
-                    k = 0;
-                    for (int w = 0; w < kLogWarps; ++w) k = sh.reduce[w] > k ? sh.reduce[w] : k;
+                    const int count = sh.count;
                     __syncthreads();
-                    if (k == 0) break;
-                    if (tid == 0) sh.list[found] = k;
-                    ++found;
-                    below = k;
+                    slow = count > kLogList;
+                    if (!slow) edge = cut_list(sh, count, p.top);
                 }
-                if (tid == 0) sh.count = found;
-                count = found;
-                __syncthreads();
-            }
-            if (g0 + kLogThreads * U >= last || g0 == first || count > p.top + kLogRoom) {
-                cut_list(sh, count, p.top);
-                if (tid < sh.kept) sh.list[tid] = sh.best[tid];
-                if (tid == 0) sh.count = sh.kept;
-                if (sh.kept == p.top) edge = key_value(sh.best[p.top - 1]);
-                __syncthreads();
-            } else if (tid == 0) {
-                sh.kept = count;  // entries that a second way starts behind
             }
         }
     }
-
-    // the CTA's part, in the order of its warps
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-        const Part b = {__shfl_xor_sync(kLanes, a.m, d), __shfl_xor_sync(kLanes, a.s, d), __shfl_xor_sync(kLanes, a.w, d)};
-        // the same order of additions in both lanes of a pair
-        Part lo = (lane & d) ? b : a;
-        join(lo, (lane & d) ? a : b);
-        a = lo;
+    if constexpr (TOP) {
+        if (slow) largest_slowly(sh, x, first, last, shift, p.V, p.top);
     }
+
+    // the parts of a warp, of the CTA's warps, and of the cluster's CTAs: relative to their largest, then added
+    const auto over = [](Part c, auto lanes) {
+        constexpr int N = decltype(lanes)::value;
+        rise(c, lanes_max<N>(c.m));
+        return Part{c.m, lanes_sum<N>(c.s), lanes_sum<N>(c.w)};
+    };
+    const Part none = {-INFINITY, 0.f, 0.f};
+    a = over(a, std::integral_constant<int, 32>());
     if (lane == 0) sh.parts[warp] = a;
     __syncthreads();
-    if (tid == 0) {
-        Part c = sh.parts[0];
-        for (int w = 1; w < kLogWarps; ++w) join(c, sh.parts[w]);
-        sh.part = c;
-    }
+    Part all = none;
+    if (warp == 0) all = over(lane < kLogWarps ? sh.parts[lane] : none, std::integral_constant<int, 32>());
     if (ctas > 1) {
-        cluster_sync_all();
-        if (rank == 0) {
-            if (tid == 0) {
-                Part c = sh.part;
-                for (uint32_t r = 1; r < ctas; ++r) {
-                    const uint32_t from = map_rank(&sh.part, r);
-                    join(c, {__uint_as_float(ld_cluster_u32(from)), __uint_as_float(ld_cluster_u32(from + 4)),
-                             __uint_as_float(ld_cluster_u32(from + 8))});
-                }
-                sh.parts[0] = c;  // (part itself stays as it is for nobody: only rank 0 reads)
-            }
-            if constexpr (TOP) {
-                // best[] of every CTA behind one another; places without an entry get keys below all
-                for (int i = tid; i < static_cast<int>(ctas) * p.top; i += kLogThreads) {
-                    const uint32_t r = i / p.top, j = i % p.top;
-                    const int kept = static_cast<int>(ld_cluster_u32(map_rank(&sh.kept, r)));
-                    uint64_t k = static_cast<uint64_t>(i);  // distinct, and below every number's key
-                    if (static_cast<int>(j) < kept) {
-                        const uint32_t from = map_rank(&sh.best[j], r);
-                        k = static_cast<uint64_t>(ld_cluster_u32(from + 4)) << 32 | ld_cluster_u32(from);
-                    }
-                    sh.list[i] = k;
-                }
-            }
+        // to the row's first CTA
+        cluster_wait();  // it runs
+        if (tid == 0) {
+            const uint32_t to = map_rank(&sh.all_parts[rank], 0);
+            st_cluster_u32(to, __float_as_uint(all.m));
+            st_cluster_u32(to + 4, __float_as_uint(all.s));
+            st_cluster_u32(to + 8, __float_as_uint(all.w));
+            if (TOP) st_cluster_u32(map_rank(&sh.all_kept[rank], 0), static_cast<uint32_t>(sh.kept));
+        }
+        if (TOP && tid < sh.kept) {
+            const uint32_t to = map_rank(&sh.all_best[rank * p.top + tid], 0);
+            st_cluster_u32(to, static_cast<uint32_t>(sh.best[tid]));
+            st_cluster_u32(to + 4, static_cast<uint32_t>(sh.best[tid] >> 32));
         }
         cluster_sync_all();
         if (rank != 0) return;
-        if constexpr (TOP) cut_list(sh, static_cast<int>(ctas) * p.top, p.top);
-    } else {
-        if (tid == 0) sh.parts[0] = sh.part;
+        if (warp == 0) all = over(lane < static_cast<int>(ctas) ? sh.all_parts[lane] : none, std::integral_constant<int, 32>());
+        if constexpr (TOP) {
+            // a key that at least `top` entries reach: the largest `top`-th of a CTA, or the smallest of every CTA's
+            // share of `top`
+            uint64_t bound = 0;
+            const int share = (p.top + static_cast<int>(ctas) - 1) / static_cast<int>(ctas);
+            uint64_t least = ~0ull;
+            for (int r = 0; r < static_cast<int>(ctas); ++r) {
+                const int kept = sh.all_kept[r];
+                if (kept == p.top && sh.all_best[r * p.top + p.top - 1] > bound) bound = sh.all_best[r * p.top + p.top - 1];
+                const uint64_t enough = kept >= share ? sh.all_best[r * p.top + share - 1] : 0;
+                least = enough < least ? enough : least;
+            }
+            bound = least > bound ? least : bound;
+            if (tid == 0) sh.count = 0;
+            __syncthreads();
+            for (int i = tid; i < static_cast<int>(ctas) * p.top; i += kLogThreads)
+                if (i % p.top < sh.all_kept[i / p.top] && sh.all_best[i] >= bound)
+                    sh.list[atomicAdd(&sh.count, 1)] = sh.all_best[i];
+            __syncthreads();
+            const int count = sh.count;
+            __syncthreads();
+            cut_list(sh, count, p.top);
+        }
     }
-    __syncthreads();
-    const Part all = sh.parts[0];
-    const float logs = all.s > 0.f ? logf(all.s) : 0.f;
-    const auto log_p = [&](float v) { return all.s > 0.f ? (v - all.m) - logs : -INFINITY; };
+    if (warp != 0) return;
+    const bool some = all.s > 0.f, far = is_far(all.m);
+    const float r = far ? 0.f : reference(all.m), logs = some ? log2f(all.s) : 0.f;
+    const auto log_p = [&](float v) {
+        return !some ? -INFINITY : far || is_far(v) ? (v - all.m) - logs * kLn2 : (fmaf(v, kLog2e, -r) - logs) * kLn2;
+    };
     if (tid == 0) {
         const int t = p.tokens[row];
         p.logprobs[row] = t >= 0 && t < p.V ? log_p(row_f32(x[t])) : 0.f;
-        p.lse[row] = all.m + logs;
-        p.entropy[row] = all.s > 0.f ? fmaxf(logs - all.w * kLn2 / all.s, 0.f) : 0.f;
+        // r's rounding, as far as the sums are relative to it, is taken out again
+        p.lse[row] = all.m + (far ? logs : logs - fmaf(all.m, kLog2e, -r)) * kLn2;
+        p.entropy[row] = some ? fmaxf((logs - all.w / all.s) * kLn2, 0.f) : 0.f;
     }
     if constexpr (TOP) {
-        if (warp != 0) return;
         const uint64_t k = lane < p.top ? sh.best[lane] : 0;
-        bool real = lane < p.top && lane < sh.kept && (k >> 32) > 0x007FFFFFu;  // above -inf's key
-        float v = real ? key_value(k) : -INFINITY;
+        const bool real = lane < p.top && lane < sh.kept;
+        const float v = real ? key_value(k) : -INFINITY;
         int at = real ? key_at(k) : 0;
         // fewer numbers above -inf than asked for: the first of the others follow
         int have = __popc(__ballot_sync(kLanes, real));

@@ -31,7 +31,7 @@ namespace dsk {
 constexpr int kProdRows = 128;                   // rows of a tile
 constexpr int kProdBlock = 128;                  // numbers along k of a block, bytes of a swizzled row
 constexpr int kProdSumWarps = 8;
-constexpr int kProdThreads = (kProdSumWarps + 2) * 32;
+constexpr int kProdThreads = (kProdSumWarps + 4) * 32;  // whole warpgroups, for the registers' split
 constexpr int kProdMaxE = 512;
 constexpr int kProdBox = 32;                     // rows of x to a copy
 constexpr int kProdMaxSplit = 8;
@@ -115,7 +115,18 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The loads before it have arrived; `r` are one's registers, which nothing uses before.
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // Shared-memory descriptor of a K-major operand in rows of 128 bytes, 128-byte swizzle: groups of 8
 // rows 1024 bytes apart.  Steps along k within the row move the address by their bytes.
@@ -258,8 +269,11 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
     // a cluster that splits tiles takes one; else tiles in turn
     const int64_t tile0 = blockIdx.x / splits, step = SPLIT ? (1LL << 40) : gridDim.x;
 
-    if (warp == kProdSumWarps) {
-        if (lane == 0) {
+    // 12 warps of 168 registers: the 8 that add up get 208 and the 4 others keep 88 (2 x 208 + 88 = 3 x 168),
+    // until the roles end
+    if (warp >= kProdSumWarps) {
+        fewer_registers<88>();
+        if (warp == kProdSumWarps && lane == 0) {
             uint32_t n = 0;  // blocks loaded so far
             Tile t;
             bool ok = true;
@@ -281,10 +295,7 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
                     const long long t0 = clock64();
                     while (!mbar_try_wait_sleep(&sh.full[j % S::STAGES], (j / S::STAGES) & 1, 1000u) && clock64() - t0 < kSpinLimit) {}
                 }
-        }
-        __syncwarp();
-    } else if (warp == kProdSumWarps + 1) {
-        if (lane == 0) {
+        } else if (warp == kProdSumWarps + 1 && lane == 0) {
             uint32_t n = 0;
             Tile t;
             bool ok = true;
@@ -305,7 +316,9 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
             }
         }
         __syncwarp();
+        more_registers<168>();
     } else {
+        more_registers<208>();
         const int quarter = warp & 3, side = warp >> 2;
         uint32_t n = 0;
         Tile t;
@@ -319,32 +332,46 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
             unsigned long long acc[S::COLS / 2];
 #pragma unroll
             for (int c = 0; c < S::COLS / 2; ++c) acc[c] = 0ull;
-            float f = some && b0 < b1 ? xs[b0] * ws[b0] : 0.f;
-            for (int b = b0; b < b1; ++b, ++n) {
-                const uint32_t d = n % S::BUFS;
-                const float next = some && b + 1 < b1 ? xs[b + 1] * ws[b + 1] : 0.f;
-                ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[d], (n / S::BUFS) & 1, failed));
-                if (!ok) break;
+            // the sums of a block come 32 columns at a time; the next 32 (or the next block's first) are on
+            // their way while these are added
+            const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * S::COLS;
+            constexpr int PARTS = S::COLS / 32;
+            uint32_t v[2][32];
+            float f = 0.f;
+            if (b0 < b1) {
+                if (some) f = xs[b0] * ws[b0];
+                ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[n % S::BUFS], (n / S::BUFS) & 1, failed));
                 tc_fence_after();
+                if (ok && some) tmem_load32(from + (n % S::BUFS) * BN, v[0]);
+            }
+            for (int b = b0; ok && b < b1; ++b, ++n) {
+                const uint32_t d = n % S::BUFS, after = (n + 1) % S::BUFS;
+                const float next = some && b + 1 < b1 ? xs[b + 1] * ws[b + 1] : 0.f;
                 if (some) {
                     const unsigned long long ff = pair_of(f, f);
-                    const uint32_t at = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + d * BN + side * S::COLS;
 #pragma unroll
-                    for (int c = 0; c < S::COLS / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_load32(at + c * 32, v);
-                        tmem_wait_load();
-                        if (c == S::COLS / 32 - 1) {
+                    for (int c = 0; c < PARTS; ++c) {
+                        uint32_t(&now)[32] = v[c & 1];
+                        tmem_wait_load(now);
+                        if (c < PARTS - 1) {
+                            tmem_load32(from + d * BN + (c + 1) * 32, v[(c + 1) & 1]);
+                        } else {
                             tc_fence_before();
                             if (lane == 0) mbar_arrive(&sh.taken[d]);
+                            if (b + 1 < b1) {
+                                ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[after], ((n + 1) / S::BUFS) & 1, failed));
+                                tc_fence_after();
+                                if (ok) tmem_load32(from + after * BN, v[(c + 1) & 1]);
+                            }
                         }
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             acc[c * 16 + j] = fma_pair(
-                                static_cast<unsigned long long>(v[2 * j + 1]) << 32 | v[2 * j], ff, acc[c * 16 + j]);
+                                static_cast<unsigned long long>(now[2 * j + 1]) << 32 | now[2 * j], ff, acc[c * 16 + j]);
                     }
-                } else if (lane == 0) {
-                    mbar_arrive(&sh.taken[d]);
+                } else {
+                    if (lane == 0) mbar_arrive(&sh.taken[d]);
+                    if (b + 1 < b1) ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[after], ((n + 1) / S::BUFS) & 1, failed));
                 }
                 f = next;
             }
@@ -386,6 +413,7 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
             }
         }
         __syncwarp();
+        fewer_registers<168>();
     }
 
     if constexpr (SPLIT) {

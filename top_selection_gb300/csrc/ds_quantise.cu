@@ -26,6 +26,7 @@ struct QuantParams {
     float* scales;
     int64_t matrices, rows, matrix_stride, stride;  // rows of each matrix
     int32_t K, blocks;                              // numbers of a row, blocks of 128 in it
+    int32_t side;                                   // log2 of the blocks of a row that a CTA takes at a time
     // the gather: k places of each row, and the rows behind the last place
     const int32_t* places;
     const int32_t* offsets;
@@ -80,50 +81,51 @@ __device__ __forceinline__ void store_eight(uint8_t* row, int first, int K, int 
     }
 }
 
-// Blocks of one row: 16 lanes to a block, kQuantUnits blocks to a lane, all loaded before the first is used.
+// Blocks of rows: 16 lanes to a block, 16 blocks to a CTA at a time, 2^side of them of one row (`side` is 4
+// where rows have more than 8 blocks); kQuantUnits rows to a lane, all loaded before the first is used.
+// blockIdx.y counts the runs of 2^side blocks of a row.
 constexpr int kQuantUnits = 4;
 
 template <typename T, bool VEC, bool GATHER>
 __global__ void __launch_bounds__(kQuantThreads) ds_quantise_rows_kernel(const QuantParams p) {
-    const int sub = threadIdx.x & 15;
+    const int sub = threadIdx.x & 15, half = threadIdx.x >> 4;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t total = p.matrices * p.rows * p.blocks;
-    constexpr int UNITS = GATHER ? 1 : kQuantUnits, HALVES = kQuantThreads / 16;
-    const int64_t unit0 = static_cast<int64_t>(blockIdx.x) * (HALVES * UNITS) + threadIdx.x / 16;
+    constexpr int UNITS = GATHER ? 1 : kQuantUnits;
+    const int64_t all_rows = p.matrices * p.rows;
+    const int down = 4 - p.side;  // log2 of the rows at a time
+    const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * UNITS << down) + (half >> p.side);
+    const int block = static_cast<int>(blockIdx.y << p.side) + (half & ((1 << p.side) - 1));
     float v[UNITS][8];
-    int64_t row[UNITS];
-    int block[UNITS];
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-        const int64_t unit = min(unit0 + i * HALVES, total - 1);
-        row[i] = unit / p.blocks;
-        block[i] = static_cast<int>(unit - row[i] * p.blocks);
-        const int64_t m = p.matrices == 1 ? 0 : row[i] / p.rows;
-        const T* src = static_cast<const T*>(p.x) + m * p.matrix_stride + (row[i] - m * p.rows) * p.stride;
-        load_eight<T, VEC>(src, block[i] * 128, p.K, sub, v[i]);
+        const int64_t r = min(row0 + (i << down), all_rows - 1);
+        const int64_t m = p.matrices == 1 ? 0 : r / p.rows;
+        const T* src = static_cast<const T*>(p.x) + m * p.matrix_stride + (r - m * p.rows) * p.stride;
+        load_eight<T, VEC>(src, block * 128, p.K, sub, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
         const float s = block_scale(lanes_max<16>(eight_max(v[i])));
         const uint2 c = eight_codes(v[i], block_inverse(s));
         if constexpr (!GATHER) {
-            if (unit0 + i * HALVES >= total) continue;  // (the warp stays whole for its shuffles)
-            store_eight<VEC>(p.codes + row[i] * p.K, block[i] * 128, p.K, sub, c);
-            if (sub == 0) p.scales[row[i] * p.blocks + block[i]] = s;
+            const int64_t row = row0 + (i << down);
+            if (row >= all_rows || block >= p.blocks) continue;  // (the warp stays whole for its shuffles)
+            store_eight<VEC>(p.codes + row * p.K, block * 128, p.K, sub, c);
+            if (sub == 0) p.scales[row * p.blocks + block] = s;
         } else {
-            if (unit0 >= total) return;
-            const int64_t slots = p.rows * p.k, first = row[i] * p.k;
+            if (row0 >= all_rows || block >= p.blocks) return;
+            const int64_t slots = p.rows * p.k, first = row0 * p.k;
             for (int j = 0; j < p.k; ++j) {
                 const int64_t at = p.places[first + j];
                 if (at < 0 || at >= slots) continue;
-                store_eight<VEC>(p.codes + at * p.K, block[i] * 128, p.K, sub, c);
-                if (sub == 0) p.scales[at * p.blocks + block[i]] = s;
+                store_eight<VEC>(p.codes + at * p.K, block * 128, p.K, sub, c);
+                if (sub == 0) p.scales[at * p.blocks + block] = s;
             }
             const int64_t filled = p.offsets[p.E];
             for (int64_t at = max(filled, first); at < first + p.k; ++at) {  // a row of zeros
-                store_eight<VEC>(p.codes + at * p.K, block[i] * 128, p.K, sub, make_uint2(0u, 0u));
-                if (sub == 0) p.scales[at * p.blocks + block[i]] = block_scale(0.f);
+                store_eight<VEC>(p.codes + at * p.K, block * 128, p.K, sub, make_uint2(0u, 0u));
+                if (sub == 0) p.scales[at * p.blocks + block] = block_scale(0.f);
             }
         }
     }
@@ -170,19 +172,21 @@ __global__ void __launch_bounds__(kQuantThreads) ds_quantise_tiles_kernel(const 
 
 // ---------------------------------------------------------------- host --------------
 template <typename T>
-static ds_status launch_quantise(const QuantParams& p, int block_rows, bool vec, bool gather, cudaStream_t stream) {
-    const auto go = [&](auto kern, int64_t ctas) {
-        if (ctas > 0x7FFFFFFFLL) return DS_ERR_UNSUPPORTED;
-        return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kQuantThreads, 0, 1, stream, p);
+static ds_status launch_quantise(QuantParams p, int block_rows, bool vec, bool gather, cudaStream_t stream) {
+    const auto go = [&](auto kern, int64_t ctas, int64_t runs) {
+        if (ctas > 0x7FFFFFFFLL || runs > 65535) return DS_ERR_UNSUPPORTED;
+        return launch_pdl(kern, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(runs)), kQuantThreads, 0, 1, stream, p);
     };
     if (block_rows == 128) {
         const int64_t ctas = p.matrices * ((p.rows + 127) / 128) * p.blocks;
-        return vec ? go(ds_quantise_tiles_kernel<T, true>, ctas) : go(ds_quantise_tiles_kernel<T, false>, ctas);
+        return vec ? go(ds_quantise_tiles_kernel<T, true>, ctas, 1) : go(ds_quantise_tiles_kernel<T, false>, ctas, 1);
     }
-    const int64_t units = p.matrices * p.rows * p.blocks, per = kQuantThreads / 16 * (gather ? 1 : kQuantUnits);
-    const int64_t ctas = (units + per - 1) / per;
-    if (gather) return vec ? go(ds_quantise_rows_kernel<T, true, true>, ctas) : go(ds_quantise_rows_kernel<T, false, true>, ctas);
-    return vec ? go(ds_quantise_rows_kernel<T, true, false>, ctas) : go(ds_quantise_rows_kernel<T, false, false>, ctas);
+    p.side = 0;
+    while (p.side < 4 && (1 << p.side) < p.blocks) ++p.side;
+    const int64_t at_once = (gather ? 1LL : kQuantUnits) << (4 - p.side), ctas = (p.matrices * p.rows + at_once - 1) / at_once;
+    const int64_t runs = (p.blocks + (1LL << p.side) - 1) >> p.side;
+    if (gather) return vec ? go(ds_quantise_rows_kernel<T, true, true>, ctas, runs) : go(ds_quantise_rows_kernel<T, false, true>, ctas, runs);
+    return vec ? go(ds_quantise_rows_kernel<T, true, false>, ctas, runs) : go(ds_quantise_rows_kernel<T, false, false>, ctas, runs);
 }
 
 static bool not_on(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; }
@@ -207,7 +211,7 @@ ds_status ds_quantise_blocks(const void* x, int32_t dtype, int64_t matrices, int
     if (!x || !codes || !scales) return DS_ERR_INVALID_ARG;
     const int es = dtype == DS_BF16 ? 2 : 4;
     if (not_on(x, es) || not_on(scales, 4)) return DS_ERR_ALIGNMENT;
-    QuantParams p = {x, static_cast<uint8_t*>(codes), scales, matrices, rows, matrix_stride, row_stride, K, (K + 127) / 128,
+    QuantParams p = {x, static_cast<uint8_t*>(codes), scales, matrices, rows, matrix_stride, row_stride, K, (K + 127) / 128, 0,
                      nullptr, nullptr, 0, 0};
     if (block_rows == 1 && (matrices == 1 || matrix_stride == rows * row_stride)) p.rows = matrices * rows, p.matrices = 1;
     const bool vec = K % 8 == 0 && aligned16(x) && !not_on(codes, 8) && row_stride * es % 16 == 0 &&
@@ -226,7 +230,7 @@ ds_status ds_expert_gather_quantised(const void* x, int32_t dtype, int64_t token
     if (!x || !places || !offsets || !codes || !scales) return DS_ERR_INVALID_ARG;
     const int es = dtype == DS_BF16 ? 2 : 4;
     if (not_on(x, es) || not_on(scales, 4) || not_on(places, 4) || not_on(offsets, 4)) return DS_ERR_ALIGNMENT;
-    const QuantParams p = {x, static_cast<uint8_t*>(codes), scales, 1, tokens, 0, row_stride, D, (D + 127) / 128,
+    const QuantParams p = {x, static_cast<uint8_t*>(codes), scales, 1, tokens, 0, row_stride, D, (D + 127) / 128, 0,
                            places, offsets, k, E};
     const bool vec = D % 8 == 0 && aligned16(x) && !not_on(codes, 8) && row_stride * es % 16 == 0;
     return dtype == DS_BF16 ? launch_quantise<__nv_bfloat16>(p, 1, vec, true, stream)
