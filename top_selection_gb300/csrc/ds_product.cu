@@ -8,7 +8,9 @@
 // each block's sums are read back, multiplied by their row's scale and added up in registers in
 // fp32, while the next blocks are being multiplied (512 / BN buffers in tensor memory).
 //
-// Warps 0 to 7 add up and store, warp 8 loads (TMA, 128-byte swizzle), warp 9 issues the products.
+// Warps 0 to 7 add up and store, warp 8 loads (TMA, 128-byte swizzle), warp 9 issues the products, warp
+// 10 brings the scales of each block to shared memory (read by the warps that add up, their latency
+// came once a block: 403 us on 32768 rows over 64 experts of 4096 x 2048).
 // A tile is up to 128 rows of one expert by BN outputs; CTAs take tiles in turn.  Rows of a
 // tile that lie behind the expert's last are computed from whatever is in shared memory and not
 // stored (no row's sums meet another's); of the rows only 32 at a time as needed are loaded.
@@ -43,6 +45,9 @@ struct ProdShape {
     static constexpr int A_BYTES = kProdRows * kProdBlock, B_BYTES = BN * kProdBlock;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int COLS = BN / 2;           // a warp's outputs of a row
+    // 12 warps of 168 registers at launch; until the roles end, the 8 that add up and the 4 others share them
+    // out anew
+    static constexpr int SUM_REGISTERS = BN == 256 ? 224 : 208, OTHER_REGISTERS = 3 * 168 - 2 * SUM_REGISTERS;
     static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + 1024;
 };
 
@@ -62,6 +67,7 @@ struct ProdParams {
 
 struct ProdShared {
     uint64_t full[8], empty[8], sums[8], taken[8];
+    float scale[4][2][kProdRows];  // of a block's sums: buffer, half of the tile's outputs, row
     int64_t tiles[kProdMaxE + 1];  // row tiles before each expert's
     int32_t first[kProdMaxE + 1];  // rows before each expert's
     int64_t scan[kProdThreads / 32];
@@ -115,13 +121,12 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&r)[32]) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
 }
-// The loads before it have arrived; `r` are one's registers, which nothing uses before.
+// The load before it has arrived; r are its registers, which nothing uses before.
 __device__ __forceinline__ void tmem_wait_load(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 template <int N>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -151,16 +156,10 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
     return true;
 }
 
-__device__ __forceinline__ unsigned long long pair_of(float a, float b) {
-    return static_cast<unsigned long long>(__float_as_uint(b)) << 32 | __float_as_uint(a);
-}
-__device__ __forceinline__ unsigned long long fma_pair(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ float pair_get(unsigned long long p, int i) {
-    return __uint_as_float(static_cast<uint32_t>(i ? p >> 32 : p));
+using Two = unsigned long long;  // two fp32 numbers, for the packed instructions
+__device__ __forceinline__ Two two(uint32_t a, uint32_t b) { return static_cast<Two>(b) << 32 | a; }
+__device__ __forceinline__ void add_product(Two& sum, Two a, Two b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum) : "l"(a), "l"(b));
 }
 
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
@@ -208,7 +207,7 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
 
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
-        for (int i = 0; i < S::BUFS; ++i) mbar_init(&sh.sums[i], 1), mbar_init(&sh.taken[i], kProdSumWarps);
+        for (int i = 0; i < S::BUFS; ++i) mbar_init(&sh.sums[i], 2), mbar_init(&sh.taken[i], kProdSumWarps);
         sh.failed = 0;
         fence_mbar_init();
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x) : "memory");
@@ -269,10 +268,8 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
     // a cluster that splits tiles takes one; else tiles in turn
     const int64_t tile0 = blockIdx.x / splits, step = SPLIT ? (1LL << 40) : gridDim.x;
 
-    // 12 warps of 168 registers: the 8 that add up get 208 and the 4 others keep 88 (2 x 208 + 88 = 3 x 168),
-    // until the roles end
     if (warp >= kProdSumWarps) {
-        fewer_registers<88>();
+        fewer_registers<S::OTHER_REGISTERS>();
         if (warp == kProdSumWarps && lane == 0) {
             uint32_t n = 0;  // blocks loaded so far
             Tile t;
@@ -314,11 +311,47 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
                     tc_commit(&sh.sums[d]);
                 }
             }
+        } else if (warp == kProdSumWarps + 2) {
+            uint32_t n = 0;
+            Tile t;
+            bool ok = true;
+            for (int64_t i = tile0; ok && tile_at<BN>(sh, p, i, t); i += step) {
+                const float* xs[4];  // four rows to a lane; rows behind the tile's last take its first's
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = lane + 32 * j;
+                    xs[j] = p.x_scales + (t.row0 + (r < t.rows ? r : 0)) * p.blocks;
+                }
+                const int nb = t.n0 / 128;
+                const float* ws = p.w_scales + (static_cast<int64_t>(t.e) * p.n_blocks + nb) * p.blocks;
+                const int64_t second = BN == 256 && nb + 1 < p.n_blocks ? p.blocks : 0;
+                float x[4], w[2];
+                const auto fetch = [&](int b) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = xs[j][b];
+                    w[0] = ws[b];
+                    w[1] = ws[b + second];
+                };
+                if (b0 < b1) fetch(b0);
+                for (int b = b0; b < b1; ++b, ++n) {
+                    const uint32_t d = n % S::BUFS;
+                    ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.taken[d], (n / S::BUFS + 1) & 1, failed));
+                    if (!ok) break;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sh.scale[d][0][lane + 32 * j] = x[j] * w[0];
+                        sh.scale[d][1][lane + 32 * j] = x[j] * w[1];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.sums[d]);
+                    if (b + 1 < b1) fetch(b + 1);
+                }
+            }
         }
         __syncwarp();
         more_registers<168>();
     } else {
-        more_registers<208>();
+        more_registers<S::SUM_REGISTERS>();
         const int quarter = warp & 3, side = warp >> 2;
         uint32_t n = 0;
         Tile t;
@@ -326,63 +359,46 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
         for (int64_t i = tile0; ok && tile_at<BN>(sh, p, i, t); i += step) {
             const int r = quarter * 32 + lane;             // the thread's row of the tile
             const bool some = quarter * 32 < t.rows;       // the warp has a row to add up
-            const float* xs = p.x_scales + (t.row0 + (r < t.rows ? r : 0)) * p.blocks;
-            const int nb = min((t.n0 + side * S::COLS) / 128, p.n_blocks - 1);
-            const float* ws = p.w_scales + (static_cast<int64_t>(t.e) * p.n_blocks + nb) * p.blocks;
-            unsigned long long acc[S::COLS / 2];
+            Two acc[S::COLS / 2];
 #pragma unroll
-            for (int c = 0; c < S::COLS / 2; ++c) acc[c] = 0ull;
-            // the sums of a block come 32 columns at a time; the next 32 (or the next block's first) are on
-            // their way while these are added
+            for (int c = 0; c < S::COLS / 2; ++c) acc[c] = 0;
             const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + side * S::COLS;
             constexpr int PARTS = S::COLS / 32;
-            uint32_t v[2][32];
-            float f = 0.f;
-            if (b0 < b1) {
-                if (some) f = xs[b0] * ws[b0];
-                ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[n % S::BUFS], (n / S::BUFS) & 1, failed));
+            for (int b = b0; b < b1; ++b, ++n) {
+                const uint32_t d = n % S::BUFS;
+                ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[d], (n / S::BUFS) & 1, failed));
+                if (!ok) break;
                 tc_fence_after();
-                if (ok && some) tmem_load32(from + (n % S::BUFS) * BN, v[0]);
-            }
-            for (int b = b0; ok && b < b1; ++b, ++n) {
-                const uint32_t d = n % S::BUFS, after = (n + 1) % S::BUFS;
-                const float next = some && b + 1 < b1 ? xs[b + 1] * ws[b + 1] : 0.f;
                 if (some) {
-                    const unsigned long long ff = pair_of(f, f);
+                    const uint32_t f = __float_as_uint(sh.scale[d][side][r]);
+                    const Two ff = two(f, f);
 #pragma unroll
                     for (int c = 0; c < PARTS; ++c) {
-                        uint32_t(&now)[32] = v[c & 1];
-                        tmem_wait_load(now);
-                        if (c < PARTS - 1) {
-                            tmem_load32(from + d * BN + (c + 1) * 32, v[(c + 1) & 1]);
-                        } else {
+                        uint32_t v[32];
+                        tmem_load32(from + d * BN + c * 32, v);
+                        tmem_wait_load(v);
+                        if (c == PARTS - 1) {
                             tc_fence_before();
+                            __syncwarp();
                             if (lane == 0) mbar_arrive(&sh.taken[d]);
-                            if (b + 1 < b1) {
-                                ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[after], ((n + 1) / S::BUFS) & 1, failed));
-                                tc_fence_after();
-                                if (ok) tmem_load32(from + after * BN, v[(c + 1) & 1]);
-                            }
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            acc[c * 16 + j] = fma_pair(
-                                static_cast<unsigned long long>(now[2 * j + 1]) << 32 | now[2 * j], ff, acc[c * 16 + j]);
+                        for (int j = 0; j < 16; ++j) add_product(acc[c * 16 + j], two(v[2 * j], v[2 * j + 1]), ff);
                     }
-                } else {
-                    if (lane == 0) mbar_arrive(&sh.taken[d]);
-                    if (b + 1 < b1) ok = __all_sync(0xFFFFFFFFu, wait_phase(&sh.sums[after], ((n + 1) / S::BUFS) & 1, failed));
+                } else if (lane == 0) {
+                    mbar_arrive(&sh.taken[d]);
                 }
-                f = next;
             }
             if (!ok) break;
+            const auto sum = [&](int c) { return __uint_as_float(static_cast<uint32_t>(c & 1 ? acc[c / 2] >> 32 : acc[c / 2])); };
             if constexpr (SPLIT) {
                 // sums to the stages' memory (all products have read it), rows 16 bytes apart in their banks
                 if (some) {
                     const uint32_t at = stage0 + (r * (BN + 4) + side * S::COLS) * 4;
 #pragma unroll
                     for (int c = 0; c < S::COLS / 4; ++c)
-                        asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + c * 16), "l"(acc[2 * c]), "l"(acc[2 * c + 1])
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + c * 16), "f"(sum(4 * c)),
+                                     "f"(sum(4 * c + 1)), "f"(sum(4 * c + 2)), "f"(sum(4 * c + 3))
                                      : "memory");
                 }
             } else if (r < t.rows) {
@@ -396,19 +412,19 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
                         if constexpr (sizeof(O) == 2) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) {
-                                const __nv_bfloat162 h = __floats2bfloat162_rn(pair_get(acc[c * 8 + j], 0), pair_get(acc[c * 8 + j], 1));
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(sum(c * 16 + 2 * j), sum(c * 16 + 2 * j + 1));
                                 w[j] = *reinterpret_cast<const uint32_t*>(&h);
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(pair_get(acc[c * 4 + j / 2], j & 1));
+                            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(sum(c * 8 + j));
                         }
                         store32(out + c * W, w);
                     }
                 } else {
 #pragma unroll
                     for (int c = 0; c < S::COLS; ++c)
-                        if (c0 + c < p.N) put_out(out + c, pair_get(acc[c / 2], c & 1));
+                        if (c0 + c < p.N) put_out(out + c, sum(c));
                 }
             }
         }
