@@ -21,7 +21,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "ds_common.cuh"
 #include "ds_host.cuh"
@@ -144,10 +146,9 @@ __host__ __device__ constexpr uint32_t instruction_desc(uint32_t n) { return 1u 
 
 // Waits for a phase, about a second at most; then (or when another wait of the CTA has run out) false.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* failed) {
-    for (int i = 0; i < 8; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
-    while (!mbar_try_wait_sleep(bar, parity, 1000u)) {
+    while (!mbar_try_wait(bar, parity)) {
         if (*failed || clock64() - t0 > kSpinLimit) {
             *failed = 1;
             return false;
@@ -529,6 +530,24 @@ static ds_status launch_product(const CUtensorMap& mx, const CUtensorMap& mw, co
     return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kProdThreads, smem, splits, stream, mx, mw, p);
 }
 
+// Outputs to a tile, 128 or 256: those whose rounds of tiles over the SMs take less.  A block of a tile takes 400
+// or 490 ns where its operands come from L2 (8192 rows by 8192 x 8192: 688 and 438 us), bound by shared
+// memory, which takes in 32 or 48 KB and gives them to the products; or the time of its weights from DRAM, 16 or
+// 32 KB at an SM's share of 45 bytes a ns, over the row tiles that share them.
+static int product_outputs(int64_t rows, int64_t E, int64_t N, int sms) {
+    const double used = static_cast<double>(rows < E ? rows : E);  // experts with a row, at most
+    // half a tile more for each expert than its rows fill
+    const double tall = std::max(used, static_cast<double>(rows) / kProdRows + 0.5 * used);
+    double least = 0;
+    int best = 128;
+    for (int bn = 128; bn <= 256; bn *= 2) {
+        const double rounds = std::ceil(tall * static_cast<double>((N + bn - 1) / bn) / sms);
+        const double time = rounds * std::max(bn == 128 ? 400.0 : 490.0, bn * 128 / 45.0 * used / tall);
+        if (bn == 128 || time < least) best = bn, least = time;
+    }
+    return best;
+}
+
 }  // namespace dsk
 
 using namespace dsk;
@@ -564,10 +583,8 @@ extern "C" ds_status ds_expert_product(const void* x, const float* x_scales, int
     p.n_blocks = (N + 127) / 128;
     p.E = E;
     p.vec = !off_by(out, 32) && static_cast<int64_t>(N) * es % 32 == 0;
-    // 256 outputs to a tile where experts have rows enough that the products bound it; 128 where the
-    // weights' bytes do, so that there are more tiles to share out
-    const bool wide = rows >= 64LL * E && N > 128;
-    const int bn = wide ? 256 : 128;
+    const int bn = product_outputs(rows, E, N, info.sms);
+    const bool wide = bn == 256;
     p.n_tiles = (N + bn - 1) / bn;
     const int64_t tall = rows / kProdRows + (rows < E ? rows : E);  // row tiles at most (one more for each expert's end)
     const int64_t tiles = tall * p.n_tiles;
