@@ -170,7 +170,7 @@ struct LogShared {
     float group[kLogGroups];
     uint64_t reduce[kLogWarps];
     Part parts[kLogWarps];
-    float edge;
+    uint32_t edge;              // as a key
     int count, kept;
     // the row's first CTA: what every CTA of the cluster found, written by them
     Part all_parts[kLogCluster];
@@ -182,12 +182,16 @@ struct LogShared {
 // the number of larger ones.  Called by all threads; list and count are complete.  Returns what all
 // later numbers have to exceed.
 __device__ __forceinline__ float cut_list(LogShared& sh, int count, int top) {
-    for (int i = threadIdx.x; i < count; i += kLogThreads) {
-        const uint64_t k = sh.list[i];
+    const int part = threadIdx.x % 4;  // four threads count together
+    for (int i0 = 0; i0 < count; i0 += kLogThreads / 4) {
+        const int i = i0 + static_cast<int>(threadIdx.x) / 4;
+        const uint64_t k = i < count ? sh.list[i] : ~0ull;
         int above = 0;
 #pragma unroll 4
-        for (int j = 0; j < count; ++j) above += sh.list[j] > k ? 1 : 0;
-        if (above < top) sh.best[above] = k;
+        for (int j = part; j < count; j += 4) above += sh.list[j] > k ? 1 : 0;
+        above += __shfl_xor_sync(kLanes, above, 1);
+        above += __shfl_xor_sync(kLanes, above, 2);
+        if (part == 0 && i < count && above < top) sh.best[above] = k;
     }
     const int kept = min(count, top);
     if (threadIdx.x == 0) sh.kept = sh.count = kept;
@@ -198,29 +202,62 @@ __device__ __forceinline__ float cut_list(LogShared& sh, int count, int top) {
     return edge;
 }
 
-// A number that at least `top` of the CTA's present numbers reach, from the maxima of groups of
-// threads (each thread's is `most`): the largest group maximum that `top` of them reach, -inf where
-// there are too few.
+// A number that at least `top` of the CTA's present numbers reach, from the maxima of 64 groups of them (a
+// thread's is `most`): the largest group maximum that `top` of them reach, -inf where there are too few.
 __device__ __forceinline__ float group_edge(LogShared& sh, float most, int top) {
-    const int tid = threadIdx.x, lane = tid & 31;
     constexpr int GROUP = kLogThreads / kLogGroups;
+    static_assert(GROUP == 4, "four threads make a group, and count for it");
+    const int tid = threadIdx.x, lane = tid & 31;
     const float g = lanes_max<GROUP>(most);
     if (lane % GROUP == 0) sh.group[tid / GROUP] = g;
+    if (tid == 0) sh.edge = 0u;
     __syncthreads();
-    if (tid < 32) {
-        const float a = sh.group[lane], b = sh.group[lane + 32];
-        int na = 0, nb = 0;
+    int reach = 0;  // how many maxima reach the thread's group's: a quarter of them each
 #pragma unroll
-        for (int j = 0; j < kLogGroups / 4; ++j) {
-            const float4 o = reinterpret_cast<const float4*>(sh.group)[j];
-            na += (o.x >= a) + (o.y >= a) + (o.z >= a) + (o.w >= a);
-            nb += (o.x >= b) + (o.y >= b) + (o.z >= b) + (o.w >= b);
-        }
-        const float c = lanes_max<32>(fmaxf(na >= top ? a : -INFINITY, nb >= top ? b : -INFINITY));
-        if (lane == 0) sh.edge = c;
+    for (int j = 0; j < kLogGroups / 16; ++j) {
+        const float4 o = reinterpret_cast<const float4*>(sh.group)[(lane % GROUP) * (kLogGroups / 16) + j];
+        reach += (o.x >= g ? 1 : 0) + (o.y >= g ? 1 : 0) + (o.z >= g ? 1 : 0) + (o.w >= g ? 1 : 0);
     }
+    reach += __shfl_xor_sync(kLanes, reach, 1);
+    reach += __shfl_xor_sync(kLanes, reach, 2);
+    const uint32_t best = __reduce_max_sync(kLanes, reach >= top ? key_f32(__float_as_uint(g + 0.f)) : 0u);
+    if (lane == 0) atomicMax(&sh.edge, best);
     __syncthreads();
-    return sh.edge;
+    const uint32_t key = sh.edge;
+    return key == 0u ? -INFINITY : __uint_as_float(unkey_f32(key));
+}
+
+// The `top` largest of the CTAs' lists all_best[r * 32 ..], each in order: lane i of each warp gets the i-th, 0 for
+// none.  Pairs of lists become one until one is left: an entry's rank is its own in its list and the number of
+// larger ones in the other (binary search).
+__device__ __forceinline__ uint64_t merge_lists(LogShared& sh, int lists, int top) {
+    static_assert(kLogList >= kLogCluster * kLogMaxTop / 2, "lists take turns in two arrays");
+    const int lane = threadIdx.x & 31;
+    uint64_t *from = sh.all_best, *to = sh.list;
+    for (; lists > 1; lists /= 2) {
+        for (int i = threadIdx.x; i < lists * kLogMaxTop; i += kLogThreads) {
+            const int mine = i / kLogMaxTop, other = mine ^ 1, at = i % kLogMaxTop;
+            const int kept = sh.all_kept[mine], others = sh.all_kept[other];
+            if (at < kept) {
+                const uint64_t k = from[i];
+                int lo = 0, hi = others;  // the first of the other's entries below k
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if (from[other * kLogMaxTop + mid] > k) lo = mid + 1;
+                    else hi = mid;
+                }
+                if (at + lo < top) to[mine / 2 * kLogMaxTop + at + lo] = k;
+            }
+        }
+        int kept = 0;
+        if (threadIdx.x < lists / 2) kept = min(top, sh.all_kept[2 * threadIdx.x] + sh.all_kept[2 * threadIdx.x + 1]);
+        __syncthreads();
+        if (threadIdx.x < lists / 2) sh.all_kept[threadIdx.x] = kept;
+        __syncthreads();
+        uint64_t* const swap = from;
+        from = to, to = swap;
+    }
+    return lane < sh.all_kept[0] ? from[lane] : 0;
 }
 
 // The `top` largest of words [first, last) of a row, to best[]: for rows where the short list did not do
@@ -316,6 +353,15 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
     if (TOP) __syncthreads();
     pdl_wait();
 
+    // the given token's logit: with the first words where a row's latency counts, else at the end
+    float given = 0.f;
+    int token = -1;
+    const auto look_up = [&]() {
+        token = p.tokens[row];
+        if (token < 0 || token >= p.V) token = -1;
+        else given = row_f32(x[token]);
+    };
+    if (tid == 0 && rank == 0 && ctas > 1) look_up();
     Part a = {-INFINITY, 0.f, 0.f};
     float edge = -INFINITY;  // at least `top` numbers seen reach it (or it is -inf): later ones have to exceed it
     bool slow = false;       // the list was too short
@@ -428,7 +474,7 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
             if (TOP) st_cluster_u32(map_rank(&sh.all_kept[rank], 0), static_cast<uint32_t>(sh.kept));
         }
         if (TOP && tid < sh.kept) {
-            const uint32_t to = map_rank(&sh.all_best[rank * p.top + tid], 0);
+            const uint32_t to = map_rank(&sh.all_best[rank * kLogMaxTop + tid], 0);
             st_cluster_u32(to, static_cast<uint32_t>(sh.best[tid]));
             st_cluster_u32(to + 4, static_cast<uint32_t>(sh.best[tid] >> 32));
         }
@@ -436,27 +482,12 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
         if (rank != 0) return;
         if (warp == 0) all = over(lane < static_cast<int>(ctas) ? sh.all_parts[lane] : none, std::integral_constant<int, 32>());
         if constexpr (TOP) {
-            // a key that at least `top` entries reach: the largest `top`-th of a CTA, or the smallest of every CTA's
-            // share of `top`
-            uint64_t bound = 0;
-            const int share = (p.top + static_cast<int>(ctas) - 1) / static_cast<int>(ctas);
-            uint64_t least = ~0ull;
-            for (int r = 0; r < static_cast<int>(ctas); ++r) {
-                const int kept = sh.all_kept[r];
-                if (kept == p.top && sh.all_best[r * p.top + p.top - 1] > bound) bound = sh.all_best[r * p.top + p.top - 1];
-                const uint64_t enough = kept >= share ? sh.all_best[r * p.top + share - 1] : 0;
-                least = enough < least ? enough : least;
+            const uint64_t mine = merge_lists(sh, static_cast<int>(ctas), p.top);
+            if (warp == 0) {
+                if (lane < p.top) sh.best[lane] = mine;
+                if (lane == 0) sh.kept = sh.all_kept[0];
+                __syncwarp();
             }
-            bound = least > bound ? least : bound;
-            if (tid == 0) sh.count = 0;
-            __syncthreads();
-            for (int i = tid; i < static_cast<int>(ctas) * p.top; i += kLogThreads)
-                if (i % p.top < sh.all_kept[i / p.top] && sh.all_best[i] >= bound)
-                    sh.list[atomicAdd(&sh.count, 1)] = sh.all_best[i];
-            __syncthreads();
-            const int count = sh.count;
-            __syncthreads();
-            cut_list(sh, count, p.top);
         }
     }
     if (warp != 0) return;
@@ -466,8 +497,8 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
         return !some ? -INFINITY : far || is_far(v) ? (v - all.m) - logs * kLn2 : (fmaf(v, kLog2e, -r) - logs) * kLn2;
     };
     if (tid == 0) {
-        const int t = p.tokens[row];
-        p.logprobs[row] = t >= 0 && t < p.V ? log_p(row_f32(x[t])) : 0.f;
+        if (ctas == 1) look_up();
+        p.logprobs[row] = token >= 0 ? log_p(given) : 0.f;
         // r's rounding, as far as the sums are relative to it, is taken out again
         p.lse[row] = all.m + (far ? logs : logs - fmaf(all.m, kLog2e, -r)) * kLn2;
         p.entropy[row] = some ? fmaxf((logs - all.w / all.s) * kLn2, 0.f) : 0.f;

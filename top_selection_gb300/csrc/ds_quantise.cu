@@ -81,37 +81,105 @@ __device__ __forceinline__ void store_eight(uint8_t* row, int first, int K, int 
     }
 }
 
-// Blocks of rows: 16 lanes to a block, 16 blocks to a CTA at a time, 2^side of them of one row (`side` is 4
-// where rows have more than 8 blocks); kQuantUnits rows to a lane, all loaded before the first is used.
+// A lane's 16 numbers of a block of 128, 8 lanes to the block: in a run (VEC), or every 8th one.
+template <typename T, bool VEC>
+struct Sixteen {
+    static constexpr int WORDS = static_cast<int>(sizeof(T));  // of 16 bytes
+    uint4 q[WORDS];
+    float v[16];
+    __device__ __forceinline__ void load(const T* row, int first, int K, int sub) {
+        if constexpr (VEC) {
+            const int at = first + sub * 16;
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i)
+                q[i] = at < K ? reinterpret_cast<const uint4*>(row + at)[i] : make_uint4(0u, 0u, 0u, 0u);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const int at = first + sub + 8 * j;
+                v[j] = at < K ? row_f32(row[at]) : 0.f;
+            }
+        }
+    }
+    __device__ __forceinline__ float most() const {  // the largest size among them
+        if constexpr (VEC && sizeof(T) == 2) {  // two bf16 numbers at a time, signs cleared
+            const auto pair = [](uint32_t u) {
+                u &= 0x7FFF7FFFu;
+                return *reinterpret_cast<const __nv_bfloat162*>(&u);
+            };
+            const auto word = [&](const uint4& w) { return __hmax2(__hmax2(pair(w.x), pair(w.y)), __hmax2(pair(w.z), pair(w.w))); };
+            const __nv_bfloat162 m = __hmax2(word(q[0]), word(q[1]));
+            return fmaxf(__low2float(m), __high2float(m));
+        } else {
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(VEC ? number(j) : v[j]));
+            return m;
+        }
+    }
+    __device__ __forceinline__ float number(int j) const {
+        if constexpr (!VEC) {
+            return v[j];
+        } else {
+            constexpr int PER = kPer<T>;
+            float f[PER];
+            unpack16(q[j / PER], f);
+            return f[j % PER];
+        }
+    }
+    __device__ __forceinline__ uint4 codes(float inv) const {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] = e4m3_four(number(4 * i) * inv, number(4 * i + 1) * inv, number(4 * i + 2) * inv, number(4 * i + 3) * inv);
+        return make_uint4(c[0], c[1], c[2], c[3]);
+    }
+};
+template <bool VEC>
+__device__ __forceinline__ void store_sixteen(uint8_t* row, int first, int K, int sub, uint4 c) {
+    if constexpr (VEC) {
+        if (first + sub * 16 < K) *reinterpret_cast<uint4*>(row + first + sub * 16) = c;
+    } else {
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int at = first + sub + 8 * j;
+            if (at < K) row[at] = static_cast<uint8_t>(w[j / 4] >> (8 * (j & 3)));
+        }
+    }
+}
+
+// Blocks of rows: 8 lanes to a block, 32 blocks to a CTA at a time, 2^side of them of one row (`side` is 4 where
+// rows have more than 8 blocks); kQuantUnits rows to a lane, all loaded before the first is used.
 // blockIdx.y counts the runs of 2^side blocks of a row.
-constexpr int kQuantUnits = 4;
+constexpr int kQuantUnits = 2;
+constexpr int kQuantLog = 5;  // log2 of the blocks to a CTA at a time
 
 template <typename T, bool VEC, bool GATHER>
 __global__ void __launch_bounds__(kQuantThreads) ds_quantise_rows_kernel(const QuantParams p) {
-    const int sub = threadIdx.x & 15, half = threadIdx.x >> 4;
+    const int sub = threadIdx.x & 7, team = threadIdx.x >> 3;
     pdl_launch_dependents();
     pdl_wait();
     constexpr int UNITS = GATHER ? 1 : kQuantUnits;
     const int64_t all_rows = p.matrices * p.rows;
-    const int down = 4 - p.side;  // log2 of the rows at a time
-    const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * UNITS << down) + (half >> p.side);
-    const int block = static_cast<int>(blockIdx.y << p.side) + (half & ((1 << p.side) - 1));
-    float v[UNITS][8];
+    const int down = kQuantLog - p.side;  // log2 of the rows at a time
+    const int64_t row0 = (static_cast<int64_t>(blockIdx.x) * UNITS << down) + (team >> p.side);
+    const int block = static_cast<int>(blockIdx.y << p.side) + (team & ((1 << p.side) - 1));
+    Sixteen<T, VEC> v[UNITS];
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
         const int64_t r = min(row0 + (i << down), all_rows - 1);
         const int64_t m = p.matrices == 1 ? 0 : r / p.rows;
-        const T* src = static_cast<const T*>(p.x) + m * p.matrix_stride + (r - m * p.rows) * p.stride;
-        load_eight<T, VEC>(src, block * 128, p.K, sub, v[i]);
+        v[i].load(static_cast<const T*>(p.x) + m * p.matrix_stride + (r - m * p.rows) * p.stride, block * 128, p.K, sub);
     }
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-        const float s = block_scale(lanes_max<16>(eight_max(v[i])));
-        const uint2 c = eight_codes(v[i], block_inverse(s));
+        const float s = block_scale(lanes_max<8>(v[i].most()));
+        const uint4 c = v[i].codes(block_inverse(s));
         if constexpr (!GATHER) {
             const int64_t row = row0 + (i << down);
             if (row >= all_rows || block >= p.blocks) continue;  // (the warp stays whole for its shuffles)
-            store_eight<VEC>(p.codes + row * p.K, block * 128, p.K, sub, c);
+            store_sixteen<VEC>(p.codes + row * p.K, block * 128, p.K, sub, c);
             if (sub == 0) p.scales[row * p.blocks + block] = s;
         } else {
             if (row0 >= all_rows || block >= p.blocks) return;
@@ -119,12 +187,12 @@ __global__ void __launch_bounds__(kQuantThreads) ds_quantise_rows_kernel(const Q
             for (int j = 0; j < p.k; ++j) {
                 const int64_t at = p.places[first + j];
                 if (at < 0 || at >= slots) continue;
-                store_eight<VEC>(p.codes + at * p.K, block * 128, p.K, sub, c);
+                store_sixteen<VEC>(p.codes + at * p.K, block * 128, p.K, sub, c);
                 if (sub == 0) p.scales[at * p.blocks + block] = s;
             }
             const int64_t filled = p.offsets[p.E];
             for (int64_t at = max(filled, first); at < first + p.k; ++at) {  // a row of zeros
-                store_eight<VEC>(p.codes + at * p.K, block * 128, p.K, sub, make_uint2(0u, 0u));
+                store_sixteen<VEC>(p.codes + at * p.K, block * 128, p.K, sub, make_uint4(0u, 0u, 0u, 0u));
                 if (sub == 0) p.scales[at * p.blocks + block] = block_scale(0.f);
             }
         }
@@ -183,7 +251,7 @@ static ds_status launch_quantise(QuantParams p, int block_rows, bool vec, bool g
     }
     p.side = 0;
     while (p.side < 4 && (1 << p.side) < p.blocks) ++p.side;
-    const int64_t at_once = (gather ? 1LL : kQuantUnits) << (4 - p.side), ctas = (p.matrices * p.rows + at_once - 1) / at_once;
+    const int64_t at_once = (gather ? 1LL : kQuantUnits) << (kQuantLog - p.side), ctas = (p.matrices * p.rows + at_once - 1) / at_once;
     const int64_t runs = (p.blocks + (1LL << p.side) - 1) >> p.side;
     if (gather) return vec ? go(ds_quantise_rows_kernel<T, true, true>, ctas, runs) : go(ds_quantise_rows_kernel<T, false, true>, ctas, runs);
     return vec ? go(ds_quantise_rows_kernel<T, true, false>, ctas, runs) : go(ds_quantise_rows_kernel<T, false, false>, ctas, runs);
@@ -214,7 +282,8 @@ ds_status ds_quantise_blocks(const void* x, int32_t dtype, int64_t matrices, int
     QuantParams p = {x, static_cast<uint8_t*>(codes), scales, matrices, rows, matrix_stride, row_stride, K, (K + 127) / 128, 0,
                      nullptr, nullptr, 0, 0};
     if (block_rows == 1 && (matrices == 1 || matrix_stride == rows * row_stride)) p.rows = matrices * rows, p.matrices = 1;
-    const bool vec = K % 8 == 0 && aligned16(x) && !not_on(codes, 8) && row_stride * es % 16 == 0 &&
+    const int run = block_rows == 1 ? 16 : 8;  // a lane's codes are stored together
+    const bool vec = K % run == 0 && aligned16(x) && !not_on(codes, run) && row_stride * es % 16 == 0 &&
                      (matrices == 1 || matrix_stride * es % 16 == 0);
     return dtype == DS_BF16 ? launch_quantise<__nv_bfloat16>(p, block_rows, vec, false, stream)
                             : launch_quantise<float>(p, block_rows, vec, false, stream);
@@ -232,7 +301,7 @@ ds_status ds_expert_gather_quantised(const void* x, int32_t dtype, int64_t token
     if (not_on(x, es) || not_on(scales, 4) || not_on(places, 4) || not_on(offsets, 4)) return DS_ERR_ALIGNMENT;
     const QuantParams p = {x, static_cast<uint8_t*>(codes), scales, 1, tokens, 0, row_stride, D, (D + 127) / 128, 0,
                            places, offsets, k, E};
-    const bool vec = D % 8 == 0 && aligned16(x) && !not_on(codes, 8) && row_stride * es % 16 == 0;
+    const bool vec = D % 16 == 0 && aligned16(x) && aligned16(codes) && row_stride * es % 16 == 0;
     return dtype == DS_BF16 ? launch_quantise<__nv_bfloat16>(p, 1, vec, true, stream)
                             : launch_quantise<float>(p, 1, vec, true, stream);
 }
