@@ -26,8 +26,7 @@
 
 namespace dsk {
 
-constexpr int kLogThreads = 256;
-constexpr int kLogWarps = kLogThreads / 32;
+constexpr int kLogThreads = 256, kLogFewThreads = 128;  // of a CTA: a cluster's, a row's own
 constexpr int kLogCluster = 16;      // most CTAs to a row
 constexpr int kLogMaxTop = 32;
 constexpr int kLogGroups = 64;       // groups of threads whose maxima give the first threshold
@@ -164,12 +163,14 @@ __device__ __forceinline__ void bounded(uint4 q, float (&v)[8]) {
     unpack16(make_uint4(raise(q.x), raise(q.y), raise(q.z), raise(q.w)), v);
 }
 
+// NT threads share a row's part.
+template <int NT>
 struct LogShared {
     uint64_t list[kLogList];
     uint64_t best[kLogMaxTop];  // the largest so far, in order
     float group[kLogGroups];
-    uint64_t reduce[kLogWarps];
-    Part parts[kLogWarps];
+    uint64_t reduce[NT / 32];
+    Part parts[NT / 32];
     uint32_t edge;              // as a key
     int count, kept;
     // the row's first CTA: what every CTA of the cluster found, written by them
@@ -181,9 +182,10 @@ struct LogShared {
 // The `top` largest of list[0 .. count), in order, to best[] and the list's begin: each entry's rank is
 // the number of larger ones.  Called by all threads; list and count are complete.  Returns what all
 // later numbers have to exceed.
-__device__ __forceinline__ float cut_list(LogShared& sh, int count, int top) {
+template <int NT>
+__device__ __forceinline__ float cut_list(LogShared<NT>& sh, int count, int top) {
     const int part = threadIdx.x % 4;  // four threads count together
-    for (int i0 = 0; i0 < count; i0 += kLogThreads / 4) {
+    for (int i0 = 0; i0 < count; i0 += NT / 4) {
         const int i = i0 + static_cast<int>(threadIdx.x) / 4;
         const uint64_t k = i < count ? sh.list[i] : ~0ull;
         int above = 0;
@@ -204,9 +206,9 @@ __device__ __forceinline__ float cut_list(LogShared& sh, int count, int top) {
 
 // A number that at least `top` of the CTA's present numbers reach, from the maxima of 64 groups of them (a
 // thread's is `most`): the largest group maximum that `top` of them reach, -inf where there are too few.
-__device__ __forceinline__ float group_edge(LogShared& sh, float most, int top) {
-    constexpr int GROUP = kLogThreads / kLogGroups;
-    static_assert(GROUP == 4, "four threads make a group, and count for it");
+template <int NT>
+__device__ __forceinline__ float group_edge(LogShared<NT>& sh, float most, int top) {
+    constexpr int GROUP = NT / kLogGroups;
     const int tid = threadIdx.x, lane = tid & 31;
     const float g = lanes_max<GROUP>(most);
     if (lane % GROUP == 0) sh.group[tid / GROUP] = g;
@@ -214,12 +216,12 @@ __device__ __forceinline__ float group_edge(LogShared& sh, float most, int top) 
     __syncthreads();
     int reach = 0;  // how many maxima reach the thread's group's: a quarter of them each
 #pragma unroll
-    for (int j = 0; j < kLogGroups / 16; ++j) {
-        const float4 o = reinterpret_cast<const float4*>(sh.group)[(lane % GROUP) * (kLogGroups / 16) + j];
+    for (int j = 0; j < kLogGroups / 4 / GROUP; ++j) {
+        const float4 o = reinterpret_cast<const float4*>(sh.group)[(lane % GROUP) * (kLogGroups / 4 / GROUP) + j];
         reach += (o.x >= g ? 1 : 0) + (o.y >= g ? 1 : 0) + (o.z >= g ? 1 : 0) + (o.w >= g ? 1 : 0);
     }
-    reach += __shfl_xor_sync(kLanes, reach, 1);
-    reach += __shfl_xor_sync(kLanes, reach, 2);
+#pragma unroll
+    for (int d = 1; d < GROUP; d <<= 1) reach += __shfl_xor_sync(kLanes, reach, d);
     const uint32_t best = __reduce_max_sync(kLanes, reach >= top ? key_f32(__float_as_uint(g + 0.f)) : 0u);
     if (lane == 0) atomicMax(&sh.edge, best);
     __syncthreads();
@@ -230,12 +232,13 @@ __device__ __forceinline__ float group_edge(LogShared& sh, float most, int top) 
 // The `top` largest of the CTAs' lists all_best[r * 32 ..], each in order: lane i of each warp gets the i-th, 0 for
 // none.  Pairs of lists become one until one is left: an entry's rank is its own in its list and the number of
 // larger ones in the other (binary search).
-__device__ __forceinline__ uint64_t merge_lists(LogShared& sh, int lists, int top) {
+template <int NT>
+__device__ __forceinline__ uint64_t merge_lists(LogShared<NT>& sh, int lists, int top) {
     static_assert(kLogList >= kLogCluster * kLogMaxTop / 2, "lists take turns in two arrays");
     const int lane = threadIdx.x & 31;
     uint64_t *from = sh.all_best, *to = sh.list;
     for (; lists > 1; lists /= 2) {
-        for (int i = threadIdx.x; i < lists * kLogMaxTop; i += kLogThreads) {
+        for (int i = threadIdx.x; i < lists * kLogMaxTop; i += NT) {
             const int mine = i / kLogMaxTop, other = mine ^ 1, at = i % kLogMaxTop;
             const int kept = sh.all_kept[mine], others = sh.all_kept[other];
             if (at < kept) {
@@ -263,19 +266,19 @@ __device__ __forceinline__ uint64_t merge_lists(LogShared& sh, int lists, int to
 // The `top` largest of words [first, last) of a row, to best[]: for rows where the short list did not do
 // (rising ones, or thousands of equal numbers).  Chunk by chunk: an edge from the chunk's maxima first;
 // where even that leaves too many, one number at a time.
-template <typename T>
-__device__ __noinline__ void largest_slowly(LogShared& sh, const T* x, int first, int last, int shift, int V, int top) {
+template <typename T, int NT>
+__device__ __noinline__ void largest_slowly(LogShared<NT>& sh, const T* x, int first, int last, int shift, int V, int top) {
     constexpr int PER = kPer<T>, U = kLogHeld / PER;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float edge = -INFINITY;
     __syncthreads();
     if (tid == 0) sh.count = sh.kept = 0;
     __syncthreads();
-    for (int g0 = first; g0 < last; g0 += kLogThreads * U) {
+    for (int g0 = first; g0 < last; g0 += NT * U) {
         float most = -INFINITY;
 #pragma unroll 1
         for (int u = 0; u < U; ++u) {
-            const int g = g0 + u * kLogThreads + tid;
+            const int g = g0 + u * NT + tid;
             if (g < last) most = fmaxf(most, word_max<T>(row_word(x, g, shift, V)));
         }
         // numbers at the edge of earlier chunks lose to those, at this chunk's they may win
@@ -284,7 +287,7 @@ __device__ __noinline__ void largest_slowly(LogShared& sh, const T* x, int first
         if (equal ? most >= e : most > e) {
 #pragma unroll 1
             for (int u = 0; u < U; ++u) {
-                const int g = g0 + u * kLogThreads + tid, at = g * PER - shift;
+                const int g = g0 + u * NT + tid, at = g * PER - shift;
                 float v[PER];
                 unpack16(g < last ? row_word(x, g, shift, V) : no_word<T>(), v);
 #pragma unroll
@@ -304,7 +307,7 @@ __device__ __noinline__ void largest_slowly(LogShared& sh, const T* x, int first
                 uint64_t k = 0;
 #pragma unroll 1
                 for (int u = 0; u < U; ++u) {
-                    const int g = g0 + u * kLogThreads + tid, at = g * PER - shift;
+                    const int g = g0 + u * NT + tid, at = g * PER - shift;
                     float v[PER];
                     unpack16(g < last ? row_word(x, g, shift, V) : no_word<T>(), v);
 #pragma unroll
@@ -321,7 +324,7 @@ __device__ __noinline__ void largest_slowly(LogShared& sh, const T* x, int first
                 if (lane == 0) sh.reduce[warp] = k;
                 __syncthreads();
                 k = 0;
-                for (int w = 0; w < kLogWarps; ++w) k = sh.reduce[w] > k ? sh.reduce[w] : k;
+                for (int w = 0; w < NT / 32; ++w) k = sh.reduce[w] > k ? sh.reduce[w] : k;
                 __syncthreads();
                 if (k == 0) break;
                 if (tid == 0) sh.list[count] = k;
@@ -334,10 +337,10 @@ __device__ __noinline__ void largest_slowly(LogShared& sh, const T* x, int first
     }
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const LogParams p) {
-    constexpr int PER = kPer<T>, U = kLogHeld / PER, CHUNK = kLogThreads * U;
-    __shared__ __align__(16) LogShared sh;
+template <typename T, int NT, bool TOP>
+__global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const LogParams p) {
+    constexpr int PER = kPer<T>, U = kLogHeld / PER, CHUNK = NT * U;
+    __shared__ __align__(16) LogShared<NT> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ctas = gridDim.x, rank = blockIdx.x;  // of the row
     const int64_t row = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
@@ -371,11 +374,11 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
         if (g0 > 0 && g0 + CHUNK <= whole) {
             const T* at = x + (static_cast<int64_t>(g0 + tid) * PER - shift);
 #pragma unroll
-            for (int u = 0; u < U; ++u) q[u] = *reinterpret_cast<const uint4*>(at + u * kLogThreads * PER);
+            for (int u = 0; u < U; ++u) q[u] = *reinterpret_cast<const uint4*>(at + u * NT * PER);
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int g = g0 + u * kLogThreads + tid;
+                const int g = g0 + u * NT + tid;
                 q[u] = g < last ? row_word(x, g, shift, p.V) : no_word<T>();
             }
         }
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
                         if (!(equal ? wm >= e : wm > e)) continue;
                         float v[PER];
                         unpack16(q[u], v);
-                        const int at = (g0 + u * kLogThreads + tid) * PER - shift;
+                        const int at = (g0 + u * NT + tid) * PER - shift;
 #pragma unroll
                         for (int j = 0; j < PER; ++j)
                             if (equal ? v[j] >= e : v[j] > e) {
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kLogThreads, 4) ds_token_logprobs_kernel(const
     if (lane == 0) sh.parts[warp] = a;
     __syncthreads();
     Part all = none;
-    if (warp == 0) all = over(lane < kLogWarps ? sh.parts[lane] : none, std::integral_constant<int, 32>());
+    if (warp == 0) all = over(lane < NT / 32 ? sh.parts[lane] : none, std::integral_constant<int, 32>());
     if (ctas > 1) {
         // to the row's first CTA
         cluster_wait();  // it runs
@@ -607,8 +610,10 @@ __global__ void __launch_bounds__(kBackThreads) ds_token_logprobs_backward_kerne
 // ---------------------------------------------------------------- host --------------
 template <typename T>
 static ds_status launch_logprobs(LogParams p, int sms, cudaStream_t stream) {
-    // a CTA to a row where rows are many; else as many as give every SM two, of 32 numbers a thread
-    // at least
+    // rows that are many have a CTA of kLogFewThreads each: they take turns on an SM, and their barriers are between
+    // fewer warps; else a cluster to a row, as many larger CTAs as give every SM two, of 32 numbers a thread at
+    // least (4099 x 32003 bf16 with one token: 64 us with 128 threads, 73 with 256; one row of 129280 fp32 with 20:
+    // 11.5 and 7.7)
     constexpr int PER = kPer<T>, CHUNK = kLogThreads * kLogHeld;
     const int64_t words = (static_cast<int64_t>(p.V) + 2 * PER - 2) / PER;
     int ctas = 1;
@@ -616,7 +621,11 @@ static ds_status launch_logprobs(LogParams p, int sms, cudaStream_t stream) {
     p.per_cta = static_cast<int32_t>((words + ctas - 1) / ctas);
     const unsigned y = static_cast<unsigned>(p.rows < 65535 ? p.rows : 65535);
     const dim3 grid(ctas, y, static_cast<unsigned>((p.rows + y - 1) / y));
-    const auto kern = p.top > 0 ? ds_token_logprobs_kernel<T, true> : ds_token_logprobs_kernel<T, false>;
+    if (ctas == 1 && p.rows >= 2 * sms) {
+        const auto kern = p.top > 0 ? ds_token_logprobs_kernel<T, kLogFewThreads, true> : ds_token_logprobs_kernel<T, kLogFewThreads, false>;
+        return launch_pdl(kern, grid, kLogFewThreads, 0, 1, stream, p);
+    }
+    const auto kern = p.top > 0 ? ds_token_logprobs_kernel<T, kLogThreads, true> : ds_token_logprobs_kernel<T, kLogThreads, false>;
     if (ctas > 8 && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return DS_ERR_CUDA;
     return launch_pdl(kern, grid, kLogThreads, 0, ctas, stream, p);
