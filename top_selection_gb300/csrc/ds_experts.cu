@@ -475,9 +475,11 @@ ds_status ds_expert_sort(const int32_t* experts, int64_t tokens, int32_t k, int3
     p.per_warp = ((p.per_cta + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
     p.warps = p.per_warp > 0 ? static_cast<int32_t>((p.per_cta + p.per_warp - 1) / p.per_warp) : 0;
     const size_t smem = static_cast<size_t>(p.warps) * E * sizeof(int32_t);
-    if (cudaFuncSetAttribute(ds_expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSortWarps * kSortMaxE * static_cast<int>(sizeof(int32_t))) != cudaSuccess ||
-        cudaFuncSetAttribute(ds_expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    if (smem > 32768 &&  // (with the kernel's own arrays, past what needs no asking)
+        cudaFuncSetAttribute(ds_expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSortWarps * kSortMaxE * static_cast<int>(sizeof(int32_t))) != cudaSuccess)
+        return DS_ERR_CUDA;
+    if (ctas > 8 && cudaFuncSetAttribute(ds_expert_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return DS_ERR_CUDA;
     // a thread for each expert, a warp for each that has slots
     const int threads = std::max((E + 31) / 32, std::max(p.warps, 1)) * 32;

@@ -8,10 +8,19 @@
 // One pass over the row: a thread keeps m, s and w of what it has seen (rescaled when its m rises),
 // 32 numbers at a time in registers.  The `top` largest are found in the same pass: a threshold
 // that at least `top` numbers reach, from the maxima of groups of threads over the first 32
-// numbers each, then what lies above it goes to a short list, cut back to its `top` largest (which
-// raises the threshold) when it has grown.  Order is by value, then by the lower index, so keys are
-// 64 bits (order-preserving value, inverted index) and distinct.  A row's parts on the CTAs of a
-// cluster are joined by the first, over distributed shared memory, in a fixed order.
+// numbers each; then 16-byte words with a number above it go to a list as they are, which is cut back to its
+// `top` largest numbers (and raises the threshold) after 2, 8, 32 .. chunks and at the end.  Order is by
+// value, then by the lower index, so keys are 64 bits (order-preserving value, inverted index) and
+// distinct.  A row's parts on the CTAs of a cluster are joined by the first, over distributed shared
+// memory, in a fixed order.
+//
+// Long rows are bound by memory (2048 x 129280 bf16: 88 us, 87 % of the copy rate; the gradient 156 us for
+// reading and writing it, the copy rate), short ones by their starts and barriers (4099 x 32003 bf16: 49 us, 79 %),
+// and the top by the cuts' barriers and single steps: 64 us with one token, 85 with 20 (numbers listed one
+// by one: 126).  One row of 129280 fp32 numbers on 16 CTAs takes 2.8 us, with 20 tokens 7.7.  Tried and not kept:
+// rings of bulk copies in shared memory (registers for 20 warps an SM: 84 us with one token), a warp to a row (73),
+// one warp that cuts while the others go on (85), CTAs that take rows in turn with the next row's first words on
+// their way (77).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -30,7 +39,9 @@ constexpr int kLogThreads = 256, kLogFewThreads = 128;  // of a CTA: a cluster's
 constexpr int kLogCluster = 16;      // most CTAs to a row
 constexpr int kLogMaxTop = 32;
 constexpr int kLogGroups = 64;       // groups of threads whose maxima give the first threshold
-constexpr int kLogList = 512;        // places of a CTA's list (and of the join: 16 x 32)
+constexpr int kLogHits = 256;        // words of a CTA's list of those with a number above the edge
+constexpr int kLogFew = 48;          // that are cut without looking for a higher edge first
+constexpr int kLogList = 512;        // numbers to be ranked (and a half of the join's lists, 16 x 32)
 constexpr int kLogHeld = 32;         // numbers a thread holds at a time
 constexpr uint32_t kLanes = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -166,25 +177,27 @@ __device__ __forceinline__ void bounded(uint4 q, float (&v)[8]) {
 // NT threads share a row's part.
 template <int NT>
 struct LogShared {
+    uint4 hit[kLogHits];        // words with a number above the edge, and their numbers in the row
+    int hit_word[kLogHits];
     uint64_t list[kLogList];
     uint64_t best[kLogMaxTop];  // the largest so far, in order
     float group[kLogGroups];
     uint64_t reduce[NT / 32];
     Part parts[NT / 32];
     uint32_t edge;              // as a key
-    int count, kept;
+    int count, kept, hits;
     // the row's first CTA: what every CTA of the cluster found, written by them
     Part all_parts[kLogCluster];
     int all_kept[kLogCluster];
     uint64_t all_best[kLogCluster * kLogMaxTop];
 };
 
-// The `top` largest of list[0 .. count), in order, to best[] and the list's begin: each entry's rank is
-// the number of larger ones.  Called by all threads; list and count are complete.  Returns what all
+// The `top` largest of list[0 .. count), in order, to best[]: an entry's rank is the number of larger ones, which
+// four threads count together.  Called by all threads; list and count are complete.  Returns what all
 // later numbers have to exceed.
 template <int NT>
 __device__ __forceinline__ float cut_list(LogShared<NT>& sh, int count, int top) {
-    const int part = threadIdx.x % 4;  // four threads count together
+    const int part = threadIdx.x % 4;
     for (int i0 = 0; i0 < count; i0 += NT / 4) {
         const int i = i0 + static_cast<int>(threadIdx.x) / 4;
         const uint64_t k = i < count ? sh.list[i] : ~0ull;
@@ -196,12 +209,9 @@ __device__ __forceinline__ float cut_list(LogShared<NT>& sh, int count, int top)
         if (part == 0 && i < count && above < top) sh.best[above] = k;
     }
     const int kept = min(count, top);
-    if (threadIdx.x == 0) sh.kept = sh.count = kept;
+    if (threadIdx.x == 0) sh.kept = kept;
     __syncthreads();
-    if (threadIdx.x < kept) sh.list[threadIdx.x] = sh.best[threadIdx.x];
-    const float edge = kept == top ? key_value(sh.best[top - 1]) : -INFINITY;
-    __syncthreads();
-    return edge;
+    return kept == top ? key_value(sh.best[top - 1]) : -INFINITY;
 }
 
 // A number that at least `top` of the CTA's present numbers reach, from the maxima of 64 groups of them (a
@@ -214,7 +224,7 @@ __device__ __forceinline__ float group_edge(LogShared<NT>& sh, float most, int t
     if (lane % GROUP == 0) sh.group[tid / GROUP] = g;
     if (tid == 0) sh.edge = 0u;
     __syncthreads();
-    int reach = 0;  // how many maxima reach the thread's group's: a quarter of them each
+    int reach = 0;  // how many maxima reach the thread's group's: the group's threads look at a part of them each
 #pragma unroll
     for (int j = 0; j < kLogGroups / 4 / GROUP; ++j) {
         const float4 o = reinterpret_cast<const float4*>(sh.group)[(lane % GROUP) * (kLogGroups / 4 / GROUP) + j];
@@ -227,6 +237,44 @@ __device__ __forceinline__ float group_edge(LogShared<NT>& sh, float most, int t
     __syncthreads();
     const uint32_t key = sh.edge;
     return key == 0u ? -INFINITY : __uint_as_float(unkey_f32(key));
+}
+
+// The `top` largest of best[0 .. kept) and of the listed words' numbers above `edge` (`equal`: at it too), to
+// best[].  Returns the new edge; NaN where the list of words (or of numbers) was too short.
+template <typename T, int NT>
+__device__ __forceinline__ float cut_hits(LogShared<NT>& sh, float edge, bool equal, int shift, int top) {
+    constexpr int PER = kPer<T>;
+    const int tid = threadIdx.x;
+    __syncthreads();
+    const int hits = sh.hits, kept = sh.kept;
+    if (hits > kLogHits) return NAN;
+    if (hits + kept > kLogFew) {  // a higher edge, so that few numbers are left to rank
+        float most = tid < kept ? key_value(sh.best[tid]) : -INFINITY;
+        for (int h = tid; h < hits; h += NT) most = fmaxf(most, word_max<T>(sh.hit[h]));
+        const float higher = group_edge(sh, most, top);
+        if (higher > edge) edge = higher, equal = true;
+    }
+    if (tid == 0) sh.count = 0;
+    __syncthreads();
+    const auto put = [&](uint64_t k) {
+        const int n = atomicAdd(&sh.count, 1);
+        if (n < kLogList) sh.list[n] = k;
+    };
+    if (tid < kept && key_value(sh.best[tid]) >= edge) put(sh.best[tid]);
+#pragma unroll 1
+    for (int h = tid; h < hits; h += NT) {
+        float v[PER];
+        unpack16(sh.hit[h], v);
+        const int at = sh.hit_word[h] * PER - shift;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (equal ? v[j] >= edge : v[j] > edge) put(order_key(v[j], at + j));
+    }
+    __syncthreads();
+    const int count = sh.count;
+    if (tid == 0) sh.hits = 0;
+    if (count > kLogList) return NAN;
+    return cut_list(sh, count, top);
 }
 
 // The `top` largest of the CTAs' lists all_best[r * 32 ..], each in order: lane i of each warp gets the i-th, 0 for
@@ -263,7 +311,7 @@ __device__ __forceinline__ uint64_t merge_lists(LogShared<NT>& sh, int lists, in
     return lane < sh.all_kept[0] ? from[lane] : 0;
 }
 
-// The `top` largest of words [first, last) of a row, to best[]: for rows where the short list did not do
+// The `top` largest of words [first, last) of a row, to best[]: for rows where the list of words did not do
 // (rising ones, or thousands of equal numbers).  Chunk by chunk: an edge from the chunk's maxima first;
 // where even that leaves too many, one number at a time.
 template <typename T, int NT>
@@ -271,10 +319,11 @@ __device__ __noinline__ void largest_slowly(LogShared<NT>& sh, const T* x, int f
     constexpr int PER = kPer<T>, U = kLogHeld / PER;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float edge = -INFINITY;
-    __syncthreads();
-    if (tid == 0) sh.count = sh.kept = 0;
-    __syncthreads();
+    int kept = 0;
     for (int g0 = first; g0 < last; g0 += NT * U) {
+        __syncthreads();
+        if (tid < kept) sh.list[tid] = sh.best[tid];
+        if (tid == 0) sh.count = kept;
         float most = -INFINITY;
 #pragma unroll 1
         for (int u = 0; u < U; ++u) {
@@ -302,7 +351,7 @@ __device__ __noinline__ void largest_slowly(LogShared<NT>& sh, const T* x, int f
         int count = sh.count;
         if (count > kLogList) {
             uint64_t below = ~0ull;
-            count = sh.kept;
+            count = kept;
             for (int i = 0; i < top; ++i) {
                 uint64_t k = 0;
 #pragma unroll 1
@@ -334,6 +383,7 @@ __device__ __noinline__ void largest_slowly(LogShared<NT>& sh, const T* x, int f
         }
         __syncthreads();
         edge = cut_list(sh, count, top);
+        kept = min(count, top);
     }
 }
 
@@ -346,7 +396,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
     const int64_t row = blockIdx.y + static_cast<int64_t>(blockIdx.z) * gridDim.y;
     pdl_launch_dependents();
     if (row >= p.rows) return;  // a whole cluster
-    if (TOP && tid == 0) sh.count = sh.kept = 0;
+    if (TOP && tid == 0) sh.hits = sh.kept = 0;
     const T* x = static_cast<const T*>(p.x) + row * p.stride;
     const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
     const int words = (p.V + shift + PER - 1) / PER;
@@ -367,8 +417,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
     if (tid == 0 && rank == 0 && ctas > 1) look_up();
     Part a = {-INFINITY, 0.f, 0.f};
     float edge = -INFINITY;  // at least `top` numbers seen reach it (or it is -inf): later ones have to exceed it
+    bool reached = false;    // numbers at the edge itself are listed as well
     bool slow = false;       // the list was too short
-    int chunk = 0, cut_at = 4;
+    int chunk = 0, cut_at = 2;
     for (int g0 = first; g0 < last; g0 += CHUNK, ++chunk) {
         uint4 q[U];
         if (g0 > 0 && g0 + CHUNK <= whole) {
@@ -382,9 +433,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
                 q[u] = g < last ? row_word(x, g, shift, p.V) : no_word<T>();
             }
         }
-        float most = word_max<T>(q[0]);
+        float top_of[U], most = -INFINITY;
 #pragma unroll
-        for (int u = 1; u < U; ++u) most = fmaxf(most, word_max<T>(q[u]));
+        for (int u = 0; u < U; ++u) top_of[u] = word_max<T>(q[u]), most = fmaxf(most, top_of[u]);
         rise(a, most);
         if (!is_far(a.m)) {
             const float r = reference(a.m);
@@ -413,40 +464,28 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
                 for (int j = 0; j < PER; ++j) a.s += v[j] == a.m ? 1.f : 0.f;
             }
         }
-        if constexpr (TOP) {
-            if (!slow) {
-                bool equal = false;
-                float e = edge;
-                if (chunk == 0) {
-                    e = group_edge(sh, most, p.top);
-                    equal = e > -INFINITY;
-                }
-                if (equal ? most >= e : most > e) {
+        if (TOP && !slow) {
+            if (chunk == 0) {
+                edge = group_edge(sh, most, p.top);
+                reached = edge > -INFINITY;
+            }
+            // words with a number above the edge are listed, of the first chunk those with one at it too
+            const bool equal = chunk == 0 && reached;
+            if (equal ? most >= edge : most > edge) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const float wm = word_max<T>(q[u]);
-                        if (!(equal ? wm >= e : wm > e)) continue;
-                        float v[PER];
-                        unpack16(q[u], v);
-                        const int at = (g0 + u * NT + tid) * PER - shift;
-#pragma unroll
-                        for (int j = 0; j < PER; ++j)
-                            if (equal ? v[j] >= e : v[j] > e) {
-                                const int n = atomicAdd(&sh.count, 1);
-                                if (n < kLogList) sh.list[n] = order_key(v[j], at + j);
-                            }
+                for (int u = 0; u < U; ++u)
+                    if (equal ? top_of[u] >= edge : top_of[u] > edge) {
+                        const int n = atomicAdd(&sh.hits, 1);
+                        if (n < kLogHits) sh.hit[n] = q[u], sh.hit_word[n] = g0 + u * NT + tid;
                     }
-                }
-                // cut after 1, 4, 16 .. chunks and at the end: in between the list grows by a few times `top`
-                // where numbers come in no order
-                if (chunk == 0 || chunk + 1 == cut_at || g0 + CHUNK >= last) {
-                    if (chunk + 1 == cut_at) cut_at *= 4;
-                    __syncthreads();
-                    const int count = sh.count;
-                    __syncthreads();
-                    slow = count > kLogList;
-                    if (!slow) edge = cut_list(sh, count, p.top);
-                }
+            }
+            // cut after 2, 8, 32 .. chunks and at the end: in between the list grows by a few times `top` where
+            // numbers come in no order
+            if (chunk + 1 == cut_at || g0 + CHUNK >= last) {
+                if (chunk + 1 == cut_at) cut_at *= 4;
+                edge = cut_hits<T>(sh, edge, reached, shift, p.top);
+                reached = false;
+                slow = edge != edge;
             }
         }
     }
