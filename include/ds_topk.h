@@ -529,10 +529,10 @@ ds_status ds_expert_gather_quantised(const void* x, int32_t dtype, int64_t token
  *               w_row_stride;  w_scales [E, ceil(N / 128), ceil(K / 128)], any fp32 scales
  *   offsets     [E + 1] int32, ascending, or NULL: one expert (E = 1) has all rows
  *   dtype, out  [rows, N] bf16 or fp32
- * K is a multiple of 16, x, w and their strides are 16-byte aligned; 0 <= rows <= 2^30, E <= 512, N and
- * K <= 2^24.  Scales whose product leaves fp32's range do not give finite numbers.  A wait inside the
- * kernel that runs out (about a second) is recorded for ds_get_device_status, and the outputs are then
- * undefined.
+ * K is a multiple of 16, x, w and their strides are 16-byte aligned, w_matrix_stride > 0 with several
+ * experts; 0 <= rows <= 2^30, E <= 512, N and K <= 2^24.  Scales whose product leaves fp32's range
+ * do not give finite numbers.  A wait inside the kernel that runs out (about a second) is recorded for
+ * ds_get_device_status, and the outputs are then undefined.
  */
 ds_status ds_expert_product(const void* x, const float* x_scales, int64_t rows, int32_t K, int64_t x_stride,
                             const void* w, const float* w_scales, int32_t E, int32_t N, int64_t w_row_stride,

@@ -188,6 +188,7 @@ def test_quantise_blocks_refuses(ds, change, want):
     (dict(x_stride=240), INVALID),
     (dict(w_row_stride=240), INVALID),
     (dict(w_matrix_stride=-16), INVALID),
+    (dict(w_matrix_stride=0), INVALID),               # one matrix for all experts
     (dict(offsets=0), INVALID),                       # several experts without offsets
     (dict(x=0), INVALID),
     (dict(x_scales=0), INVALID),

