@@ -406,6 +406,23 @@ def test_expert_product_rows_outside(ds, dtype, T, E, N, K):
     assert bool(torch.isnan(got[bad]).all()) and bool(torch.isnan(got[int(offsets[E - 1]):int(offsets[E]), 5]).all())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,E,N,K", [(20000, 4, 261, 144), (20000, 4, 268, 144), (20000, 30, 1000, 64), (40001, 3, 520, 272),
+                                     (25000, 9, 392, 400), (6000, 1, 1304, 528)])
+def test_expert_product_of_many_rows(ds, dtype, T, E, N, K):
+    """Tiles of 256 outputs, stored by bulk copies where rows allow it: experts' ends within 32 rows, outputs
+    that end within a box, rows that start on 2, 4, 8 and 16 bytes, and rows of nobody around them."""
+    g = gen(T + N + K)
+    x, xs, w, ws = operands(g, T, E, N, K)
+    a, b = 3, T - 77
+    offsets = (a + spread(g, b - a, E)).int()
+    want, size = ref.product(x, xs, w, ws, offsets)
+    got = ds.expert_product(x, xs, w, ws, offsets, dtype=dtype)
+    check_product(got, want, size, K, dtype)
+    assert not bool(got[:a].any()) and not bool(got[b:].any())
+    assert torch.equal(got, ds.expert_product(x, xs, w, ws, offsets, dtype=dtype))
+
+
 def test_expert_product_strides(ds):
     g = gen(9)
     x, xs, w, ws = operands(g, 70, 3, 50, 160)
@@ -510,6 +527,27 @@ def test_layer_captured_and_on_another_stream(ds):
         graph.replay()
         assert torch.equal(out, layer(v)[0])
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T,V", [(1, 129280), (700, 1003)])
+def test_log_probabilities_captured(ds, T, V):
+    """Forward and backward in a graph, replayed on other logits: one row on a cluster, and many rows."""
+    x, tokens = rows_of(torch.bfloat16, T, V, 5)
+    grad = normal(gen(6), T)
+
+    def step(x):
+        lp, lse, H, top_lp, top = ds.token_logprobs(x, tokens, top=9)
+        return lp, lse, H, top_lp, top, ds.token_logprobs_backward(grad, x, tokens, lse, grad_entropy=grad, entropy=H)
+    step(x)
+    held = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(held)
+    other, _ = rows_of(torch.bfloat16, T, V, 7)
+    for v in (x, other, x):
+        held.copy_(v)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(out, step(v)))
 
 
 def test_two_streams_at_once(ds):

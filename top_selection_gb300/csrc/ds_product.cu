@@ -17,15 +17,16 @@
 // Few tiles: the CTAs of a cluster split a tile's blocks, and add their sums over distributed shared
 // memory in a fixed order.
 //
-// 32768 rows over 64 experts of 4096 x 2048: 293 us, 1877 TFLOP/s (8192 rows by 8192 x 8192: 2514), tensor
-// pipe 46 %; with experts of few rows the weights' bytes bound it (512 rows over 64 experts of 2048 x 4096: 90
-// us, 6.0 TB/s).  With the sums left out the first takes 260 us, with three quarters of the products left
-// out as well 239; three stages of loads instead of four change nothing: what bounds it is the round of
-// products, sums and products again over the two buffers that tensor memory holds, and a tile's stores
-// (46 us of the 293; as lines of 1 KB they would take 24).  Tried and not kept: pairs of CTAs
-// (cta_group::2), whose round goes between two SMs for every block (359); the weights' tiles multicast to
-// two CTAs (316); sums loaded 64 columns at a time (296) or a load ahead (375, for want of registers); plain
-// fp32 instructions for the sums (323).
+// 32768 rows over 64 experts of 4096 x 2048: 277 us, 1985 TFLOP/s (8192 rows by 8192 x 8192: 2385; cuBLAS
+// reaches 1895 on bf16), the tensor pipe at half; with experts of few rows the weights' bytes bound it (512 rows
+// over 64 experts of 2048 x 4096: 90 us, 6.0 TB/s).  Wide tiles are stored by bulk copies from shared memory while
+// the next tile is multiplied: stores of 32 bytes a lane took 46 us of 293, and a stage of loads is given up
+// for it (four stages instead of three: 8192 x 8192 x 8192 in 438 us, the others the same).  A block of a
+// tile takes about 510 ns, with the sums left out 450: loads, products and sums bound it together.  Order of
+// the tiles, one copy of 128 rows instead of four, and the copies' L2 promotion change nothing.  Tried and not
+// kept (us, of 293): pairs of CTAs (cta_group::2), whose round of products and sums goes between two SMs for
+// every block (359); the weights' tiles multicast to two CTAs (316); sums loaded 64 columns at a time (296) or a
+// load ahead (375, for want of registers); plain fp32 instructions for the sums (323).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -53,7 +54,7 @@ constexpr int kProdMaxSplit = 8;
 // BN outputs to a tile.
 template <int BN>
 struct ProdShape {
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
+    static constexpr int STAGES = BN == 256 ? 3 : 6;
     static constexpr int BUFS = 512 / BN;
     static constexpr int A_BYTES = kProdRows * kProdBlock, B_BYTES = BN * kProdBlock;
     static constexpr int STAGE = A_BYTES + B_BYTES;
@@ -61,7 +62,9 @@ struct ProdShape {
     // 12 warps of 168 registers at launch; until the roles end, the 8 that add up and the 4 others share them
     // out anew
     static constexpr int SUM_REGISTERS = BN == 256 ? 224 : 208, OTHER_REGISTERS = 3 * 168 - 2 * SUM_REGISTERS;
-    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + 1024;
+    // wide tiles leave through shared memory: 8 KB a warp
+    static constexpr int OUT = BN == 256 ? 8192 : 0;
+    static constexpr size_t SMEM = static_cast<size_t>(STAGES) * STAGE + kProdSumWarps * OUT + 1024;
 };
 
 struct ProdParams {
@@ -76,6 +79,7 @@ struct ProdParams {
     int32_t n_tiles;      // tiles of BN outputs
     int32_t E;
     int32_t vec;          // rows of out start on 32 bytes
+    int32_t bulk;         // rows of out start on 16 bytes: wide tiles are stored by bulk copies
 };
 
 struct ProdShared {
@@ -102,6 +106,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
+// A box from shared to global memory; what lies outside of the tensor is left out.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void stores_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The thread's stores have read their shared memory; or have been written.
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t columns) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(columns)
                  : "memory");
@@ -209,7 +223,8 @@ __device__ __forceinline__ void put_out(O* p, float v) { row_put(p, v); }
 
 template <int BN, typename O, bool SPLIT>
 __global__ void __launch_bounds__(kProdThreads, 1)
-ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w, const ProdParams p) {
+ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+                         const __grid_constant__ CUtensorMap map_out, const ProdParams p) {
     using S = ProdShape<BN>;
     extern __shared__ uint8_t sh_raw[];
     __shared__ ProdShared sh;
@@ -413,6 +428,43 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
                                      "f"(sum(4 * c + 1)), "f"(sum(4 * c + 2)), "f"(sum(4 * c + 3))
                                      : "memory");
                 }
+            } else if (S::OUT > 0 && p.bulk && quarter * 32 + 32 <= t.rows) {
+                // the warp's 32 rows by way of its 8 KB, swizzled as the copies expect it: two boxes of 128 bytes a row
+                // at a time, written while the next tile is multiplied (rows that another expert's follow within the
+                // 32 go the other way)
+                constexpr int BOX = 128 / static_cast<int>(sizeof(O));  // outputs of a row in a box
+                const uint32_t base = stage0 + S::STAGES * S::STAGE + warp * S::OUT;
+                const int c0 = t.n0 + side * S::COLS;
+#pragma unroll
+                for (int c = 0; c < S::COLS; c += 2 * BOX) {
+                    if (lane == 0) stores_read();
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {  // 16 bytes each
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if constexpr (sizeof(O) == 2) {
+                                const __nv_bfloat162 h = __floats2bfloat162_rn(sum(c + i * 8 + 2 * j), sum(c + i * 8 + 2 * j + 1));
+                                w[j] = *reinterpret_cast<const uint32_t*>(&h);
+                            } else {
+                                w[j] = __float_as_uint(sum(c + i * 4 + j));
+                            }
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         base + (i / 8) * 4096 + lane * 128 + ((i % 8) ^ (lane & 7)) * 16),
+                                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int y = static_cast<int>(t.row0) + quarter * 32;
+                        if (c0 + c < p.N) tma_store_2d(&map_out, base, (c0 + c) * static_cast<int>(sizeof(O)), y);
+                        if (c0 + c + BOX < p.N) tma_store_2d(&map_out, base + 4096, (c0 + c + BOX) * static_cast<int>(sizeof(O)), y);
+                        stores_commit();
+                    }
+                }
             } else if (r < t.rows) {
                 const int c0 = t.n0 + side * S::COLS;
                 O* out = static_cast<O*>(p.out) + (t.row0 + r) * p.N + c0;
@@ -440,6 +492,7 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
                 }
             }
         }
+        if (S::OUT > 0 && lane == 0) stores_done();
         __syncwarp();
         fewer_registers<168>();
     }
@@ -532,19 +585,18 @@ static bool byte_map(CUtensorMap& map, const void* base, int dims, int64_t K, in
 }
 
 template <int BN, typename O, bool SPLIT>
-static ds_status launch_product(const CUtensorMap& mx, const CUtensorMap& mw, const ProdParams& p, int64_t ctas, int splits,
-                                cudaStream_t stream) {
+static ds_status launch_product(const CUtensorMap& mx, const CUtensorMap& mw, const CUtensorMap& mo, const ProdParams& p,
+                                int64_t ctas, int splits, cudaStream_t stream) {
     const auto kern = ds_expert_product_kernel<BN, O, SPLIT>;
     const size_t smem = ProdShape<BN>::SMEM;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
         return DS_ERR_CUDA;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kProdThreads, smem, splits, stream, mx, mw, p);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), kProdThreads, smem, splits, stream, mx, mw, mo, p);
 }
 
 // Outputs to a tile, 128 or 256: those whose rounds of tiles over the SMs take less.  A block of a tile takes 400
-// or 490 ns where its operands come from L2 (8192 rows by 8192 x 8192: 688 and 438 us), bound by shared
-// memory, which takes in 32 or 48 KB and gives them to the products; or the time of its weights from DRAM, 16 or
-// 32 KB at an SM's share of 45 bytes a ns, over the row tiles that share them.
+// or 510 ns where its operands come from L2 (8192 rows by 8192 x 8192: 688 and 461 us), or the time of its weights
+// from DRAM, 16 or 32 KB at an SM's share of 45 bytes a ns, over the row tiles that share them.
 static int product_outputs(int64_t rows, int64_t E, int64_t N, int sms) {
     const double used = static_cast<double>(rows < E ? rows : E);  // experts with a row, at most
     // half a tile more for each expert than its rows fill
@@ -553,7 +605,7 @@ static int product_outputs(int64_t rows, int64_t E, int64_t N, int sms) {
     int best = 128;
     for (int bn = 128; bn <= 256; bn *= 2) {
         const double rounds = std::ceil(tall * static_cast<double>((N + bn - 1) / bn) / sms);
-        const double time = rounds * std::max(bn == 128 ? 400.0 : 490.0, bn * 128 / 45.0 * used / tall);
+        const double time = rounds * std::max(bn == 128 ? 400.0 : 510.0, bn * 128 / 45.0 * used / tall);
         if (bn == 128 || time < least) best = bn, least = time;
     }
     return best;
@@ -594,6 +646,7 @@ extern "C" ds_status ds_expert_product(const void* x, const float* x_scales, int
     p.n_blocks = (N + 127) / 128;
     p.E = E;
     p.vec = !off_by(out, 32) && static_cast<int64_t>(N) * es % 32 == 0;
+    p.bulk = aligned16(out) && static_cast<int64_t>(N) * es % 16 == 0;
     const int bn = product_outputs(rows, E, N, info.sms);
     const bool wide = bn == 256;
     p.n_tiles = (N + bn - 1) / bn;
@@ -602,17 +655,19 @@ extern "C" ds_status ds_expert_product(const void* x, const float* x_scales, int
     int splits = 1;
     if (!wide)
         while (splits < kProdMaxSplit && tiles * splits * 2 <= info.sms && p.blocks >= splits * 4) splits *= 2;
-    CUtensorMap mx, mw;
+    CUtensorMap mx, mw, mo = {};
     if (!byte_map(mx, x, 2, K, rows, 1, x_stride, 0, kProdBox) ||
         !byte_map(mw, w, 3, K, N, E, w_row_stride, E > 1 ? w_matrix_stride : w_row_stride, bn))
         return DS_ERR_CUDA;
+    if (wide && p.bulk && !byte_map(mo, out, 2, static_cast<int64_t>(N) * es, rows, 1, static_cast<int64_t>(N) * es, 0, 32))
+        return DS_ERR_CUDA;
     const int64_t ctas = splits > 1 ? tiles * splits : tiles < info.sms ? tiles : info.sms;
     if (wide)
-        return dtype == DS_BF16 ? launch_product<256, __nv_bfloat16, false>(mx, mw, p, ctas, 1, stream)
-                                : launch_product<256, float, false>(mx, mw, p, ctas, 1, stream);
+        return dtype == DS_BF16 ? launch_product<256, __nv_bfloat16, false>(mx, mw, mo, p, ctas, 1, stream)
+                                : launch_product<256, float, false>(mx, mw, mo, p, ctas, 1, stream);
     if (splits > 1)
-        return dtype == DS_BF16 ? launch_product<128, __nv_bfloat16, true>(mx, mw, p, ctas, splits, stream)
-                                : launch_product<128, float, true>(mx, mw, p, ctas, splits, stream);
-    return dtype == DS_BF16 ? launch_product<128, __nv_bfloat16, false>(mx, mw, p, ctas, 1, stream)
-                            : launch_product<128, float, false>(mx, mw, p, ctas, 1, stream);
+        return dtype == DS_BF16 ? launch_product<128, __nv_bfloat16, true>(mx, mw, mo, p, ctas, splits, stream)
+                                : launch_product<128, float, true>(mx, mw, mo, p, ctas, splits, stream);
+    return dtype == DS_BF16 ? launch_product<128, __nv_bfloat16, false>(mx, mw, mo, p, ctas, 1, stream)
+                            : launch_product<128, float, false>(mx, mw, mo, p, ctas, 1, stream);
 }
