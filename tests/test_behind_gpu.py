@@ -100,6 +100,24 @@ def test_token_logprobs(ds, dtype, T, V, top, pad, offset):
     check_logprobs(ds, x, tokens, top)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V", [(1, 20), (5, 1405), (400, 1405), (2, 129280)])
+def test_nearly_certain_tokens(ds, dtype, T, V):
+    """A token far above the others has a log probability -log(1 + t) near 0: its error is absolute, not
+    relative to t.  The 1 is a sum's term like others, and each addition to a partial sum that holds it (in a
+    thread, over lanes, warps and CTAs) rounds by up to a half step of a number in [1, 2), 2^-24: the V / 256 + 40
+    additions of sum_error.  Its own exponential is off by 2^-22 and its argument moves it by 2^-23, the rest of
+    sum_error; logarithm, difference and result round once more each."""
+    x, _ = rows_of(dtype, T, V, V)
+    tokens = torch.arange(T, device="cuda").int() % V
+    gap = torch.linspace(4.0, 16.0, T, device="cuda") + math.log(V)
+    x[torch.arange(T, device="cuda"), tokens.long()] = (x.amax(-1).float() + gap).to(dtype)
+    lp = ds.token_logprobs(x, tokens, top=1)[0].double()
+    want = ref.logprobs(x, tokens)[0]
+    assert bool((want > -0.02).all()) and bool((want < 0).all())
+    assert bool(((lp - want).abs() <= sum_error(V) + 4 * U * (want.abs() + 1)).all())
+
+
 def masked_rows(dtype, V):
     """Rows whose masks leave little, and rows of equal or ordered numbers."""
     inf = math.inf
