@@ -480,8 +480,8 @@ ds_status ds_token_logprobs_backward(const float* grad_logprobs, const void* log
  * ds_expert_combine_backward, for the gradient `grad` of out and y [tokens * k, D]:
  *   grad_y[places[t, i]] = weights[t, i] * grad[t] (rows behind the last choice: zeros),
  *   grad_weights[t, i] = grad[t] . y[places[t, i]] (0 for no choice); sums in fp32.
- * tokens >= 0, 1 <= k <= 32, tokens * k < 2^31, E <= 512, D >= 1; x, y and grad take a row stride >= D
- * in elements, outputs are contiguous and overlap no input.  places and offsets are those of one
+ * tokens >= 0, 1 <= k <= 32, tokens * k < 2^31, E <= 512, 1 <= D <= 2^30; x, y and grad take a row
+ * stride >= D in elements, outputs are contiguous and overlap no input.  places and offsets are those of one
  * ds_expert_sort (places outside the rows are left out whatever they hold).
  */
 ds_status ds_expert_sort(const int32_t* experts, int64_t tokens, int32_t k, int32_t E, int32_t* places,
@@ -508,8 +508,9 @@ ds_status ds_expert_combine_backward(const void* grad, int64_t grad_stride, cons
  *   block_rows  1 or 128
  *   codes       [matrices, rows, K] bytes;  scales [matrices, ceil(rows / block_rows),
  *               ceil(K / 128)] floats
+ *   1 <= K <= 2^26
  * ds_expert_gather_quantised is ds_expert_gather with rows in that form: codes [tokens * k, D] bytes,
- * scales [tokens * k, ceil(D / 128)]; rows behind the last choice are the form of zeros.
+ * scales [tokens * k, ceil(D / 128)], D <= 2^26; rows behind the last choice are the form of zeros.
  */
 ds_status ds_quantise_blocks(const void* x, int32_t dtype, int64_t matrices, int64_t rows, int32_t K,
                              int64_t matrix_stride, int64_t row_stride, int32_t block_rows, void* codes, float* scales,

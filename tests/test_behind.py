@@ -179,6 +179,25 @@ def test_quantise_blocks_refuses(ds, change, want):
     assert ds.ds_quantise_blocks(**a) == want
 
 
+@pytest.mark.parametrize("D", [(1 << 30) + 1, (1 << 31) - 1])
+def test_exchange_refuses_long_rows(ds, D):
+    """Columns are counted in 32 bits, a stretch of the row past the last one."""
+    rows = dict(dtype=0, D=D, row_stride=D, places=P, tokens=1, k=1)
+    assert ds.ds_expert_gather(x=P, out=P, offsets=P, E=1, **rows) == UNSUPPORTED
+    assert ds.ds_expert_combine(y=P, out=P, rows=1, weights=P, **rows) == UNSUPPORTED
+    assert ds.ds_expert_combine_backward(grad=P, grad_stride=D, y=P, offsets=P, E=1, weights=P, grad_y=P, grad_weights=P,
+                                         **rows) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("K", [(1 << 26) + 1, (1 << 31) - 127, (1 << 31) - 1])
+def test_8_bit_form_refuses_long_rows(ds, K):
+    for block_rows in (1, 128):
+        assert ds.ds_quantise_blocks(x=P, dtype=0, matrices=1, rows=1, K=K, matrix_stride=K, row_stride=K,
+                                     block_rows=block_rows, codes=P, scales=P) == UNSUPPORTED
+    assert ds.ds_expert_gather_quantised(x=P, dtype=0, tokens=1, D=K, row_stride=K, places=P, k=1, offsets=P, E=1, codes=P,
+                                         scales=P) == UNSUPPORTED
+
+
 @pytest.mark.parametrize("change,want", [
     (dict(dtype=2), INVALID),
     (dict(rows=-1), INVALID),

@@ -31,6 +31,7 @@ constexpr int kSortWarps = 32;
 constexpr int kSortCluster = 16;
 constexpr int kSortMaxE = 512;
 constexpr int kMaxChoices = 32;    // one lane per choice
+constexpr int kMaxColumns = 1 << 30;  // counted in 32 bits, a CTA's stretch of a row past the last one
 constexpr uint32_t kEvery = 0xFFFFFFFFu;
 
 // ---------------------------------------------------------------- sort --------------
@@ -448,7 +449,7 @@ static ds_status device_sms(int& sms) {
 
 static ds_status check_exchange(int64_t tokens, int32_t k, int32_t D) {
     if (tokens < 0 || k < 1 || D < 1) return DS_ERR_INVALID_ARG;
-    if (k > kMaxChoices || tokens > 0x7FFFFFFFLL / k) return DS_ERR_UNSUPPORTED;
+    if (k > kMaxChoices || D > kMaxColumns || tokens > 0x7FFFFFFFLL / k) return DS_ERR_UNSUPPORTED;
     return DS_OK;
 }
 

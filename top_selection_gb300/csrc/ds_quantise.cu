@@ -20,6 +20,7 @@ namespace dsk {
 
 constexpr int kQuantThreads = 256;
 constexpr int kQuantMaxE = 512, kQuantMaxK = 32;
+constexpr int kQuantMaxColumns = 1 << 26;  // 32768 runs of 16 blocks (a grid has 65535); columns are counted in 32 bits
 
 struct QuantParams {
     const void* x;
@@ -233,6 +234,7 @@ ds_status ds_quantise_blocks(const void* x, int32_t dtype, int64_t matrices, int
     if ((dtype != DS_BF16 && dtype != DS_FP32) || matrices < 0 || rows < 0 || K < 1 || row_stride < K || matrix_stride < 0 ||
         (block_rows != 1 && block_rows != 128))
         return DS_ERR_INVALID_ARG;
+    if (K > kQuantMaxColumns) return DS_ERR_UNSUPPORTED;
     const int64_t limit = 1LL << 40;  // numbers in all, and their reach in x
     if (rows > limit / K || (rows > 0 && matrices > limit / K / rows) || (rows > 0 && row_stride > (limit << 8) / rows) ||
         (matrices > 0 && matrix_stride > (limit << 8) / matrices))
@@ -255,7 +257,7 @@ ds_status ds_expert_gather_quantised(const void* x, int32_t dtype, int64_t token
                                      float* scales, cudaStream_t stream) {
     if ((dtype != DS_BF16 && dtype != DS_FP32) || tokens < 0 || D < 1 || k < 1 || row_stride < D || E < 1)
         return DS_ERR_INVALID_ARG;
-    if (k > kQuantMaxK || E > kQuantMaxE || tokens > 0x7FFFFFFFLL / k) return DS_ERR_UNSUPPORTED;
+    if (k > kQuantMaxK || E > kQuantMaxE || D > kQuantMaxColumns || tokens > 0x7FFFFFFFLL / k) return DS_ERR_UNSUPPORTED;
     if (tokens == 0) return DS_OK;
     if (!x || !places || !offsets || !codes || !scales) return DS_ERR_INVALID_ARG;
     const int es = dtype == DS_BF16 ? 2 : 4;
