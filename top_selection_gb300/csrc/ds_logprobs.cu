@@ -66,24 +66,22 @@ struct LogParams {
     int32_t per_cta;  // 16-byte words of a row to a CTA
 };
 
-// Sums over a part of a row whose largest number is m, relative to 2^r with r = m log2 e as fp32 rounds it: s
-// of 2^y and w of 2^y y, with y = x log2 e - r, one rounding (fma).  Every term and every result is
-// taken relative to the same r, so its rounding cancels.
+// Sums over a part of a row whose largest number is m: s of 2^y and w of 2^y y, with y = (x - m) log2 e.  The
+// difference comes first: it is exact where x lies within a factor of two of m, so that a term is off by
+// roundings of y alone, whatever the size of m.
 struct Part {
     float m, s, w;
 };
 
-// Numbers beyond this leave fp32's range when they are multiplied by log2 e, or their differences do.  fp32's
-// steps are 10^30 there: beside a part's largest number of that size only its equals count.
+// Differences of larger numbers may leave fp32's range.  fp32's steps are 10^30 there: beside a part's largest
+// number of that size only its equals count.
 constexpr float kFar = 1e37f;
 __device__ __forceinline__ bool is_far(float m) { return fabsf(m) > kFar; }
-// r of a part: never contracted with what follows, so that it is the same number everywhere
-__device__ __forceinline__ float reference(float m) { return __fmul_rn(m, kLog2e); }
 
 __device__ __forceinline__ void rise(Part& a, float m) {  // to a larger m
     if (m > a.m) {
         if (a.s > 0.f) {
-            const float d = is_far(m) || is_far(a.m) ? -150.f : fmaxf(reference(a.m) - reference(m), -150.f), f = exp2_term(d);
+            const float d = fmaxf((a.m - m) * kLog2e, -150.f), f = exp2_term(d);
             a.w = f * fmaf(a.s, d, a.w);
             a.s *= f;
         }
@@ -99,6 +97,11 @@ __device__ __forceinline__ float upper(Two a) { return __uint_as_float(static_ca
 __device__ __forceinline__ Two fma_two(Two a, Two b, Two c) {
     Two d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ Two mul_two(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ Two add_two(Two a, Two b) {
@@ -438,8 +441,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
         for (int u = 0; u < U; ++u) top_of[u] = word_max<T>(q[u]), most = fmaxf(most, top_of[u]);
         rise(a, most);
         if (!is_far(a.m)) {
-            const float r = reference(a.m);
-            const Two nr = two(-r, -r), l2e = two(kLog2e, kLog2e);
+            const Two nm = two(-a.m, -a.m), l2e = two(kLog2e, kLog2e);
             Two s = 0, w = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
                 bounded(q[u], v);
 #pragma unroll
                 for (int j = 0; j < PER; j += 2) {
-                    const Two y = fma_two(two(v[j], v[j + 1]), l2e, nr);
+                    const Two y = mul_two(add_two(two(v[j], v[j + 1]), nm), l2e);
                     const Two e = two(exp2_term(lower(y)), exp2_term(upper(y)));
                     s = add_two(s, e);
                     w = fma_two(e, y, w);
@@ -533,16 +535,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
         }
     }
     if (warp != 0) return;
-    const bool some = all.s > 0.f, far = is_far(all.m);
-    const float r = far ? 0.f : reference(all.m), logs = some ? log2f(all.s) : 0.f;
-    const auto log_p = [&](float v) {
-        return !some ? -INFINITY : far || is_far(v) ? (v - all.m) - logs * kLn2 : (fmaf(v, kLog2e, -r) - logs) * kLn2;
-    };
+    const bool some = all.s > 0.f;
+    const float logs = some ? log2f(all.s) : 0.f;
+    const auto log_p = [&](float v) { return some ? (v - all.m) - logs * kLn2 : -INFINITY; };
     if (tid == 0) {
         if (ctas == 1) look_up();
         p.logprobs[row] = token >= 0 ? log_p(given) : 0.f;
-        // r's rounding, as far as the sums are relative to it, is taken out again
-        p.lse[row] = all.m + (far ? logs : logs - fmaf(all.m, kLog2e, -r)) * kLn2;
+        p.lse[row] = all.m + logs * kLn2;
         p.entropy[row] = some ? fmaxf((logs - all.w / all.s) * kLn2, 0.f) : 0.f;
     }
     if constexpr (TOP) {
