@@ -458,8 +458,8 @@ ds_status ds_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int
  *   grad_logits     rows of V elements of dtype, row r at element r * grad_stride (>= V); every
  *                   element is written; must not overlap logits
  * A row without a given token has the entropy's part alone, a row of -inf alone zeros.  The top tokens'
- * log probabilities have no gradient here.  lse is rounded to fp32, which moves a row's p by 2^-24 |lse|
- * of themselves.
+ * log probabilities have no gradient here.  lse is rounded to fp32, which moves a row's p by at most 2^-19 of
+ * themselves up to |lse| = 64; a row beyond is summed once more, so that p keeps its digits there too.
  */
 ds_status ds_token_logprobs_backward(const float* grad_logprobs, const void* logits, int32_t dtype, int64_t rows,
                                      int64_t V, int64_t row_stride, const int32_t* tokens, const float* lse,

@@ -66,3 +66,80 @@ def test_token_logprobs_of_large_logits(ds, dtype, V, top):
     for r in range(x.shape[0]):                   # one row: a cluster to it
         base.check_logprobs(ds, x[r:r + 1], tokens[r:r + 1], top)
     base.check_logprobs(ds, x.repeat(9, 1), tokens.repeat(9), top)  # as many rows as take a CTA each
+
+
+def check_gradient(ds, x, tokens, g, h):
+    """The gradient from the kernel's own lse.  log p = (x - lse) - rest, where rest is what lse lost when it was rounded:
+    up to |lse| = 64 it is left out, which moves p by half a step of numbers in [32, 64], 2^-19 = 32 U; beyond
+    that it is taken from a sum over the row again, off by sum_error and by 2 U |log|.  The two
+    differences round by U of their results, of which the first is log p + rest, |rest| <= 43 (numbers' steps
+    next to lse up to twice log V, beyond that log V itself); p's argument by U |log p|."""
+    V = x.shape[1]
+    _, lse, H, _, _ = ds.token_logprobs(x, tokens)
+    got = ds.token_logprobs_backward(g, x, tokens, lse, grad_entropy=h, entropy=H if h is not None else None)
+    # the formula, with the largest logit and log s apart: 64 bits lose log s beside 1e30 too
+    y = x.double() - x.double().amax(-1, keepdim=True)
+    lpd = y - torch.log(torch.exp(y).sum(-1, keepdim=True))
+    p, lps = torch.exp(lpd), lpd.abs().clamp(max=1e6)
+    plogp = torch.where(p > 0, p * lpd, 0.0)
+    there = (tokens >= 0)[:, None]
+    hot = (tokens[:, None] == torch.arange(V, device="cuda")).double()
+    gd = torch.where(there, g.double()[:, None], 0.0)
+    want = gd * (hot - p)
+    size, more = gd.abs(), 0.0
+    rel = 2 * sum_error(V) + U * (32 + 3 * 43 + 4 * lps) + 8 * U
+    if h is not None:
+        hd = h.double()[:, None]
+        want = want - hd * (plogp - p * plogp.sum(-1, keepdim=True))
+        size = size + hd.abs() * (lps + 1 + math.log(V))
+        # the entropy's own error and log p's enter by h p
+        more = hd.abs() * p * (4 * sum_error(V) * (1 + math.log(V)) + rel)
+    limit = p * size * rel + more + half_step(x.dtype) * want.abs() * 1.01 + 2 * U * gd.abs() + 1e-37
+    assert got.dtype == x.dtype and got.shape == x.shape
+    assert bool(((got.double() - want).abs() <= limit).all())
+
+
+def offset_rows(dtype, V, seed):
+    g = gen(seed)
+    rows = [torch.full((V,), c, device="cuda") for c in (-1e9, -1e30, -1e4, 77.0, 3e9, torch.finfo(dtype).min, torch.finfo(dtype).max)]
+    rows += [c + 2.0 * normal(g, V) for c in (0.0, 50.0, -63.0, 66.0, 300.0, -1e4, 3e5, -1e7, 1e9)]
+    part = torch.full((V,), -1e9, device="cuda")
+    part[V // 2:] += 700.0 * normal(g, V - V // 2)  # steps of 64: the largest and few besides
+    rows.append(part)
+    part = torch.full((V,), -math.inf, device="cuda")
+    part[::3] = -1e9                                # an exact mask within a finite one
+    rows.append(part)
+    x = torch.stack(rows).to(dtype)
+    tokens = torch.randint(V, (x.shape[0],), device="cuda", generator=g).int()
+    tokens[1] = tokens[9] = -1
+    return g, x, tokens
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("entropy", [False, True])
+@pytest.mark.parametrize("V,pad,offset", [(1, 0, 0), (50, 0, 0), (5003, 0, 0), (5003, 4, 1), (20001, 8, 3), (129280, 0, 0)])
+def test_token_logprobs_backward_of_large_logits(ds, dtype, entropy, V, pad, offset):
+    """Every p keeps its digits whatever the logits' common offset: a row of -1e9 has 1 / V."""
+    g, rows, tokens = offset_rows(dtype, V, V + pad)
+    T = rows.shape[0]
+    flat = torch.full((T * (V + pad) + offset,), math.nan, dtype=dtype, device="cuda")
+    x = flat[offset:].view(T, V + pad)[:, :V]
+    x.copy_(rows)
+    check_gradient(ds, x, tokens, normal(g, T), normal(g, T) if entropy else None)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gradient_of_a_row_of_one_number(ds, dtype):
+    """1 / V for every token but the given one, which has 1 / V - 1.  The sum is off by sum_error(4096) = 62 U, roundings of lse
+    (8.3: 2^-21), differences, arguments and the exponential by less than 32 U: below 2^-17 in all."""
+    V = 4096
+    for c in (0.0, -1e4, -1e9, -1e30, 3e38, float(torch.finfo(dtype).min)):
+        x = torch.full((3, V), c, device="cuda").to(dtype)
+        t = torch.tensor([5, 4000, -1], dtype=torch.int32, device="cuda")
+        _, lse, _, _, _ = ds.token_logprobs(x, t)
+        got = ds.token_logprobs_backward(-torch.ones(3, device="cuda"), x, t, lse).double()
+        want = torch.full((3, V), 1.0 / V, dtype=torch.float64, device="cuda")
+        want[0, 5] -= 1.0
+        want[1, 4000] -= 1.0
+        want[2] = 0.0
+        assert bool(((got - want).abs() <= (half_step(dtype) + 2.0 ** -17) * want.abs()).all())

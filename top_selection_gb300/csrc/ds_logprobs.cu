@@ -14,7 +14,7 @@
 // distinct.  A row's parts on the CTAs of a cluster are joined by the first, over distributed shared
 // memory, in a fixed order.
 //
-// Long rows are bound by memory (2048 x 129280 bf16: 88 us, 87 % of the copy rate; the gradient 156 us for
+// Long rows are bound by memory (2048 x 129280 bf16: 88 us, 87 % of the copy rate; the gradient 153 us for
 // reading and writing it, the copy rate), short ones by their starts and barriers (4099 x 32003 bf16: 49 us, 79 %),
 // and the top by the cuts' barriers and single steps: 64 us with one token, 85 with 20 (numbers listed one
 // by one: 126).  One row of 129280 fp32 numbers on 16 CTAs takes 2.8 us, with 20 tokens 7.7.  Tried and not kept:
@@ -566,9 +566,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
 }
 
 // ---------------------------------------------------------------- gradient ----------
-// One number in, one out; a CTA takes a run of one row.  lse is rounded to fp32 (2^-24 of its size),
-// which moves every p of the row by that much of itself.
-constexpr int kBackThreads = 256;
+// One number in, one out; a CTA takes a run of one row.  log p = x - lse, and lse is rounded to fp32: up to
+// |lse| = 64 that moves every p of the row by at most 2^-19 of itself.  A row beyond (logits with a common
+// offset, a row masked with -1e9 throughout: lse = m, and what it lost is log V) has one CTA, which first
+// sums exp(x - lse) over it: log p = (x - lse) - log of that sum.  Memory bounds both: 2048 x 129280 bf16 in 153 us,
+// in 286 where every row is summed again (a row alone, by one CTA: 30 us, 2.7 without).
+constexpr int kBackThreads = 256, kBackWords = 4;
+constexpr float kLseKept = 64.f;
 
 struct LogBackParams {
     const void* x;
@@ -583,56 +587,60 @@ struct LogBackParams {
     int32_t runs;  // CTAs to a row
 };
 
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kBackThreads) ds_token_logprobs_backward_kernel(const LogBackParams p) {
-    constexpr int PER = kPer<T>, U = 4;
-    pdl_launch_dependents();
-    pdl_wait();
-    const int64_t row = blockIdx.x / p.runs;
-    const int run = static_cast<int>(blockIdx.x % p.runs);
-    const T* x = static_cast<const T*>(p.x) + row * p.stride;
-    T* out = static_cast<T*>(p.out) + row * p.out_stride;
-    int t = p.tokens[row];
-    const float lse = p.lse[row];
-    float g = p.grad[row], h = 0.f, H = 0.f;
-    if (p.grad_entropy) h = p.grad_entropy[row], H = p.entropy[row];
-    if (t < 0 || t >= p.V) t = -1, g = 0.f;
-    const bool none = lse == -INFINITY;  // a row of -inf alone has no probabilities: no gradient
-    const float z = none ? 0.f : lse;
+// A row with what its gradient takes.
+template <typename T>
+struct BackRow {
+    const T* x;
+    T* out;
+    int V, t;      // t: the given token, -1 for none
+    float g, h, H, lse;
+    float rest;    // log sum exp(x - lse), where lse is not enough
+    bool none;     // a row of -inf alone has no probabilities: no gradient
+    int shift;     // numbers before the row's start in its first 16 bytes
+};
+
+// A thread's words of run number `run` of a row.
+template <typename T>
+__device__ __forceinline__ void load_run(const BackRow<T>& r, int run, uint4 (&q)[kBackWords]) {
+    const int words = (r.V + r.shift + kPer<T> - 1) / kPer<T>, w0 = run * (kBackThreads * kBackWords);
+#pragma unroll
+    for (int u = 0; u < kBackWords; ++u) {
+        const int w = w0 + u * kBackThreads + threadIdx.x;
+        q[u] = w < words ? row_word(r.x, w, r.shift, r.V) : no_word<T>();
+    }
+}
+
+// The gradient of the run whose words are q (VEC; else they are not used); REST: with the row's rest.
+template <typename T, bool VEC, bool REST>
+__device__ __forceinline__ void put_run(const BackRow<T>& r, int run, const uint4 (&q)[kBackWords]) {
+    constexpr int PER = kPer<T>, U = kBackWords;
     // -p (g + h (log p + H)), with log p bounded so that 0 times it stays 0
     const auto grad_of = [&](float v) {
-        const float lp = fmaxf(v - z, -150.f);
-        return -exp2_term(lp * kLog2e) * fmaf(h, lp + H, g);
+        const float lp = fmaxf(REST ? (v - r.lse) - r.rest : v - r.lse, -150.f);
+        return -exp2_term(lp * kLog2e) * fmaf(r.h, lp + r.H, r.g);
     };
     if (VEC) {
         // both rows lie alike against 16-byte boundaries
-        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(T));
-        const int words = (p.V + shift + PER - 1) / PER, w0 = run * (kBackThreads * U);
-        uint4 q[U];
+        const int words = (r.V + r.shift + PER - 1) / PER, w0 = run * (kBackThreads * U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int w = w0 + u * kBackThreads + threadIdx.x;
-            q[u] = w < words ? row_word(x, w, shift, p.V) : no_word<T>();
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int w = w0 + u * kBackThreads + threadIdx.x, at = w * PER - shift;
+            const int w = w0 + u * kBackThreads + threadIdx.x, at = w * PER - r.shift;
             if (w >= words) break;
             float v[PER];
             unpack16(q[u], v);
 #pragma unroll
-            for (int j = 0; j < PER; ++j) v[j] = none ? 0.f : grad_of(v[j]);
-            if (!none && t >= at && t < at + PER) {
+            for (int j = 0; j < PER; ++j) v[j] = r.none ? 0.f : grad_of(v[j]);
+            if (!r.none && r.t >= at && r.t < at + PER) {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    if (at + j == t) v[j] += g;
+                    if (at + j == r.t) v[j] += r.g;
             }
-            if (at >= 0 && at + PER <= p.V) {
-                *reinterpret_cast<uint4*>(out + at) = pack16(v);
+            if (at >= 0 && at + PER <= r.V) {
+                *reinterpret_cast<uint4*>(r.out + at) = pack16(v);
             } else {
 #pragma unroll
                 for (int j = 0; j < PER; ++j)
-                    if (at + j >= 0 && at + j < p.V) row_put(out + at + j, v[j]);
+                    if (at + j >= 0 && at + j < r.V) row_put(r.out + at + j, v[j]);
             }
         }
     } else {
@@ -640,9 +648,67 @@ __global__ void __launch_bounds__(kBackThreads) ds_token_logprobs_backward_kerne
 #pragma unroll 8
         for (int i = 0; i < U * PER; ++i) {
             const int64_t c = c0 + i * kBackThreads + threadIdx.x;
-            if (c < p.V) row_put(out + c, none ? 0.f : grad_of(row_f32(x[c])) + (c == t ? g : 0.f));
+            if (c < r.V) row_put(r.out + c, r.none ? 0.f : grad_of(row_f32(r.x[c])) + (c == r.t ? r.g : 0.f));
         }
     }
+}
+
+// A row whose lse is not enough, by one CTA.
+template <typename T, bool VEC>
+__device__ __noinline__ void put_row(BackRow<T> r, int runs) {
+    __shared__ float sh_sum[kBackThreads / 32];
+    uint4 q[kBackWords];
+    float sum = 0.f;
+    for (int run = 0; run < runs; ++run) {
+        load_run(r, run, q);
+#pragma unroll
+        for (int u = 0; u < kBackWords; ++u) {
+            float v[kPer<T>];
+            unpack16(q[u], v);
+#pragma unroll
+            for (int j = 0; j < kPer<T>; ++j) sum += exp2_term((v[j] - r.lse) * kLog2e);
+        }
+    }
+    sum = lanes_sum<32>(sum);
+    if (threadIdx.x % 32 == 0) sh_sum[threadIdx.x / 32] = sum;
+    __syncthreads();
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBackThreads / 32; ++w) sum += sh_sum[w];
+    r.rest = log2f(sum) * kLn2;
+    for (int run = 0; run < runs; ++run) {
+        if (VEC) load_run(r, run, q);
+        put_run<T, VEC, true>(r, run, q);
+    }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kBackThreads) ds_token_logprobs_backward_kernel(const LogBackParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t row = blockIdx.x / p.runs;
+    const int run = static_cast<int>(blockIdx.x % p.runs);
+    BackRow<T> r;
+    r.x = static_cast<const T*>(p.x) + row * p.stride;
+    r.out = static_cast<T*>(p.out) + row * p.out_stride;
+    r.V = p.V;
+    r.shift = static_cast<int>(reinterpret_cast<uintptr_t>(r.x) % 16 / sizeof(T));
+    const float lse = p.lse[row];
+    uint4 q[kBackWords];
+    if (VEC) load_run(r, run, q);  // on their way while lse is looked at (2048 x 129280 bf16: 158 us else, 153)
+    r.t = p.tokens[row];
+    r.g = p.grad[row], r.h = 0.f, r.H = 0.f;
+    if (p.grad_entropy) r.h = p.grad_entropy[row], r.H = p.entropy[row];
+    if (r.t < 0 || r.t >= p.V) r.t = -1, r.g = 0.f;
+    r.none = lse == -INFINITY;
+    r.lse = r.none ? 0.f : lse;
+    r.rest = 0.f;
+    const float size = fabsf(r.lse);
+    if (size > kLseKept && size < INFINITY) {
+        if (run == 0) put_row<T, VEC>(r, p.runs);
+        return;
+    }
+    put_run<T, VEC, false>(r, run, q);
 }
 
 // ---------------------------------------------------------------- host --------------
@@ -711,7 +777,7 @@ ds_status ds_token_logprobs_backward(const float* grad_logprobs, const void* log
     if (misaligned(logits, es) || misaligned(grad_logits, es) || misaligned(tokens, 4) || misaligned(grad_logprobs, 4) ||
         misaligned(lse, 4) || misaligned(grad_entropy, 4) || misaligned(entropy, 4))
         return DS_ERR_ALIGNMENT;
-    const int64_t per = 16 / es, words = (V + 2 * per - 2) / per, runs = (words + kBackThreads * 4 - 1) / (kBackThreads * 4);
+    const int64_t per = 16 / es, words = (V + 2 * per - 2) / per, runs = (words + kBackThreads * kBackWords - 1) / (kBackThreads * kBackWords);
     if (rows > 0x7FFFFFFFLL / runs) return DS_ERR_UNSUPPORTED;
     const LogBackParams p = {logits, tokens, grad_logprobs, lse, grad_entropy, entropy, grad_logits, rows, row_stride,
                              grad_stride, static_cast<int32_t>(V), static_cast<int32_t>(runs)};
