@@ -441,7 +441,9 @@ ds_status ds_cache_attention_workspace_bytes(int32_t dtype, int64_t sequences, i
  *   tokens          [rows] int32; outside [0, V): none is given, log probability 0
  *   out_logprobs, out_lse, out_entropy   [rows] floats
  *   out_top_logprobs, out_top_tokens     [rows, top] floats and int32 (unused with top = 0)
- * A row of -inf alone: lse and log probabilities -inf, entropy 0, its first tokens as the top.  Sums
+ * A row of -inf alone: lse and log probabilities -inf, entropy 0, its first tokens as the top.  A row with a NaN or
+ * +inf: NaN for lse, entropy and all log probabilities (0 still where no token is given); its top lists NaN of either
+ * sign before +inf.  Sums
  * are fp32, of exponentials off by 2^-22 of each; x is taken relative to the row's largest
  * before anything is rounded.
  */
@@ -457,7 +459,8 @@ ds_status ds_token_logprobs(const void* logits, int32_t dtype, int64_t rows, int
  *   lse, entropy    as ds_token_logprobs gave them (entropy may be NULL where grad_entropy is)
  *   grad_logits     rows of V elements of dtype, row r at element r * grad_stride (>= V); every
  *                   element is written; must not overlap logits
- * A row without a given token has the entropy's part alone, a row of -inf alone zeros.  The top tokens'
+ * A row without a given token has the entropy's part alone, a row of -inf alone zeros, a row whose lse is NaN
+ * NaN throughout.  The top tokens'
  * log probabilities have no gradient here.  lse is rounded to fp32, which moves a row's p by at most 2^-19 of
  * themselves up to |lse| = 64; a row beyond is summed once more, so that p keeps its digits there too.
  */

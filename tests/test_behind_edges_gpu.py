@@ -1,5 +1,5 @@
 """The operators behind the selections at the ends of their ranges, on the GPU against their
-definitions in 64 bits: logits of any size."""
+definitions in 64 bits: logits of any size, numbers that are none."""
 import math
 
 import pytest
@@ -143,3 +143,65 @@ def test_gradient_of_a_row_of_one_number(ds, dtype):
         want[1, 4000] -= 1.0
         want[2] = 0.0
         assert bool(((got - want).abs() <= (half_step(dtype) + 2.0 ** -17) * want.abs()).all())
+
+
+# ------------------------------------------------------------------ numbers that are none ----
+
+def order_of(x, top):
+    """NaN first, then by value; equals by index.  (The CPU's stable sort puts NaN of either sign on top.)"""
+    return x.double().cpu().sort(dim=-1, descending=True, stable=True).indices[:, :top].to(x.device)
+
+
+def spoilt_rows(dtype, V):
+    """Ordinary rows with a NaN or an infinity in their first, a middle and their last word, many of them, and nothing
+    else; every other row is whole."""
+    g, nan, inf = gen(V), math.nan, math.inf
+    rows = []
+
+    def add(change):
+        rows.append(normal(g, V))
+        rows.append(normal(g, V))
+        change(rows[-1])
+    for at in (0, V // 2, V - 1):
+        for c in (nan, inf, -nan):
+            add(lambda r: r.__setitem__(at, c))
+    add(lambda r: r.fill_(nan))
+    add(lambda r: r.fill_(inf))
+    add(lambda r: (r.fill_(-inf), r.__setitem__(V // 3, nan)))
+    add(lambda r: (r.__setitem__(slice(0, V // 2), -inf), r.__setitem__(V // 4, nan)))
+    add(lambda r: (r.fill_(3e38), r.__setitem__(V // 3, nan)))
+    add(lambda r: (r.__setitem__(slice(None, None, 3), nan), r.__setitem__(slice(1, None, 3), inf)))
+    add(lambda r: (r.__setitem__(V - 1, nan), r.__setitem__(0, inf)))
+    x = torch.stack(rows).to(dtype)
+    tokens = torch.randint(V, (x.shape[0],), device="cuda", generator=g).int()
+    tokens[3] = -1                                # a spoilt row without a token
+    return x, tokens
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("V,top", [(1, 1), (9, 5), (300, 0), (1000, 20), (9001, 1), (40000, 32), (140000, 3)])
+def test_numbers_that_are_none(ds, dtype, V, top):
+    """A NaN or +inf among its logits makes a row's lse, log probabilities and entropy NaN, and its gradient; its top
+    tokens are the NaN ones first, then +inf.  Rows beside it are as without it."""
+    x, tokens = spoilt_rows(dtype, V)
+    T = x.shape[0]
+    bad = torch.arange(T, device="cuda") % 2 == 1
+    order = order_of(x, top)
+    clean = x.clone()
+    clean[1::2] = x[::2]
+    base.check_logprobs(ds, clean, tokens, top)
+    for many in (1, 12):
+        xs, ts, bads = x.repeat(many, 1), tokens.repeat(many), bad.repeat(many)
+        lp, lse, H, top_lp, top_tokens = ds.token_logprobs(xs, ts, top=top)
+        given = bads & (ts >= 0)
+        assert bool(lse[bads].isnan().all()) and bool(H[bads].isnan().all()) and bool(lp[given].isnan().all())
+        assert not bool(lp[ts < 0].any())
+        assert bool(top_lp[bads].isnan().all())
+        assert torch.equal(top_tokens.long(), order.repeat(many, 1))
+        whole = ds.token_logprobs(clean.repeat(many, 1), ts, top=top)
+        for a, b in zip((lp, lse, H, top_lp, top_tokens), whole):
+            assert torch.equal(a[~bads], b[~bads])
+        g = normal(gen(1), T * many)
+        for h in (None, g):
+            grad = ds.token_logprobs_backward(g, xs, ts, lse, grad_entropy=h, entropy=None if h is None else H)
+            assert bool(grad[bads].isnan().all()) and not bool(grad[~bads].isnan().any())

@@ -584,7 +584,8 @@ def token_logprobs(logits, tokens, top: int = 0, stream=None):
 
     ``tokens`` (rows,) int32; one outside [0, V) stands for none: 0, without a gradient.  Returns
     (logprobs (rows,), lse (rows,), entropy (rows,), top_logprobs (rows, top), top_tokens (rows, top)
-    int32), float32, the likeliest first, ties to the lower token; ``top`` is at most 32.  The
+    int32), float32, the likeliest first, ties to the lower token; ``top`` is at most 32.  A NaN or +inf
+    logit makes its row's results NaN, and NaN tokens lead its top.  The
     results carry no autograd history: ``token_logprobs_backward`` gives their gradient."""
     return (_binding or _load_binding()).token_logprobs(logits, tokens, top, stream)
 

@@ -10,7 +10,7 @@
 // that at least `top` numbers reach, from the maxima of groups of threads over the first 32
 // numbers each; then 16-byte words with a number above it go to a list as they are, which is cut back to its
 // `top` largest numbers (and raises the threshold) after 2, 8, 32 .. chunks and at the end.  Order is by
-// value, then by the lower index, so keys are 64 bits (order-preserving value, inverted index) and
+// value, NaN first, then by the lower index, so keys are 64 bits (order-preserving value, inverted index) and
 // distinct.  A row's parts on the CTAs of a cluster are joined by the first, over distributed shared
 // memory, in a fixed order.
 //
@@ -137,7 +137,27 @@ __device__ __forceinline__ uint4 no_word() {
     return make_uint4(f, f, f, f);
 }
 
-// The largest of a word's numbers.
+// The larger number, NaN where one of them is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// The largest of a word's numbers, NaN where one of them is.
+template <typename T>
+__device__ __forceinline__ float word_max_or_nan(const uint4& q) {
+    if constexpr (sizeof(T) == 4) {
+        return max_or_nan(max_or_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
+                          max_or_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
+    } else {
+        const auto pair = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+        const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(pair(q.x), pair(q.y)), __hmax2_nan(pair(q.z), pair(q.w)));
+        return max_or_nan(__low2float(m), __high2float(m));
+    }
+}
+
+// The largest of a word's numbers, NaN left out.
 template <typename T>
 __device__ __forceinline__ float word_max(const uint4& q) {
     if constexpr (sizeof(T) == 4) {
@@ -438,9 +458,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
         }
         float top_of[U], most = -INFINITY;
 #pragma unroll
-        for (int u = 0; u < U; ++u) top_of[u] = word_max<T>(q[u]), most = fmaxf(most, top_of[u]);
+        for (int u = 0; u < U; ++u) top_of[u] = word_max_or_nan<T>(q[u]), most = max_or_nan(most, top_of[u]);
         rise(a, most);
-        if (!is_far(a.m)) {
+        if (most != most) {  // the row has no sums, and its top is found without the list of words
+            a.s = NAN;
+            if (TOP) atomicMax(&sh.hits, kLogHits + 1);
+        } else if (!is_far(a.m)) {
             const Two nm = two(-a.m, -a.m), l2e = two(kLog2e, kLog2e);
             Two s = 0, w = 0;
 #pragma unroll
@@ -535,24 +558,47 @@ __global__ void __launch_bounds__(NT, 1024 / NT) ds_token_logprobs_kernel(const 
         }
     }
     if (warp != 0) return;
-    const bool some = all.s > 0.f;
+    if (all.m == INFINITY) all.s = NAN;  // inf - inf
+    const bool some = all.s != 0.f, spoilt = all.s != all.s;
     const float logs = some ? log2f(all.s) : 0.f;
     const auto log_p = [&](float v) { return some ? (v - all.m) - logs * kLn2 : -INFINITY; };
     if (tid == 0) {
         if (ctas == 1) look_up();
         p.logprobs[row] = token >= 0 ? log_p(given) : 0.f;
         p.lse[row] = all.m + logs * kLn2;
-        p.entropy[row] = some ? fmaxf((logs - all.w / all.s) * kLn2, 0.f) : 0.f;
+        const float H = (logs - all.w / all.s) * kLn2;
+        p.entropy[row] = spoilt ? NAN : some && H > 0.f ? H : 0.f;
     }
     if constexpr (TOP) {
-        const uint64_t k = lane < p.top ? sh.best[lane] : 0;
-        const bool real = lane < p.top && lane < sh.kept;
+        int at = 0, have = 0;  // the lane's token, and how many lanes have theirs
+        if (spoilt) {  // the NaN ones come first
+            for (int i0 = 0; have < p.top && i0 < p.V; i0 += 32 * 8) {
+                float v[8];
+                bool any = false;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    v[u] = i0 + u * 32 + lane < p.V ? row_f32(x[i0 + u * 32 + lane]) : 0.f;
+                    any |= v[u] != v[u];
+                }
+                if (!__any_sync(kLanes, any)) continue;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t which = __ballot_sync(kLanes, v[u] != v[u]);
+                    const int n = __popc(which);
+                    if (lane >= have && lane < have + n) at = i0 + u * 32 + static_cast<int>(__fns(which, 0, lane - have + 1));
+                    have += n;
+                }
+            }
+        }
+        const int numbers = lane - have;  // its place among the numbers
+        const bool real = numbers >= 0 && lane < p.top && numbers < sh.kept;
+        const uint64_t k = real ? sh.best[numbers] : 0;
         const float v = real ? key_value(k) : -INFINITY;
-        int at = real ? key_at(k) : 0;
+        if (real) at = key_at(k);
         // fewer numbers above -inf than asked for: the first of the others follow
-        int have = __popc(__ballot_sync(kLanes, real));
+        have += __popc(__ballot_sync(kLanes, real));
         for (int i0 = 0; have < p.top && i0 < p.V; i0 += 32) {
-            const bool other = i0 + lane < p.V && !(row_f32(x[i0 + lane]) > -INFINITY);
+            const bool other = i0 + lane < p.V && row_f32(x[i0 + lane]) == -INFINITY;
             const uint32_t which = __ballot_sync(kLanes, other);
             const int n = __popc(which);
             if (lane >= have && lane < have + n) at = i0 + static_cast<int>(__fns(which, 0, lane - have + 1));
@@ -614,9 +660,9 @@ __device__ __forceinline__ void load_run(const BackRow<T>& r, int run, uint4 (&q
 template <typename T, bool VEC, bool REST>
 __device__ __forceinline__ void put_run(const BackRow<T>& r, int run, const uint4 (&q)[kBackWords]) {
     constexpr int PER = kPer<T>, U = kBackWords;
-    // -p (g + h (log p + H)), with log p bounded so that 0 times it stays 0
+    // -p (g + h (log p + H)), with log p bounded so that 0 times it stays 0; NaN where lse is
     const auto grad_of = [&](float v) {
-        const float lp = fmaxf(REST ? (v - r.lse) - r.rest : v - r.lse, -150.f);
+        const float lp = max_or_nan(REST ? (v - r.lse) - r.rest : v - r.lse, -150.f);
         return -exp2_term(lp * kLog2e) * fmaf(r.h, lp + r.H, r.g);
     };
     if (VEC) {
