@@ -543,6 +543,15 @@ ds_status ds_expert_product(const void* x, const float* x_scales, int64_t rows, 
                             int64_t w_matrix_stride, const int32_t* offsets, int32_t dtype, void* out,
                             cudaStream_t stream);
 
+/* ds_expert_product in which every CTA gives its first tile up before that tile's block number `block` (>= 0) along
+ * k, as if a wait had run out there: copies and products are in flight then.  The kernel records
+ * DS_ERR_TIMEOUT for ds_get_device_status and returns, and out is undefined; tiles of no more blocks end as ever.
+ * Checks the kernel's failure path without a GPU fault. */
+ds_status ds_expert_product_probe(int32_t block, const void* x, const float* x_scales, int64_t rows, int32_t K,
+                                  int64_t x_stride, const void* w, const float* w_scales, int32_t E, int32_t N,
+                                  int64_t w_row_stride, int64_t w_matrix_stride, const int32_t* offsets, int32_t dtype,
+                                  void* out, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,6 @@
 """The operators behind the selections at the ends of their ranges, on the GPU against their
-definitions in 64 bits: logits of any size, numbers that are none."""
+definitions in 64 bits: logits of any size, numbers that are none, and a kernel
+that gives up."""
 import math
 
 import pytest
@@ -205,3 +206,34 @@ def test_numbers_that_are_none(ds, dtype, V, top):
         for h in (None, g):
             grad = ds.token_logprobs_backward(g, xs, ts, lse, grad_entropy=h, entropy=None if h is None else H)
             assert bool(grad[bads].isnan().all()) and not bool(grad[~bads].isnan().any())
+
+
+# ------------------------------------------------------------------ a product that gives up ----
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,E,N,K", [(1, 1, 1000, 4096), (300, 1, 400, 1536), (700, 8, 130, 512), (20000, 4, 272, 144),
+                                     (6000, 1, 1304, 528)])
+def test_product_that_gives_up(ds, dtype, T, E, N, K):
+    """Blocks split over a cluster, narrow and wide tiles: each CTA gives up with copies, or copies and products, in
+    flight.  The call records the timeout and returns; the next one is as ever."""
+    g = gen(T + N)
+    x, xs, w, ws = base.operands(g, T, E, N, K)
+    offsets = base.spread(g, T, E)
+    want = ds.expert_product(x, xs, w, ws, offsets, dtype=dtype)
+    out = torch.empty_like(want)
+
+    def probe(block):
+        return ds.ds_expert_product_probe(block, x.data_ptr(), xs.data_ptr(), T, K, K, w.data_ptr(), ws.data_ptr(), E, N, K,
+                                          N * K, offsets.data_ptr(), int(dtype == torch.float32), out.data_ptr(),
+                                          torch.cuda.current_stream().cuda_stream)
+    assert ds.ds_get_device_status() == 0
+    for block in (0, 1):                           # every form here has two blocks to a tile at least
+        assert probe(block) == 0
+        again = ds.expert_product(x, xs, w, ws, offsets, dtype=dtype)  # right behind it on the stream
+        assert ds.ds_get_device_status() == 5      # DS_ERR_TIMEOUT
+        assert torch.equal(again, want)
+    for block in (2, 3, 7):                        # some have no more
+        assert probe(block) == 0
+        assert ds.ds_get_device_status() in (0, 5)
+    assert probe(2 ** 31 - 1) == 0                 # no tile has as many
+    assert ds.ds_get_device_status() == 0 and torch.equal(out, want)

@@ -36,6 +36,7 @@ __all__ = [
     "route", "route_backward", "verify_drafts", "cache_store", "cache_load", "cache_attention",
     "ds_token_logprobs", "ds_token_logprobs_backward", "ds_expert_sort", "ds_expert_gather", "ds_expert_combine",
     "ds_expert_combine_backward", "ds_quantise_blocks", "ds_expert_gather_quantised", "ds_expert_product",
+    "ds_expert_product_probe",
     "token_logprobs", "token_logprobs_backward", "expert_sort", "expert_gather", "expert_combine",
     "expert_combine_backward", "quantise_blocks", "expert_product",
 ]
@@ -168,6 +169,8 @@ def load():
         lib.ds_expert_gather_quantised.restype = ctypes.c_int
         lib.ds_expert_product.argtypes = [vp, vp, i64, i32, i64, vp, vp, i32, i32, i64, i64, vp, i32, vp, vp]
         lib.ds_expert_product.restype = ctypes.c_int
+        lib.ds_expert_product_probe.argtypes = [i32] + lib.ds_expert_product.argtypes
+        lib.ds_expert_product_probe.restype = ctypes.c_int
         _lib = lib
         return lib
 
@@ -477,6 +480,14 @@ def ds_expert_product(x, x_scales, rows, K, x_stride, w, w_scales, E, N, w_row_s
     return load().ds_expert_product(int(x) or None, int(x_scales) or None, rows, K, x_stride, int(w) or None,
                                     int(w_scales) or None, E, N, w_row_stride, w_matrix_stride, int(offsets) or None,
                                     dtype, int(out) or None, int(stream) or None)
+
+
+def ds_expert_product_probe(block, x, x_scales, rows, K, x_stride, w, w_scales, E, N, w_row_stride, w_matrix_stride,
+                            offsets, dtype, out, stream=0) -> int:
+    """Raw C call (device pointers as ints); returns the ds_status code."""
+    return load().ds_expert_product_probe(block, int(x) or None, int(x_scales) or None, rows, K, x_stride, int(w) or None,
+                                          int(w_scales) or None, E, N, w_row_stride, w_matrix_stride, int(offsets) or None,
+                                          dtype, int(out) or None, int(stream) or None)
 
 
 class _Names(dict):

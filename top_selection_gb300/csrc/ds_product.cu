@@ -80,7 +80,9 @@ struct ProdParams {
     int32_t E;
     int32_t vec;          // rows of out start on 32 bytes
     int32_t bulk;         // rows of out start on 16 bytes: wide tiles are stored by bulk copies
+    int32_t give_up;      // the block of a tile at which its products are given up (ds_expert_product_probe); else kNever
 };
+constexpr int32_t kNever = 1 << 30;  // blocks are at most 2^17
 
 struct ProdShared {
     uint64_t full[8], empty[8], sums[8], taken[8];
@@ -90,6 +92,7 @@ struct ProdShared {
     int64_t scan[kProdThreads / 32];
     uint32_t tmem;
     int failed;
+    uint32_t loaded, multiplied;   // blocks whose copies, products were started
 };
 
 // ---------------------------------------------------------------- PTX ---------------
@@ -182,6 +185,21 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
     return true;
 }
 
+// What a CTA that gives up has started: the copies of its last blocks land in shared memory, and its products end,
+// before it frees its tensor memory and leaves.  Block n uses slot n % STAGES, whose barriers complete a phase
+// for each; none but these blocks' are outstanding, and no later block uses their slots.
+template <int STAGES>
+__device__ __forceinline__ void await_started(ProdShared& sh) {
+    const auto await = [](uint64_t* bar, uint32_t parity) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(bar, parity) && clock64() - t0 < kSpinLimit) {}
+    };
+    const uint32_t n = sh.loaded;
+    for (uint32_t j = n > STAGES ? n - STAGES : 0; j < n; ++j) await(&sh.full[j % STAGES], (j / STAGES) & 1);
+    // the commit behind the last block's products tells that all before are done
+    if (const uint32_t last = sh.multiplied; last > 0) await(&sh.empty[(last - 1) % STAGES], ((last - 1) / STAGES) & 1);
+}
+
 using Two = unsigned long long;  // two fp32 numbers, for the packed instructions
 __device__ __forceinline__ Two two(uint32_t a, uint32_t b) { return static_cast<Two>(b) << 32 | a; }
 __device__ __forceinline__ void add_product(Two& sum, Two a, Two b) {
@@ -236,6 +254,7 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
         for (int i = 0; i < S::STAGES; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
         for (int i = 0; i < S::BUFS; ++i) mbar_init(&sh.sums[i], 2), mbar_init(&sh.taken[i], kProdSumWarps);
         sh.failed = 0;
+        sh.loaded = sh.multiplied = 0;
         fence_mbar_init();
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_x) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_w) : "memory");
@@ -314,17 +333,14 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
                                     static_cast<int>(t.row0) + x * kProdBox, &sh.full[s]);
                 }
             }
-            if (!ok)  // copies in flight land before the CTA leaves
-                for (uint32_t j = n > S::STAGES ? n - S::STAGES : 0; j < n; ++j) {
-                    const long long t0 = clock64();
-                    while (!mbar_try_wait_sleep(&sh.full[j % S::STAGES], (j / S::STAGES) & 1, 1000u) && clock64() - t0 < kSpinLimit) {}
-                }
+            sh.loaded = n;
         } else if (warp == kProdSumWarps + 1 && lane == 0) {
+            const int end = min(b1, b0 + p.give_up);
             uint32_t n = 0;
             Tile t;
             bool ok = true;
             for (int64_t i = tile0; ok && tile_at<BN>(sh, p, i, t); i += step) {
-                for (int b = b0; b < b1; ++b, ++n) {
+                for (int b = b0; b < end; ++b, ++n) {
                     const uint32_t s = n % S::STAGES, d = n % S::BUFS;
                     ok = wait_phase(&sh.taken[d], (n / S::BUFS + 1) & 1, failed) && wait_phase(&sh.full[s], (n / S::STAGES) & 1, failed);
                     if (!ok) break;
@@ -337,7 +353,9 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
                     tc_commit(&sh.empty[s]);
                     tc_commit(&sh.sums[d]);
                 }
+                if (end < b1) *failed = 1, ok = false;
             }
+            sh.multiplied = n;
         } else if (warp == kProdSumWarps + 2) {
             uint32_t n = 0;
             Tile t;
@@ -542,7 +560,10 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
         for (int64_t j = tail + at; j < all; j += stride) put_out(out + j, 0.f);
     }
     tc_fence_before();
-    __syncthreads();
+    if (__syncthreads_or(sh.failed)) {  // (who gave up has set it)
+        if (tid == 0) await_started<S::STAGES>(sh);
+        __syncthreads();
+    }
     if (warp == kProdSumWarps + 1) {
         tc_fence_after();
         tmem_free(tmem, 512);
@@ -615,10 +636,10 @@ static int product_outputs(int64_t rows, int64_t E, int64_t N, int sms) {
 
 using namespace dsk;
 
-extern "C" ds_status ds_expert_product(const void* x, const float* x_scales, int64_t rows, int32_t K, int64_t x_stride,
-                                       const void* w, const float* w_scales, int32_t E, int32_t N, int64_t w_row_stride,
-                                       int64_t w_matrix_stride, const int32_t* offsets, int32_t dtype, void* out,
-                                       cudaStream_t stream) {
+static ds_status expert_product(int32_t give_up, const void* x, const float* x_scales, int64_t rows, int32_t K,
+                                int64_t x_stride, const void* w, const float* w_scales, int32_t E, int32_t N,
+                                int64_t w_row_stride, int64_t w_matrix_stride, const int32_t* offsets, int32_t dtype,
+                                void* out, cudaStream_t stream) {
     if ((dtype != DS_BF16 && dtype != DS_FP32) || rows < 0 || K < 1 || N < 1 || E < 1 || x_stride < K || w_row_stride < K ||
         w_matrix_stride < (E > 1 ? 1 : 0) || (!offsets && E != 1))
         return DS_ERR_INVALID_ARG;
@@ -634,6 +655,7 @@ extern "C" ds_status ds_expert_product(const void* x, const float* x_scales, int
     int dev = 0;
     DevInfo info;
     ProdParams p = {};
+    p.give_up = give_up;
     if (cudaGetDevice(&dev) != cudaSuccess || !dev_info(dev, info) || !(p.status = status_word())) return DS_ERR_CUDA;
     p.x_scales = x_scales;
     p.w_scales = w_scales;
@@ -671,3 +693,23 @@ extern "C" ds_status ds_expert_product(const void* x, const float* x_scales, int
     return dtype == DS_BF16 ? launch_product<128, __nv_bfloat16, false>(mx, mw, mo, p, ctas, 1, stream)
                             : launch_product<128, float, false>(mx, mw, mo, p, ctas, 1, stream);
 }
+
+extern "C" {
+
+ds_status ds_expert_product(const void* x, const float* x_scales, int64_t rows, int32_t K, int64_t x_stride, const void* w,
+                            const float* w_scales, int32_t E, int32_t N, int64_t w_row_stride, int64_t w_matrix_stride,
+                            const int32_t* offsets, int32_t dtype, void* out, cudaStream_t stream) {
+    return expert_product(kNever, x, x_scales, rows, K, x_stride, w, w_scales, E, N, w_row_stride, w_matrix_stride, offsets,
+                          dtype, out, stream);
+}
+
+ds_status ds_expert_product_probe(int32_t block, const void* x, const float* x_scales, int64_t rows, int32_t K,
+                                  int64_t x_stride, const void* w, const float* w_scales, int32_t E, int32_t N,
+                                  int64_t w_row_stride, int64_t w_matrix_stride, const int32_t* offsets, int32_t dtype,
+                                  void* out, cudaStream_t stream) {
+    if (block < 0) return DS_ERR_INVALID_ARG;
+    return expert_product(block < kNever ? block : kNever, x, x_scales, rows, K, x_stride, w, w_scales, E, N, w_row_stride,
+                          w_matrix_stride, offsets, dtype, out, stream);
+}
+
+}  // extern "C"
