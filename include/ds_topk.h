@@ -531,7 +531,8 @@ ds_status ds_expert_gather_quantised(const void* x, int32_t dtype, int64_t token
  *   x           [rows, K] e4m3 codes, row r at byte r * x_stride;  x_scales [rows, ceil(K / 128)]
  *   w           [E, N, K] e4m3 codes, row n of expert e at byte e * w_matrix_stride + n *
  *               w_row_stride;  w_scales [E, ceil(N / 128), ceil(K / 128)], any fp32 scales
- *   offsets     [E + 1] int32, ascending, or NULL: one expert (E = 1) has all rows
+ *   offsets     [E + 1] int32, ascending, or NULL: one expert (E = 1) has all rows.  Others leave rows of out
+ *               undefined; those outside [0, rows] count as its ends
  *   dtype, out  [rows, N] bf16 or fp32
  * K is a multiple of 16, x, w and their strides are 16-byte aligned, w_matrix_stride > 0 with several
  * experts; 0 <= rows <= 2^30, E <= 512, N and K <= 2^24.  Scales whose product leaves fp32's range

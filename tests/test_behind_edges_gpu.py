@@ -1,6 +1,6 @@
 """The operators behind the selections at the ends of their ranges, on the GPU against their
-definitions in 64 bits: logits of any size, numbers that are none, and a kernel
-that gives up."""
+definitions in 64 bits: logits of any size, numbers that are none, a kernel that gives
+up, and offsets in no order."""
 import math
 
 import pytest
@@ -237,3 +237,29 @@ def test_product_that_gives_up(ds, dtype, T, E, N, K):
         assert ds.ds_get_device_status() in (0, 5)
     assert probe(2 ** 31 - 1) == 0                 # no tile has as many
     assert ds.ds_get_device_status() == 0 and torch.equal(out, want)
+
+
+# ------------------------------------------------------------------ offsets ----
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,E,N,K", [(6, 4, 200, 2048), (900, 8, 130, 512), (20000, 5, 272, 144)])
+def test_product_of_offsets_in_no_order(ds, dtype, T, E, N, K):
+    """Offsets that descend, or lie outside of the rows: nothing outside of out is written, and rows of one expert alone
+    have their products."""
+    g = gen(T)
+    x, xs, w, ws = base.operands(g, T, E, N, K)
+    held = torch.full((T + 64, N), 7.0, device="cuda", dtype=dtype)
+    out = held[32:32 + T]
+
+    def product(offsets):
+        o = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        assert ds.ds_expert_product(x.data_ptr(), xs.data_ptr(), T, K, K, w.data_ptr(), ws.data_ptr(), E, N, K, N * K, o.data_ptr(),
+                                    int(dtype == torch.float32), out.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+        assert bool((held[:32] == 7.0).all()) and bool((held[32 + T:] == 7.0).all())
+    product([T - T * e // E for e in range(E + 1)])
+    product([0] + [(7919 * e) % (T + 1) for e in range(E)])
+    product([-5] * E + [T + 100])                  # outside: the last expert has all rows
+    want, size = ref.product(x, xs, w, ws, [0] * E + [T])
+    base.check_product(out, want, size, K, dtype)
+    product([2 ** 31 - 1] * (E + 1))               # all rows before the first expert
+    assert not bool(out.any())

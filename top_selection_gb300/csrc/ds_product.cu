@@ -262,21 +262,20 @@ ds_expert_product_kernel(const __grid_constant__ CUtensorMap map_x, const __grid
     if (warp == kProdSumWarps + 1) tmem_alloc(&sh.tmem, 512);
     pdl_launch_dependents();
     pdl_wait();
-    // rows of each expert, ends in ascending order and within the rows whatever the offsets say;
-    // E <= 512: up to two experts to a thread
+    // rows of each expert, within the rows whatever the offsets say.  (They are ascending.  Where they are not, an expert
+    // that ends before it starts has no rows, and rows of two experts or of none behind the first hold anything.)
     if (p.offsets) {
-        if (tid <= p.E || tid + kProdThreads <= p.E)
-            for (int e = tid; e <= p.E; e += kProdThreads) {
-                const int64_t v = p.offsets[e];
-                sh.first[e] = static_cast<int32_t>(v < 0 ? 0 : v > p.rows ? p.rows : v);
-            }
+        for (int e = tid; e <= p.E; e += kProdThreads) {
+            const int64_t v = p.offsets[e];
+            sh.first[e] = static_cast<int32_t>(v < 0 ? 0 : v > p.rows ? p.rows : v);
+        }
     } else if (tid == 0) {
         sh.first[0] = 0;
         sh.first[1] = static_cast<int32_t>(p.rows);
     }
     __syncthreads();
     {
-        int64_t mine[2], sum = 0;
+        int64_t mine[2], sum = 0;  // E <= 512: up to two experts to a thread
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int e = tid * 2 + i;
