@@ -506,7 +506,8 @@ ds_status ds_expert_combine_backward(const void* grad, int64_t grad_stride, cons
  * stands for c * s.
  *
  * ds_quantise_blocks: s is the least power of two >= 2^-126 with max |x| <= 448 s, c = e4m3(x / s),
- * rounded to nearest, ties to even (x / s is exact).
+ * rounded to nearest, ties to even (x / s is exact).  Infinities and NaN have the code NaN; for its block's scale
+ * an infinity counts as fp32's largest number (s = 2^120), a NaN as 0.
  *   x, dtype    row r of matrix m at element m * matrix_stride + r * row_stride, K numbers
  *   block_rows  1 or 128
  *   codes       [matrices, rows, K] bytes;  scales [matrices, ceil(rows / block_rows),

@@ -208,6 +208,37 @@ def test_numbers_that_are_none(ds, dtype, V, top):
             assert bool(grad[bads].isnan().all()) and not bool(grad[~bads].isnan().any())
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("N,K", [(1, 8), (3, 300), (130, 264), (300, 1000)])
+def test_8_bits_of_numbers_that_are_none(ds, dtype, N, K):
+    """The codes of infinities and NaN are NaN.  An infinity counts as the largest number for its block's
+    scale, a NaN not at all."""
+    g = gen(N + K)
+    x = normal(g, N, K).to(dtype)
+    spoilt = x.clone()
+    spoilt[0, K // 2] = math.inf
+    spoilt[N - 1, K - 1] = -math.inf
+    spoilt[N // 2, K // 3] = math.nan
+    if N > 2:
+        spoilt[1] = math.nan
+    most = 3.3895313892515355e38                  # the largest bf16: 448 * 2^120 is above it, 448 * 2^119 below
+    stand_in = torch.where(spoilt.isinf(), most, torch.where(spoilt.isnan(), 0.0, spoilt.float())).to(dtype)
+    for block in (1, 128):
+        for off in (0, 1):                        # rows on 16 bytes, and not
+            held = torch.empty(N * K + off, dtype=dtype, device="cuda")[off:].view(N, K)
+            held.copy_(spoilt)
+            codes, scales = ds.quantise_blocks(held, block_rows=block)
+            want, want_scales = ref.quantise(stand_in[None], block)
+            assert torch.equal(scales.double(), want_scales[0])
+            none = ~torch.isfinite(spoilt)
+            assert bool(codes.float()[none].isnan().all())
+            assert torch.equal(codes.double()[~none], want[0][~none])
+    places, offsets = ds.expert_sort(torch.zeros(N, 1, dtype=torch.int32, device="cuda"), 1)
+    codes, scales = ds.expert_gather(spoilt, places, offsets, quantise=True)
+    want, want_scales = ds.quantise_blocks(spoilt)
+    assert torch.equal(codes.view(torch.uint8), want.view(torch.uint8)) and torch.equal(scales, want_scales)
+
+
 # ------------------------------------------------------------------ a product that gives up ----
 
 @pytest.mark.parametrize("dtype", DTYPES)

@@ -643,7 +643,7 @@ def expert_combine_backward(grad, y, places, offsets, weights, stream=None):
 def quantise_blocks(x, block_rows: int = 1, stream=None):
     """``x`` (rows, K) or (matrices, rows, K) in 8 bits: (codes float8_e4m3fn of x's shape, scales
     float32), a scale for each ``block_rows`` (1 or 128) x 128 numbers, the least power of two that
-    brings their largest to 448 or below.  A code stands for code * scale."""
+    brings their largest to 448 or below.  A code stands for code * scale; infinities and NaN become NaN."""
     return (_binding or _load_binding()).quantise_blocks(x, block_rows, stream)
 
 

@@ -5,10 +5,12 @@
 // A block of numbers (128 of a row, or 128 x 128 of a matrix) has the scale s, the least power of
 // two that brings its largest number to e4m3's 448 or below, and codes e4m3(x / s).  The division by
 // a power of two is exact, so a code is x / s rounded once: half a step, 2^-4 of the number (or
-// 2^-10 s below 2^-6 s).  Bound by memory: 16411 x 2048 bf16 in 14.4 us (7.1 TB/s), 16 x 2000 x 4096 fp32 in
+// 2^-10 s below 2^-6 s).  Infinities and NaN have the code NaN; for its block's scale an infinity counts like the largest
+// number, a NaN not at all.  Bound by memory: 16411 x 2048 bf16 in 14.4 us (7.1 TB/s), 16 x 2000 x 4096 fp32 in
 // blocks of 128 x 128 in 94.5 (6.9), bf16 in 56.9.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "ds_common.cuh"
@@ -64,7 +66,7 @@ struct Sixteen {
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = 0.f;
     }
-    __device__ __forceinline__ float most() const {  // the largest size among them
+    __device__ __forceinline__ float most() const {  // the largest size among them, NaN left out
         if constexpr (VEC && sizeof(T) == 2) {  // two bf16 numbers at a time, signs cleared
             const auto pair = [](uint32_t u) {
                 u &= 0x7FFF7FFFu;
@@ -72,7 +74,7 @@ struct Sixteen {
             };
             const auto word = [&](const uint4& w) { return __hmax2(__hmax2(pair(w.x), pair(w.y)), __hmax2(pair(w.z), pair(w.w))); };
             const __nv_bfloat162 m = __hmax2(word(q[0]), word(q[1]));
-            return fmaxf(__low2float(m), __high2float(m));
+            return fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f);
         } else {
             float m = 0.f;
 #pragma unroll
@@ -90,11 +92,19 @@ struct Sixteen {
             return f[j % PER];
         }
     }
-    __device__ __forceinline__ uint4 codes(float inv) const {
+    // Codes of numbers in a block whose largest size is `top` and scale s.  The conversion saturates: an infinity, which
+    // no code stands for, is made a NaN before it.
+    __device__ __forceinline__ uint4 codes(float top, float s) const {
+        const float inv = block_inverse(s);
+        if (top == INFINITY) return each([=](float x) { return fabsf(x) == INFINITY ? NAN : x * inv; });
+        return each([=](float x) { return x * inv; });
+    }
+    template <typename F>
+    __device__ __forceinline__ uint4 each(F f) const {
         uint32_t c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            c[i] = e4m3_four(number(4 * i) * inv, number(4 * i + 1) * inv, number(4 * i + 2) * inv, number(4 * i + 3) * inv);
+            c[i] = e4m3_four(f(number(4 * i)), f(number(4 * i + 1)), f(number(4 * i + 2)), f(number(4 * i + 3)));
         return make_uint4(c[0], c[1], c[2], c[3]);
     }
 };
@@ -139,8 +149,8 @@ __global__ void __launch_bounds__(kQuantThreads) ds_quantise_rows_kernel(const Q
     }
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-        const float s = block_scale(lanes_max<8>(v[i].most()));
-        const uint4 c = v[i].codes(block_inverse(s));
+        const float top = lanes_max<8>(v[i].most()), s = block_scale(top);
+        const uint4 c = v[i].codes(top, s);
         if constexpr (!GATHER) {
             const int64_t row = row0 + (i << down);
             if (row >= all_rows || block >= p.blocks) continue;  // (the warp stays whole for its shuffles)
@@ -192,11 +202,11 @@ __global__ void __launch_bounds__(kQuantThreads) ds_quantise_tiles_kernel(const 
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kQuantThreads / 32; ++w) top = fmaxf(top, sh_max[w]);
-    const float s = block_scale(top), inv = block_inverse(s);
+    const float s = block_scale(top);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int64_t r = row0 + team + i * TEAMS;
-        if (r < p.rows) store_sixteen<VEC>(p.codes + (m * p.rows + r) * p.K, block * 128, p.K, sub, v[i].codes(inv));
+        if (r < p.rows) store_sixteen<VEC>(p.codes + (m * p.rows + r) * p.K, block * 128, p.K, sub, v[i].codes(top, s));
     }
     if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
 }
