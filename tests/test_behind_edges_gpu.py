@@ -1,6 +1,6 @@
 """The operators behind the selections at the ends of their ranges, on the GPU against their
 definitions in 64 bits: logits of any size, numbers that are none, a kernel that gives
-up, and offsets in no order."""
+up, offsets in no order, and the products' gradient."""
 import math
 
 import pytest
@@ -294,3 +294,42 @@ def test_product_of_offsets_in_no_order(ds, dtype, T, E, N, K):
     base.check_product(out, want, size, K, dtype)
     product([2 ** 31 - 1] * (E + 1))               # all rows before the first expert
     assert not bool(out.any())
+
+
+# ------------------------------------------------------------------ the products' gradient ----
+
+@pytest.mark.parametrize("T,E,N,K", [(37, 3, 144, 272), (700, 4, 400, 512), (9, 1, 2048, 128)])
+def test_gradient_of_the_products_rows(ds, T, E, N, K):
+    """The gradient with respect to the rows: the outputs' gradient in 8 bits along N, times the transposed codes and
+    scales, against 64 bits of the same codes, and against differences of the product itself."""
+    g = gen(T + N)
+    x, xs, w, ws = base.operands(g, T, E, N, K)
+    ws = ws * 2.0 ** -10
+    offsets = base.spread(g, T, E, 0.0)
+    grad = normal(g, T, N)
+    codes, scales = ds.quantise_blocks(grad)
+    w_t, ws_t = w.transpose(1, 2).contiguous(), ws.transpose(1, 2).contiguous()
+    got = ds.expert_product(codes, scales, w_t, ws_t, offsets, dtype=torch.float32)
+    # grad_x[r, k] = sum_n grad[r, n] w[e, n, k]: the definition, of the codes' values
+    tall, wide = torch.arange(N, device="cuda") // 128, torch.arange(K, device="cuda") // 128
+    back = codes.double() * scales.double()[:, tall]
+    want, size = torch.zeros(T, K, dtype=torch.float64, device="cuda"), torch.zeros(T, K, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        m = w[e].double() * ws[e].double()[tall][:, wide]
+        want[a:b], size[a:b] = back[a:b] @ m, back[a:b].abs() @ m.abs()
+    base.check_product(got, want, size, N, torch.float32)
+    # linear in the rows: a step of one code's value along k gives that column of the weights
+    def f(x):
+        return (back * ds.expert_product(x, xs, w, ws, offsets, dtype=torch.float32).double()).sum(-1)
+    for k in (0, K // 2, K - 1):
+        up, down = x.float(), x.float()
+        up[:, k], down[:, k] = 8.0, -8.0
+        slope = (f(up.to(x.dtype)) - f(down.to(x.dtype))) / (16.0 * xs.double()[:, k // 128])
+        # each f is off by its product's error, (blocks + 11) 2^-23 of its sizes, summed over N
+        for r in {0, T // 2, T - 1}:
+            e = int((offsets[1:] <= r).sum())
+            m = w[e].double() * ws[e].double()[tall][:, wide]
+            sizes = (back[r].abs() * (m.abs() @ (x[r].double().abs().clamp(min=8.0) * xs[r].double()[wide]))).sum()
+            off = 2 * (-(-K // 128) + 11) * 2 * U * sizes / (16.0 * xs[r, k // 128].double())
+            assert abs(float(slope[r] - want[r, k])) <= float(off)

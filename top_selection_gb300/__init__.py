@@ -655,6 +655,94 @@ def expert_product(x, x_scales, w, w_scales, offsets=None, dtype=None, stream=No
     ceil(N / 128), ceil(K / 128)), any float32 scales; ``offsets`` (experts + 1,) int32, ``expert_sort``'s
     -- None, with w (N, K) or one expert, for all rows.  K is a multiple of 16.  Returns (rows, N) in
     ``dtype`` (bfloat16, the default, or float32); rows outside the offsets are zeros.  The weights
+    are constants.  The gradient with respect to x is the same product: the outputs' gradient in 8 bits along N
+    (``quantise_blocks(grad)``, N a multiple of 16), times w transposed -- codes and the 128 x 128 blocks' scales alike,
+    ``w.transpose(1, 2).contiguous()`` and ``w_scales.transpose(1, 2).contiguous()``, laid out once."""
+    ops = _binding or _load_binding()
+    if dtype is not None and str(dtype) not in ("torch.bfloat16", "torch.float32"):
+        raise TypeError(f"dtype: unsupported dtype {dtype}: bfloat16 and float32 only")
+    return ops.cache_load(cache, scales, slots, str(dtype) == "torch.float32", stream)
+
+
+def cache_attention(q, cache, scales, table, lens, indices=None, scale=None, stream=None):
+    """Attention of each sequence's newest tokens ``q`` (B, Q, query heads, D) over a 4-bit cache.
+
+    ``table`` (B, width) int32 holds the page of each run of ``page`` positions, ``lens`` (B,) int32
+    the positions stored, the Q new ones among them: token i sees those below lens - (Q - 1 - i),
+    or those of them that ``indices`` (B, Q, K) int32 lists (``topk``'s columns; -1 pads).  ``scale``
+    is 1 / sqrt(D) by default.  Returns (out (B, Q, query heads, D) in q's dtype, lse (B, Q, query
+    heads) float32); a token that sees nothing gives 0 and -inf."""
+    return (_binding or _load_binding()).cache_attention(q, cache, scales, table, lens, indices, scale, stream)
+
+
+# --------------------------------------------- behind the selections ----------------
+
+def token_logprobs(logits, tokens, top: int = 0, stream=None):
+    """The log probability of each row's given token under the softmax of ``logits`` (rows, V), with
+    the distribution's entropy and its ``top`` likeliest tokens.
+
+    ``tokens`` (rows,) int32; one outside [0, V) stands for none: 0, without a gradient.  Returns
+    (logprobs (rows,), lse (rows,), entropy (rows,), top_logprobs (rows, top), top_tokens (rows, top)
+    int32), float32, the likeliest first, ties to the lower token; ``top`` is at most 32.  A NaN or +inf
+    logit makes its row's results NaN, and NaN tokens lead its top.  The
+    results carry no autograd history: ``token_logprobs_backward`` gives their gradient."""
+    return (_binding or _load_binding()).token_logprobs(logits, tokens, top, stream)
+
+
+def token_logprobs_backward(grad_logprobs, logits, tokens, lse, grad_entropy=None, entropy=None, stream=None):
+    """The gradient of ``token_logprobs``' log probabilities, and of its entropies with
+    ``grad_entropy`` (rows,) and the ``entropy`` it gave, with respect to its ``logits``: (rows, V) in
+    the logits' dtype.  ``lse`` is the one it gave."""
+    return (_binding or _load_binding()).token_logprobs_backward(grad_logprobs, logits, tokens, lse, grad_entropy, entropy,
+                                                                 stream)
+
+
+def expert_sort(experts, E: int, stream=None):
+    """Ranks the choices ``experts`` (tokens, k) int32 of a gate of ``E`` experts (``route``'s) by
+    expert, equal ones by token and choice; one outside [0, E) is no choice (a padded token).
+
+    Returns (places (tokens, k) int32 -- each choice's rank, -1 for none -- and offsets (E + 1,)
+    int32: each expert's first rank, then the number of choices)."""
+    return (_binding or _load_binding()).expert_sort(experts, E, stream)
+
+
+def expert_gather(x, places, offsets, quantise: bool = False, stream=None):
+    """The rows of ``x`` (tokens, D) in the order of the experts: row ``places[t, i]`` of the result
+    (tokens * k, D) is row t; rows behind the last choice are zeros.  Its gradient is
+    ``expert_combine`` without weights.  With ``quantise`` the rows come in 8 bits, as
+    ``quantise_blocks`` gives them: (codes, scales)."""
+    return (_binding or _load_binding()).expert_gather(x, places, offsets, quantise, stream)
+
+
+def expert_combine(y, places, weights=None, stream=None):
+    """The experts' outputs ``y`` (tokens * k, D) back at their tokens: (tokens, D) sums of
+    ``weights[t, i] * y[places[t, i]]`` (weights (tokens, k) float32, None: 1), in y's dtype.  Its
+    gradient is ``expert_combine_backward``."""
+    return (_binding or _load_binding()).expert_combine(y, places, weights, stream)
+
+
+def expert_combine_backward(grad, y, places, offsets, weights, stream=None):
+    """The gradients of ``expert_combine``'s result with respect to ``y`` and ``weights``, for its
+    gradient ``grad`` (tokens, D): ((tokens * k, D) in y's dtype, zeros behind the last choice, and
+    (tokens, k) float32)."""
+    return (_binding or _load_binding()).expert_combine_backward(grad, y, places, offsets, weights, stream)
+
+
+def quantise_blocks(x, block_rows: int = 1, stream=None):
+    """``x`` (rows, K) or (matrices, rows, K) in 8 bits: (codes float8_e4m3fn of x's shape, scales
+    float32), a scale for each ``block_rows`` (1 or 128) x 128 numbers, the least power of two that
+    brings their largest to 448 or below.  A code stands for code * scale; infinities and NaN become NaN."""
+    return (_binding or _load_binding()).quantise_blocks(x, block_rows, stream)
+
+
+def expert_product(x, x_scales, w, w_scales, offsets=None, dtype=None, stream=None):
+    """Rows sorted by expert times each expert's weights, both in 8 bits.
+
+    ``x`` (rows, K) float8_e4m3fn and ``x_scales`` (rows, ceil(K / 128)) as ``expert_gather`` or
+    ``quantise_blocks`` give them; ``w`` (experts, N, K) float8_e4m3fn with ``w_scales`` (experts,
+    ceil(N / 128), ceil(K / 128)), any float32 scales; ``offsets`` (experts + 1,) int32, ``expert_sort``'s
+    -- None, with w (N, K) or one expert, for all rows.  K is a multiple of 16.  Returns (rows, N) in
+    ``dtype`` (bfloat16, the default, or float32); rows outside the offsets are zeros.  The weights
     are constants: the gradient with respect to x is the same product of the outputs' gradient with
     w transposed, whose 128 x 128 blocks' scales are the transposed ones."""
     ops = _binding or _load_binding()
