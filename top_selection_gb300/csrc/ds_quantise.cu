@@ -10,7 +10,6 @@
 // blocks of 128 x 128 in 94.5 (6.9), bf16 in 56.9.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
 #include "ds_common.cuh"
@@ -23,6 +22,8 @@ namespace dsk {
 constexpr int kQuantThreads = 256;
 constexpr int kQuantMaxE = 512, kQuantMaxK = 32;
 constexpr int kQuantMaxColumns = 1 << 26;  // 32768 runs of 16 blocks (a grid has 65535); columns are counted in 32 bits
+
+constexpr float kMostScale = 1329227995784915872903807060280344576.f;  // 2^120, of a block that holds an infinity
 
 struct QuantParams {
     const void* x;
@@ -92,19 +93,19 @@ struct Sixteen {
             return f[j % PER];
         }
     }
-    // Codes of numbers in a block whose largest size is `top` and scale s.  The conversion saturates: an infinity, which
-    // no code stands for, is made a NaN before it.
-    __device__ __forceinline__ uint4 codes(float top, float s) const {
+    // Codes of numbers in a block of scale s.  The conversion saturates, and no code stands for an infinity: at
+    // s = 2^120 finite numbers are 2^8 at most, so that 448 (0x7E) there is an infinity, and becomes NaN (0x7F).
+    // (A select for each number instead: ALU 64 % instead of 40, gathers 2 % slower.)
+    __device__ __forceinline__ uint4 codes(float s) const {
         const float inv = block_inverse(s);
-        if (top == INFINITY) return each([=](float x) { return fabsf(x) == INFINITY ? NAN : x * inv; });
-        return each([=](float x) { return x * inv; });
-    }
-    template <typename F>
-    __device__ __forceinline__ uint4 each(F f) const {
         uint32_t c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            c[i] = e4m3_four(f(number(4 * i)), f(number(4 * i + 1)), f(number(4 * i + 2)), f(number(4 * i + 3)));
+            c[i] = e4m3_four(number(4 * i) * inv, number(4 * i + 1) * inv, number(4 * i + 2) * inv, number(4 * i + 3) * inv);
+        if (s == kMostScale) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] |= (((c[i] & 0x7F7F7F7Fu) + 0x02020202u) >> 7) & 0x01010101u;
+        }
         return make_uint4(c[0], c[1], c[2], c[3]);
     }
 };
@@ -149,8 +150,8 @@ __global__ void __launch_bounds__(kQuantThreads) ds_quantise_rows_kernel(const Q
     }
 #pragma unroll
     for (int i = 0; i < UNITS; ++i) {
-        const float top = lanes_max<8>(v[i].most()), s = block_scale(top);
-        const uint4 c = v[i].codes(top, s);
+        const float s = block_scale(lanes_max<8>(v[i].most()));
+        const uint4 c = v[i].codes(s);
         if constexpr (!GATHER) {
             const int64_t row = row0 + (i << down);
             if (row >= all_rows || block >= p.blocks) continue;  // (the warp stays whole for its shuffles)
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kQuantThreads) ds_quantise_tiles_kernel(const 
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int64_t r = row0 + team + i * TEAMS;
-        if (r < p.rows) store_sixteen<VEC>(p.codes + (m * p.rows + r) * p.K, block * 128, p.K, sub, v[i].codes(top, s));
+        if (r < p.rows) store_sixteen<VEC>(p.codes + (m * p.rows + r) * p.K, block * 128, p.K, sub, v[i].codes(s));
     }
     if (threadIdx.x == 0) p.scales[blockIdx.x] = s;
 }
