@@ -14,10 +14,11 @@
 // distinct.  A row's parts on the CTAs of a cluster are joined by the first, over distributed shared
 // memory, in a fixed order.
 //
-// Long rows are bound by memory (2048 x 129280 bf16: 88 us, 87 % of the copy rate; the gradient 153 us for
+// Long rows are bound by memory (2048 x 129280 bf16: 89 us, 88 % of the copy rate; the gradient 153 us for
 // reading and writing it, the copy rate), short ones by their starts and barriers (4099 x 32003 bf16: 49 us, 79 %),
-// and the top by the cuts' barriers and single steps: 64 us with one token, 85 with 20 (numbers listed one
-// by one: 126).  One row of 129280 fp32 numbers on 16 CTAs takes 2.8 us, with 20 tokens 7.7.  Tried and not kept:
+// and the top by the cuts' barriers and single steps: 66 us with one token, 88 with 20 (numbers listed one
+// by one: 126).  One row of 129280 fp32 numbers on 16 CTAs takes 2.7 us, with 20 tokens 7.9.  Terms from one fma,
+// x log2 e - m log2 e, took 1 % less of the rows with a top, and lost all digits of rows of large logits.  Tried and not kept:
 // rings of bulk copies in shared memory (registers for 20 warps an SM: 84 us with one token), a warp to a row (73),
 // one warp that cuts while the others go on (85), CTAs that take rows in turn with the next row's first words on
 // their way (77).

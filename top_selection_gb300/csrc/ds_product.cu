@@ -17,8 +17,9 @@
 // Few tiles: the CTAs of a cluster split a tile's blocks, and add their sums over distributed shared
 // memory in a fixed order.
 //
-// 32768 rows over 64 experts of 4096 x 2048: 277 us, 1985 TFLOP/s (8192 rows by 8192 x 8192: 2385; cuBLAS
-// reaches 1895 on bf16), the tensor pipe at half; with experts of few rows the weights' bytes bound it (512 rows
+// 32768 rows over 64 experts of 4096 x 2048: 277 us, 1985 TFLOP/s, in a short graph, 310 us one call after another
+// (1.77 PFLOP/s, at the power limit's clock); 8192 rows by 8192 x 8192: 2385 TFLOP/s (cuBLAS reaches 1895 on
+// bf16); the tensor pipe at half; with experts of few rows the weights' bytes bound it (512 rows
 // over 64 experts of 2048 x 4096: 90 us, 6.0 TB/s).  Wide tiles are stored by bulk copies from shared memory while
 // the next tile is multiplied: stores of 32 bytes a lane took 46 us of 293, and a stage of loads is given up
 // for it (four stages instead of three: 8192 x 8192 x 8192 in 438 us, the others the same).  A block of a
